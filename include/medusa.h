@@ -589,6 +589,149 @@ MEDUSA_API medusa_status medusa_step_run(medusa_step_exec *exec, medusa_stream s
 MEDUSA_API medusa_status medusa_step_wait(medusa_step_exec *exec, medusa_stream stream);
 MEDUSA_API void medusa_step_destroy(medusa_step_exec *exec);
 
+/* ------------------------------------------------------------------------
+ * 8. Norms of queries and keys and the position rotation, in one pass.
+ *
+ * The pages leave the rotation to the caller (tree_attention reads q and K
+ * as they are, with the tree's pos_id at hand); this is that step.  For
+ * every head vector x of row (b, i), at position p = pos[b][i]:
+ *     y = x / sqrt(mean(x^2) + eps) * weight         if norm (else y = x)
+ *     (y_a, y_b) -> (y_a cos t - y_b sin t, y_a sin t + y_b cos t),
+ *     t = p * inv_freq[j],  j = 0 .. rot/2 - 1
+ * for the pairs (a, b) = (j, j + rot/2), or (2j, 2j+1) if interleaved;
+ * elements from rot on are not rotated.  Angles are exact to about 2^-23 of a
+ * turn at every position.
+ *
+ *   q [B,R,H,dh], k [B,R,Hkv,dh] dtype; consecutive rows lie q_stride and
+ *            k_stride elements apart (H*dh and Hkv*dh when dense; more when
+ *            q, k and v are slices of one projection), a multiple of 16 bytes
+ *   q_weight, k_weight [dh] dtype, or NULL for ones; NULL without norm
+ *   pos      [B,R] int32, any sign (the tree's pos_id)
+ *   inv_freq [rot/2] fp32 (device), radians per position
+ *   n_rows   [B] int32 (device) or NULL: rows i >= n_rows[b] are not read and
+ *            their outputs are left as they were
+ *   q_out [B,R,H,dh], k_out [B,R,Hkv,dh] dtype, dense; q_out may be q and
+ *            k_out may be k (dense), no other overlap
+ * Requirements: H <= 1024, a multiple of Hkv; dh in {64,128}; rot a multiple
+ * of 16 in 0..dh; eps >= 0; pointers 16-byte aligned.
+ *
+ * medusa_qk_norm_rope_append writes the finished K rows, and copies the V
+ * rows [B,R,Hkv,dh] (v_stride apart), into sequence b's cache slots
+ * prefix_len[b] + i instead of k_out: the caches of medusa_tree_attention,
+ * [>= P_max+R, Hkv, dh] dtype.  A prefix outside 0..P_max
+ * (MEDUSA_DEV_BAD_PREFIX) or a bad cache pointer (MEDUSA_DEV_BAD_CACHE)
+ * leaves that sequence's outputs and caches untouched.  Workspace:
+ * MEDUSA_WS_HEADER bytes (the status word).
+ * ---------------------------------------------------------------------- */
+MEDUSA_API medusa_status medusa_qk_norm_rope(
+    medusa_dtype dtype, const void *q, const void *k, int64_t q_stride, int64_t k_stride,
+    const void *q_weight, const void *k_weight, float eps, int norm, const int32_t *pos,
+    const float *inv_freq, int rot, int interleaved, const int32_t *n_rows, int B, int R, int H,
+    int Hkv, int dh, void *q_out, void *k_out, medusa_stream stream);
+
+MEDUSA_API medusa_status medusa_qk_norm_rope_append(
+    medusa_dtype dtype, const void *q, const void *k, const void *v, int64_t q_stride,
+    int64_t k_stride, int64_t v_stride, const void *q_weight, const void *k_weight, float eps,
+    int norm, const int32_t *pos, const float *inv_freq, int rot, int interleaved,
+    const int32_t *n_rows, void *const *k_cache, void *const *v_cache, const int32_t *prefix_len,
+    int P_max, int B, int R, int H, int Hkv, int dh, void *q_out, void *ws, size_t ws_bytes,
+    medusa_stream stream);
+
+/* ------------------------------------------------------------------------
+ * 9. Tree attention with a sliding window and sinks, grouped KV heads.
+ *
+ * medusa_tree_attention with a bounded reach.  Prefix slot j is position j,
+ * tree slot P_b + t position P_b + depth[b][t].  Row i, at position
+ * p = P_b + depth[b][i], sees
+ *     prefix slot j    iff  j < sinks  or  p - j < window
+ *     tree slot P_b+t  iff  bit t of anc_mask[b,i] is set and
+ *                           (P_b + depth[t] < sinks or p - (P_b + depth[t]) < window)
+ * window = 0: no bound (sinks must be 0, depth may be NULL).  The work does
+ * not grow with the prefix: only sinks + window - 1 + R slots are read.
+ * Query head h reads KV head h / (H / Hkv).  A row that sees nothing gets
+ * zeros.  What slots hold that a row does not see (infinities and NaNs
+ * included) does not change that row.
+ *
+ *   q, out   [B,R,H,dh] dtype; caches [>= P_b+R, Hkv, dh] dtype
+ *   depth    [B,R] int32 from medusa_build_tree; outside 0..R-1:
+ *            MEDUSA_DEV_BAD_DEPTH, and the value counts as the nearest bound
+ * Other arguments as medusa_tree_attention.  A prefix outside 0..P_max or a
+ * bad cache pointer sets the status and gives that sequence zeros.
+ * Requirements: R <= 256; H <= 1024, a multiple of Hkv; dh in {64,128};
+ * 0 <= P_max <= 2^29; scale > 0.
+ * ---------------------------------------------------------------------- */
+MEDUSA_API size_t medusa_tree_attention_window_workspace_size(medusa_dtype dtype, int B, int R,
+                                                              int H, int Hkv, int dh, int P_max,
+                                                              int window, int sinks);
+
+MEDUSA_API medusa_status medusa_tree_attention_window(
+    medusa_dtype dtype, const void *q, const void *const *k_cache, const void *const *v_cache,
+    const int32_t *prefix_len, int P_max, const uint64_t *anc_mask, const int32_t *depth,
+    int window, int sinks, int B, int R, int H, int Hkv, int dh, float scale, void *out, void *ws,
+    size_t ws_bytes, medusa_stream stream);
+
+/* ------------------------------------------------------------------------
+ * 10. The cache in 4 bits.
+ *
+ * One cache row (one slot) of medusa_kv4_row_bytes(Hkv, dh) bytes holds, head
+ * after head, Hkv*dh/2 bytes of e2m1 codes (two a byte, the lower element in
+ * the lower half), then Hkv*dh/16 e4m3 scales, one for 16 consecutive
+ * elements, and padding up to a multiple of 16 bytes.  A block x is stored as
+ *     s = e4m3 nearest to max|x| / 6 (ties to even, at most 448),
+ *     c = e2m1 nearest to x / s      (ties to even, at most 6; 0 if s = 0)
+ * and stands for c * s, exact in bf16.  A block that holds an infinity or a
+ * NaN is stored as NaN.  A sequence's K (and V) cache is
+ * [>= P_max+R][row bytes], 16-byte aligned, named by the same arrays of
+ * device pointers as the other caches; Hkv*dh*9/8 bytes a slot for K and V
+ * against Hkv*dh*4 in bf16.
+ *
+ *   medusa_kv4_append   rows k, v [B,R,Hkv,dh] dtype (k_stride, v_stride
+ *       elements apart) into slots prefix_len[b] + i
+ *   medusa_kv4_unpack   the values of slots prefix_len[b] + i into dense
+ *       k_out, v_out [B,R,Hkv,dh] dtype
+ *   n_rows [B] int32 (device) or NULL: rows i >= n_rows[b] are left alone
+ *   medusa_commit_kv4   medusa_commit_kv on these rows
+ *   medusa_tree_attention_kv4   medusa_tree_attention_window on these rows
+ *       (window = 0: the whole prefix); q and out are dtype.  The values
+ *       enter the products exactly; bf16 q is scaled by a power of two for
+ *       each row into fp16, where its elements keep their eight bits down to
+ *       2^-14 of the row's largest.
+ * A prefix outside 0..P_max or a bad cache pointer sets the status and leaves
+ * that sequence untouched (attention: zeros).  Requirements: dh in {64,128};
+ * append and unpack: R <= 65535; attention and commit: R <= 256.  Workspace of
+ * append, unpack and commit: MEDUSA_WS_HEADER bytes.
+ * ---------------------------------------------------------------------- */
+MEDUSA_API size_t medusa_kv4_row_bytes(int Hkv, int dh);
+
+MEDUSA_API medusa_status medusa_kv4_append(medusa_dtype dtype, const void *k, const void *v,
+                                           int64_t k_stride, int64_t v_stride,
+                                           void *const *k_cache, void *const *v_cache,
+                                           const int32_t *prefix_len, int P_max,
+                                           const int32_t *n_rows, int B, int R, int Hkv, int dh,
+                                           void *ws, size_t ws_bytes, medusa_stream stream);
+
+MEDUSA_API medusa_status medusa_kv4_unpack(medusa_dtype dtype, const void *const *k_cache,
+                                           const void *const *v_cache, const int32_t *prefix_len,
+                                           int P_max, const int32_t *n_rows, int B, int R, int Hkv,
+                                           int dh, void *k_out, void *v_out, void *ws,
+                                           size_t ws_bytes, medusa_stream stream);
+
+MEDUSA_API medusa_status medusa_commit_kv4(void *const *k_cache, void *const *v_cache,
+                                           const int32_t *prefix_len, const int32_t *path,
+                                           const int32_t *accept_len, int B, int K, int R, int Hkv,
+                                           int dh, int32_t *new_prefix_len, void *ws,
+                                           size_t ws_bytes, medusa_stream stream);
+
+MEDUSA_API size_t medusa_tree_attention_kv4_workspace_size(medusa_dtype dtype, int B, int R, int H,
+                                                           int Hkv, int dh, int P_max, int window,
+                                                           int sinks);
+
+MEDUSA_API medusa_status medusa_tree_attention_kv4(
+    medusa_dtype dtype, const void *q, const void *const *k_cache, const void *const *v_cache,
+    const int32_t *prefix_len, int P_max, const uint64_t *anc_mask, const int32_t *depth,
+    int window, int sinks, int B, int R, int H, int Hkv, int dh, float scale, void *out, void *ws,
+    size_t ws_bytes, medusa_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -8,7 +8,8 @@ the compiled library is missing, importing the calls fails loudly.
 
 Public calls (same names as the C ABI in include/medusa.h):
     heads, heads_lm, heads_sample, heads_noalloc, build_tree, build_tree_static, tree_attention, evaluate_posterior,
-    speculative_posterior, commit_kv, evaluate_posterior_commit
+    speculative_posterior, commit_kv, evaluate_posterior_commit, qk_norm_rope, qk_norm_rope_append,
+    tree_attention_window, kv4_append, kv4_unpack, commit_kv4, tree_attention_kv4
 plus workspace-size queries, device-status helpers, launch_count,
 ``StepExecutor`` (medusa_step_create / medusa_step_run: the whole step, input
 copies included, issued by one native call), and ``StepGraph``, which
@@ -17,6 +18,7 @@ replays it per step.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -53,7 +55,11 @@ EXPORTS = ("medusa_status_string", "medusa_last_error", "medusa_launch_count",
            "medusa_evaluate_posterior_commit", "medusa_commit_kv", "medusa_heads_sample",
            "medusa_speculative_workspace_size", "medusa_speculative_posterior",
            "medusa_step_desc_size", "medusa_step_create", "medusa_step_run",
-           "medusa_step_wait", "medusa_step_destroy")
+           "medusa_step_wait", "medusa_step_destroy",
+           "medusa_qk_norm_rope", "medusa_qk_norm_rope_append",
+           "medusa_tree_attention_window_workspace_size", "medusa_tree_attention_window",
+           "medusa_kv4_row_bytes", "medusa_kv4_append", "medusa_kv4_unpack", "medusa_commit_kv4",
+           "medusa_tree_attention_kv4_workspace_size", "medusa_tree_attention_kv4")
 
 
 class _Copy(ctypes.Structure):
@@ -99,7 +105,7 @@ def lib() -> ctypes.CDLL:
             "`python -c 'import __graft_entry__ as g; g.build()'` (needs nvcc, sm_103a)")
     L = ctypes.CDLL(LIB_PATH)
     P, I, F, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
-    U64 = ctypes.c_uint64
+    U64, I64 = ctypes.c_uint64, ctypes.c_int64
     sig = {
         "medusa_status_string": ([I], ctypes.c_char_p),
         "medusa_last_error": ([], ctypes.c_char_p),
@@ -131,7 +137,19 @@ def lib() -> ctypes.CDLL:
         "medusa_step_run": ([P, P, I], I),
         "medusa_step_wait": ([P, P], I),
         "medusa_step_destroy": ([P], None),
+        "medusa_qk_norm_rope": ([I, P, P, I64, I64, P, P, F, I, P, P, I, I, P, I, I, I, I, I, P, P,
+                                 P], I),
+        "medusa_qk_norm_rope_append": ([I, P, P, P, I64, I64, I64, P, P, F, I, P, P, I, I, P, P, P, P,
+                                        I, I, I, I, I, I, P, P, S, P], I),
+        "medusa_kv4_row_bytes": ([I, I], S),
+        "medusa_kv4_append": ([I, P, P, I64, I64, P, P, P, I, P, I, I, I, I, P, S, P], I),
+        "medusa_kv4_unpack": ([I, P, P, P, I, P, I, I, I, I, P, P, P, S, P], I),
+        "medusa_commit_kv4": ([P, P, P, P, P, I, I, I, I, I, P, P, S, P], I),
     }
+    for kind in ("window", "kv4"):
+        sig[f"medusa_tree_attention_{kind}_workspace_size"] = ([I] * 9, S)
+        sig[f"medusa_tree_attention_{kind}"] = ([I, P, P, P, P, I, P, P, I, I, I, I, I, I, I, F, P, P,
+                                                 S, P], I)
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
         fn.argtypes = args
@@ -534,6 +552,268 @@ def speculative_posterior(logits, tokens, draft_logits, temperature: float, seed
         float(temperature), int(seed), int(step), _ptr(out.accept_len), _ptr(out.path_tokens),
         _ptr(out.next_token), _ptr(out.accept), _ptr(ws), ws.numel(), _stream(stream)))
     return out
+
+
+# ------------------------------------------- rotation, 4-bit cache, windows ---
+
+def _on_device(ref: torch.Tensor, stream, **tensors):
+    """Argument checks shared by the calls below: CUDA tensors, all on the
+    current device; returns the stream to launch on.  The names of int32 /
+    int64 arrays end in _i32 / _i64."""
+    dev = ref.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError("tensors must be on the current CUDA device")
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.get_device() != dev:
+            raise ValueError(f"{name.rsplit('_i', 1)[0]} must be a CUDA tensor on the same device")
+        want = (torch.int32 if name.endswith("_i32") else torch.int64 if name.endswith("_i64")
+                else torch.float32 if name.endswith("_f32") else None)
+        if want is not None and (t.dtype != want or not t.is_contiguous()):
+            raise ValueError(f"{name[:-4]} must be contiguous and {want}")
+    return torch.cuda.current_stream() if stream is None else stream
+
+
+def _size_is(t: Optional[torch.Tensor], n: int, name: str):
+    if t is not None and t.numel() != n:
+        raise ValueError(f"{name} must hold {n} elements, got {tuple(t.shape)}")
+
+
+def _rows(t: torch.Tensor, name: str):
+    """Row stride in elements of [B,R,heads,dh] rows: heads and dh dense, all
+    rows evenly apart (a dense tensor, or a slice of a wider projection)."""
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [B,R,heads,dh]")
+    B, R, H, dh = t.shape
+    s = t.stride()
+    if s[3] != 1 or (H > 1 and s[2] != dh) or (B > 1 and R > 1 and s[0] != R * s[1]):
+        raise ValueError(f"{name}: heads must be dense and rows evenly apart")
+    return s[1] if R > 1 else s[0] if B > 1 else H * dh
+
+
+def _issue_on(stream):
+    """Allocations belong to the stream that uses them, so that their memory is
+    not handed out again while that stream still works on it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _scratch(ws, nbytes: int, device, stream):
+    """The caller's workspace, or one made on the launch stream with the status
+    word at 0 (the rest needs no clearing)."""
+    if ws is not None:
+        return ws
+    with _issue_on(stream):
+        t = torch.empty((max(int(nbytes), WS_HEADER) + 255) // 256 * 256, dtype=torch.uint8,
+                        device=device)
+        t[:WS_HEADER].zero_()
+    return t
+
+
+def _new(stream, like: torch.Tensor, shape=None, dtype=None):
+    """An output tensor made on the launch stream."""
+    with _issue_on(stream):
+        return torch.empty(like.shape if shape is None else shape, dtype=dtype or like.dtype,
+                           device=like.device)
+
+
+def _out(t: torch.Tensor, like: torch.Tensor, name: str, shape=None):
+    if t.shape != (like.shape if shape is None else shape) or t.dtype != like.dtype \
+            or not t.is_contiguous() or t.get_device() != like.get_device():
+        raise ValueError(f"{name} must be a dense {like.dtype} tensor of "
+                         f"{tuple(like.shape if shape is None else shape)} on the same device")
+
+
+def _rope_args(q, k, pos, inv_freq, q_weight, k_weight, norm, n_rows):
+    B, R, H, dh = q.shape
+    dt = _dtype(q)
+    if k.dtype != q.dtype or k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != dh:
+        raise ValueError("k must be [B,R,Hkv,dh] of q's dtype")
+    _size_is(pos, B * R, "pos")
+    _size_is(n_rows, B, "n_rows")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _size_is(w, dh, name)
+            if w.dtype != q.dtype or not w.is_contiguous():
+                raise ValueError(f"{name} must be contiguous and of q's dtype")
+    return dt, B, R, H, k.shape[2], dh
+
+
+def qk_norm_rope(q, k, pos, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 norm: bool = True, interleaved: bool = False, n_rows=None, out=None, stream=None):
+    """Per-head RMS norms of q [B,R,H,dh] and k [B,R,Hkv,dh] and their rotation to
+    the positions ``pos`` (int32 [B,R], e.g. ``Tree.pos_id``), in one pass.
+    ``inv_freq`` (fp32 [rot/2]) holds radians per position; ``norm=False``
+    rotates only.  q and k may be slices of one wider projection.  Rows
+    i >= n_rows[b] are left alone.  Returns (q_out, k_out), ``out`` if given
+    (it may be (q, k))."""
+    dt, B, R, H, Hkv, dh = _rope_args(q, k, pos, inv_freq, q_weight, k_weight, norm, n_rows)
+    s = _on_device(q, stream, k=k, pos_i32=pos, inv_freq_f32=inv_freq, q_weight=q_weight,
+                   k_weight=k_weight, n_rows_i32=n_rows)
+    if out is None:
+        out = (_new(stream, q), _new(stream, k))
+    qo, ko = out
+    _out(qo, q, "q_out")
+    _out(ko, k, "k_out")
+    _check(lib().medusa_qk_norm_rope(dt, _ptr(q), _ptr(k), _rows(q, "q"), _rows(k, "k"),
+                                     _ptr(q_weight), _ptr(k_weight), eps, 1 if norm else 0, _ptr(pos),
+                                     _ptr(inv_freq), 2 * inv_freq.numel(), 1 if interleaved else 0,
+                                     _ptr(n_rows), B, R, H, Hkv, dh, _ptr(qo), _ptr(ko), s.cuda_stream))
+    return qo, ko
+
+
+def qk_norm_rope_append(q, k, v, pos, inv_freq, k_ptrs, v_ptrs, prefix_len, P_max: int,
+                        q_weight=None, k_weight=None, eps: float = 1e-6, norm: bool = True,
+                        interleaved: bool = False, n_rows=None, out=None, ws=None, stream=None):
+    """qk_norm_rope with the finished K rows, and the V rows, written into cache
+    slots prefix_len[b] + i of the caches behind k_ptrs / v_ptrs
+    ([>= P_max+R, Hkv, dh]).  Returns q_out."""
+    dt, B, R, H, Hkv, dh = _rope_args(q, k, pos, inv_freq, q_weight, k_weight, norm, n_rows)
+    if v.dtype != k.dtype or v.shape != k.shape:
+        raise ValueError("v must have k's shape and dtype")
+    s = _on_device(q, stream, k=k, v=v, pos_i32=pos, inv_freq_f32=inv_freq, q_weight=q_weight,
+                   k_weight=k_weight, n_rows_i32=n_rows, k_ptrs_i64=k_ptrs, v_ptrs_i64=v_ptrs,
+                   prefix_len_i32=prefix_len, ws=ws)
+    for t, name in ((k_ptrs, "k_ptrs"), (v_ptrs, "v_ptrs"), (prefix_len, "prefix_len")):
+        _size_is(t, B, name)
+    if out is None:
+        out = _new(stream, q)
+    _out(out, q, "out")
+    ws = _scratch(ws, WS_HEADER, q.device, stream)
+    _check(lib().medusa_qk_norm_rope_append(
+        dt, _ptr(q), _ptr(k), _ptr(v), _rows(q, "q"), _rows(k, "k"), _rows(v, "v"), _ptr(q_weight),
+        _ptr(k_weight), eps, 1 if norm else 0, _ptr(pos), _ptr(inv_freq), 2 * inv_freq.numel(),
+        1 if interleaved else 0, _ptr(n_rows), _ptr(k_ptrs), _ptr(v_ptrs), _ptr(prefix_len),
+        int(P_max), B, R, H, Hkv, dh, _ptr(out), _ptr(ws), ws.numel(), s.cuda_stream))
+    return out
+
+
+def kv4_row_bytes(Hkv: int, dh: int) -> int:
+    """Bytes of one slot of a 4-bit cache (one of K and V)."""
+    return int(lib().medusa_kv4_row_bytes(int(Hkv), int(dh)))
+
+
+def kv4_cache(slots: int, Hkv: int, dh: int, device=None) -> torch.Tensor:
+    """A zeroed 4-bit cache of one sequence: uint8 [slots, row bytes]."""
+    n = kv4_row_bytes(Hkv, dh)
+    if n == 0:
+        raise ValueError(f"Hkv={Hkv}, dh={dh}: dh must be 64 or 128, Hkv in 1..1024")
+    return torch.zeros((slots, n), dtype=torch.uint8, device=device or "cuda")
+
+
+def kv4_append(k, v, k_ptrs, v_ptrs, prefix_len, P_max: int, n_rows=None, ws=None, stream=None):
+    """Rows k, v [B,R,Hkv,dh] into slots prefix_len[b] + i of the 4-bit caches behind
+    k_ptrs / v_ptrs (see kv4_cache, at least P_max + R slots each).  Rows
+    i >= n_rows[b] are left alone."""
+    dt = _dtype(k)
+    if v.dtype != k.dtype or v.shape != k.shape:
+        raise ValueError("v must have k's shape and dtype")
+    ks, vs = _rows(k, "k"), _rows(v, "v")
+    B, R, Hkv, dh = k.shape
+    s = _on_device(k, stream, v=v, k_ptrs_i64=k_ptrs, v_ptrs_i64=v_ptrs, prefix_len_i32=prefix_len,
+                   n_rows_i32=n_rows, ws=ws)
+    for t, name in ((k_ptrs, "k_ptrs"), (v_ptrs, "v_ptrs"), (prefix_len, "prefix_len"),
+                    (n_rows, "n_rows")):
+        _size_is(t, B, name)
+    ws = _scratch(ws, WS_HEADER, k.device, stream)
+    _check(lib().medusa_kv4_append(dt, _ptr(k), _ptr(v), ks, vs, _ptr(k_ptrs), _ptr(v_ptrs),
+                                   _ptr(prefix_len), int(P_max), _ptr(n_rows), B, R, Hkv, dh,
+                                   _ptr(ws), ws.numel(), s.cuda_stream))
+
+
+def kv4_unpack(k_ptrs, v_ptrs, prefix_len, P_max: int, R: int, Hkv: int, dh: int,
+               dtype=torch.bfloat16, n_rows=None, out=None, ws=None, stream=None):
+    """The values of slots prefix_len[b] + i, i < R, of 4-bit caches: (k, v)
+    [B,R,Hkv,dh].  Rows i >= n_rows[b] are left as ``out`` has them."""
+    s = _on_device(k_ptrs, stream, k_ptrs_i64=k_ptrs, v_ptrs_i64=v_ptrs, prefix_len_i32=prefix_len,
+                   n_rows_i32=n_rows, ws=ws)
+    B = k_ptrs.numel()
+    for t, name in ((v_ptrs, "v_ptrs"), (prefix_len, "prefix_len"), (n_rows, "n_rows")):
+        _size_is(t, B, name)
+    shape = (B, int(R), int(Hkv), int(dh))
+    if out is None:
+        out = (_new(stream, k_ptrs, shape, dtype), _new(stream, k_ptrs, shape, dtype))
+    ko, vo = out
+    _out(ko, ko, "k_out", shape)
+    _out(vo, ko, "v_out", shape)
+    if ko.get_device() != k_ptrs.get_device():
+        raise ValueError("k_out must be a CUDA tensor on the same device")
+    ws = _scratch(ws, WS_HEADER, k_ptrs.device, stream)
+    _check(lib().medusa_kv4_unpack(_dtype(ko), _ptr(k_ptrs), _ptr(v_ptrs), _ptr(prefix_len),
+                                   int(P_max), _ptr(n_rows), B, int(R), int(Hkv), int(dh), _ptr(ko),
+                                   _ptr(vo), _ptr(ws), ws.numel(), s.cuda_stream))
+    return ko, vo
+
+
+def commit_kv4(k_ptrs, v_ptrs, prefix_len, path, accept_len, R: int, Hkv: int, dh: int,
+               new_prefix_len=None, ws=None, stream=None):
+    """commit_kv on 4-bit caches; returns new_prefix_len = P_b + L + 1."""
+    s = _on_device(path, stream, k_ptrs_i64=k_ptrs, v_ptrs_i64=v_ptrs, prefix_len_i32=prefix_len,
+                   path_i32=path, accept_len_i32=accept_len, new_prefix_len_i32=new_prefix_len, ws=ws)
+    B, K1 = path.shape
+    for t, name in ((k_ptrs, "k_ptrs"), (v_ptrs, "v_ptrs"), (prefix_len, "prefix_len"),
+                    (accept_len, "accept_len"), (new_prefix_len, "new_prefix_len")):
+        _size_is(t, B, name)
+    if new_prefix_len is None:
+        new_prefix_len = _new(stream, prefix_len)
+    ws = _scratch(ws, WS_HEADER, path.device, stream)
+    _check(lib().medusa_commit_kv4(_ptr(k_ptrs), _ptr(v_ptrs), _ptr(prefix_len), _ptr(path),
+                                   _ptr(accept_len), B, K1 - 1, int(R), int(Hkv), int(dh),
+                                   _ptr(new_prefix_len), _ptr(ws), ws.numel(), s.cuda_stream))
+    return new_prefix_len
+
+
+def tree_attention_window_workspace_size(dtype: int, B: int, R: int, H: int, Hkv: int, dh: int,
+                                         P_max: int, window: int = 0, sinks: int = 0,
+                                         kv4: bool = False) -> int:
+    """Workspace of tree_attention_window, or with kv4 of tree_attention_kv4."""
+    fn = (lib().medusa_tree_attention_kv4_workspace_size if kv4
+          else lib().medusa_tree_attention_window_workspace_size)
+    return int(fn(dtype, B, R, H, Hkv, dh, int(P_max), int(window), int(sinks)))
+
+
+def _cache_attention(kv4, q, k_ptrs, v_ptrs, prefix_len, P_max, anc_mask, Hkv, depth, window, sinks,
+                     scale, out, ws, stream):
+    _need(q, "q")
+    B, R, H, dh = q.shape
+    dt = _dtype(q)
+    Hkv, P_max = int(H if Hkv is None else Hkv), int(P_max)
+    s = _on_device(q, stream, k_ptrs_i64=k_ptrs, v_ptrs_i64=v_ptrs, prefix_len_i32=prefix_len,
+                   anc_mask_i64=anc_mask, depth_i32=depth, ws=ws)
+    for t, name in ((k_ptrs, "k_ptrs"), (v_ptrs, "v_ptrs"), (prefix_len, "prefix_len")):
+        _size_is(t, B, name)
+    _size_is(anc_mask, B * R * ((R + 63) // 64), "anc_mask")
+    _size_is(depth, B * R, "depth")
+    if out is None:
+        out = _new(stream, q)
+    _out(out, q, "out")
+    if ws is None:
+        ws = _scratch(None, tree_attention_window_workspace_size(dt, B, R, H, Hkv, dh, P_max, window,
+                                                                 sinks, kv4), q.device, stream)
+    fn = lib().medusa_tree_attention_kv4 if kv4 else lib().medusa_tree_attention_window
+    _check(fn(dt, _ptr(q), _ptr(k_ptrs), _ptr(v_ptrs), _ptr(prefix_len), P_max, _ptr(anc_mask),
+              _ptr(depth), int(window), int(sinks), B, R, H, Hkv, dh,
+              1.0 / math.sqrt(dh) if scale is None else float(scale), _ptr(out), _ptr(ws), ws.numel(),
+              s.cuda_stream))
+    return out
+
+
+def tree_attention_window(q, k_ptrs, v_ptrs, prefix_len, P_max: int, anc_mask, Hkv=None, depth=None,
+                          window: int = 0, sinks: int = 0, scale=None, out=None, ws=None,
+                          stream=None):
+    """Tree attention in which a row sees the last ``window`` positions up to its
+    own and the first ``sinks`` ones (window 0: everything); ``depth`` is
+    Tree.depth.  q [B,R,H,dh]; caches [>= P_b+R, Hkv, dh], query head h reads
+    KV head h // (H // Hkv)."""
+    return _cache_attention(False, q, k_ptrs, v_ptrs, prefix_len, P_max, anc_mask, Hkv, depth, window,
+                            sinks, scale, out, ws, stream)
+
+
+def tree_attention_kv4(q, k_ptrs, v_ptrs, prefix_len, P_max: int, anc_mask, Hkv=None, depth=None,
+                       window: int = 0, sinks: int = 0, scale=None, out=None, ws=None, stream=None):
+    """tree_attention_window over 4-bit caches (kv4_cache, kv4_append)."""
+    return _cache_attention(True, q, k_ptrs, v_ptrs, prefix_len, P_max, anc_mask, Hkv, depth, window,
+                            sinks, scale, out, ws, stream)
 
 
 # ------------------------------------------------------------- step graph ---

@@ -595,3 +595,279 @@ medusa_status medusa_commit_kv(medusa_dtype dtype, void *const *k_cache, void *c
 }
 
 }  // extern "C"
+
+// ------------------------------------------ rotation, 4-bit cache, windows ---
+
+namespace {
+
+constexpr int kMaxPrefix = 1 << 29;  // sums of prefix, sinks and window stay in an int
+
+bool is_dtype(medusa_dtype d) { return d == MEDUSA_F32 || d == MEDUSA_BF16; }
+
+// Shape checks shared by every call on cache rows: B sequences, R rows (at
+// most max_rows), H query heads over Hkv KV heads of dh elements.
+medusa_status check_heads_shape(const char *who, medusa_dtype dtype, int B, int R, int max_rows,
+                                int H, int Hkv, int dh) {
+    if (!is_dtype(dtype)) return fail(MEDUSA_ERR_INVALID_ARG, "%s: unknown dtype %d", who, (int)dtype);
+    if (B < 1 || B > 65535) return fail(MEDUSA_ERR_INVALID_ARG, "%s: B=%d outside 1..65535", who, B);
+    if (R < 1 || R > max_rows)
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: R=%d outside 1..%d", who, R, max_rows);
+    if (Hkv < 1 || H < Hkv || H > 1024 || H % Hkv)
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: H=%d query heads over Hkv=%d KV heads (H <= 1024, "
+                    "a multiple of Hkv)", who, H, Hkv);
+    if (dh != 64 && dh != 128)
+        return fail(MEDUSA_ERR_UNSUPPORTED, "%s: dh=%d (64 or 128)", who, dh);
+    return MEDUSA_OK;
+}
+
+medusa_status check_caches(const char *who, const void *k_cache, const void *v_cache,
+                           const void *prefix_len, int P_max) {
+    if (!k_cache || !v_cache || !prefix_len)
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+    if (!aligned16(k_cache) || !aligned16(v_cache))
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: cache pointer arrays must be 16-byte aligned", who);
+    if (P_max < 0 || P_max > kMaxPrefix)
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: P_max=%d outside 0..%d", who, P_max, kMaxPrefix);
+    return MEDUSA_OK;
+}
+
+// Distance between consecutive rows of `heads` vectors (in elements): at
+// least a row, and rows keep 16-byte alignment.
+medusa_status check_row_stride(const char *who, const char *name, medusa_dtype dtype, int64_t stride,
+                               int heads, int dh) {
+    const int64_t align = dtype == MEDUSA_BF16 ? 8 : 4;
+    if (stride < (int64_t)heads * dh || stride % align || stride > (int64_t)1 << 40)
+        return fail(MEDUSA_ERR_INVALID_ARG,
+                    "%s: %s=%lld must be at least a row (%d) and a multiple of 16 bytes", who, name,
+                    (long long)stride, heads * dh);
+    return MEDUSA_OK;
+}
+
+medusa_status check_rope(const char *who, medusa_dtype dtype, const void *q, const void *k,
+                         int64_t q_stride, int64_t k_stride, const void *q_weight,
+                         const void *k_weight, float eps, int norm, const int32_t *pos,
+                         const float *inv_freq, int rot, int B, int R, int H, int Hkv, int dh,
+                         const void *q_out) {
+    if (medusa_status s = check_heads_shape(who, dtype, B, R, 1 << 24, H, Hkv, dh)) return s;
+    if ((long long)B * R > 0x7fffffffLL)
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: B * R exceeds 2^31 - 1 rows", who);
+    if (!q || !k || !q_out || !pos) return fail(MEDUSA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+    if (rot < 0 || rot > dh || rot % 16)
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: rot=%d must be a multiple of 16 in 0..dh", who, rot);
+    if (rot && !inv_freq) return fail(MEDUSA_ERR_INVALID_ARG, "%s: NULL inv_freq", who);
+    if (!norm && (q_weight || k_weight))
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: weights given, but norm is 0", who);
+    if (norm && (!(eps >= 0.f) || !(eps < 1e30f)))
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: eps must be finite and not negative", who);
+    if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || (q_weight && !aligned16(q_weight)) ||
+        (k_weight && !aligned16(k_weight)))
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: tensor pointers must be 16-byte aligned", who);
+    if (medusa_status s = check_row_stride(who, "q_stride", dtype, q_stride, H, dh)) return s;
+    return check_row_stride(who, "k_stride", dtype, k_stride, Hkv, dh);
+}
+
+medusa_status check_kv4_rows(const char *who, medusa_dtype dtype, const void *k, const void *v,
+                             int64_t k_stride, int64_t v_stride, const void *k_cache,
+                             const void *v_cache, const int32_t *prefix_len, int P_max, int B,
+                             int R, int Hkv, int dh, const void *ws, size_t ws_bytes) {
+    // rows are the grid's second dimension
+    if (medusa_status s = check_heads_shape(who, dtype, B, R, 65535, Hkv, Hkv, dh)) return s;
+    if (!k || !v) return fail(MEDUSA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+    if (!aligned16(k) || !aligned16(v))
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: tensor pointers must be 16-byte aligned", who);
+    if (medusa_status s = check_row_stride(who, "k_stride", dtype, k_stride, Hkv, dh)) return s;
+    if (medusa_status s = check_row_stride(who, "v_stride", dtype, v_stride, Hkv, dh)) return s;
+    if (medusa_status s = check_caches(who, k_cache, v_cache, prefix_len, P_max)) return s;
+    return check_ws(ws, ws_bytes, MEDUSA_WS_HEADER, who);
+}
+
+bool attention_shape_ok(medusa_dtype dtype, int B, int R, int H, int Hkv, int dh, int P_max,
+                        int window, int sinks) {
+    return is_dtype(dtype) && B >= 1 && B <= 65535 && R >= 1 && R <= MEDUSA_MAX_TREE_ROWS &&
+           Hkv >= 1 && H >= Hkv && H <= 1024 && H % Hkv == 0 && (dh == 64 || dh == 128) &&
+           P_max >= 0 && P_max <= kMaxPrefix && window >= 0 && sinks >= 0;
+}
+
+medusa_status cache_attention(const char *who, bool kv4, medusa_dtype dtype, const void *q,
+                              const void *const *k_cache, const void *const *v_cache,
+                              const int32_t *prefix_len, int P_max, const uint64_t *anc_mask,
+                              const int32_t *depth, int window, int sinks, int B, int R, int H,
+                              int Hkv, int dh, float scale, void *out, void *ws, size_t ws_bytes,
+                              medusa_stream stream) {
+    if (medusa_status s = check_heads_shape(who, dtype, B, R, MEDUSA_MAX_TREE_ROWS, H, Hkv, dh))
+        return s;
+    if (!q || !anc_mask || !out) return fail(MEDUSA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+    if (medusa_status s = check_caches(who, k_cache, v_cache, prefix_len, P_max)) return s;
+    if (window < 0 || sinks < 0)
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: window=%d, sinks=%d", who, window, sinks);
+    if (window == 0 && sinks != 0)
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: sinks=%d without a window", who, sinks);
+    if (window && !depth)
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: a window needs the rows' depth", who);
+    if (!(scale > 0.f) || !(scale < 1e30f))
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: scale must be positive and finite", who);
+    if (!aligned16(q) || !aligned16(out))
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: tensor pointers must be 16-byte aligned", who);
+    if (medusa_status s = check_ws(ws, ws_bytes,
+                                   cache_attention_workspace_bytes(dtype, kv4, B, R, H, Hkv, dh,
+                                                                   P_max, window, sinks),
+                                   who))
+        return s;
+    cudaError_t e = launch_cache_attention(dtype, kv4, q, k_cache, v_cache, prefix_len, P_max,
+                                           anc_mask, depth, window, sinks, B, R, H, Hkv, dh, scale,
+                                           out, ws, static_cast<cudaStream_t>(stream));
+    if (e) return cuda_fail(e, who);
+    return MEDUSA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+medusa_status medusa_qk_norm_rope(medusa_dtype dtype, const void *q, const void *k,
+                                  int64_t q_stride, int64_t k_stride, const void *q_weight,
+                                  const void *k_weight, float eps, int norm, const int32_t *pos,
+                                  const float *inv_freq, int rot, int interleaved,
+                                  const int32_t *n_rows, int B, int R, int H, int Hkv, int dh,
+                                  void *q_out, void *k_out, medusa_stream stream) {
+    const NvtxRange range("medusa_qk_norm_rope");
+    const char *who = "medusa_qk_norm_rope";
+    if (medusa_status s = check_rope(who, dtype, q, k, q_stride, k_stride, q_weight, k_weight, eps,
+                                     norm, pos, inv_freq, rot, B, R, H, Hkv, dh, q_out))
+        return s;
+    if (!k_out) return fail(MEDUSA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+    if (!aligned16(k_out))
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: tensor pointers must be 16-byte aligned", who);
+    cudaError_t e = launch_qk_norm_rope(dtype, q, k, nullptr, q_stride, k_stride, 0, q_weight,
+                                        k_weight, eps, norm, pos, inv_freq, rot, interleaved,
+                                        n_rows, nullptr, nullptr, nullptr, 0, B, R, H, Hkv, dh,
+                                        q_out, k_out, nullptr, static_cast<cudaStream_t>(stream));
+    if (e) return cuda_fail(e, who);
+    return MEDUSA_OK;
+}
+
+medusa_status medusa_qk_norm_rope_append(
+    medusa_dtype dtype, const void *q, const void *k, const void *v, int64_t q_stride,
+    int64_t k_stride, int64_t v_stride, const void *q_weight, const void *k_weight, float eps,
+    int norm, const int32_t *pos, const float *inv_freq, int rot, int interleaved,
+    const int32_t *n_rows, void *const *k_cache, void *const *v_cache, const int32_t *prefix_len,
+    int P_max, int B, int R, int H, int Hkv, int dh, void *q_out, void *ws, size_t ws_bytes,
+    medusa_stream stream) {
+    const NvtxRange range("medusa_qk_norm_rope_append");
+    const char *who = "medusa_qk_norm_rope_append";
+    if (medusa_status s = check_rope(who, dtype, q, k, q_stride, k_stride, q_weight, k_weight, eps,
+                                     norm, pos, inv_freq, rot, B, R, H, Hkv, dh, q_out))
+        return s;
+    if (!v) return fail(MEDUSA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+    if (!aligned16(v))
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: tensor pointers must be 16-byte aligned", who);
+    if (medusa_status s = check_row_stride(who, "v_stride", dtype, v_stride, Hkv, dh)) return s;
+    if (medusa_status s = check_caches(who, k_cache, v_cache, prefix_len, P_max)) return s;
+    if (medusa_status s = check_ws(ws, ws_bytes, MEDUSA_WS_HEADER, who)) return s;
+    cudaError_t e = launch_qk_norm_rope(dtype, q, k, v, q_stride, k_stride, v_stride, q_weight,
+                                        k_weight, eps, norm, pos, inv_freq, rot, interleaved,
+                                        n_rows, k_cache, v_cache, prefix_len, P_max, B, R, H, Hkv,
+                                        dh, q_out, nullptr, ws, static_cast<cudaStream_t>(stream));
+    if (e) return cuda_fail(e, who);
+    return MEDUSA_OK;
+}
+
+size_t medusa_kv4_row_bytes(int Hkv, int dh) {
+    if (Hkv < 1 || Hkv > 1024 || (dh != 64 && dh != 128)) return 0;
+    return ((size_t)Hkv * dh / 2 + (size_t)Hkv * dh / 16 + 15) / 16 * 16;
+}
+
+medusa_status medusa_kv4_append(medusa_dtype dtype, const void *k, const void *v, int64_t k_stride,
+                                int64_t v_stride, void *const *k_cache, void *const *v_cache,
+                                const int32_t *prefix_len, int P_max, const int32_t *n_rows, int B,
+                                int R, int Hkv, int dh, void *ws, size_t ws_bytes,
+                                medusa_stream stream) {
+    const NvtxRange range("medusa_kv4_append");
+    const char *who = "medusa_kv4_append";
+    if (medusa_status s = check_kv4_rows(who, dtype, k, v, k_stride, v_stride, k_cache, v_cache,
+                                         prefix_len, P_max, B, R, Hkv, dh, ws, ws_bytes))
+        return s;
+    cudaError_t e = launch_kv4_rows(dtype, true, k, v, k_stride, v_stride, k_cache, v_cache,
+                                    prefix_len, P_max, n_rows, B, R, Hkv, dh, ws,
+                                    static_cast<cudaStream_t>(stream));
+    if (e) return cuda_fail(e, who);
+    return MEDUSA_OK;
+}
+
+medusa_status medusa_kv4_unpack(medusa_dtype dtype, const void *const *k_cache,
+                                const void *const *v_cache, const int32_t *prefix_len, int P_max,
+                                const int32_t *n_rows, int B, int R, int Hkv, int dh, void *k_out,
+                                void *v_out, void *ws, size_t ws_bytes, medusa_stream stream) {
+    const NvtxRange range("medusa_kv4_unpack");
+    const char *who = "medusa_kv4_unpack";
+    const int64_t row = (int64_t)Hkv * dh;
+    if (medusa_status s = check_kv4_rows(who, dtype, k_out, v_out, row, row, k_cache, v_cache,
+                                         prefix_len, P_max, B, R, Hkv, dh, ws, ws_bytes))
+        return s;
+    cudaError_t e = launch_kv4_rows(dtype, false, k_out, v_out, row, row,
+                                    const_cast<void *const *>(k_cache),
+                                    const_cast<void *const *>(v_cache), prefix_len, P_max, n_rows,
+                                    B, R, Hkv, dh, ws, static_cast<cudaStream_t>(stream));
+    if (e) return cuda_fail(e, who);
+    return MEDUSA_OK;
+}
+
+medusa_status medusa_commit_kv4(void *const *k_cache, void *const *v_cache,
+                                const int32_t *prefix_len, const int32_t *path,
+                                const int32_t *accept_len, int B, int K, int R, int Hkv, int dh,
+                                int32_t *new_prefix_len, void *ws, size_t ws_bytes,
+                                medusa_stream stream) {
+    const NvtxRange range("medusa_commit_kv4");
+    const char *who = "medusa_commit_kv4";
+    if (medusa_status s = check_heads_shape(who, MEDUSA_BF16, B, R, MEDUSA_MAX_TREE_ROWS, Hkv, Hkv, dh))
+        return s;
+    // the row is moved as raw bytes: 2-byte elements, one head of row_bytes / 2
+    const int row = (int)medusa_kv4_row_bytes(Hkv, dh);
+    if (medusa_status s = check_commit(who, MEDUSA_BF16, k_cache, v_cache, prefix_len,
+                                       new_prefix_len, 1, row / 2))
+        return s;
+    if (!path || !accept_len) return fail(MEDUSA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+    if (K < 0 || K > MEDUSA_MAX_HEADS)
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: K=%d outside 0..%d", who, K, MEDUSA_MAX_HEADS);
+    if (medusa_status s = check_ws(ws, ws_bytes, MEDUSA_WS_HEADER, who)) return s;
+    cudaError_t e = launch_commit_kv(1, k_cache, v_cache, prefix_len, path, accept_len, B, K, R, 1,
+                                     row, new_prefix_len, ws, static_cast<cudaStream_t>(stream));
+    if (e) return cuda_fail(e, who);
+    return MEDUSA_OK;
+}
+
+size_t medusa_tree_attention_window_workspace_size(medusa_dtype dtype, int B, int R, int H, int Hkv,
+                                                   int dh, int P_max, int window, int sinks) {
+    if (!attention_shape_ok(dtype, B, R, H, Hkv, dh, P_max, window, sinks)) return 0;
+    return cache_attention_workspace_bytes(dtype, false, B, R, H, Hkv, dh, P_max, window, sinks);
+}
+
+size_t medusa_tree_attention_kv4_workspace_size(medusa_dtype dtype, int B, int R, int H, int Hkv,
+                                                int dh, int P_max, int window, int sinks) {
+    if (!attention_shape_ok(dtype, B, R, H, Hkv, dh, P_max, window, sinks)) return 0;
+    return cache_attention_workspace_bytes(dtype, true, B, R, H, Hkv, dh, P_max, window, sinks);
+}
+
+medusa_status medusa_tree_attention_window(
+    medusa_dtype dtype, const void *q, const void *const *k_cache, const void *const *v_cache,
+    const int32_t *prefix_len, int P_max, const uint64_t *anc_mask, const int32_t *depth,
+    int window, int sinks, int B, int R, int H, int Hkv, int dh, float scale, void *out, void *ws,
+    size_t ws_bytes, medusa_stream stream) {
+    const NvtxRange range("medusa_tree_attention_window");
+    return cache_attention("medusa_tree_attention_window", false, dtype, q, k_cache, v_cache,
+                           prefix_len, P_max, anc_mask, depth, window, sinks, B, R, H, Hkv, dh,
+                           scale, out, ws, ws_bytes, stream);
+}
+
+medusa_status medusa_tree_attention_kv4(
+    medusa_dtype dtype, const void *q, const void *const *k_cache, const void *const *v_cache,
+    const int32_t *prefix_len, int P_max, const uint64_t *anc_mask, const int32_t *depth,
+    int window, int sinks, int B, int R, int H, int Hkv, int dh, float scale, void *out, void *ws,
+    size_t ws_bytes, medusa_stream stream) {
+    const NvtxRange range("medusa_tree_attention_kv4");
+    return cache_attention("medusa_tree_attention_kv4", true, dtype, q, k_cache, v_cache,
+                           prefix_len, P_max, anc_mask, depth, window, sinks, B, R, H, Hkv, dh,
+                           scale, out, ws, ws_bytes, stream);
+}
+
+}  // extern "C"

@@ -117,4 +117,32 @@ cudaError_t launch_commit_kv(size_t elt, void *const *k_cache, void *const *v_ca
                              const int32_t *accept_len, int B, int K, int R, int H, int dh,
                              int32_t *new_prefix_len, void *ws, cudaStream_t stream);
 
+// K/V rows into the 4-bit cache (append) or back out of it (k, v are then
+// the destinations); strides in elements between rows.
+cudaError_t launch_kv4_rows(medusa_dtype dtype, bool append, const void *k, const void *v,
+                            long long k_stride, long long v_stride, void *const *k_cache,
+                            void *const *v_cache, const int32_t *prefix_len, int P_max,
+                            const int32_t *n_rows, int B, int R, int Hkv, int dh, void *ws,
+                            cudaStream_t stream);
+
+// k_cache == nullptr: keys to k_out, no values; otherwise K and V rows into
+// the caches' slots prefix_len[b] + i.
+cudaError_t launch_qk_norm_rope(medusa_dtype dtype, const void *q, const void *k, const void *v,
+                                long long q_stride, long long k_stride, long long v_stride,
+                                const void *q_weight, const void *k_weight, float eps, int norm,
+                                const int32_t *pos, const float *inv_freq, int rot,
+                                int interleaved, const int32_t *n_rows, void *const *k_cache,
+                                void *const *v_cache, const int32_t *prefix_len, int P_max, int B,
+                                int R, int H, int Hkv, int dh, void *q_out, void *k_out, void *ws,
+                                cudaStream_t stream);
+
+size_t cache_attention_workspace_bytes(medusa_dtype dtype, bool kv4, int B, int R, int H, int Hkv,
+                                       int dh, int P_max, int window, int sinks);
+cudaError_t launch_cache_attention(medusa_dtype dtype, bool kv4, const void *q,
+                                   const void *const *k_cache, const void *const *v_cache,
+                                   const int32_t *prefix_len, int P_max, const uint64_t *anc_mask,
+                                   const int32_t *depth, int window, int sinks, int B, int R, int H,
+                                   int Hkv, int dh, float scale, void *out, void *ws,
+                                   cudaStream_t stream);
+
 }  // namespace medusa
