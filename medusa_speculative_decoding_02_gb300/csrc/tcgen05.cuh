@@ -259,7 +259,16 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int b_mn_major) 
            | ((uint32_t)(M >> 4) << 24);   // M / 16
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]; issued by one thread.  A (16-bit) sits one
+// The same with both operands fp16.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn_major) {
+    return (1u << 4)                       // D format fp32; A and B format 0: fp16
+           | ((uint32_t)b_mn_major << 16)  // B major
+           | ((uint32_t)(N >> 3) << 17)    // N / 8
+           | ((uint32_t)(M >> 4) << 24);   // M / 16
+}
+
+// D[tmem] (+)= A[tmem] * B[smem] (bf16, or fp16 with idesc_f16); issued by
+// one thread.  A (16-bit) sits one
 // row per lane, two consecutive K elements per 32-bit column (the lower K
 // index in the low half).
 __device__ __forceinline__ void mma_bf16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
