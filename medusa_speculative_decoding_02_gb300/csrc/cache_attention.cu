@@ -272,19 +272,20 @@ __global__ void __launch_bounds__(kSimtThreads) cache_attn_simt_kernel(CacheAttn
 //
 // bf16 queries.  One CTA (nine warps, two CTAs an SM) per (128-row tile, KV
 // head, key range, sequence), its keys in stages of 64:
-//   warps 4-7  load: K and V of a stage into shared memory as 128-byte swizzled
-//              tiles, a ring of three stages.  A bf16 cache comes by cp.async;
-//              a 4-bit row is read into registers three stages ahead, widened
-//              to fp16 (exact) and stored.
-//   warp 8     one thread issues the products: S = Q K^T, then, when the
-//              weights are there, O += P V.
+//   warps 4-7  load: K and V tiles of a stage into shared memory as 128-byte
+//              swizzled blocks, a ring of tiles in the order of their use
+//              (K0 K1 V0 K2 V1 ..).  A bf16 cache comes by cp.async; a 4-bit
+//              tile is read into registers six tiles ahead, widened to fp16
+//              (exact) and stored.
+//   warp 8     one thread issues the products: S_j+1 = Q K^T as soon as the
+//              scores of stage j are in registers, then O += P_j V.
 //   warps 0-3  softmax: thread t owns row t of the tile, reads its 64 scores
 //              from tensor memory, keeps the row's reference m and sum l in
 //              registers (no exchange between threads), and writes the
-//              weights P over the scores.
-// Tensor memory (256 columns): [0,64) S in fp32, then P in 16 bits; [64,128)
-// Q; [128,256) O.  S of stage j+1 overwrites P of stage j, so it is issued
-// after O of stage j has arrived; the other CTA of the SM fills that gap.
+//              weights P to shared memory, the product's A operand.
+// Tensor memory (256 columns): [0,64) S in fp32, [64,128) Q, [128,256) O.
+// P in shared memory costs 32 KB of its traffic a stage; over the S columns
+// it made each stage wait for the product before (S, softmax, O in a chain).
 // The reference m moves only when a stage's maximum exceeds it by 2^8, and O
 // is then rescaled in tensor memory; P may thus reach 2^8.
 //
@@ -301,22 +302,36 @@ __global__ void __launch_bounds__(kSimtThreads) cache_attn_simt_kernel(CacheAttn
 // such elements, add them to the rows that see them and clear them before the
 // product.  Every wait is bounded; on a timeout the CTA sets the status, waits
 // (bounded) for its products, frees its tensor memory and publishes nothing.
-constexpr int kSub = 64, kStages = 3, kTcThreads = 288;
+constexpr int kSub = 64, kTcThreads = 288;
 constexpr float kRescaleLog2 = 8.f;
 constexpr float kF16Bias = 7.f;
 constexpr uint32_t kDrainPolls = 1u << 16;
+constexpr int kAhead = 6;  // 4-bit tiles held in a loader's registers
 
-template <int DH>
+template <int DH, bool KV4>
 struct CacheSmem {
     static constexpr int NB = DH / 64;
     static constexpr int TILE = NB * kSub * 128;
-    static constexpr int STAGE = 2 * TILE;
-    static constexpr int BAR = kStages * STAGE;
-    // full[3], empty[3], s, p, o, drain; then words
-    static constexpr int WORDS = BAR + 10 * 8;
+    // ring tiles: what fits beside P
+    static constexpr int NT = 4 * (128 / DH);
+    static constexpr int PW = NT * TILE;          // two P buffers: 128 rows of 64 weights
+    static constexpr int P_BYTES = 128 * 128;
+    static constexpr int BAR = PW + 2 * P_BYTES;
+    // full[NT], empty[NT], q, s, sfree, drain, p[2], o[2]; then words
+    static constexpr int WORDS = BAR + (2 * NT + 8) * 8;
     static constexpr int TOTAL = WORDS + 12 * 4;
     static_assert(2 * (TOTAL + 1024) <= 196 * 1024, "two CTAs per SM in the heads' carveout");
 };
+
+// Tile `i` of a range of n stages, in the order K0 K1 V0 K2 V1 .. V(n-1).
+__device__ __forceinline__ bool tile_is_v(int i, int n) {
+    return (i > 0 && (i & 1) == 0) || i == 2 * n - 1;
+}
+__device__ __forceinline__ int tile_stage(int i, int n) {
+    return i == 0 ? 0 : i == 2 * n - 1 ? n - 1 : (i & 1) ? (i + 1) / 2 : i / 2 - 1;
+}
+__device__ __forceinline__ int k_tile(int j) { return j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ int v_tile(int j, int n) { return min(2 * j + 2, 2 * n - 1); }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool ok) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
@@ -385,14 +400,13 @@ __device__ __forceinline__ uint32_t pack_weights(float a, float b) {
 // ---- loader, bf16 cache: 128 threads; thread t copies 16-byte column t % CPR
 // of key rows t / CPR + RPP u (rows RPP apart share the swizzle phase)
 template <int DH>
-__device__ __forceinline__ void load_stage_bf16(unsigned char *st, const bf16 *kc, const bf16 *vc,
-                                                const KeyRun &run, int k0, int kend, int Hkv, int g,
-                                                int t) {
+__device__ __forceinline__ void load_tile_bf16(unsigned char *tile, const bf16 *cache,
+                                               const KeyRun &run, int k0, int kend, int Hkv, int g,
+                                               int t) {
     constexpr int CPR = DH / 8, RPP = 128 / CPR;
     static_assert(RPP % 8 == 0, "passes keep the swizzle phase");
     const int c16 = t % CPR, r0 = t / CPR;
-    const uint32_t so0 =
-        tc::smem_addr(st) + (c16 >> 3) * kSub * 128 + tc::sw128(r0, c16 & 7);
+    const uint32_t so0 = tc::smem_addr(tile) + (c16 >> 3) * kSub * 128 + tc::sw128(r0, c16 & 7);
     const size_t row = (size_t)Hkv * DH;
     const size_t col = (size_t)g * DH + c16 * 8;
 #pragma unroll
@@ -400,23 +414,36 @@ __device__ __forceinline__ void load_stage_bf16(unsigned char *st, const bf16 *k
         const int x = k0 + r0 + u * RPP;
         const bool ok = x < kend;
         const size_t off = ok ? (size_t)run.slot(x) * row + col : 0;
-        cp_async16(so0 + u * RPP * 128, kc + off, ok);
-        cp_async16(so0 + u * RPP * 128 + CacheSmem<DH>::TILE, vc + off, ok);
+        cp_async16(so0 + u * RPP * 128, cache + off, ok);
     }
     asm volatile("cp.async.commit_group;\n");
 }
 
-// ---- loader, 4-bit cache: a stage of one of K and V is 64 keys x DH/32 groups
-// of 32 elements (16 code bytes, two scales); thread t takes groups t + 128 u
+// ---- loader, 4-bit cache: a tile is 64 keys x DH/32 groups of 32 elements (16
+// code bytes, two scales); thread t takes groups t + 128 u
 template <int DH>
 struct Kv4Regs {
     static constexpr int N = DH / 64;
-    uint4 code[2][N];
-    uint32_t scale[2][N];
+    uint4 code[N];
+    uint32_t scale[N];
 };
 
+// loads that stay where they are written: ahead of their use by kAhead tiles
+__device__ __forceinline__ uint4 ld_ahead16(const void *p) {
+    uint4 r;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint32_t ld_ahead2(const void *p) {
+    uint16_t r;
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(r) : "l"(p));
+    return r;
+}
+
 template <int DH>
-__device__ __forceinline__ void load_regs_kv4(Kv4Regs<DH> &r, const uint8_t *kc, const uint8_t *vc,
+__device__ __forceinline__ void load_regs_kv4(Kv4Regs<DH> &r, const uint8_t *cache,
                                               const KeyRun &run, int k0, int kend, int Hkv, int g,
                                               int t) {
     constexpr int GPK = DH / 32;  // groups per key
@@ -425,26 +452,37 @@ __device__ __forceinline__ void load_regs_kv4(Kv4Regs<DH> &r, const uint8_t *kc,
     for (int u = 0; u < Kv4Regs<DH>::N; ++u) {
         const int c = t + 128 * u, x = k0 + c / GPK, q = c % GPK;
         if (x < kend) {
-            const size_t off = (size_t)run.slot(x) * rb;
-            const int co = g * (DH / 2) + q * 16, so = cb + g * (DH / 16) + q * 2;
-            r.code[0][u] = ld_stream16(kc + off + co);
-            r.code[1][u] = ld_stream16(vc + off + co);
-            r.scale[0][u] = __ldg(reinterpret_cast<const unsigned short *>(kc + off + so));
-            r.scale[1][u] = __ldg(reinterpret_cast<const unsigned short *>(vc + off + so));
+            const uint8_t *row = cache + (size_t)run.slot(x) * rb;
+            r.code[u] = ld_ahead16(row + g * (DH / 2) + q * 16);
+            r.scale[u] = ld_ahead2(row + cb + g * (DH / 16) + q * 2);
         } else {
-            r.code[0][u] = r.code[1][u] = make_uint4(0, 0, 0, 0);
-            r.scale[0][u] = r.scale[1][u] = 0;
+            r.code[u] = make_uint4(0, 0, 0, 0);
+            r.scale[u] = 0;
         }
     }
 }
 
-__device__ __forceinline__ uint32_t widen_pair(uint32_t byte, __half2 s) {
-    const __half2 v = __hmul2(e2m1x2_half2(byte), s);  // exact
-    return *reinterpret_cast<const uint32_t *>(&v);
+// the eight codes of a word as four fp16 pairs, times s (exact)
+__device__ __forceinline__ uint4 widen_word(uint32_t w, __half2 s) {
+    uint32_t h[4];
+    asm("{\n.reg .b8 b0, b1, b2, b3;\n"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&h[i]), s);
+        h[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
 template <int DH>
-__device__ __forceinline__ void store_regs_kv4(const Kv4Regs<DH> &r, unsigned char *st, int t) {
+__device__ __forceinline__ void store_regs_kv4(const Kv4Regs<DH> &r, unsigned char *tile, int t) {
     constexpr int GPK = DH / 32;
 #pragma unroll
     for (int u = 0; u < Kv4Regs<DH>::N; ++u) {
@@ -453,24 +491,17 @@ __device__ __forceinline__ void store_regs_kv4(const Kv4Regs<DH> &r, unsigned ch
         // order 2,3,0,1: the eight lanes of a store phase (two keys, four
         // groups) then hit eight different bank groups
         const bool flip = (q >> 1) & 1;
-        const uint32_t base = (q >> 1) * kSub * 128;
+        unsigned char *blk = tile + (q >> 1) * kSub * 128;
+        const uint4 w = r.code[u];
+        const __half2 s2 =
+            __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)r.scale[u], __NV_E4M3));
+        const __half2 sa = flip ? __high2half2(s2) : __low2half2(s2);
+        const __half2 sb = flip ? __low2half2(s2) : __high2half2(s2);
+        const uint32_t word[4] = {flip ? w.z : w.x, flip ? w.w : w.y, flip ? w.x : w.z, flip ? w.y : w.w};
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-            const uint4 w = r.code[kv][u];
-            const __half2_raw sr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)r.scale[kv][u], __NV_E4M3);
-            const __half2 s2 = __half2(sr);
-            const __half2 sa = flip ? __high2half2(s2) : __low2half2(s2);
-            const __half2 sb = flip ? __low2half2(s2) : __high2half2(s2);
-            const uint32_t word[4] = {flip ? w.z : w.x, flip ? w.w : w.y, flip ? w.x : w.z, flip ? w.y : w.w};
-            unsigned char *tile = st + kv * CacheSmem<DH>::TILE + base;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __half2 s = i < 2 ? sa : sb;
-                const int ch = (q & 1) * 4 + (i ^ (flip ? 2 : 0));
-                *reinterpret_cast<uint4 *>(tile + tc::sw128(key, ch)) =
-                    make_uint4(widen_pair(word[i], s), widen_pair(word[i] >> 8, s),
-                               widen_pair(word[i] >> 16, s), widen_pair(word[i] >> 24, s));
-            }
+        for (int i = 0; i < 4; ++i) {
+            const int ch = (q & 1) * 4 + (i ^ (flip ? 2 : 0));
+            *reinterpret_cast<uint4 *>(blk + tc::sw128(key, ch)) = widen_word(word[i], i < 2 ? sa : sb);
         }
     }
 }
@@ -478,10 +509,14 @@ __device__ __forceinline__ void store_regs_kv4(const Kv4Regs<DH> &r, unsigned ch
 template <int DH, bool KV4>
 __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnArgs a) {
     pdl_enter();
-    using L = CacheSmem<DH>;
+    using L = CacheSmem<DH, KV4>;
     extern __shared__ __align__(1024) unsigned char sm[];
-    uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BAR), *empty = full + kStages;
-    uint64_t *bar_s = full + 6, *bar_p = full + 7, *bar_o = full + 8, *bar_drain = full + 9;
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BAR), *empty = full + L::NT;
+    // p and o have a barrier for each P buffer: a warp may be a stage ahead of
+    // another, and its arrival for the next stage must not count for this one
+    // (at stage j + 2 it has waited for the product of j, hence for all of j)
+    uint64_t *bar_q = empty + L::NT, *bar_s = bar_q + 1, *bar_sfree = bar_q + 2,
+             *bar_drain = bar_q + 3, *bar_p = bar_q + 4, *bar_o = bar_q + 6;
     volatile int *failed = reinterpret_cast<volatile int *>(sm + L::WORDS);
     volatile int *o_started = failed + 1;                        // O holds something before stage 0
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(sm + L::WORDS + 8);
@@ -521,13 +556,18 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
 
     if (tid == 0) {
 #pragma unroll
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < L::NT; ++i) {
             tc::mbar_init(full + i, 128);
             tc::mbar_init(empty + i, 1);
         }
+        tc::mbar_init(bar_q, 128);
         tc::mbar_init(bar_s, 1);
-        tc::mbar_init(bar_p, 128);
-        tc::mbar_init(bar_o, 1);
+        tc::mbar_init(bar_sfree, 128);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(bar_p + i, 128);
+            tc::mbar_init(bar_o + i, 1);
+        }
         tc::mbar_init(bar_drain, 1);
         *failed = 0;
         *o_started = 0;
@@ -541,92 +581,105 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
     const uint32_t tmem = *tmem_holder;
     const uint32_t t_s = tmem, t_q = tmem + 64, t_o = tmem + 128;
 
+    auto slot_of = [&](int i) { return sm + (i % L::NT) * L::TILE; };
+    auto wait_full = [&](int i) {
+        return wait_or_fail(full + i % L::NT, (i / L::NT) & 1, a.wait_polls, failed);
+    };
+    auto wait_product = [&](int j) {  // O += P_j V done
+        return wait_or_fail(bar_o + (j & 1), (j >> 1) & 1, a.wait_polls, failed);
+    };
     if (warp >= 4 && warp < 8) {
         // ------------------------------------------------------------ loaders
-        const int t = tid - 128;
-        auto wait_empty = [&](int j) {  // stage of j free: the product of j - 3 is done
-            return j < kStages ||
-                   wait_or_fail(empty + j % kStages, (j / kStages - 1) & 1, a.wait_polls, failed);
+        const int t = tid - 128, n_tiles = 2 * nsub;
+        auto wait_empty = [&](int i) {  // slot of tile i free: tile i - NT was used
+            return i < L::NT ||
+                   wait_or_fail(empty + i % L::NT, (i / L::NT - 1) & 1, a.wait_polls, failed);
         };
         if constexpr (KV4) {
             const uint8_t *k8 = static_cast<const uint8_t *>(kc), *v8 = static_cast<const uint8_t *>(vc);
-            Kv4Regs<DH> buf[kStages];
+            Kv4Regs<DH> buf[kAhead];
+            auto fetch = [&](Kv4Regs<DH> &r, int i) {
+                if (i < n_tiles)
+                    load_regs_kv4<DH>(r, tile_is_v(i, nsub) ? v8 : k8, run,
+                                      kbeg + tile_stage(i, nsub) * kSub, kend, a.Hkv, g, t);
+            };
 #pragma unroll
-            for (int u = 0; u < kStages; ++u)
-                load_regs_kv4<DH>(buf[u], k8, v8, run, kbeg + u * kSub, kend, a.Hkv, g, t);
+            for (int u = 0; u < kAhead; ++u) fetch(buf[u], u);
             bool go = true;
-            for (int j0 = 0; j0 < nsub && go; j0 += kStages) {
+            for (int i0 = 0; i0 < n_tiles && go; i0 += kAhead) {
 #pragma unroll
-                for (int u = 0; u < kStages; ++u) {
-                    const int j = j0 + u;
-                    if (j < nsub && go) {
-                        go = wait_empty(j);
+                for (int u = 0; u < kAhead; ++u) {
+                    const int i = i0 + u;
+                    if (i < n_tiles && go) {
+                        go = wait_empty(i);
                         if (go) {
-                            store_regs_kv4<DH>(buf[u], sm + u * L::STAGE, t);
+                            store_regs_kv4<DH>(buf[u], slot_of(i), t);
                             tc::fence_proxy_async_smem();
-                            tc::mbar_arrive(full + u);
-                            load_regs_kv4<DH>(buf[u], k8, v8, run, kbeg + (j + kStages) * kSub, kend,
-                                              a.Hkv, g, t);
+                            tc::mbar_arrive(full + i % L::NT);
+                            fetch(buf[u], i + kAhead);
                         }
                     }
                 }
             }
         } else {
+            // LAG younger copies stay in flight when a tile is announced
+            constexpr int LAG = L::NT - 1;
             const bf16 *k16 = static_cast<const bf16 *>(kc), *v16 = static_cast<const bf16 *>(vc);
-            int j = 0;
-            for (; j < nsub; ++j) {
-                if (!wait_empty(j)) break;
-                load_stage_bf16<DH>(sm + (j % kStages) * L::STAGE, k16, v16, run, kbeg + j * kSub, kend,
-                                    a.Hkv, g, t);
-                if (j >= 2) {  // two younger groups stay in flight
-                    asm volatile("cp.async.wait_group 2;\n");
-                    tc::fence_proxy_async_smem();
-                    tc::mbar_arrive(full + (j - 2) % kStages);
+            bool go = true;
+            for (int i = 0; i < n_tiles + LAG && go; ++i) {
+                if (i < n_tiles) {
+                    go = wait_empty(i);
+                    if (!go) break;
+                    load_tile_bf16<DH>(slot_of(i), tile_is_v(i, nsub) ? v16 : k16, run,
+                                       kbeg + tile_stage(i, nsub) * kSub, kend, a.Hkv, g, t);
+                } else {
+                    asm volatile("cp.async.commit_group;\n");  // keeps the count of groups
                 }
-            }
-            if (j == nsub) {
-                if (nsub >= 2) {
-                    asm volatile("cp.async.wait_group 1;\n");
+                if (i >= LAG) {
+                    asm volatile("cp.async.wait_group %0;\n" ::"n"(LAG));
                     tc::fence_proxy_async_smem();
-                    tc::mbar_arrive(full + (nsub - 2) % kStages);
+                    tc::mbar_arrive(full + (i - LAG) % L::NT);
                 }
-                asm volatile("cp.async.wait_group 0;\n");
-                tc::fence_proxy_async_smem();
-                tc::mbar_arrive(full + (nsub - 1) % kStages);
             }
             asm volatile("cp.async.wait_group 0;\n");
         }
     } else if (warp == 8) {
         // ----------------------------------------------------------- products
-        // (Q is in tensor memory before the softmax warps' first arrival on bar_p)
         if (lane == 0) {
             constexpr uint32_t id_s = KV4 ? tc::idesc_f16(128, kSub, 0) : tc::idesc_bf16(128, kSub, 0);
             constexpr uint32_t id_o = KV4 ? tc::idesc_f16(128, DH, 1) : tc::idesc_bf16(128, DH, 1);
-            bool go = wait_or_fail(bar_p, 0, a.wait_polls, failed);  // Q written
-            for (int j = 0; j < nsub && go; ++j) {
-                const unsigned char *st = sm + (j % kStages) * L::STAGE;
-                go = wait_or_fail(full + j % kStages, (j / kStages) & 1, a.wait_polls, failed);
-                // S overwrites P of j - 1, which the product of j - 1 reads
-                if (go && j > 0) go = wait_or_fail(bar_o, (j - 1) & 1, a.wait_polls, failed);
-                if (!go) break;
+            auto scores = [&](int j) {
+                const int i = k_tile(j);
+                if (!wait_full(i)) return false;
+                // the scores before are in registers
+                if (j > 0 && !wait_or_fail(bar_sfree, (j - 1) & 1, a.wait_polls, failed)) return false;
                 tc::fence_after_sync();
-                const uint64_t kd = tc::sdesc_sw128(tc::smem_addr(st), 16, 1024);
+                const uint64_t kd = tc::sdesc_sw128(tc::smem_addr(slot_of(i)), 16, 1024);
 #pragma unroll
                 for (int ks = 0; ks < DH / 16; ++ks)
                     tc::mma_bf16_ts(t_s, t_q + ks * 8, kd + (((ks >> 2) * kSub * 128 + (ks & 3) * 32) >> 4),
                                     id_s, ks > 0);
+                tc::mma_commit(empty + i % L::NT);
                 tc::mma_commit(bar_s);
-                go = wait_or_fail(bar_p, (j + 1) & 1, a.wait_polls, failed);
-                if (!go) break;
+                return true;
+            };
+            bool go = wait_or_fail(bar_q, 0, a.wait_polls, failed) && scores(0);
+            for (int j = 0; j < nsub && go; ++j) {
+                if (j + 1 < nsub && !scores(j + 1)) break;
+                const int i = v_tile(j, nsub);
+                if (!wait_or_fail(bar_p + (j & 1), (j >> 1) & 1, a.wait_polls, failed) ||
+                    !wait_full(i)) break;
                 tc::fence_after_sync();
-                const uint64_t vd = tc::sdesc_sw128(tc::smem_addr(st + L::TILE), kSub * 128, 1024);
+                const uint64_t vd = tc::sdesc_sw128(tc::smem_addr(slot_of(i)), kSub * 128, 1024);
+                const uint64_t pd =
+                    tc::sdesc_sw128(tc::smem_addr(sm + L::PW + (j & 1) * L::P_BYTES), 16, 1024);
                 const uint32_t acc0 = j > 0 || *o_started;
 #pragma unroll
                 for (int ks = 0; ks < kSub / 16; ++ks)
-                    tc::mma_bf16_ts(t_o, t_s + ks * 8, vd + ((ks * 16 * 128) >> 4), id_o,
+                    tc::mma_bf16_ss(t_o, pd + ((ks * 32) >> 4), vd + ((ks * 16 * 128) >> 4), id_o,
                                     ks > 0 ? 1u : acc0);
-                tc::mma_commit(empty + j % kStages);
-                tc::mma_commit(bar_o);
+                tc::mma_commit(empty + i % L::NT);
+                tc::mma_commit(bar_o + (j & 1));
             }
             // every product issued above is done before the tensor memory is freed
             tc::mma_commit(bar_drain);
@@ -688,7 +741,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
             }
             tc::tmem_wait_st();
             tc::fence_before_sync();
-            tc::mbar_arrive(bar_p);
+            tc::mbar_arrive(bar_q);
         }
         // ---- what this row sees, in numbered keys
         const int my_depth = a.window ? row_depth(a, b, r) : 0;
@@ -732,11 +785,13 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
         for (int j = 0; j < nsub; ++j) {
             const int k0 = kbeg + j * kSub;
             const bool masked = !(k0 + kSub <= min(kend, x_tree) && (k0 >= x_all || k0 + kSub <= run.n_sink));
+            unsigned char *p_row = sm + L::PW + (j & 1) * L::P_BYTES;
+            // the scores are there, and the product of j - 2 has read this P buffer
             if (!dead)
-                dead = !__all_sync(0xffffffffu, wait_or_fail(bar_s, j & 1, a.wait_polls, failed));
+                dead = !__all_sync(0xffffffffu, wait_or_fail(bar_s, j & 1, a.wait_polls, failed) &&
+                                                    (j < 2 || wait_product(j - 2)));
             tc::fence_after_sync();
-            bool grew = false;
-            float alpha = 1.f;
+            if (!dead && !rows_live) tc::mbar_arrive(bar_sfree);
             if (!dead && rows_live) {
                 float x[kSub];
                 {
@@ -744,7 +799,11 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
                     float (&hi)[32] = *reinterpret_cast<float (*)[32]>(x + 32);
                     tc::tmem_ld32(t_s + lane_base, lo);
                     tc::tmem_ld32(t_s + lane_base + 32, hi);
+                    tc::fence_before_sync();
                 }
+                tc::mbar_arrive(bar_sfree);
+                bool grew = false;
+                float alpha = 1.f;
                 if (masked) {
                     uint64_t vis = (bits_below(x_tree - k0) & ~bits_below(x_win - k0)) |
                                    (bits_below(x_sink - k0) & ~bits_below(run.n_sink - k0)) |
@@ -769,14 +828,15 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
                         x[e + 32] = (v1 >> e) & 1u ? x[e + 32] : -INFINITY;
                     }
                 }
-                float ma = max3f(x[0], x[1], x[2]), mb = max3f(x[3], x[4], x[5]);
+                float mx[4];
 #pragma unroll
-                for (int e = 6; e + 3 < kSub; e += 4) {
-                    ma = max3f(ma, x[e], x[e + 1]);
-                    mb = max3f(mb, x[e + 2], x[e + 3]);
+                for (int q = 0; q < 4; ++q) {
+                    mx[q] = max3f(x[q], x[q + 4], x[q + 8]);
+#pragma unroll
+                    for (int e = 12; e + 4 < kSub; e += 8) mx[q] = max3f(mx[q], x[q + e], x[q + e + 4]);
+                    mx[q] = fmaxf(mx[q], x[q + kSub - 4]);
                 }
-                ma = max3f(ma, x[kSub - 2], x[kSub - 1]);
-                const float cm = fmaxf(ma, mb) * row_scale;
+                const float cm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * row_scale;
                 if (cm > m_run + kRescaleLog2) {  // m_run = -inf: the first visible key
                     alpha = exp2f(m_run - cm);
                     m_run = cm;
@@ -797,38 +857,40 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
                 const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-mu, -mu);
                 float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t pk[16];
+                for (int c = 0; c < kSub / 8; ++c) {
+                    uint32_t pk[4];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float2 t = __ffma2_rn(make_float2(x[q * 32 + e], x[q * 32 + e + 1]), sc2, nm2);
+                    for (int e = 0; e < 8; e += 2) {
+                        const float2 t = __ffma2_rn(make_float2(x[c * 8 + e], x[c * 8 + e + 1]), sc2, nm2);
                         const float p0 = ex2_approx(t.x), p1 = ex2_approx(t.y);
                         // rounded for the product only; the sum adds the fp32 weights
                         pk[e / 2] = pack_weights<KV4>(p0, p1);
                         ls[(e / 2) & 1] = __fadd2_rn(ls[(e / 2) & 1], make_float2(p0, p1));
                     }
-                    tc::tmem_st16(t_s + lane_base + q * 16, pk);
+                    *reinterpret_cast<uint4 *>(p_row + tc::sw128(tid, c)) =
+                        make_uint4(pk[0], pk[1], pk[2], pk[3]);
                 }
                 l_run += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
-                if (__any_sync(0xffffffffu, grew && (j > 0 || *o_started))) {
-                    // O of the stages before is complete: S of j came after it
+                tc::fence_proxy_async_smem();
+                if (__any_sync(0xffffffffu, grew && j > 0)) {
+                    dead = !__all_sync(0xffffffffu, wait_product(j - 1));
+                    tc::fence_after_sync();
+                    if (!dead) {
 #pragma unroll 1
-                    for (int c = 0; c < DH; c += 32) {
-                        float ov[32];
-                        tc::tmem_ld32(t_o + lane_base + c, ov);
+                        for (int c = 0; c < DH; c += 32) {
+                            float ov[32];
+                            tc::tmem_ld32(t_o + lane_base + c, ov);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) ov[e] *= alpha;
-                        tc::tmem_st32(t_o + lane_base + c, ov);
+                            for (int e = 0; e < 32; ++e) ov[e] *= alpha;
+                            tc::tmem_st32(t_o + lane_base + c, ov);
+                        }
                     }
                 }
-                tc::tmem_wait_st();
             }
             if (masked) {
                 // ---- infinities and NaNs in V of a stage that some row does not see
-                unsigned char *vt = sm + (j % kStages) * L::STAGE + L::TILE;
-                if (!dead)
-                    dead = !__all_sync(0xffffffffu, wait_or_fail(full + j % kStages, (j / kStages) & 1,
-                                                                 a.wait_polls, failed));
+                unsigned char *vt = slot_of(v_tile(j, nsub));
+                if (!dead) dead = !__all_sync(0xffffffffu, wait_full(v_tile(j, nsub)));
                 // thread t scans half a key row: 128-byte rows t, t + 128, ... of the tile
                 bool bad = false;
                 if (!dead)
@@ -844,6 +906,10 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
                             }
                         }
                 if (softmax_any(bad)) {
+                    if (!dead && j > 0) {
+                        dead = !__all_sync(0xffffffffu, wait_product(j - 1));
+                        tc::fence_after_sync();
+                    }
                     if (!dead && j == 0) {  // O has no product yet: it starts from zeros
                         float z[32];
 #pragma unroll
@@ -856,8 +922,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
 #pragma unroll 1
                         for (int key = 0; key < kSub; ++key) {
                             if (!((bad_keys[key >> 5] >> (key & 31)) & 1u)) continue;
-                            const uint32_t pw = __float_as_uint(tc::tmem_ld1(t_s + lane_base + key / 2));
-                            const float p = half_of_pair<KV4>(pw, key & 1);
+                            const float p = half_of_pair<KV4>(*reinterpret_cast<const uint16_t *>(
+                                p_row + tc::sw128(tid, key >> 3) + (key & 7) * 2), 0);
 #pragma unroll 1
                             for (int c = 0; c < DH; ++c) {
                                 const uint32_t w = *reinterpret_cast<const uint16_t *>(
@@ -884,12 +950,12 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
             }
             if (!dead) {
                 tc::fence_before_sync();
-                tc::mbar_arrive(bar_p);
+                tc::mbar_arrive(bar_p + (j & 1));
             }
         }
         // ---- the last product, then the row
         if (!dead)
-            dead = !__all_sync(0xffffffffu, wait_or_fail(bar_o, (nsub - 1) & 1, a.wait_polls, failed));
+            dead = !__all_sync(0xffffffffu, wait_product(nsub - 1));
         tc::fence_after_sync();
         if (dead) {
             publish_nothing();
@@ -930,20 +996,42 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
 
 // One warp per (sequence, head, row): out = sum_s 2^(m_s - M) O_s / sum_s
 // 2^(m_s - M) l_s over the key ranges.  An empty range (l = 0) has no O row.
+// Lane s reads range s's (m, l); the O rows do not depend on them and are
+// loaded eight at a time, the first eight in the same round.
 template <typename T, int DH>
 __global__ void __launch_bounds__(256)
 cache_attn_combine_kernel(const float *__restrict__ part_o, const float2 *__restrict__ part_ml,
                           int B, int R, int H, int NS, T *__restrict__ out) {
     pdl_enter();
-    constexpr int PER = DH / 32;
+    constexpr int PER = DH / 32, AHEAD = 8;
     const int lane = threadIdx.x & 31;
     const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (item >= (long long)B * H * R) return;
     const int r = (int)(item % R);
     const long long bh = item / R;
     const float2 *ml = part_ml + bh * NS * R + r;
-    float M = -INFINITY;
-    for (int s = lane; s < NS; s += 32) {
+    const float *po = part_o + (bh * NS * R + r) * DH + lane * PER;
+    const size_t step = (size_t)R * DH;
+    float2 row[AHEAD][PER / 2];
+    auto load = [&](int s0) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (s0 + i < NS) {
+                const float *p = po + (s0 + i) * step;
+                if constexpr (PER == 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(p);
+                    row[i][0] = make_float2(v.x, v.y);
+                    row[i][1] = make_float2(v.z, v.w);
+                } else {
+                    row[i][0] = *reinterpret_cast<const float2 *>(p);
+                }
+            }
+    };
+    const float2 empty = make_float2(-INFINITY, 0.f);
+    const float2 first = lane < NS ? ml[(size_t)lane * R] : empty;
+    load(0);
+    float M = first.y != 0.f ? first.x : -INFINITY;
+    for (int s = lane + 32; s < NS; s += 32) {
         const float2 x = ml[(size_t)s * R];
         if (x.y != 0.f) M = fmaxf(M, x.x);
     }
@@ -953,20 +1041,38 @@ cache_attn_combine_kernel(const float *__restrict__ part_o, const float2 *__rest
     float L = 0.f, acc[PER];
 #pragma unroll
     for (int p = 0; p < PER; ++p) acc[p] = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < NS; ++s) {
-        const float2 x = ml[(size_t)s * R];
-        if (x.y == 0.f) continue;
-        const float w = exp2f(x.x - mu);
-        L = fmaf(w, x.y, L);
-        const float *o = part_o + ((bh * NS + s) * R + r) * DH + lane * PER;
+    float w_l = 0.f;
+    for (int s0 = 0; s0 < NS; s0 += AHEAD) {
+        if (s0 > 0) load(s0);
+        if ((s0 & 31) == 0) {
+            const float2 x = s0 == 0 ? first : s0 + lane < NS ? ml[(size_t)(s0 + lane) * R] : empty;
+            w_l = x.y != 0.f ? exp2f(x.x - mu) : 0.f;
+            if (x.y != 0.f) L = fmaf(w_l, x.y, L);
+        }
 #pragma unroll
-        for (int p = 0; p < PER; ++p) acc[p] = fmaf(w, o[p], acc[p]);
+        for (int i = 0; i < AHEAD; ++i) {
+            const float w = __shfl_sync(0xffffffffu, w_l, (s0 + i) & 31);
+            if (s0 + i < NS && w != 0.f) {
+#pragma unroll
+                for (int p = 0; p < PER / 2; ++p) {
+                    acc[2 * p] = fmaf(w, row[i][p].x, acc[2 * p]);
+                    acc[2 * p + 1] = fmaf(w, row[i][p].y, acc[2 * p + 1]);
+                }
+            }
+        }
     }
+    L = warp_sum(L);
     const float inv = L == 0.f ? 0.f : 1.f / L;
     T *dst = out + (((bh / H) * R + r) * H + bh % H) * DH + lane * PER;
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int p = 0; p < PER; ++p) store_out(dst + p, acc[p] * inv);
+        for (int p = 0; p < PER; ++p) dst[p] = acc[p] * inv;
+    } else {
+#pragma unroll
+        for (int p = 0; p < PER; p += 2)
+            *reinterpret_cast<__nv_bfloat162 *>(dst + p) =
+                __floats2bfloat162_rn(acc[p] * inv, acc[p + 1] * inv);
+    }
 }
 
 // ------------------------------------------------------------------- host ---
@@ -1066,7 +1172,8 @@ cudaError_t launch_cache_attention(medusa_dtype dtype, bool kv4, const void *q,
     } else {
         auto kern = kv4 ? (dh == 128 ? cache_attn_tc_kernel<128, true> : cache_attn_tc_kernel<64, true>)
                         : (dh == 128 ? cache_attn_tc_kernel<128, false> : cache_attn_tc_kernel<64, false>);
-        const int smem = dh == 128 ? CacheSmem<128>::TOTAL : CacheSmem<64>::TOTAL;
+        const int smem = kv4 ? (dh == 128 ? CacheSmem<128, true>::TOTAL : CacheSmem<64, true>::TOTAL)
+                             : (dh == 128 ? CacheSmem<128, false>::TOTAL : CacheSmem<64, false>::TOTAL);
         if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
             return e;
         e = launch_pdl(kern, grid, dim3(kTcThreads), (size_t)smem, stream, a);
