@@ -306,7 +306,7 @@ constexpr int kSub = 64, kTcThreads = 288;
 constexpr float kRescaleLog2 = 8.f;
 constexpr float kF16Bias = 7.f;
 constexpr uint32_t kDrainPolls = 1u << 16;
-constexpr int kAhead = 6;  // 4-bit tiles held in a loader's registers
+constexpr int kAhead = 4;  // 4-bit tiles held in a loader's registers
 
 template <int DH, bool KV4>
 struct CacheSmem {
@@ -352,12 +352,13 @@ __device__ __forceinline__ bool softmax_any(bool p) {
     return r != 0;
 }
 
-// Wait for a phase, giving up after `limit` polls or once the CTA has failed.
+// Wait of a converged warp for a phase, giving up after `limit` polls or once
+// the CTA has failed.  The votes keep the loop free of divergence.
 __device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, uint32_t limit,
                                              volatile int *failed) {
     for (uint32_t i = 0; i < limit; ++i) {
-        if (tc::mbar_try_wait(bar, parity)) return true;
-        if (*failed) return false;
+        if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, *failed)) return false;
     }
     *failed = 1;
     return false;
@@ -428,37 +429,40 @@ struct Kv4Regs {
     uint32_t scale[N];
 };
 
-// loads that stay where they are written: ahead of their use by kAhead tiles
-__device__ __forceinline__ uint4 ld_ahead16(const void *p) {
-    uint4 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "l"(p));
-    return r;
+// Loads that stay where they are written, ahead of their use by kAhead tiles.
+// The condition is inside: a load in a branch would be waited for where its
+// register is merged with the other side's.
+__device__ __forceinline__ void ld_ahead16(uint4 &r, const void *p, bool on) {
+    asm volatile(
+        "{\n.reg .pred q;\n"
+        "setp.ne.b32 q, %5, 0;\n"
+        "@q ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n}\n"
+        : "+r"(r.x), "+r"(r.y), "+r"(r.z), "+r"(r.w)
+        : "l"(p), "r"((int)on));
 }
-__device__ __forceinline__ uint32_t ld_ahead2(const void *p) {
-    uint16_t r;
-    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(r) : "l"(p));
-    return r;
+__device__ __forceinline__ void ld_ahead2(uint32_t &r, const void *p, bool on) {
+    asm volatile(
+        "{\n.reg .pred q;\n"
+        "setp.ne.b32 q, %2, 0;\n"
+        "@q ld.global.nc.u16 %0, [%1];\n}\n"
+        : "+r"(r)
+        : "l"(p), "r"((int)on));
 }
 
+// (keys past the range read its last row; their scale is cleared on the way to
+// shared memory)
 template <int DH>
 __device__ __forceinline__ void load_regs_kv4(Kv4Regs<DH> &r, const uint8_t *cache,
                                               const KeyRun &run, int k0, int kend, int Hkv, int g,
-                                              int t) {
+                                              int t, bool on) {
     constexpr int GPK = DH / 32;  // groups per key
     const int rb = kv4_row_bytes(Hkv, DH), cb = kv4_code_bytes(Hkv, DH);
 #pragma unroll
     for (int u = 0; u < Kv4Regs<DH>::N; ++u) {
-        const int c = t + 128 * u, x = k0 + c / GPK, q = c % GPK;
-        if (x < kend) {
-            const uint8_t *row = cache + (size_t)run.slot(x) * rb;
-            r.code[u] = ld_ahead16(row + g * (DH / 2) + q * 16);
-            r.scale[u] = ld_ahead2(row + cb + g * (DH / 16) + q * 2);
-        } else {
-            r.code[u] = make_uint4(0, 0, 0, 0);
-            r.scale[u] = 0;
-        }
+        const int c = t + 128 * u, x = min(k0 + c / GPK, kend - 1), q = c % GPK;
+        const uint8_t *row = cache + (size_t)run.slot(x) * rb;
+        ld_ahead16(r.code[u], row + g * (DH / 2) + q * 16, on);
+        ld_ahead2(r.scale[u], row + cb + g * (DH / 16) + q * 2, on);
     }
 }
 
@@ -482,7 +486,8 @@ __device__ __forceinline__ uint4 widen_word(uint32_t w, __half2 s) {
 }
 
 template <int DH>
-__device__ __forceinline__ void store_regs_kv4(const Kv4Regs<DH> &r, unsigned char *tile, int t) {
+__device__ __forceinline__ void store_regs_kv4(const Kv4Regs<DH> &r, unsigned char *tile, int k0,
+                                               int kend, int t) {
     constexpr int GPK = DH / 32;
 #pragma unroll
     for (int u = 0; u < Kv4Regs<DH>::N; ++u) {
@@ -494,7 +499,8 @@ __device__ __forceinline__ void store_regs_kv4(const Kv4Regs<DH> &r, unsigned ch
         unsigned char *blk = tile + (q >> 1) * kSub * 128;
         const uint4 w = r.code[u];
         const __half2 s2 =
-            __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)r.scale[u], __NV_E4M3));
+            __half2(__nv_cvt_fp8x2_to_halfraw2(
+                (__nv_fp8x2_storage_t)(k0 + key < kend ? r.scale[u] : 0u), __NV_E4M3));
         const __half2 sa = flip ? __high2half2(s2) : __low2half2(s2);
         const __half2 sb = flip ? __low2half2(s2) : __high2half2(s2);
         const uint32_t word[4] = {flip ? w.z : w.x, flip ? w.w : w.y, flip ? w.x : w.z, flip ? w.y : w.w};
@@ -514,7 +520,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BAR), *empty = full + L::NT;
     // p and o have a barrier for each P buffer: a warp may be a stage ahead of
     // another, and its arrival for the next stage must not count for this one
-    // (at stage j + 2 it has waited for the product of j, hence for all of j)
+    // (at stage j + 2 the scores it has waited for came after the product of j)
     uint64_t *bar_q = empty + L::NT, *bar_s = bar_q + 1, *bar_sfree = bar_q + 2,
              *bar_drain = bar_q + 3, *bar_p = bar_q + 4, *bar_o = bar_q + 6;
     volatile int *failed = reinterpret_cast<volatile int *>(sm + L::WORDS);
@@ -526,7 +532,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
     const int g = blockIdx.x / a.row_tiles, rt = blockIdx.x - g * a.row_tiles;
     const int split = blockIdx.y, b = blockIdx.z;
     const int R = a.R, G = a.H / a.Hkv, M = R * G;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     int P;
     const void *kc, *vc;
     const bool ok = sequence_ok(a, b, P, kc, vc);
@@ -597,11 +603,10 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
         };
         if constexpr (KV4) {
             const uint8_t *k8 = static_cast<const uint8_t *>(kc), *v8 = static_cast<const uint8_t *>(vc);
-            Kv4Regs<DH> buf[kAhead];
+            Kv4Regs<DH> buf[kAhead] = {};
             auto fetch = [&](Kv4Regs<DH> &r, int i) {
-                if (i < n_tiles)
-                    load_regs_kv4<DH>(r, tile_is_v(i, nsub) ? v8 : k8, run,
-                                      kbeg + tile_stage(i, nsub) * kSub, kend, a.Hkv, g, t);
+                load_regs_kv4<DH>(r, tile_is_v(i, nsub) ? v8 : k8, run,
+                                  kbeg + tile_stage(i, nsub) * kSub, kend, a.Hkv, g, t, i < n_tiles);
             };
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) fetch(buf[u], u);
@@ -613,12 +618,13 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
                     if (i < n_tiles && go) {
                         go = wait_empty(i);
                         if (go) {
-                            store_regs_kv4<DH>(buf[u], slot_of(i), t);
+                            store_regs_kv4<DH>(buf[u], slot_of(i), kbeg + tile_stage(i, nsub) * kSub,
+                                               kend, t);
                             tc::fence_proxy_async_smem();
                             tc::mbar_arrive(full + i % L::NT);
-                            fetch(buf[u], i + kAhead);
                         }
                     }
+                    fetch(buf[u], i + kAhead);
                 }
             }
         } else {
@@ -645,50 +651,58 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
         }
     } else if (warp == 8) {
         // ----------------------------------------------------------- products
-        if (lane == 0) {
-            constexpr uint32_t id_s = KV4 ? tc::idesc_f16(128, kSub, 0) : tc::idesc_bf16(128, kSub, 0);
-            constexpr uint32_t id_o = KV4 ? tc::idesc_f16(128, DH, 1) : tc::idesc_bf16(128, DH, 1);
-            auto scores = [&](int j) {
-                const int i = k_tile(j);
-                if (!wait_full(i)) return false;
-                // the scores before are in registers
-                if (j > 0 && !wait_or_fail(bar_sfree, (j - 1) & 1, a.wait_polls, failed)) return false;
-                tc::fence_after_sync();
-                const uint64_t kd = tc::sdesc_sw128(tc::smem_addr(slot_of(i)), 16, 1024);
+        // (the warp stays converged; one elected lane issues)
+        constexpr uint32_t id_s = KV4 ? tc::idesc_f16(128, kSub, 0) : tc::idesc_bf16(128, kSub, 0);
+        constexpr uint32_t id_o = KV4 ? tc::idesc_f16(128, DH, 1) : tc::idesc_bf16(128, DH, 1);
+        const uint64_t kd0 = tc::sdesc_sw128(tc::smem_addr(sm), 16, 1024);
+        const uint64_t vd0 = tc::sdesc_sw128(tc::smem_addr(sm), kSub * 128, 1024);
+        const uint64_t pd0 = tc::sdesc_sw128(tc::smem_addr(sm + L::PW), 16, 1024);
+        auto scores = [&](int j) {
+            const int i = k_tile(j);
+            // the scores before are in registers
+            if (!wait_full(i)) return false;
+            if (j > 0 && !wait_or_fail(bar_sfree, (j - 1) & 1, a.wait_polls, failed)) return false;
+            tc::fence_after_sync();
+            const int slot = i % L::NT;
+            if (tc::elect_one()) {
+                const uint64_t kd = kd0 + (uint64_t)(slot * (L::TILE >> 4));
 #pragma unroll
                 for (int ks = 0; ks < DH / 16; ++ks)
                     tc::mma_bf16_ts(t_s, t_q + ks * 8, kd + (((ks >> 2) * kSub * 128 + (ks & 3) * 32) >> 4),
                                     id_s, ks > 0);
-                tc::mma_commit(empty + i % L::NT);
                 tc::mma_commit(bar_s);
-                return true;
-            };
-            bool go = wait_or_fail(bar_q, 0, a.wait_polls, failed) && scores(0);
-            for (int j = 0; j < nsub && go; ++j) {
-                if (j + 1 < nsub && !scores(j + 1)) break;
-                const int i = v_tile(j, nsub);
-                if (!wait_or_fail(bar_p + (j & 1), (j >> 1) & 1, a.wait_polls, failed) ||
-                    !wait_full(i)) break;
-                tc::fence_after_sync();
-                const uint64_t vd = tc::sdesc_sw128(tc::smem_addr(slot_of(i)), kSub * 128, 1024);
-                const uint64_t pd =
-                    tc::sdesc_sw128(tc::smem_addr(sm + L::PW + (j & 1) * L::P_BYTES), 16, 1024);
-                const uint32_t acc0 = j > 0 || *o_started;
+                tc::mma_commit(empty + slot);
+            }
+            __syncwarp();
+            return true;
+        };
+        bool go = wait_or_fail(bar_q, 0, a.wait_polls, failed) && scores(0);
+        for (int j = 0; j < nsub && go; ++j) {
+            if (j + 1 < nsub && !scores(j + 1)) break;
+            const int i = v_tile(j, nsub);
+            if (!wait_or_fail(bar_p + (j & 1), (j >> 1) & 1, a.wait_polls, failed) || !wait_full(i)) break;
+            tc::fence_after_sync();
+            const uint32_t acc0 = j > 0 || *o_started;
+            const int slot = i % L::NT;
+            if (tc::elect_one()) {
+                const uint64_t vd = vd0 + (uint64_t)(slot * (L::TILE >> 4));
+                const uint64_t pd = pd0 + (uint64_t)((j & 1) * (L::P_BYTES >> 4));
 #pragma unroll
                 for (int ks = 0; ks < kSub / 16; ++ks)
                     tc::mma_bf16_ss(t_o, pd + ((ks * 32) >> 4), vd + ((ks * 16 * 128) >> 4), id_o,
                                     ks > 0 ? 1u : acc0);
-                tc::mma_commit(empty + i % L::NT);
                 tc::mma_commit(bar_o + (j & 1));
+                tc::mma_commit(empty + slot);
             }
-            // every product issued above is done before the tensor memory is freed
-            tc::mma_commit(bar_drain);
-            if (!tc::mbar_wait_bounded(bar_drain, 0, kDrainPolls)) {
-                *failed = 1;
-                if (a.status) atomicExch(a.status, MEDUSA_DEV_DRAIN_TIMEOUT);
-            }
+            __syncwarp();
         }
+        // every product issued above is done before the tensor memory is freed
+        if (tc::elect_one()) tc::mma_commit(bar_drain);
         __syncwarp();
+        if (!__all_sync(0xffffffffu, tc::mbar_wait_bounded(bar_drain, 0, kDrainPolls))) {
+            *failed = 1;
+            if (lane == 0 && a.status) atomicExch(a.status, MEDUSA_DEV_DRAIN_TIMEOUT);
+        }
     } else {
         // ------------------------------------------------------------ softmax
         const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
@@ -786,21 +800,15 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
             const int k0 = kbeg + j * kSub;
             const bool masked = !(k0 + kSub <= min(kend, x_tree) && (k0 >= x_all || k0 + kSub <= run.n_sink));
             unsigned char *p_row = sm + L::PW + (j & 1) * L::P_BYTES;
-            // the scores are there, and the product of j - 2 has read this P buffer
-            if (!dead)
-                dead = !__all_sync(0xffffffffu, wait_or_fail(bar_s, j & 1, a.wait_polls, failed) &&
-                                                    (j < 2 || wait_product(j - 2)));
+            // the scores are there; their commit also covers the product of j - 2,
+            // issued before them, which read this P buffer
+            if (!dead) dead = !wait_or_fail(bar_s, j & 1, a.wait_polls, failed);
             tc::fence_after_sync();
             if (!dead && !rows_live) tc::mbar_arrive(bar_sfree);
             if (!dead && rows_live) {
                 float x[kSub];
-                {
-                    float (&lo)[32] = *reinterpret_cast<float (*)[32]>(x);
-                    float (&hi)[32] = *reinterpret_cast<float (*)[32]>(x + 32);
-                    tc::tmem_ld32(t_s + lane_base, lo);
-                    tc::tmem_ld32(t_s + lane_base + 32, hi);
-                    tc::fence_before_sync();
-                }
+                tc::tmem_ld64(t_s + lane_base, x);
+                tc::fence_before_sync();
                 tc::mbar_arrive(bar_sfree);
                 bool grew = false;
                 float alpha = 1.f;
@@ -873,7 +881,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
                 l_run += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
                 tc::fence_proxy_async_smem();
                 if (__any_sync(0xffffffffu, grew && j > 0)) {
-                    dead = !__all_sync(0xffffffffu, wait_product(j - 1));
+                    dead = !wait_product(j - 1);
                     tc::fence_after_sync();
                     if (!dead) {
 #pragma unroll 1
@@ -890,7 +898,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
             if (masked) {
                 // ---- infinities and NaNs in V of a stage that some row does not see
                 unsigned char *vt = slot_of(v_tile(j, nsub));
-                if (!dead) dead = !__all_sync(0xffffffffu, wait_full(v_tile(j, nsub)));
+                if (!dead) dead = !wait_full(v_tile(j, nsub));
                 // thread t scans half a key row: 128-byte rows t, t + 128, ... of the tile
                 bool bad = false;
                 if (!dead)
@@ -907,7 +915,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
                         }
                 if (softmax_any(bad)) {
                     if (!dead && j > 0) {
-                        dead = !__all_sync(0xffffffffu, wait_product(j - 1));
+                        dead = !wait_product(j - 1);
                         tc::fence_after_sync();
                     }
                     if (!dead && j == 0) {  // O has no product yet: it starts from zeros
@@ -955,7 +963,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
         }
         // ---- the last product, then the row
         if (!dead)
-            dead = !__all_sync(0xffffffffu, wait_product(nsub - 1));
+            dead = !wait_product(nsub - 1);
         tc::fence_after_sync();
         if (dead) {
             publish_nothing();
