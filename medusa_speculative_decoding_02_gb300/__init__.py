@@ -555,29 +555,45 @@ def speculative_posterior(logits, tokens, draft_logits, temperature: float, seed
 
 
 # ------------------------------------------- rotation, 4-bit cache, windows ---
+#
+# These calls run in a few microseconds on the GPU, so their checks are one
+# short function per tensor, and the current stream is taken as its handle.
 
-def _on_device(ref: torch.Tensor, stream, **tensors):
-    """Argument checks shared by the calls below: CUDA tensors, all on the
-    current device; returns the stream to launch on.  The names of int32 /
-    int64 arrays end in _i32 / _i64."""
+_INT = torch.int32
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _launch_on(ref: torch.Tensor, stream):
+    """(device index, stream handle) of a call whose tensors must all be on the
+    current device."""
     dev = ref.get_device()
-    if dev != torch.cuda.current_device():
+    if dev < 0 or dev != torch.cuda.current_device():
         raise ValueError("tensors must be on the current CUDA device")
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if t.get_device() != dev:
-            raise ValueError(f"{name.rsplit('_i', 1)[0]} must be a CUDA tensor on the same device")
-        want = (torch.int32 if name.endswith("_i32") else torch.int64 if name.endswith("_i64")
-                else torch.float32 if name.endswith("_f32") else None)
-        if want is not None and (t.dtype != want or not t.is_contiguous()):
-            raise ValueError(f"{name[:-4]} must be contiguous and {want}")
-    return torch.cuda.current_stream() if stream is None else stream
+    if stream is not None:
+        return dev, stream.cuda_stream
+    return dev, _raw_stream(dev) if _raw_stream else torch.cuda.current_stream().cuda_stream
 
 
-def _size_is(t: Optional[torch.Tensor], n: int, name: str):
-    if t is not None and t.numel() != n:
-        raise ValueError(f"{name} must hold {n} elements, got {tuple(t.shape)}")
+def _vec(t, n: int, dtype, dev: int, name: str):
+    """Address of an array argument: n dense elements of dtype on device dev."""
+    if t.dtype is not dtype or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous {dtype} elements on the same device, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _dense(t, shape, dtype, dev: int, name: str):
+    """Address of a dense tensor argument of the given shape."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a dense {dtype} tensor of {tuple(shape)} on the same device, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _ws_args(ws, dev: int):
+    if ws.get_device() != dev or ws.dtype is not torch.uint8 or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous uint8 tensor on the same device")
+    return ws.data_ptr(), ws.numel()
 
 
 def _rows(t: torch.Tensor, name: str):
@@ -586,6 +602,8 @@ def _rows(t: torch.Tensor, name: str):
     if t.dim() != 4:
         raise ValueError(f"{name} must be [B,R,heads,dh]")
     B, R, H, dh = t.shape
+    if t.is_contiguous():
+        return H * dh
     s = t.stride()
     if s[3] != 1 or (H > 1 and s[2] != dh) or (B > 1 and R > 1 and s[0] != R * s[1]):
         raise ValueError(f"{name}: heads must be dense and rows evenly apart")
@@ -598,11 +616,9 @@ def _issue_on(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
-def _scratch(ws, nbytes: int, device, stream):
-    """The caller's workspace, or one made on the launch stream with the status
-    word at 0 (the rest needs no clearing)."""
-    if ws is not None:
-        return ws
+def _scratch(nbytes: int, device, stream):
+    """A workspace made on the launch stream with the status word at 0 (the rest
+    needs no clearing)."""
     with _issue_on(stream):
         t = torch.empty((max(int(nbytes), WS_HEADER) + 255) // 256 * 256, dtype=torch.uint8,
                         device=device)
@@ -617,26 +633,13 @@ def _new(stream, like: torch.Tensor, shape=None, dtype=None):
                            device=like.device)
 
 
-def _out(t: torch.Tensor, like: torch.Tensor, name: str, shape=None):
-    if t.shape != (like.shape if shape is None else shape) or t.dtype != like.dtype \
-            or not t.is_contiguous() or t.get_device() != like.get_device():
-        raise ValueError(f"{name} must be a dense {like.dtype} tensor of "
-                         f"{tuple(like.shape if shape is None else shape)} on the same device")
-
-
-def _rope_args(q, k, pos, inv_freq, q_weight, k_weight, norm, n_rows):
-    B, R, H, dh = q.shape
-    dt = _dtype(q)
-    if k.dtype != q.dtype or k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != dh:
-        raise ValueError("k must be [B,R,Hkv,dh] of q's dtype")
-    _size_is(pos, B * R, "pos")
-    _size_is(n_rows, B, "n_rows")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _size_is(w, dh, name)
-            if w.dtype != q.dtype or not w.is_contiguous():
-                raise ValueError(f"{name} must be contiguous and of q's dtype")
-    return dt, B, R, H, k.shape[2], dh
+def _rope_args(q, k, q_weight, k_weight, dev):
+    if k.dtype is not q.dtype or k.get_device() != dev or k.dim() != 4 or q.dim() != 4 \
+            or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3]:
+        raise ValueError("q must be [B,R,H,dh] and k [B,R,Hkv,dh] of the same dtype and device")
+    dh = q.shape[3]
+    return (None if q_weight is None else _vec(q_weight, dh, q.dtype, dev, "q_weight"),
+            None if k_weight is None else _vec(k_weight, dh, q.dtype, dev, "k_weight"))
 
 
 def qk_norm_rope(q, k, pos, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -647,19 +650,21 @@ def qk_norm_rope(q, k, pos, inv_freq, q_weight=None, k_weight=None, eps: float =
     rotates only.  q and k may be slices of one wider projection.  Rows
     i >= n_rows[b] are left alone.  Returns (q_out, k_out), ``out`` if given
     (it may be (q, k))."""
-    dt, B, R, H, Hkv, dh = _rope_args(q, k, pos, inv_freq, q_weight, k_weight, norm, n_rows)
-    s = _on_device(q, stream, k=k, pos_i32=pos, inv_freq_f32=inv_freq, q_weight=q_weight,
-                   k_weight=k_weight, n_rows_i32=n_rows)
+    dt = _dtype(q)
+    dev, st = _launch_on(q, stream)
+    qw, kw = _rope_args(q, k, q_weight, k_weight, dev)
+    B, R, H, dh = q.shape
+    half = inv_freq.numel()
     if out is None:
         out = (_new(stream, q), _new(stream, k))
-    qo, ko = out
-    _out(qo, q, "q_out")
-    _out(ko, k, "k_out")
-    _check(lib().medusa_qk_norm_rope(dt, _ptr(q), _ptr(k), _rows(q, "q"), _rows(k, "k"),
-                                     _ptr(q_weight), _ptr(k_weight), eps, 1 if norm else 0, _ptr(pos),
-                                     _ptr(inv_freq), 2 * inv_freq.numel(), 1 if interleaved else 0,
-                                     _ptr(n_rows), B, R, H, Hkv, dh, _ptr(qo), _ptr(ko), s.cuda_stream))
-    return qo, ko
+    _check(lib().medusa_qk_norm_rope(
+        dt, q.data_ptr(), k.data_ptr(), _rows(q, "q"), _rows(k, "k"), qw, kw, eps, 1 if norm else 0,
+        _vec(pos, B * R, _INT, dev, "pos"), _vec(inv_freq, half, torch.float32, dev, "inv_freq"),
+        2 * half, 1 if interleaved else 0,
+        None if n_rows is None else _vec(n_rows, B, _INT, dev, "n_rows"), B, R, H, k.shape[2], dh,
+        _dense(out[0], q.shape, q.dtype, dev, "q_out"), _dense(out[1], k.shape, q.dtype, dev, "k_out"),
+        st))
+    return out
 
 
 def qk_norm_rope_append(q, k, v, pos, inv_freq, k_ptrs, v_ptrs, prefix_len, P_max: int,
@@ -668,23 +673,26 @@ def qk_norm_rope_append(q, k, v, pos, inv_freq, k_ptrs, v_ptrs, prefix_len, P_ma
     """qk_norm_rope with the finished K rows, and the V rows, written into cache
     slots prefix_len[b] + i of the caches behind k_ptrs / v_ptrs
     ([>= P_max+R, Hkv, dh]).  Returns q_out."""
-    dt, B, R, H, Hkv, dh = _rope_args(q, k, pos, inv_freq, q_weight, k_weight, norm, n_rows)
-    if v.dtype != k.dtype or v.shape != k.shape:
-        raise ValueError("v must have k's shape and dtype")
-    s = _on_device(q, stream, k=k, v=v, pos_i32=pos, inv_freq_f32=inv_freq, q_weight=q_weight,
-                   k_weight=k_weight, n_rows_i32=n_rows, k_ptrs_i64=k_ptrs, v_ptrs_i64=v_ptrs,
-                   prefix_len_i32=prefix_len, ws=ws)
-    for t, name in ((k_ptrs, "k_ptrs"), (v_ptrs, "v_ptrs"), (prefix_len, "prefix_len")):
-        _size_is(t, B, name)
+    dt = _dtype(q)
+    dev, st = _launch_on(q, stream)
+    qw, kw = _rope_args(q, k, q_weight, k_weight, dev)
+    if v.dtype is not k.dtype or v.shape != k.shape or v.get_device() != dev:
+        raise ValueError("v must have k's shape, dtype and device")
+    B, R, H, dh = q.shape
+    half = inv_freq.numel()
     if out is None:
         out = _new(stream, q)
-    _out(out, q, "out")
-    ws = _scratch(ws, WS_HEADER, q.device, stream)
+    if ws is None:
+        ws = _scratch(WS_HEADER, q.device, stream)
+    ws_ptr, ws_n = _ws_args(ws, dev)
     _check(lib().medusa_qk_norm_rope_append(
-        dt, _ptr(q), _ptr(k), _ptr(v), _rows(q, "q"), _rows(k, "k"), _rows(v, "v"), _ptr(q_weight),
-        _ptr(k_weight), eps, 1 if norm else 0, _ptr(pos), _ptr(inv_freq), 2 * inv_freq.numel(),
-        1 if interleaved else 0, _ptr(n_rows), _ptr(k_ptrs), _ptr(v_ptrs), _ptr(prefix_len),
-        int(P_max), B, R, H, Hkv, dh, _ptr(out), _ptr(ws), ws.numel(), s.cuda_stream))
+        dt, q.data_ptr(), k.data_ptr(), v.data_ptr(), _rows(q, "q"), _rows(k, "k"), _rows(v, "v"), qw,
+        kw, eps, 1 if norm else 0, _vec(pos, B * R, _INT, dev, "pos"),
+        _vec(inv_freq, half, torch.float32, dev, "inv_freq"), 2 * half, 1 if interleaved else 0,
+        None if n_rows is None else _vec(n_rows, B, _INT, dev, "n_rows"),
+        _vec(k_ptrs, B, torch.int64, dev, "k_ptrs"), _vec(v_ptrs, B, torch.int64, dev, "v_ptrs"),
+        _vec(prefix_len, B, _INT, dev, "prefix_len"), P_max, B, R, H, k.shape[2], dh,
+        _dense(out, q.shape, q.dtype, dev, "out"), ws_ptr, ws_n, st))
     return out
 
 
@@ -706,60 +714,58 @@ def kv4_append(k, v, k_ptrs, v_ptrs, prefix_len, P_max: int, n_rows=None, ws=Non
     k_ptrs / v_ptrs (see kv4_cache, at least P_max + R slots each).  Rows
     i >= n_rows[b] are left alone."""
     dt = _dtype(k)
-    if v.dtype != k.dtype or v.shape != k.shape:
-        raise ValueError("v must have k's shape and dtype")
+    dev, st = _launch_on(k, stream)
+    if v.dtype is not k.dtype or v.shape != k.shape or v.get_device() != dev:
+        raise ValueError("v must have k's shape, dtype and device")
     ks, vs = _rows(k, "k"), _rows(v, "v")
     B, R, Hkv, dh = k.shape
-    s = _on_device(k, stream, v=v, k_ptrs_i64=k_ptrs, v_ptrs_i64=v_ptrs, prefix_len_i32=prefix_len,
-                   n_rows_i32=n_rows, ws=ws)
-    for t, name in ((k_ptrs, "k_ptrs"), (v_ptrs, "v_ptrs"), (prefix_len, "prefix_len"),
-                    (n_rows, "n_rows")):
-        _size_is(t, B, name)
-    ws = _scratch(ws, WS_HEADER, k.device, stream)
-    _check(lib().medusa_kv4_append(dt, _ptr(k), _ptr(v), ks, vs, _ptr(k_ptrs), _ptr(v_ptrs),
-                                   _ptr(prefix_len), int(P_max), _ptr(n_rows), B, R, Hkv, dh,
-                                   _ptr(ws), ws.numel(), s.cuda_stream))
+    if ws is None:
+        ws = _scratch(WS_HEADER, k.device, stream)
+    ws_ptr, ws_n = _ws_args(ws, dev)
+    _check(lib().medusa_kv4_append(
+        dt, k.data_ptr(), v.data_ptr(), ks, vs, _vec(k_ptrs, B, torch.int64, dev, "k_ptrs"),
+        _vec(v_ptrs, B, torch.int64, dev, "v_ptrs"), _vec(prefix_len, B, _INT, dev, "prefix_len"), P_max,
+        None if n_rows is None else _vec(n_rows, B, _INT, dev, "n_rows"), B, R, Hkv, dh, ws_ptr, ws_n,
+        st))
 
 
 def kv4_unpack(k_ptrs, v_ptrs, prefix_len, P_max: int, R: int, Hkv: int, dh: int,
                dtype=torch.bfloat16, n_rows=None, out=None, ws=None, stream=None):
     """The values of slots prefix_len[b] + i, i < R, of 4-bit caches: (k, v)
     [B,R,Hkv,dh].  Rows i >= n_rows[b] are left as ``out`` has them."""
-    s = _on_device(k_ptrs, stream, k_ptrs_i64=k_ptrs, v_ptrs_i64=v_ptrs, prefix_len_i32=prefix_len,
-                   n_rows_i32=n_rows, ws=ws)
+    dev, st = _launch_on(k_ptrs, stream)
     B = k_ptrs.numel()
-    for t, name in ((v_ptrs, "v_ptrs"), (prefix_len, "prefix_len"), (n_rows, "n_rows")):
-        _size_is(t, B, name)
-    shape = (B, int(R), int(Hkv), int(dh))
+    shape = (B, R, Hkv, dh)
     if out is None:
         out = (_new(stream, k_ptrs, shape, dtype), _new(stream, k_ptrs, shape, dtype))
     ko, vo = out
-    _out(ko, ko, "k_out", shape)
-    _out(vo, ko, "v_out", shape)
-    if ko.get_device() != k_ptrs.get_device():
-        raise ValueError("k_out must be a CUDA tensor on the same device")
-    ws = _scratch(ws, WS_HEADER, k_ptrs.device, stream)
-    _check(lib().medusa_kv4_unpack(_dtype(ko), _ptr(k_ptrs), _ptr(v_ptrs), _ptr(prefix_len),
-                                   int(P_max), _ptr(n_rows), B, int(R), int(Hkv), int(dh), _ptr(ko),
-                                   _ptr(vo), _ptr(ws), ws.numel(), s.cuda_stream))
-    return ko, vo
+    if ws is None:
+        ws = _scratch(WS_HEADER, k_ptrs.device, stream)
+    ws_ptr, ws_n = _ws_args(ws, dev)
+    _check(lib().medusa_kv4_unpack(
+        _dtype(ko), _vec(k_ptrs, B, torch.int64, dev, "k_ptrs"),
+        _vec(v_ptrs, B, torch.int64, dev, "v_ptrs"), _vec(prefix_len, B, _INT, dev, "prefix_len"), P_max,
+        None if n_rows is None else _vec(n_rows, B, _INT, dev, "n_rows"), B, R, Hkv, dh,
+        _dense(ko, shape, ko.dtype, dev, "k_out"), _dense(vo, shape, ko.dtype, dev, "v_out"), ws_ptr,
+        ws_n, st))
+    return out
 
 
 def commit_kv4(k_ptrs, v_ptrs, prefix_len, path, accept_len, R: int, Hkv: int, dh: int,
                new_prefix_len=None, ws=None, stream=None):
     """commit_kv on 4-bit caches; returns new_prefix_len = P_b + L + 1."""
-    s = _on_device(path, stream, k_ptrs_i64=k_ptrs, v_ptrs_i64=v_ptrs, prefix_len_i32=prefix_len,
-                   path_i32=path, accept_len_i32=accept_len, new_prefix_len_i32=new_prefix_len, ws=ws)
+    dev, st = _launch_on(path, stream)
     B, K1 = path.shape
-    for t, name in ((k_ptrs, "k_ptrs"), (v_ptrs, "v_ptrs"), (prefix_len, "prefix_len"),
-                    (accept_len, "accept_len"), (new_prefix_len, "new_prefix_len")):
-        _size_is(t, B, name)
     if new_prefix_len is None:
         new_prefix_len = _new(stream, prefix_len)
-    ws = _scratch(ws, WS_HEADER, path.device, stream)
-    _check(lib().medusa_commit_kv4(_ptr(k_ptrs), _ptr(v_ptrs), _ptr(prefix_len), _ptr(path),
-                                   _ptr(accept_len), B, K1 - 1, int(R), int(Hkv), int(dh),
-                                   _ptr(new_prefix_len), _ptr(ws), ws.numel(), s.cuda_stream))
+    if ws is None:
+        ws = _scratch(WS_HEADER, path.device, stream)
+    ws_ptr, ws_n = _ws_args(ws, dev)
+    _check(lib().medusa_commit_kv4(
+        _vec(k_ptrs, B, torch.int64, dev, "k_ptrs"), _vec(v_ptrs, B, torch.int64, dev, "v_ptrs"),
+        _vec(prefix_len, B, _INT, dev, "prefix_len"), _vec(path, B * K1, _INT, dev, "path"),
+        _vec(accept_len, B, _INT, dev, "accept_len"), B, K1 - 1, R, Hkv, dh,
+        _vec(new_prefix_len, B, _INT, dev, "new_prefix_len"), ws_ptr, ws_n, st))
     return new_prefix_len
 
 
@@ -774,27 +780,27 @@ def tree_attention_window_workspace_size(dtype: int, B: int, R: int, H: int, Hkv
 
 def _cache_attention(kv4, q, k_ptrs, v_ptrs, prefix_len, P_max, anc_mask, Hkv, depth, window, sinks,
                      scale, out, ws, stream):
-    _need(q, "q")
-    B, R, H, dh = q.shape
     dt = _dtype(q)
-    Hkv, P_max = int(H if Hkv is None else Hkv), int(P_max)
-    s = _on_device(q, stream, k_ptrs_i64=k_ptrs, v_ptrs_i64=v_ptrs, prefix_len_i32=prefix_len,
-                   anc_mask_i64=anc_mask, depth_i32=depth, ws=ws)
-    for t, name in ((k_ptrs, "k_ptrs"), (v_ptrs, "v_ptrs"), (prefix_len, "prefix_len")):
-        _size_is(t, B, name)
-    _size_is(anc_mask, B * R * ((R + 63) // 64), "anc_mask")
-    _size_is(depth, B * R, "depth")
+    dev, st = _launch_on(q, stream)
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    B, R, H, dh = q.shape
+    if Hkv is None:
+        Hkv = H
     if out is None:
         out = _new(stream, q)
-    _out(out, q, "out")
     if ws is None:
-        ws = _scratch(None, tree_attention_window_workspace_size(dt, B, R, H, Hkv, dh, P_max, window,
-                                                                 sinks, kv4), q.device, stream)
+        ws = _scratch(tree_attention_window_workspace_size(dt, B, R, H, Hkv, dh, P_max, window, sinks,
+                                                           kv4), q.device, stream)
+    ws_ptr, ws_n = _ws_args(ws, dev)
     fn = lib().medusa_tree_attention_kv4 if kv4 else lib().medusa_tree_attention_window
-    _check(fn(dt, _ptr(q), _ptr(k_ptrs), _ptr(v_ptrs), _ptr(prefix_len), P_max, _ptr(anc_mask),
-              _ptr(depth), int(window), int(sinks), B, R, H, Hkv, dh,
-              1.0 / math.sqrt(dh) if scale is None else float(scale), _ptr(out), _ptr(ws), ws.numel(),
-              s.cuda_stream))
+    _check(fn(dt, q.data_ptr(), _vec(k_ptrs, B, torch.int64, dev, "k_ptrs"),
+              _vec(v_ptrs, B, torch.int64, dev, "v_ptrs"),
+              _vec(prefix_len, B, _INT, dev, "prefix_len"), P_max,
+              _vec(anc_mask, B * R * ((R + 63) // 64), torch.int64, dev, "anc_mask"),
+              None if depth is None else _vec(depth, B * R, _INT, dev, "depth"), window, sinks, B, R, H,
+              Hkv, dh, dh ** -0.5 if scale is None else scale,
+              _dense(out, q.shape, q.dtype, dev, "out"), ws_ptr, ws_n, st))
     return out
 
 

@@ -152,13 +152,24 @@ def test_binding_refuses_before_the_library():
     assert m._rows(torch.zeros(2, 3, 8, 64)[:, :, 2:5], "k") == 512
     assert m._rows(torch.zeros(5, 1, 8, 64)[:, :, 2:5], "k") == 512
     assert m._rows(torch.zeros(1, 1, 8, 64)[:, :, 2:5], "k") == 192
-    for bad in (dict(k=torch.zeros(1, 2, 4, 128)), dict(k=q.bfloat16()), dict(pos=torch.zeros(3)),
-                dict(q_weight=torch.zeros(63)), dict(n_rows=torch.zeros(2))):
-        a = dict(k=q, pos=torch.zeros(2), inv_freq=torch.zeros(32), q_weight=None, k_weight=None, norm=True,
-                 n_rows=None)
+    # (a CPU tensor has device index -1: the checks run without a GPU)
+    for bad in (dict(k=torch.zeros(1, 2, 4, 128)), dict(k=q.bfloat16()), dict(k=torch.zeros(1, 3, 4, 64)),
+                dict(q_weight=torch.zeros(63)), dict(k_weight=torch.zeros(64).bfloat16()),
+                dict(q_weight=torch.zeros(128)[::2])):
+        a = dict(k=q, q_weight=None, k_weight=None, dev=-1)
         a.update(bad)
         with pytest.raises(ValueError):
             m._rope_args(q, *a.values())
+    assert m._rope_args(q, q, None, torch.zeros(64), -1)[0] is None
+    i32 = torch.zeros(6, dtype=torch.int32)
+    assert m._vec(i32, 6, torch.int32, -1, "x") == i32.data_ptr()
+    for t, n, dev in ((i32, 5, -1), (i32.long(), 6, -1), (i32, 6, 0), (i32[::2], 3, -1)):
+        with pytest.raises(ValueError):
+            m._vec(t, n, torch.int32, dev, "x")
+    with pytest.raises(ValueError):
+        m._dense(q.transpose(1, 2), (1, 4, 2, 64), torch.float32, -1, "out")
+    with pytest.raises(ValueError):
+        m._launch_on(q, None)
     with pytest.raises(ValueError):
         m.kv4_cache(4, 1, 100)
     with pytest.raises(TypeError):
