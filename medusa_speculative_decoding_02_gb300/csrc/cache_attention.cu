@@ -107,14 +107,7 @@ __device__ __forceinline__ void cache_load8(const void *cache, int slot, int Hkv
     if constexpr (KV4) {
         const uint8_t *row = static_cast<const uint8_t *>(cache) + (size_t)slot * kv4_row_bytes(Hkv, DH);
         const uint32_t w = *reinterpret_cast<const uint32_t *>(row + (g * DH + e0) / 2);
-        const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(
-            row[kv4_code_bytes(Hkv, DH) + (g * DH + e0) / 16], __NV_E4M3)));
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const float2 f = __half22float2(e2m1x2_half2(w >> (8 * u)));
-            x[2 * u] = f.x * s;
-            x[2 * u + 1] = f.y * s;
-        }
+        kv4_widen(w, e4m3_half(row[kv4_code_bytes(Hkv, DH) + (g * DH + e0) / 16]), x);
     } else {
         const T *p = static_cast<const T *>(cache) + ((size_t)slot * Hkv + g) * DH + e0;
         constexpr int N = Vec16<T>::N;
@@ -466,25 +459,6 @@ __device__ __forceinline__ void load_regs_kv4(Kv4Regs<DH> &r, const uint8_t *cac
     }
 }
 
-// the eight codes of a word as four fp16 pairs, times s (exact)
-__device__ __forceinline__ uint4 widen_word(uint32_t w, __half2 s) {
-    uint32_t h[4];
-    asm("{\n.reg .b8 b0, b1, b2, b3;\n"
-        "mov.b32 {b0, b1, b2, b3}, %4;\n"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n"
-        "cvt.rn.f16x2.e2m1x2 %1, b1;\n"
-        "cvt.rn.f16x2.e2m1x2 %2, b2;\n"
-        "cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(w));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&h[i]), s);
-        h[i] = *reinterpret_cast<const uint32_t *>(&v);
-    }
-    return make_uint4(h[0], h[1], h[2], h[3]);
-}
-
 template <int DH>
 __device__ __forceinline__ void store_regs_kv4(const Kv4Regs<DH> &r, unsigned char *tile, int k0,
                                                int kend, int t) {
@@ -507,7 +481,7 @@ __device__ __forceinline__ void store_regs_kv4(const Kv4Regs<DH> &r, unsigned ch
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int ch = (q & 1) * 4 + (i ^ (flip ? 2 : 0));
-            *reinterpret_cast<uint4 *>(blk + tc::sw128(key, ch)) = widen_word(word[i], i < 2 ? sa : sb);
+            *reinterpret_cast<uint4 *>(blk + tc::sw128(key, ch)) = kv4_widen(word[i], i < 2 ? sa : sb);
         }
     }
 }

@@ -1,11 +1,12 @@
 // kv4.cu -- rows into and out of the 4-bit cache (layout: kv4.cuh).
 //
-// kv4_append_kernel: one thread per block of 16 elements of K or V: it reads
-// them, picks the scale and the codes and stores eight bytes of codes and one
-// scale byte.  Consecutive threads take consecutive blocks of a row, so both
-// stores of a warp are contiguous.  kv4_unpack_kernel is the inverse.  Both
-// are bound by the bytes they move (per element 2 or 4 bytes on the wide side
-// and 9/16 on the narrow one).
+// kv4_append_kernel: one thread per block of 16 elements of K or V (kItems
+// blocks a CTA's width apart, their loads issued together): it picks the scale
+// and the codes and stores eight bytes of codes and one scale byte.
+// Consecutive threads take consecutive blocks of a sequence's rows, K's then
+// V's, so both stores of a warp are contiguous.  kv4_unpack_kernel is the
+// inverse.  Both are bound by the bytes they move (per element 2 or 4 bytes on
+// the wide side and 9/16 on the narrow one).
 #include <algorithm>
 
 #include "kv4.cuh"
@@ -16,6 +17,7 @@ namespace medusa {
 namespace {
 
 constexpr int kKv4Threads = 256;
+constexpr int kItems = 2;
 
 struct Kv4Args {
     const void *k, *v;        // wide rows (append: in; unpack: out)
@@ -28,116 +30,131 @@ struct Kv4Args {
     int *status;
 };
 
-// Row checks shared by both directions: the cache row of wide row i of
-// sequence b, or null when there is nothing to do.
-__device__ __forceinline__ uint8_t *kv4_row(const Kv4Args &a, int b, int i, bool is_v) {
-    if (a.n_rows && i >= a.n_rows[b]) return nullptr;
-    uint8_t *kc = a.kc[b], *vc = a.vc[b];
+// One block of a call: the wide elements and the cache row they belong to, or
+// row = null when there is nothing to do (past the end, or the sequence's
+// checks failed).
+template <typename T>
+struct Kv4Block {
+    T *wide;
+    uint8_t *row;
+    int e;  // block within the row
+    __device__ __forceinline__ Kv4Block(const Kv4Args &a, int b, unsigned idx, int live) {
+        const unsigned per = (unsigned)(a.Hkv * a.dh / 16);  // blocks of a K row, and of a V row
+        const unsigned i = idx / (2 * per);
+        unsigned blk = idx - i * (2 * per);
+        const bool is_v = blk >= per;
+        if (is_v) blk -= per;
+        e = (int)blk;
+        row = nullptr;
+        if ((int)i >= live) return;
+        row = (is_v ? a.vc : a.kc)[b] + (size_t)(a.prefix_len[b] + (int)i) * kv4_row_bytes(a.Hkv, a.dh);
+        const long long r = (long long)b * a.R + i;
+        wide = static_cast<T *>(const_cast<void *>(is_v ? a.v : a.k)) +
+               r * (is_v ? a.v_stride : a.k_stride) + blk * 16;
+    }
+};
+
+// Rows of sequence b to handle: 0 when its checks fail.
+__device__ __forceinline__ int kv4_live_rows(const Kv4Args &a, int b) {
+    const uint8_t *kc = a.kc[b], *vc = a.vc[b];
     if (!kc || !vc || ((reinterpret_cast<uintptr_t>(kc) | reinterpret_cast<uintptr_t>(vc)) & 15u)) {
         set_status(a.status, MEDUSA_DEV_BAD_CACHE);
-        return nullptr;
+        return 0;
     }
     const int P = a.prefix_len[b];
     if (P < 0 || P > a.P_max) {
         set_status(a.status, MEDUSA_DEV_BAD_PREFIX);
-        return nullptr;
+        return 0;
     }
-    return (is_v ? vc : kc) + (size_t)(P + i) * kv4_row_bytes(a.Hkv, a.dh);
+    return a.n_rows ? min(a.R, a.n_rows[b]) : a.R;
 }
 
-template <typename T>
-__device__ __forceinline__ void load16(const T *p, float (&x)[16]) {
-    constexpr int N = Vec16<T>::N;
-#pragma unroll
-    for (int u = 0; u < 16 / N; ++u) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(p + u * N);
-        float f[N];
-        Vec16<T>::widen(w, f);
-#pragma unroll
-        for (int e = 0; e < N; ++e) x[u * N + e] = f[e];
-    }
-}
-
-// grid (blocks of a row pair over 256 threads, R, B)
+// grid (blocks of a sequence over kItems * 256, B)
 template <typename T>
 __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(Kv4Args a) {
     pdl_enter();
-    const int per = a.Hkv * a.dh / 16;  // blocks of a K row, and of a V row
-    const int blk = blockIdx.x * kKv4Threads + threadIdx.x;
-    if (blk >= 2 * per) return;
-    const bool is_v = blk >= per;
-    const int e = is_v ? blk - per : blk;
-    const int i = blockIdx.y, b = blockIdx.z;
-    uint8_t *row = kv4_row(a, b, i, is_v);
-    if (!row) return;
-    const long long r = (long long)b * a.R + i;
-    const T *src = is_v ? static_cast<const T *>(a.v) + r * a.v_stride
-                        : static_cast<const T *>(a.k) + r * a.k_stride;
-    float x[16];
-    load16(src + e * 16, x);
-    float amax = 0.f;
-    bool finite = true;
+    constexpr int N = Vec16<T>::N, V = 16 / N;
+    const int b = blockIdx.y;
+    const int live = kv4_live_rows(a, b);
+    const unsigned first = blockIdx.x * (kItems * kKv4Threads) + threadIdx.x;
+    uint4 raw[kItems][V];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        amax = fmaxf(amax, fabsf(x[j]));
-        finite = finite && fabsf(x[j]) < INFINITY;  // false for NaN too
+    for (int u = 0; u < kItems; ++u) {
+        const Kv4Block<T> k(a, b, first + u * kKv4Threads, live);
+        if (k.row)
+#pragma unroll
+            for (int c = 0; c < V; ++c) raw[u][c] = ld_stream16(k.wide + c * N);
     }
-    uint32_t sb = kE4m3Nan, lo = 0, hi = 0;
-    if (finite) {
-        sb = kv4_scale_byte(amax);
-        if (sb) {
-            const float s = e4m3_value(sb);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                lo |= kv4_code(x[j], s) << (4 * j);
-                hi |= kv4_code(x[j + 8], s) << (4 * j);
+    for (int u = 0; u < kItems; ++u) {
+        const Kv4Block<T> k(a, b, first + u * kKv4Threads, live);
+        if (!k.row) return;  // the blocks after it lie further on
+        float x[16];
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+            float f[N];
+            Vec16<T>::widen(raw[u][c], f);
+#pragma unroll
+            for (int j = 0; j < N; ++j) x[c * N + j] = f[j];
+        }
+        // the largest magnitude, by its bits: infinities and NaNs come out on top
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+        uint32_t sb = kE4m3Nan, lo = 0, hi = 0;
+        if (top < 0x7f800000u) {
+            sb = kv4_scale_byte(__uint_as_float(top));
+            if (sb) {
+                const float s = e4m3_value(sb);
+                lo = kv4_codes(x, s, T());
+                hi = kv4_codes(x + 8, s, T());
             }
         }
+        *reinterpret_cast<uint2 *>(k.row + k.e * 8) = make_uint2(lo, hi);
+        k.row[kv4_code_bytes(a.Hkv, a.dh) + k.e] = (uint8_t)sb;
     }
-    *reinterpret_cast<uint2 *>(row + e * 8) = make_uint2(lo, hi);
-    row[kv4_code_bytes(a.Hkv, a.dh) + e] = (uint8_t)sb;
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kKv4Threads) kv4_unpack_kernel(Kv4Args a) {
     pdl_enter();
-    const int per = a.Hkv * a.dh / 16;
-    const int blk = blockIdx.x * kKv4Threads + threadIdx.x;
-    if (blk >= 2 * per) return;
-    const bool is_v = blk >= per;
-    const int e = is_v ? blk - per : blk;
-    const int i = blockIdx.y, b = blockIdx.z;
-    const uint8_t *row = kv4_row(a, b, i, is_v);
-    if (!row) return;
-    const long long r = (long long)b * a.R + i;
-    T *dst = is_v ? static_cast<T *>(const_cast<void *>(a.v)) + r * a.v_stride
-                  : static_cast<T *>(const_cast<void *>(a.k)) + r * a.k_stride;
-    dst += e * 16;
-    const uint2 c = *reinterpret_cast<const uint2 *>(row + e * 8);
-    const __half s =
-        __half(__nv_cvt_fp8_to_halfraw(row[kv4_code_bytes(a.Hkv, a.dh) + e], __NV_E4M3));
-    float x[16];
+    const int b = blockIdx.y;
+    const int live = kv4_live_rows(a, b);
+    const unsigned first = blockIdx.x * (kItems * kKv4Threads) + threadIdx.x;
+    uint2 codes[kItems];
+    uint32_t scale[kItems];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t byte = (j < 4 ? c.x : c.y) >> (8 * (j & 3));
-        const float2 f = __half22float2(__hmul2(e2m1x2_half2(byte), __half2half2(s)));
-        x[2 * j] = f.x;
-        x[2 * j + 1] = f.y;
-    }
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            *reinterpret_cast<float4 *>(dst + 4 * u) =
-                make_float4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
-    } else {
-        uint32_t w[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * u], x[2 * u + 1]);
-            w[u] = *reinterpret_cast<const uint32_t *>(&p);
+    for (int u = 0; u < kItems; ++u) {
+        const Kv4Block<T> k(a, b, first + u * kKv4Threads, live);
+        if (k.row) {
+            codes[u] = *reinterpret_cast<const uint2 *>(k.row + k.e * 8);
+            scale[u] = k.row[kv4_code_bytes(a.Hkv, a.dh) + k.e];
         }
-        *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4 *>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+#pragma unroll
+    for (int u = 0; u < kItems; ++u) {
+        const Kv4Block<T> k(a, b, first + u * kKv4Threads, live);
+        if (!k.row) return;
+        const __half s = e4m3_half(scale[u]);
+        float x[2][8];
+        kv4_widen(codes[u].x, s, x[0]);
+        kv4_widen(codes[u].y, s, x[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            T *dst = k.wide + 8 * h;
+            if constexpr (sizeof(T) == 4) {
+                *reinterpret_cast<float4 *>(dst) = make_float4(x[h][0], x[h][1], x[h][2], x[h][3]);
+                *reinterpret_cast<float4 *>(dst + 4) = make_float4(x[h][4], x[h][5], x[h][6], x[h][7]);
+            } else {
+                uint32_t w[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const __nv_bfloat162 p = __floats2bfloat162_rn(x[h][2 * c], x[h][2 * c + 1]);
+                    w[c] = *reinterpret_cast<const uint32_t *>(&p);
+                }
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
     }
 }
 
@@ -162,10 +179,11 @@ cudaError_t launch_kv4_rows(medusa_dtype dtype, bool append, const void *k, cons
     a.dh = dh;
     a.P_max = P_max;
     a.status = static_cast<int *>(ws);
-    const int gx = (2 * Hkv * dh / 16 + kKv4Threads - 1) / kKv4Threads;
+    const unsigned blocks = (unsigned)R * (unsigned)(2 * Hkv * dh / 16);  // < 2^30
+    const unsigned gx = (blocks + kItems * kKv4Threads - 1) / (kItems * kKv4Threads);
     auto kern = append ? (dtype == MEDUSA_F32 ? kv4_append_kernel<float> : kv4_append_kernel<bf16>)
                        : (dtype == MEDUSA_F32 ? kv4_unpack_kernel<float> : kv4_unpack_kernel<bf16>);
-    cudaError_t e = launch_pdl(kern, dim3(gx, R, B), dim3(kKv4Threads), 0, stream, a);
+    cudaError_t e = launch_pdl(kern, dim3(gx, B), dim3(kKv4Threads), 0, stream, a);
     note_launch();
     return e;
 }

@@ -34,11 +34,39 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
     return __half2float(__half(h));
 }
 
-// two e2m1 codes (one byte) -> two halves (exact)
-__device__ __forceinline__ __half2 e2m1x2_half2(uint32_t byte) {
-    const __half2_raw h =
-        __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(byte & 0xffu), __NV_E2M1);
-    return __half2(h);
+// the eight codes of a word as four fp16 pairs, times s (exact)
+__device__ __forceinline__ uint4 kv4_widen(uint32_t w, __half2 s) {
+    uint32_t h[4];
+    asm("{\n.reg .b8 b0, b1, b2, b3;\n"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&h[i]), s);
+        h[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+// the eight values of a word in fp32
+__device__ __forceinline__ void kv4_widen(uint32_t w, __half s, float (&x)[8]) {
+    const uint4 v = kv4_widen(w, __half2half2(s));
+    const uint32_t h[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+
+__device__ __forceinline__ __half e4m3_half(uint32_t byte) {
+    return __half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3));
 }
 
 // Scale byte of a block whose largest magnitude is `amax` (finite): the e4m3
@@ -67,6 +95,37 @@ __device__ __forceinline__ uint32_t kv4_code(float x, float s) {
     uint32_t c = (a > 0.25f * s) + (a >= 0.75f * s) + (a > 1.25f * s) + (a >= 1.75f * s) +
                  (a > 2.5f * s) + (a >= 3.5f * s) + (a > 5.f * s);
     return c | (x < 0.f ? 8u : 0u);
+}
+
+// The codes of eight elements.  For bf16 elements the hardware's conversion of
+// y = x * (1/s) serves: a bf16 x (eight bits) is either exactly a midpoint
+// times s (seven bits at most) or off it by a relative 2^-8, and y, off by
+// 2^-23, is rounded to 16 bits first, which puts the exact ties back on the
+// midpoints and moves nothing across one.  fp32 elements can lie closer to a
+// midpoint than that, so they are compared (14 instructions each against 4).
+__device__ __forceinline__ uint32_t kv4_codes(const float *x, float s, float) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w |= kv4_code(x[j], s) << (4 * j);
+    return w;
+}
+__device__ __forceinline__ uint32_t kv4_codes(const float *x, float s, bf16) {
+    const float inv = 1.f / s;
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        // (the + 0 makes a -0 a +0)
+        y[j] = __uint_as_float((__float_as_uint(fmaf(x[j], inv, 0.f)) + 0x80u) & 0xffffff00u);
+    uint32_t w;
+    asm("{\n.reg .b8 b0, b1, b2, b3;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
+        "mov.b32 %0, {b0, b1, b2, b3};\n}\n"
+        : "=r"(w)
+        : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+    return w;
 }
 
 }  // namespace medusa

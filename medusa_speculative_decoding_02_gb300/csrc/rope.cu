@@ -50,13 +50,12 @@ struct RopeArgs {
 };
 
 template <typename T>
-__device__ __forceinline__ void load8(const T *p, float (&x)[8]) {
+__device__ __forceinline__ void widen8(const uint4 (&w)[8 / Vec16<T>::N], float (&x)[8]) {
     constexpr int N = Vec16<T>::N;
 #pragma unroll
     for (int u = 0; u < 8 / N; ++u) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(p + u * N);
         float f[N];
-        Vec16<T>::widen(w, f);
+        Vec16<T>::widen(w[u], f);
 #pragma unroll
         for (int e = 0; e < N; ++e) x[u * N + e] = f[e];
     }
@@ -106,7 +105,8 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(RopeArgs a) 
     }
     const int nv = a.H + a.Hkv + (a.kc ? a.Hkv : 0);
     const int v0 = blockIdx.y * (VPP * NP) + tid / LPV;
-    float x[NP][8];
+    constexpr int W = 8 / Vec16<T>::N;           // 16-byte words of a lane's elements
+    uint4 raw[NP][W];
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
         const int v = v0 + n * VPP;
@@ -114,12 +114,9 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(RopeArgs a) 
                        : v < a.H + a.Hkv ? static_cast<const T *>(a.k) + row * a.k_stride + (v - a.H) * DH
                        : v < nv ? static_cast<const T *>(a.v) + row * a.v_stride + (v - a.H - a.Hkv) * DH
                                 : nullptr;
-        if (src) {
-            load8(src + e0, x[n]);
-        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[n][e] = 0.f;
-        }
+        for (int c = 0; c < W; ++c)
+            raw[n][c] = src ? ld_stream16(src + e0 + c * Vec16<T>::N) : make_uint4(0, 0, 0, 0);
     }
     const int half = a.rot / 2;
     if (tid < half) {
@@ -145,34 +142,42 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(RopeArgs a) 
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
         const int v = v0 + n * VPP;
+        float x[8];
+        widen8<T>(raw[n], x);
         if (a.norm) {  // uniform: the shuffles below run in every lane
             float ss = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(x[n][e], x[n][e], ss);
+            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
             for (int o = LPV / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
             const T *w = static_cast<const T *>(v < a.H ? a.qw : a.kw);
             if (v < a.H + a.Hkv) {
                 const float inv = 1.f / sqrtf(ss / DH + a.eps);
                 float wf[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-                if (w) load8(w + e0, wf);
+                if (w) {
+                    uint4 ww[W];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[n][e] = x[n][e] * inv * wf[e];
+                    for (int c = 0; c < W; ++c)
+                        ww[c] = *reinterpret_cast<const uint4 *>(w + e0 + c * Vec16<T>::N);
+                    widen8<T>(ww, wf);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * wf[e];
             }
         }
         float y[8];
         if (a.interleaved) {
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
-                y[e] = turned ? x[n][e] * t[e].x - x[n][e + 1] * t[e].y : x[n][e];
-                y[e + 1] = turned ? x[n][e] * t[e].y + x[n][e + 1] * t[e].x : x[n][e + 1];
+                y[e] = turned ? x[e] * t[e].x - x[e + 1] * t[e].y : x[e];
+                y[e + 1] = turned ? x[e] * t[e].y + x[e + 1] * t[e].x : x[e + 1];
             }
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float o = __shfl_sync(0xffffffffu, x[n][e], partner);
+                const float o = __shfl_sync(0xffffffffu, x[e], partner);
                 // lower half: a cos - b sin; upper half: b cos + a sin
-                y[e] = turned ? x[n][e] * t[e].x + (e0 < half ? -o : o) * t[e].y : x[n][e];
+                y[e] = turned ? x[e] * t[e].x + (e0 < half ? -o : o) * t[e].y : x[e];
             }
         }
         if (v < a.H)
@@ -180,7 +185,7 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(RopeArgs a) 
         else if (v < a.H + a.Hkv)
             store8(krow + (v - a.H) * DH + e0, y);
         else if (v < nv)
-            store8(vrow + (v - a.H - a.Hkv) * DH + e0, x[n]);
+            store8(vrow + (v - a.H - a.Hkv) * DH + e0, x);
     }
 }
 
@@ -223,12 +228,20 @@ cudaError_t launch_qk_norm_rope(medusa_dtype dtype, const void *q, const void *k
     const int nv = H + Hkv + (k_cache ? Hkv : 0);
     const long long rows = (long long)B * R;
     const int vpp = kRopeThreads / (dh / 8);
-    // one pass per CTA
-    auto kern = dtype == MEDUSA_F32
-                    ? (dh == 128 ? qk_norm_rope_kernel<float, 128, 1> : qk_norm_rope_kernel<float, 64, 1>)
-                    : (dh == 128 ? qk_norm_rope_kernel<bf16, 128, 1> : qk_norm_rope_kernel<bf16, 64, 1>);
-    cudaError_t e = launch_pdl(kern, dim3((unsigned)rows, (nv + vpp - 1) / vpp), dim3(kRopeThreads),
-                               0, stream, a);
+    // With few rows one pass per CTA puts more CTAs to work; with enough of them
+    // four passes share a row's angles and keep four loads a lane in flight.
+    const int passes = (nv + vpp - 1) / vpp;
+    const bool many = rows * passes >= 16LL * device_sm_count();
+    auto pick = [&](auto one, auto four) { return many ? four : one; };
+    auto kern =
+        dtype == MEDUSA_F32
+            ? (dh == 128 ? pick(qk_norm_rope_kernel<float, 128, 1>, qk_norm_rope_kernel<float, 128, 4>)
+                         : pick(qk_norm_rope_kernel<float, 64, 1>, qk_norm_rope_kernel<float, 64, 4>))
+            : (dh == 128 ? pick(qk_norm_rope_kernel<bf16, 128, 1>, qk_norm_rope_kernel<bf16, 128, 4>)
+                         : pick(qk_norm_rope_kernel<bf16, 64, 1>, qk_norm_rope_kernel<bf16, 64, 4>));
+    const int per_cta = many ? 4 : 1;
+    cudaError_t e = launch_pdl(kern, dim3((unsigned)rows, (passes + per_cta - 1) / per_cta),
+                               dim3(kRopeThreads), 0, stream, a);
     note_launch();
     return e;
 }
