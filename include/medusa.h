@@ -599,7 +599,7 @@ MEDUSA_API void medusa_step_destroy(medusa_step_exec *exec);
  *     (y_a, y_b) -> (y_a cos t - y_b sin t, y_a sin t + y_b cos t),
  *     t = p * inv_freq[j],  j = 0 .. rot/2 - 1
  * for the pairs (a, b) = (j, j + rot/2), or (2j, 2j+1) if interleaved;
- * elements from rot on are not rotated.  Angles are exact to about 2^-23 of a
+ * elements from rot on are not rotated.  Angles are exact to about 2^-25 of a
  * turn at every position.
  *
  *   q [B,R,H,dh], k [B,R,Hkv,dh] dtype; consecutive rows lie q_stride and

@@ -602,8 +602,9 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
                 }
             }
         } else {
-            // LAG younger copies stay in flight when a tile is announced
-            constexpr int LAG = L::NT - 1;
+            // half the ring of younger copies stays in flight when a tile is announced:
+            // with all of it, each tile waited for the slot of the one NT before it
+            constexpr int LAG = L::NT / 2;
             const bf16 *k16 = static_cast<const bf16 *>(kc), *v16 = static_cast<const bf16 *>(vc);
             bool go = true;
             for (int i = 0; i < n_tiles + LAG && go; ++i) {

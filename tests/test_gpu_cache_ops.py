@@ -392,6 +392,18 @@ def test_attention_every_length_around_a_tile(dev, dtype, kv4):
 
 
 @pytest.mark.parametrize("kv4", [False, True])
+@pytest.mark.parametrize("B", [2, 31, 32, 33, 70])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 7)])
+def test_attention_many_ragged(dev, kv4, B, window, sinks):
+    """Batches split by their real lengths (up to 32) and evenly (more): a few long
+    sequences among short ones and one without a prefix."""
+    prefix = [(37 * b * b) % 190 for b in range(B)]
+    prefix[0], prefix[-1], prefix[B // 2] = 2500, 1700, 0
+    a = attn_inputs(B, 3, 2, 2, 64, prefix, BF, kv4, dev, seed=B)
+    check_attn(call_attn(a, window, sinks, 2, kv4, dev), a, window, sinks, kv4=kv4)
+
+
+@pytest.mark.parametrize("kv4", [False, True])
 def test_attention_long(dev, kv4):
     """Long contexts in many key ranges, peaked and flat scores, a scale of its own."""
     for std, scale in ((0.1, None), (8.0, None), (1.0, 1.0)):
