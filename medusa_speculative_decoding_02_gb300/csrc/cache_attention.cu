@@ -21,87 +21,23 @@
 // row r * G + g being tree row r and query head hk * G + g.
 #include <algorithm>
 
-#include "kv4.cuh"
-#include "launch.h"
+#include "cache_attention.cuh"
 #include "tcgen05.cuh"
 
 namespace medusa {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-
-struct CacheAttnArgs {
-    const void *q;
-    const void *const *kc;
-    const void *const *vc;
-    const int32_t *prefix_len;
-    const uint64_t *anc_mask;
-    const int32_t *depth;  // null without a window
-    int B, R, H, Hkv, P_max;
-    int window, sinks;
-    int chunk, ns, row_tiles;
-    float scale_log2;
-    uint32_t wait_polls;   // poll limit of the tensor-core path's waits
-    float *part_o;         // [B, H, ns, R, dh]
-    float2 *part_ml;       // [B, H, ns, R] (m in log2 units, l)
-    void *out;
-    int *status;
-};
-
-// A sequence's visible slots, numbered without a gap.
-struct KeyRun {
-    int n_sink, lo, len;
-    __device__ __forceinline__ KeyRun(int P, int R, int window, int sinks) {
-        lo = window ? max(0, P - window + 1) : 0;
-        n_sink = min(sinks, lo);
-        len = n_sink + (P + R - lo);
-    }
-    __device__ __forceinline__ int slot(int x) const { return x < n_sink ? x : x - n_sink + lo; }
-};
-
-// depth of tree row t, clamped into 0..R-1 (out of range: BAD_DEPTH)
-__device__ __forceinline__ int row_depth(const CacheAttnArgs &a, int b, int t) {
-    if (!a.depth) return 0;
-    const int d = a.depth[(size_t)b * a.R + t];
-    if (d < 0 || d >= a.R) {
-        set_status(a.status, MEDUSA_DEV_BAD_DEPTH);
-        return d < 0 ? 0 : a.R - 1;
-    }
-    return d;
-}
-
-// Sequence b's prefix and caches, checked; false (and the status set) when
-// the sequence cannot run.
-__device__ __forceinline__ bool sequence_ok(const CacheAttnArgs &a, int b, int &P, const void *&kc,
-                                            const void *&vc) {
-    P = a.prefix_len[b];
-    kc = a.kc[b];
-    vc = a.vc[b];
-    if (!kc || !vc || ((reinterpret_cast<uintptr_t>(kc) | reinterpret_cast<uintptr_t>(vc)) & 15u)) {
-        set_status(a.status, MEDUSA_DEV_BAD_CACHE);
-        return false;
-    }
-    if (P < 0 || P > a.P_max) {
-        set_status(a.status, MEDUSA_DEV_BAD_PREFIX);
-        return false;
-    }
-    return true;
-}
-
-__device__ __forceinline__ void store_out(float *p, float v) { *p = v; }
-__device__ __forceinline__ void store_out(bf16 *p, float v) { *p = __float2bfloat16_rn(v); }
-
 // ------------------------------------------------------------- CUDA cores ---
 //
-// 128 threads, 16 rows, 32 keys at a time: K and V of the tile are widened to
+// fp32.  128 threads, 16 rows, 32 keys at a time: K and V of the tile are widened to
 // fp32 in shared memory, thread (row tid/8, u = tid%8) scores keys u, u+8,
 // u+16, u+24 and owns output columns 4u + 32c .. +3.  The running maximum and sum of a row live
 // in its eight threads.
 constexpr int kRows = 16, kKeys = 32, kSimtThreads = 128;
 
 // eight elements of head g of cache row `slot` from element e0 on
-template <typename T, bool KV4, int DH>
+template <bool KV4, int DH>
 __device__ __forceinline__ void cache_load8(const void *cache, int slot, int Hkv, int g, int e0,
                                             float (&x)[8]) {
     if constexpr (KV4) {
@@ -109,42 +45,41 @@ __device__ __forceinline__ void cache_load8(const void *cache, int slot, int Hkv
         const uint32_t w = *reinterpret_cast<const uint32_t *>(row + (g * DH + e0) / 2);
         kv4_widen(w, e4m3_half(row[kv4_code_bytes(Hkv, DH) + (g * DH + e0) / 16]), x);
     } else {
-        const T *p = static_cast<const T *>(cache) + ((size_t)slot * Hkv + g) * DH + e0;
-        constexpr int N = Vec16<T>::N;
+        const float *p = static_cast<const float *>(cache) + ((size_t)slot * Hkv + g) * DH + e0;
+        constexpr int N = Vec16<float>::N;
 #pragma unroll
         for (int u = 0; u < 8 / N; ++u) {
             float f[N];
-            Vec16<T>::widen(*reinterpret_cast<const uint4 *>(p + u * N), f);
+            Vec16<float>::widen(*reinterpret_cast<const uint4 *>(p + u * N), f);
 #pragma unroll
             for (int e = 0; e < N; ++e) x[u * N + e] = f[e];
         }
     }
 }
 
-template <typename T, bool KV4, int DH>
+template <bool KV4, int DH>
 __global__ void __launch_bounds__(kSimtThreads) cache_attn_simt_kernel(CacheAttnArgs a) {
     pdl_enter();
     constexpr int LD = DH + 4;
     __shared__ float qs[kRows][LD], ks[kKeys][LD], vs[kKeys][LD];
     __shared__ float ps[kRows][kKeys];
     const int g = blockIdx.x / a.row_tiles, rt = blockIdx.x - g * a.row_tiles;  // KV head, tile
-    const int split = blockIdx.y, b = blockIdx.z;
     const int R = a.R, G = a.H / a.Hkv, M = R * G;
     const int tid = threadIdx.x, lr = tid >> 3, u = tid & 7;
     const int m = rt * kRows + lr;  // row of the KV head
     const bool live = m < M;
     const int r = live ? m / G : 0, h = g * G + (live ? m - r * G : 0);
-    const size_t prow = (((size_t)b * a.H + h) * a.ns + split) * R + r;
-    T *dst = static_cast<T *>(a.out) + (((size_t)b * R + r) * a.H + h) * DH;
-    int P;
-    const void *kc, *vc;
-    const bool ok = sequence_ok(a, b, P, kc, vc);
-    const KeyRun run(ok ? P : 0, R, a.window, a.sinks);
-    const int kbeg = split * a.chunk, kend = ok ? min(kbeg + a.chunk, run.len) : 0;
+    CacheItem it;
+    find_item<false, kKeys>(a, [&](int P) { return KeyRun(P, R, a.window, a.sinks).len; }, it);
+    const int b = it.b, P = it.P, kbeg = it.kbeg, kend = it.kend;
+    const void *kc = it.kc, *vc = it.vc;
+    const KeyRun run(P, R, a.window, a.sinks);
+    const size_t prow = ((size_t)it.range * a.H + h) * R + r;
+    float *dst = static_cast<float *>(a.out) + (((size_t)b * R + r) * a.H + h) * DH;
     if (kbeg >= kend) {  // uniform over the CTA
         if (!live) return;
         if (a.ns == 1)
-            for (int c = u; c < DH; c += 8) store_out(dst + c, 0.f);
+            for (int c = u; c < DH; c += 8) dst[c] = 0.f;
         else if (u == 0)
             a.part_ml[prow] = make_float2(-INFINITY, 0.f);
         return;
@@ -156,7 +91,7 @@ __global__ void __launch_bounds__(kSimtThreads) cache_attn_simt_kernel(CacheAttn
         float x = 0.f;
         if (mm < M) {
             const int rr = mm / G, hh = g * G + mm - rr * G;
-            x = Vec16<T>::load1(static_cast<const T *>(a.q) + (((size_t)b * R + rr) * a.H + hh) * DH + c);
+            x = Vec16<float>::load1(static_cast<const float *>(a.q) + (((size_t)b * R + rr) * a.H + hh) * DH + c);
         }
         qs[row][c] = x;
     }
@@ -171,8 +106,8 @@ __global__ void __launch_bounds__(kSimtThreads) cache_attn_simt_kernel(CacheAttn
             float x[8] = {}, y[8] = {};
             if (k0 + kk < kend) {
                 const int slot = run.slot(k0 + kk);
-                cache_load8<T, KV4, DH>(kc, slot, a.Hkv, g, e0, x);
-                cache_load8<T, KV4, DH>(vc, slot, a.Hkv, g, e0, y);
+                cache_load8<KV4, DH>(kc, slot, a.Hkv, g, e0, x);
+                cache_load8<KV4, DH>(vc, slot, a.Hkv, g, e0, y);
             }
 #pragma unroll
             for (int c = 0; c < 8; c += 4) {
@@ -250,7 +185,7 @@ __global__ void __launch_bounds__(kSimtThreads) cache_attn_simt_kernel(CacheAttn
     if (a.ns == 1) {
         const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
 #pragma unroll
-        for (int c = 0; c < DH / 8; ++c) store_out(dst + (c / 4) * 32 + u * 4 + c % 4, acc[c] * inv);
+        for (int c = 0; c < DH / 8; ++c) dst[(c / 4) * 32 + u * 4 + c % 4] = acc[c] * inv;
     } else {
         float *po = a.part_o + prow * DH;
 #pragma unroll
@@ -296,8 +231,6 @@ __global__ void __launch_bounds__(kSimtThreads) cache_attn_simt_kernel(CacheAttn
 // product.  Every wait is bounded; on a timeout the CTA sets the status, waits
 // (bounded) for its products, frees its tensor memory and publishes nothing.
 constexpr int kSub = 64, kTcThreads = 288;
-constexpr float kRescaleLog2 = 8.f;
-constexpr float kF16Bias = 7.f;
 constexpr uint32_t kDrainPolls = 1u << 16;
 constexpr int kAhead = 4;  // 4-bit tiles held in a loader's registers
 
@@ -360,35 +293,6 @@ __device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, uin
 // the lowest n bits (n may be negative or past 64)
 __device__ __forceinline__ uint64_t bits_below(int n) {
     return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
-}
-
-// 16-bit pairs with at least one infinity or NaN (all exponent bits set)
-template <bool KV4>
-__device__ __forceinline__ bool pair_bad(uint32_t w) {
-    constexpr uint32_t E = KV4 ? 0x7c00u : 0x7f80u;
-    return (w & E) == E || ((w >> 16) & E) == E;
-}
-template <bool KV4>
-__device__ __forceinline__ float half_of_pair(uint32_t w, int hi) {
-    const uint16_t v = (uint16_t)(hi ? w >> 16 : w);
-    if constexpr (KV4) {
-        __half_raw r;
-        r.x = v;
-        return __half2float(__half(r));
-    } else {
-        return bf16_to_f(v);
-    }
-}
-
-template <bool KV4>
-__device__ __forceinline__ uint32_t pack_weights(float a, float b) {
-    if constexpr (KV4) {
-        const __half2 h = __floats2half2_rn(a, b);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    }
 }
 
 // ---- loader, bf16 cache: 128 threads; thread t copies 16-byte column t % CPR
@@ -486,7 +390,7 @@ __device__ __forceinline__ void store_regs_kv4(const Kv4Regs<DH> &r, unsigned ch
     }
 }
 
-template <int DH, bool KV4>
+template <int DH, bool KV4, bool DEAL>
 __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnArgs a) {
     pdl_enter();
     using L = CacheSmem<DH, KV4>;
@@ -504,20 +408,19 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
     uint32_t *bad_keys = reinterpret_cast<uint32_t *>(sm + L::WORDS + 32);  // [2]
 
     const int g = blockIdx.x / a.row_tiles, rt = blockIdx.x - g * a.row_tiles;
-    const int split = blockIdx.y, b = blockIdx.z;
     const int R = a.R, G = a.H / a.Hkv, M = R * G;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    int P;
-    const void *kc, *vc;
-    const bool ok = sequence_ok(a, b, P, kc, vc);
-    const KeyRun run(ok ? P : 0, R, a.window, a.sinks);
-    const int kbeg = split * a.chunk, kend = ok ? min(kbeg + a.chunk, run.len) : 0;
+    CacheItem it;
+    if (!find_item<DEAL>(a, [&](int P) { return KeyRun(P, R, a.window, a.sinks).len; }, it)) return;
+    const int b = it.b, P = it.P, kbeg = it.kbeg, kend = it.kend;
+    const void *kc = it.kc, *vc = it.vc;
+    const KeyRun run(P, R, a.window, a.sinks);
 
     // row of a softmax thread
     const int m = rt * 128 + tid;
     const bool live = tid < 128 && m < M;
     const int r = live ? m / G : 0, h = g * G + (live ? m - r * G : 0);
-    const size_t prow = (((size_t)b * a.H + h) * a.ns + split) * R + r;
+    const size_t prow = ((size_t)it.range * a.H + h) * R + r;
     bf16 *dst = static_cast<bf16 *>(a.out) + (((size_t)b * R + r) * a.H + h) * DH;
     auto publish_nothing = [&] {
         if (!live) return;
@@ -984,7 +887,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
 template <typename T, int DH>
 __global__ void __launch_bounds__(256)
 cache_attn_combine_kernel(const float *__restrict__ part_o, const float2 *__restrict__ part_ml,
-                          int B, int R, int H, int NS, T *__restrict__ out) {
+                          const int *__restrict__ starts, int B, int R, int H, int ns,
+                          T *__restrict__ out) {
     pdl_enter();
     constexpr int PER = DH / 32, AHEAD = 8;
     const int lane = threadIdx.x & 31;
@@ -992,9 +896,11 @@ cache_attn_combine_kernel(const float *__restrict__ part_o, const float2 *__rest
     if (item >= (long long)B * H * R) return;
     const int r = (int)(item % R);
     const long long bh = item / R;
-    const float2 *ml = part_ml + bh * NS * R + r;
-    const float *po = part_o + (bh * NS * R + r) * DH + lane * PER;
-    const size_t step = (size_t)R * DH;
+    const int b = (int)(bh / H), first_range = starts ? starts[b] : b * ns;
+    const int NS = starts ? starts[b + 1] - first_range : ns;
+    const size_t ml_step = (size_t)H * R, step = ml_step * DH;
+    const float2 *ml = part_ml + first_range * ml_step + (bh % H) * R + r;
+    const float *po = part_o + (first_range * ml_step + (bh % H) * R + r) * DH + lane * PER;
     float2 row[AHEAD][PER / 2];
     auto load = [&](int s0) {
 #pragma unroll
@@ -1011,11 +917,11 @@ cache_attn_combine_kernel(const float *__restrict__ part_o, const float2 *__rest
             }
     };
     const float2 empty = make_float2(-INFINITY, 0.f);
-    const float2 first = lane < NS ? ml[(size_t)lane * R] : empty;
+    const float2 first = lane < NS ? ml[lane * ml_step] : empty;
     load(0);
     float M = first.y != 0.f ? first.x : -INFINITY;
     for (int s = lane + 32; s < NS; s += 32) {
-        const float2 x = ml[(size_t)s * R];
+        const float2 x = ml[s * ml_step];
         if (x.y != 0.f) M = fmaxf(M, x.x);
     }
 #pragma unroll
@@ -1028,7 +934,7 @@ cache_attn_combine_kernel(const float *__restrict__ part_o, const float2 *__rest
     for (int s0 = 0; s0 < NS; s0 += AHEAD) {
         if (s0 > 0) load(s0);
         if ((s0 & 31) == 0) {
-            const float2 x = s0 == 0 ? first : s0 + lane < NS ? ml[(size_t)(s0 + lane) * R] : empty;
+            const float2 x = s0 == 0 ? first : s0 + lane < NS ? ml[(s0 + lane) * ml_step] : empty;
             w_l = x.y != 0.f ? exp2f(x.x - mu) : 0.f;
             if (x.y != 0.f) L = fmaf(w_l, x.y, L);
         }
@@ -1063,12 +969,14 @@ cache_attn_combine_kernel(const float *__restrict__ part_o, const float2 *__rest
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct CachePlan {
-    int row_tiles, ns, chunk, window, sinks;
+    int row_tiles, ns, window, sinks;
+    bool few;   // at most kFewRows rows a KV head
+    bool deal;  // ranges dealt out by the sequences' lengths
 };
 
 // Key ranges: the count that makes (waves of CTAs) x (stages per CTA + the
 // fixed cost of a CTA, in stages) smallest, joining included.
-CachePlan cache_plan(medusa_dtype dtype, int B, int R, int H, int Hkv, int P_max, int window,
+CachePlan cache_plan(medusa_dtype dtype, bool kv4, int B, int R, int H, int Hkv, int P_max, int window,
                      int sinks) {
     CachePlan p;
     // a window no row's oldest key falls out of is none
@@ -1078,14 +986,15 @@ CachePlan cache_plan(medusa_dtype dtype, int B, int R, int H, int Hkv, int P_max
         p.window ? std::min(P_max, p.sinks + p.window - 1) + R : P_max + R;  // longest KeyRun
     const int M = R * (H / Hkv);
     const bool simt = dtype == MEDUSA_F32;
-    const int rows = simt ? kRows : 128, sub = simt ? kKeys : kSub;
-    const int slots = (simt ? 4 : 2) * device_sm_count();
+    p.few = !simt && M <= kFewRows;
+    const int rows = simt ? kRows : 128;
+    const int sub = simt ? kKeys : kRangeUnit;
+    const int slots = (simt ? 4 : p.few ? cache_few_ctas_per_sm(kv4, M) : 2) * device_sm_count();
     p.row_tiles = (M + rows - 1) / rows;
-    const int subs = (keys + sub - 1) / sub;
+    const int subs = (keys + (p.few && p.sinks ? 15 : 0) + sub - 1) / sub;  // (few: a gap after the sinks)
     const long long ctas = (long long)B * Hkv * p.row_tiles;
     double best = 0;
     p.ns = 1;
-    int per_best = subs;
     for (int ns = 1; ns <= std::min(subs, 512); ++ns) {
         const int per = (subs + ns - 1) / ns;
         if ((subs + per - 1) / per != ns) continue;  // the same split as a smaller ns
@@ -1094,21 +1003,23 @@ CachePlan cache_plan(medusa_dtype dtype, int B, int R, int H, int Hkv, int P_max
         if (ns == 1 || cost < best) {
             best = cost;
             p.ns = ns;
-            per_best = per;
         }
     }
-    p.chunk = per_best * sub;
+    // Lengths differ (behind a window they are about alike): the deal.  It costs
+    // 2 us at the start and in the join (a 65-row step over 1024 slots 15 -> 17).
+    p.deal = !simt && p.ns > 1 && B > 1 && B <= 32 && !p.window;
     return p;
 }
 
 }  // namespace
 
-size_t cache_attention_workspace_bytes(medusa_dtype dtype, bool, int B, int R, int H, int Hkv, int dh,
+size_t cache_attention_workspace_bytes(medusa_dtype dtype, bool kv4, int B, int R, int H, int Hkv, int dh,
                                        int P_max, int window, int sinks) {
-    const CachePlan p = cache_plan(dtype, B, R, H, Hkv, P_max, window, sinks);
+    const CachePlan p = cache_plan(dtype, kv4, B, R, H, Hkv, P_max, window, sinks);
     if (p.ns == 1) return MEDUSA_WS_HEADER;
     const size_t rows = (size_t)B * H * p.ns * R;
-    return MEDUSA_WS_HEADER + align256(rows * dh * sizeof(float)) + align256(rows * sizeof(float2));
+    return MEDUSA_WS_HEADER + align256(rows * dh * sizeof(float)) + align256(rows * sizeof(float2)) +
+           (p.deal ? align256((B + 1) * sizeof(int)) : 0);
 }
 
 cudaError_t launch_cache_attention(medusa_dtype dtype, bool kv4, const void *q,
@@ -1117,7 +1028,7 @@ cudaError_t launch_cache_attention(medusa_dtype dtype, bool kv4, const void *q,
                                    const int32_t *depth, int window, int sinks, int B, int R, int H,
                                    int Hkv, int dh, float scale, void *out, void *ws,
                                    cudaStream_t stream) {
-    const CachePlan p = cache_plan(dtype, B, R, H, Hkv, P_max, window, sinks);
+    const CachePlan p = cache_plan(dtype, kv4, B, R, H, Hkv, P_max, window, sinks);
     CacheAttnArgs a;
     a.q = q;
     a.kc = k_cache;
@@ -1132,7 +1043,6 @@ cudaError_t launch_cache_attention(medusa_dtype dtype, bool kv4, const void *q,
     a.P_max = P_max;
     a.window = p.window;
     a.sinks = p.sinks;
-    a.chunk = p.chunk;
     a.ns = p.ns;
     a.row_tiles = p.row_tiles;
     a.scale_log2 = scale * kLog2e;
@@ -1140,6 +1050,9 @@ cudaError_t launch_cache_attention(medusa_dtype dtype, bool kv4, const void *q,
     char *w = static_cast<char *>(ws) + MEDUSA_WS_HEADER;
     a.part_o = reinterpret_cast<float *>(w);
     a.part_ml = reinterpret_cast<float2 *>(w + align256(rows * dh * sizeof(float)));
+    a.starts = p.deal ? reinterpret_cast<int *>(reinterpret_cast<char *>(a.part_ml) +
+                                                     align256(rows * sizeof(float2)))
+                           : nullptr;
     a.out = out;
     a.status = static_cast<int *>(ws);
     a.wait_polls = wait_budget();
@@ -1147,14 +1060,18 @@ cudaError_t launch_cache_attention(medusa_dtype dtype, bool kv4, const void *q,
     const dim3 grid(Hkv * p.row_tiles, p.ns, B);
     cudaError_t e;
     if (f32) {
-        auto kern = kv4 ? (dh == 128 ? cache_attn_simt_kernel<float, true, 128>
-                                     : cache_attn_simt_kernel<float, true, 64>)
-                        : (dh == 128 ? cache_attn_simt_kernel<float, false, 128>
-                                     : cache_attn_simt_kernel<float, false, 64>);
+        auto kern = kv4 ? (dh == 128 ? cache_attn_simt_kernel<true, 128> : cache_attn_simt_kernel<true, 64>)
+                        : (dh == 128 ? cache_attn_simt_kernel<false, 128> : cache_attn_simt_kernel<false, 64>);
         e = launch_pdl(kern, grid, dim3(kSimtThreads), 0, stream, a);
+    } else if (p.few) {
+        e = launch_cache_attention_few(a, kv4, dh, stream);
     } else {
-        auto kern = kv4 ? (dh == 128 ? cache_attn_tc_kernel<128, true> : cache_attn_tc_kernel<64, true>)
-                        : (dh == 128 ? cache_attn_tc_kernel<128, false> : cache_attn_tc_kernel<64, false>);
+        auto pick = [&](auto own, auto deal) { return p.deal ? deal : own; };
+        auto kern =
+            kv4 ? (dh == 128 ? pick(cache_attn_tc_kernel<128, true, false>, cache_attn_tc_kernel<128, true, true>)
+                             : pick(cache_attn_tc_kernel<64, true, false>, cache_attn_tc_kernel<64, true, true>))
+                : (dh == 128 ? pick(cache_attn_tc_kernel<128, false, false>, cache_attn_tc_kernel<128, false, true>)
+                             : pick(cache_attn_tc_kernel<64, false, false>, cache_attn_tc_kernel<64, false, true>));
         const int smem = kv4 ? (dh == 128 ? CacheSmem<128, true>::TOTAL : CacheSmem<64, true>::TOTAL)
                              : (dh == 128 ? CacheSmem<128, false>::TOTAL : CacheSmem<64, false>::TOTAL);
         if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
@@ -1168,10 +1085,12 @@ cudaError_t launch_cache_attention(medusa_dtype dtype, bool kv4, const void *q,
     const float2 *pm = a.part_ml;
     if (f32)
         e = launch_pdl(dh == 128 ? cache_attn_combine_kernel<float, 128> : cache_attn_combine_kernel<float, 64>,
-                       dim3(blocks), dim3(256), 0, stream, po, pm, B, R, H, p.ns, static_cast<float *>(out));
+                       dim3(blocks), dim3(256), 0, stream, po, pm, (const int *)a.starts, B, R, H, p.ns,
+                       static_cast<float *>(out));
     else
         e = launch_pdl(dh == 128 ? cache_attn_combine_kernel<bf16, 128> : cache_attn_combine_kernel<bf16, 64>,
-                       dim3(blocks), dim3(256), 0, stream, po, pm, B, R, H, p.ns, static_cast<bf16 *>(out));
+                       dim3(blocks), dim3(256), 0, stream, po, pm, (const int *)a.starts, B, R, H, p.ns,
+                       static_cast<bf16 *>(out));
     note_launch();
     return e;
 }
