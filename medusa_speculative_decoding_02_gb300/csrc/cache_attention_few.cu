@@ -77,7 +77,25 @@ struct FewTile {
     static constexpr int ROW = KV4 ? DH / 2 : DH * 2, SCALES = KV4 ? DH / 16 : 0;
     static constexpr int BYTES = 32 * (ROW + SCALES);
     const char *at;  // this tile
-    int g, t;
+    // the lane's pieces: of key g of K, of keys 2t and 2t+1 of V, and their scales
+    // (eight rows further on a piece has the same place in its line)
+    struct Lane {
+        int k, v[2], ks, vs;
+        __device__ __forceinline__ Lane(int g, int t) {
+            if constexpr (KV4 && DH == 64)
+                k = g * ROW + t * 8;
+            else
+                k = piece(g, t);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                v[i] = 16 * ROW + (!KV4        ? piece(2 * t + i, g)
+                                   : DH == 128 ? piece(2 * t + i, g >> 1) + (g & 1) * 8
+                                               : (2 * t + i) * ROW + g * 4);
+            ks = 32 * ROW + g * SCALES + t * (DH / 64);
+            vs = 32 * ROW + (16 + 2 * t) * SCALES + g * SCALES / 8;
+        }
+    };
+    const Lane &p;
 
     // byte of a row's piece c (16 bytes)
     static __device__ __forceinline__ int piece(int row, int c) {
@@ -88,42 +106,52 @@ struct FewTile {
         else
             return row * ROW + (c << 4);
     }
-    // The copy of slots s0 .. s0 + 15 (past the last slot: the last) into dst.
-    static __device__ __forceinline__ void copy(uint32_t dst, const char *k, const char *v, int row_bytes,
-                                                int head, int scales_at, int s0, int last, int lane) {
-        constexpr int C = ROW / 16, RPP = 32 / C;  // pieces a row, rows a pass
-        const int row = lane / C, c = lane % C;
+    // Copies of slots s0 .. s0 + 15 (past the last slot: the last): a lane's pieces
+    // of the rows and its scales, and where they go.
+    struct Copy {
+        static constexpr int C = ROW / 16, RPP = 32 / C;  // pieces a row, rows a pass
+        const char *k, *v, *s;
+        int row, to, s_to;
+        __device__ __forceinline__ Copy(const CacheItem &it, int head, int scales_at, int lane) {
+            const int c = lane % C;
+            row = lane / C;
+            to = piece(row, c);
+            k = static_cast<const char *>(it.kc) + head * ROW + c * 16;
+            v = static_cast<const char *>(it.vc) + head * ROW + c * 16;
+            s = static_cast<const char *>(lane < 16 ? it.kc : it.vc) + scales_at + head * SCALES;
+            s_to = 32 * ROW + lane * SCALES;
+        }
+        __device__ __forceinline__ void operator()(uint32_t dst, uint32_t row_bytes, int s0, int last,
+                                                   int lane) const {
 #pragma unroll
-        for (int p = 0; p < 16 / RPP; ++p) {
-            const int r = row + p * RPP;
-            const size_t off = (size_t)(uint32_t)min(s0 + r, last) * (uint32_t)row_bytes + head * ROW + c * 16;
-            copy_async<16>(dst + piece(r, c), k + off);
-            copy_async<16>(dst + 16 * ROW + piece(r, c), v + off);
+            for (int p = 0; p < 16 / RPP; ++p) {
+                // (a pass of fewer than eight rows changes the place in the line)
+                const int place = RPP % 8 == 0 ? to + p * RPP * ROW : piece(row + p * RPP, lane % C);
+                const size_t off = (size_t)(uint32_t)min(s0 + row + p * RPP, last) * row_bytes;
+                copy_async<16>(dst + place, k + off);
+                copy_async<16>(dst + place + 16 * ROW, v + off);
+            }
+            if constexpr (KV4)
+                copy_async<SCALES>(dst + s_to, s + (size_t)(uint32_t)min(s0 + (lane & 15), last) * row_bytes);
         }
-        if constexpr (KV4) {
-            const int r = lane & 15;
-            const char *src = (lane < 16 ? k : v) +
-                              (size_t)(uint32_t)min(s0 + r, last) * (uint32_t)row_bytes + scales_at + head * SCALES;
-            copy_async<SCALES>(dst + 32 * ROW + lane * SCALES, src);
-        }
-    }
+    };
     // the lane's elements 8i .. 8i+7 of key g + 8h, as four pairs
     struct KWords {
         uint4 w[NI];
     };
     __device__ __forceinline__ KWords k_words(int h) const {
         KWords r;
-        const int row = g + 8 * h;
+        const char *k = at + p.k + 8 * h * ROW, *ks = at + p.ks + 8 * h * SCALES;
         if constexpr (KV4) {
             uint32_t w[NI], s;
             if constexpr (DH == 128) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(at + piece(row, t));
+                const uint4 x = *reinterpret_cast<const uint4 *>(k);
                 w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-                s = *reinterpret_cast<const uint16_t *>(at + 32 * ROW + row * SCALES + t * 2);
+                s = *reinterpret_cast<const uint16_t *>(ks);
             } else {
-                const uint2 x = *reinterpret_cast<const uint2 *>(at + row * ROW + t * 8);
+                const uint2 x = *reinterpret_cast<const uint2 *>(k);
                 w[0] = x.x, w[1] = x.y;
-                s = *reinterpret_cast<const uint8_t *>(at + 32 * ROW + row * SCALES + t);
+                s = *reinterpret_cast<const uint8_t *>(ks);
             }
             const uint32_t s2 = e4m3_halves(s);  // DH = 128: of words 0, 1 and of words 2, 3
 #pragma unroll
@@ -131,7 +159,8 @@ struct FewTile {
                 r.w[i] = kv4_widen(w[i], as_half2(__byte_perm(s2, 0, i >= 2 ? 0x3232 : 0x1010)));
         } else {
 #pragma unroll
-            for (int i = 0; i < NI; ++i) r.w[i] = *reinterpret_cast<const uint4 *>(at + piece(row, i * 4 + t));
+            for (int i = 0; i < NI; ++i)
+                r.w[i] = *reinterpret_cast<const uint4 *>(at + ((p.k ^ (i & 1) << 6) + (i >> 1) * 128 + 8 * h * ROW));
         }
         return r;
     }
@@ -143,28 +172,26 @@ struct FewTile {
         VRaw r;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int row = 2 * t + (i & 1) + 8 * (i >> 1);
-            const char *v = at + 16 * ROW;
+            const char *v = at + p.v[i & 1] + 8 * (i >> 1) * ROW;
             if constexpr (KV4) {
                 if constexpr (DH == 128) {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(v + piece(row, g >> 1) + (g & 1) * 8);
+                    const uint2 x = *reinterpret_cast<const uint2 *>(v);
                     r.w[i][0] = x.x, r.w[i][NJ - 1] = x.y;
                 } else {
-                    r.w[i][0] = *reinterpret_cast<const uint32_t *>(v + row * ROW + g * 4);
+                    r.w[i][0] = *reinterpret_cast<const uint32_t *>(v);
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(v + piece(row, j * 8 + g));
+                    const uint4 x = *reinterpret_cast<const uint4 *>(v + j * 128);
                     r.w[i][4 * j] = x.x, r.w[i][4 * j + 1] = x.y, r.w[i][4 * j + 2] = x.z, r.w[i][4 * j + 3] = x.w;
                 }
             }
         }
         if constexpr (KV4) {
-            const uint8_t *s = reinterpret_cast<const uint8_t *>(at + 32 * ROW + 16 * SCALES) + g * SCALES / 8;
+            const uint8_t *s = reinterpret_cast<const uint8_t *>(at + p.vs);
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
-                r.s[p] = s[(2 * t + 8 * p) * SCALES] | (uint32_t)s[(2 * t + 8 * p + 1) * SCALES] << 8;
+            for (int h = 0; h < 2; ++h) r.s[h] = s[8 * h * SCALES] | (uint32_t)s[(8 * h + 1) * SCALES] << 8;
         }
         return r;
     }
@@ -219,12 +246,12 @@ struct FewTile {
 };
 
 // Tiles of a warp's ring (all but one of them in flight) and CTAs an SM.
-template <int DH, bool KV4> constexpr int kFewRing = KV4 ? 4 : 3;
-template <bool KV4, int NQ> constexpr int kFewCtas = KV4 ? (NQ == 1 ? 4 : 3) : 2;
+constexpr int kFewRing = 3;
+template <bool KV4, int NQ> constexpr int kFewCtas = KV4 && NQ == 1 ? 3 : 2;
 
 template <int DH, bool KV4, int NQ>
 struct FewSmem {
-    static constexpr int WARP = kFewRing<DH, KV4> * FewTile<DH, KV4>::BYTES;
+    static constexpr int WARP = kFewRing * FewTile<DH, KV4>::BYTES;
     static constexpr int LD = DH + 4, Q = 8 * NQ;
     // after the loop, in place of the rings: O of each warp [Q][LD], then (m, l)
     static constexpr int JOIN = kFewWarps * Q * (LD * 4 + 8);
@@ -237,7 +264,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<KV4, NQ>) cache_attn_few
     pdl_enter();
     using Tile = FewTile<DH, KV4>;
     using S = FewSmem<DH, KV4, NQ>;
-    constexpr int NI = Tile::NI, NJ = Tile::NJ, Q = 8 * NQ, LD = S::LD, D = kFewRing<DH, KV4>;
+    constexpr int NI = Tile::NI, NJ = Tile::NJ, Q = 8 * NQ, LD = S::LD, D = kFewRing;
     constexpr float kBias = KV4 ? kF16Bias : 0.f;
     extern __shared__ __align__(128) char sm[];
     __shared__ uint64_t row_mask[Q];  // tree slots a row sees
@@ -276,13 +303,11 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<KV4, NQ>) cache_attn_few
     static_assert(kRangeUnit % 16 == 0, "ranges begin at a tile");
     const int x_warp = kbeg + warp * 16;
     const int row_bytes = KV4 ? kv4_row_bytes(a.Hkv, DH) : a.Hkv * DH * 2;
-    const int scales_at = KV4 ? kv4_code_bytes(a.Hkv, DH) : 0;
     char *ring = sm + warp * S::WARP;
     const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
-    auto copy = [&](int x, int slot_in_ring) {
-        if (x < kend)
-            Tile::copy(ring_at + slot_in_ring * Tile::BYTES, static_cast<const char *>(it.kc),
-                       static_cast<const char *>(it.vc), row_bytes, head, scales_at, slot(x), last, lane);
+    const typename Tile::Copy copy_tile(it, head, KV4 ? kv4_code_bytes(a.Hkv, DH) : 0, lane);
+    auto copy = [&](int x, int place) {
+        if (x < kend) copy_tile(ring_at + place * Tile::BYTES, row_bytes, slot(x), last, lane);
         asm volatile("cp.async.commit_group;\n" ::: "memory");
     };
 #pragma unroll
@@ -366,46 +391,51 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<KV4, NQ>) cache_attn_few
         return x >= row_win[m] || x < run.n_sink || (x >= n_pad && x < x_sink);
     };
 
-    float o[NQ][4 * NJ][4], m_run[NQ][2], l_run[NQ][2];
+    float o[NQ][4 * NJ][4], m_run[NQ][2], mu[NQ][2], l_run[NQ][2];
+    bool huge = false;  // uniform over the warp
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
 #pragma unroll
         for (int i = 0; i < 4 * NJ; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
         m_run[n][0] = m_run[n][1] = -INFINITY;
+        mu[n][0] = mu[n][1] = -kBias;
         l_run[n][0] = l_run[n][1] = 0.f;
     }
 
+    const typename Tile::Lane place(g, t);
     int at = 0;  // ring place of the tile at x0
 #pragma unroll 1
     for (int x0 = x_warp; x0 < kend; x0 += kStep) {
         asm volatile("cp.async.wait_group %0;\n" ::"n"(D - 2) : "memory");
         __syncwarp();  // every lane's copies are there, and the tile before is read
         copy(x0 + (D - 1) * kStep, at == 0 ? D - 1 : at - 1);
-        const Tile tl{ring + at * Tile::BYTES, g, t};
+        const Tile tl{ring + at * Tile::BYTES, place};
         at = at == D - 1 ? 0 : at + 1;
-        // c[0], c[1]: key g, rows 8n + 2t and + 1; c[2], c[3]: key g + 8
-        // (two chains of products, added up: half the latency)
-        float s[NQ][4], s2[NQ][4];
+        // s[..][0], [1]: key g, rows 8n + 2t and + 1; s[..][2], [3]: key g + 8
+        float s[NQ][4];
+        {
+            const typename Tile::KWords k0 = tl.k_words(0), k1 = tl.k_words(1);
+            float s2[NQ][4];  // two chains of products, added up: half the latency
 #pragma unroll
-        for (int n = 0; n < NQ; ++n)
+            for (int n = 0; n < NQ; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
-        const typename Tile::KWords k0 = tl.k_words(0), k1 = tl.k_words(1);
+                for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const uint4 lo = k0.w[i], hi = k1.w[i];
+            for (int i = 0; i < NI; ++i) {
+                const uint4 lo = k0.w[i], hi = k1.w[i];
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-                mma16816<KV4>(s[n], lo.x, hi.x, lo.y, hi.y, qf[n][4 * i], qf[n][4 * i + 1]);
-                mma16816<KV4>(s2[n], lo.z, hi.z, lo.w, hi.w, qf[n][4 * i + 2], qf[n][4 * i + 3]);
+                for (int n = 0; n < NQ; ++n) {
+                    mma16816<KV4>(s[n], lo.x, hi.x, lo.y, hi.y, qf[n][4 * i], qf[n][4 * i + 1]);
+                    mma16816<KV4>(s2[n], lo.z, hi.z, lo.w, hi.w, qf[n][4 * i + 2], qf[n][4 * i + 3]);
+                }
             }
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[n][e] += s2[n][e];
         }
-        const typename Tile::VRaw vr = tl.v_raw();
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[n][e] += s2[n][e];
-        const bool masked = !(x0 + 16 <= min(kend, x_tree) && (x0 >= x_all || x0 + 16 <= run.n_sink));
+        const bool masked =
+            !(x0 + 16 <= min(kend, x_tree) && (x0 >= x_all || x0 + 16 <= run.n_sink));
         if (masked) {
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
@@ -433,6 +463,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<KV4, NQ>) cache_attn_few
                     if (x > m_run[n][c] + kRescaleLog2) {
                         const float alpha = exp2f(m_run[n][c] - x);
                         m_run[n][c] = x;
+                        mu[n][c] = x - kBias;
                         l_run[n][c] *= alpha;
 #pragma unroll
                         for (int i = 0; i < 4 * NJ; ++i) {
@@ -440,6 +471,10 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<KV4, NQ>) cache_attn_few
                             o[n][i][c + 2] *= alpha;
                         }
                     }
+                    // past 2^16 the scores are rounded before the difference, as the
+                    // maximum was: the fused form keeps bits of the product that the
+                    // maximum lost, and the largest weight would leave 1
+                    huge = huge || __any_sync(0xffffffffu, fabsf(mu[n][c]) > 65536.f);
                 }
         }
         uint32_t pb[NQ][2];
@@ -448,22 +483,19 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<KV4, NQ>) cache_attn_few
             float p[4];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const float mu = (m_run[n][c] == -INFINITY ? 0.f : m_run[n][c]) - kBias;
-                // past 2^16 the scores are rounded before the difference, as the
-                // maximum was: the fused form keeps bits of the product that the
-                // maximum lost, and the largest weight would leave 1
-                if (fabsf(mu) > 65536.f) {
-                    p[c] = ex2_approx(__fmul_rn(s[n][c], scale[n][c]) - mu);
-                    p[c + 2] = ex2_approx(__fmul_rn(s[n][c + 2], scale[n][c]) - mu);
+                if (huge) {
+                    p[c] = ex2_approx(__fmul_rn(s[n][c], scale[n][c]) - mu[n][c]);
+                    p[c + 2] = ex2_approx(__fmul_rn(s[n][c + 2], scale[n][c]) - mu[n][c]);
                 } else {
-                    p[c] = ex2_approx(fmaf(s[n][c], scale[n][c], -mu));
-                    p[c + 2] = ex2_approx(fmaf(s[n][c + 2], scale[n][c], -mu));
+                    p[c] = ex2_approx(fmaf(s[n][c], scale[n][c], -mu[n][c]));
+                    p[c + 2] = ex2_approx(fmaf(s[n][c + 2], scale[n][c], -mu[n][c]));
                 }
                 l_run[n][c] += p[c] + p[c + 2];  // the sum adds the fp32 weights
             }
             pb[n][0] = transpose8(pack_weights<KV4>(p[0], p[1]));
             pb[n][1] = transpose8(pack_weights<KV4>(p[2], p[3]));
         }
+        const typename Tile::VRaw vr = tl.v_raw();
         if (masked && __any_sync(0xffffffffu, Tile::v_bad(vr))) {
             // Infinities or NaNs in V where some row may not see them: one row at a
             // time, with the keys of weight 0 cleared from V for it.
@@ -505,10 +537,12 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<KV4, NQ>) cache_attn_few
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        mma16816<KV4>(o[n][4 * j + i], v[i][0], v[i][1], v[i][2], v[i][3], pb[n][0], pb[n][1]);
+                        mma16816<KV4>(o[n][4 * j + i], v[i][0], v[i][1], v[i][2], v[i][3], pb[n][0],
+                                      pb[n][1]);
             }
         }
     }
+
     // ---- the warps' parts joined (every copy has landed, or none was begun)
     asm volatile("cp.async.wait_group 0;\n" ::: "memory");
     __syncthreads();
