@@ -609,6 +609,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
                     row_scale *= __uint_as_float(eb << 23);
                 }
             }
+            // a masked score, -inf, times the scale has to stay -inf
+            row_scale = fmaxf(row_scale, 0x1p-126f);
 #pragma unroll
             for (int half = 0; half < DH / 64; ++half) {
                 uint32_t qr[32];

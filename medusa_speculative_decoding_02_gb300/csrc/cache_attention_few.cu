@@ -579,9 +579,9 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<KV4, NQ>) cache_attn_few
 #pragma unroll
         for (int w = 0; w < kFewWarps; ++w) {
             const float f = exp2f(ml[w].x - mu);
+            l = fmaf(f, ml[w].y, l);  // (also with f = 0: a row of NaN scores has m = -inf, l = NaN)
             if (f == 0.f) continue;
             const float4 v = *reinterpret_cast<const float4 *>(so + (w * Q + m) * LD + c);
-            l = fmaf(f, ml[w].y, l);
             acc.x = fmaf(f, v.x, acc.x);
             acc.y = fmaf(f, v.y, acc.y);
             acc.z = fmaf(f, v.z, acc.z);
