@@ -13,9 +13,12 @@
 // before the window of the first row (position P), and everything from
 // P - window + 1 on.  They are numbered 0 .. len-1 without a gap (KeyRun), so
 // the work does not grow with the prefix.  The numbered keys are split into
-// ranges of `chunk` keys; one CTA computes an unnormalised partial (O, m, l)
-// of a tile of rows over one range, and cache_attn_combine_kernel joins the
-// ranges.  With one range the CTA writes the output itself.
+// ranges (find_item); one CTA computes an unnormalised partial (O, m, l) of a
+// tile of rows over one range, and cache_attn_combine_kernel joins the ranges.
+// With one range the CTA writes the output itself.
+//
+// Three kernels: fp32 on the CUDA cores and bf16 on the tensor cores here, and
+// bf16 with at most 16 rows a KV head in cache_attention_few.cu.
 //
 // The rows of a tile are the R * G (G = H / Hkv) rows that share a KV head,
 // row r * G + g being tree row r and query head hk * G + g.
@@ -203,7 +206,7 @@ __global__ void __launch_bounds__(kSimtThreads) cache_attn_simt_kernel(CacheAttn
 //   warps 4-7  load: K and V tiles of a stage into shared memory as 128-byte
 //              swizzled blocks, a ring of tiles in the order of their use
 //              (K0 K1 V0 K2 V1 ..).  A bf16 cache comes by cp.async; a 4-bit
-//              tile is read into registers six tiles ahead, widened to fp16
+//              tile is read into registers four tiles ahead, widened to fp16
 //              (exact) and stored.
 //   warp 8     one thread issues the products: S_j+1 = Q K^T as soon as the
 //              scores of stage j are in registers, then O += P_j V.
@@ -223,6 +226,18 @@ __global__ void __launch_bounds__(kSimtThreads) cache_attn_simt_kernel(CacheAttn
 // largest, and an absolute 2^-25 of it below).  The weights are biased by 2^7:
 // they reach 2^15, and what fp16 drops is below 2^-32 of the reference, so
 // even 2^20 keys there lose less than 2^-12 of the sum.
+//
+// What bounds it is neither the products (a stage's take 0.33 us of an SM at the
+// measured bf16 rate) nor the bytes, but passing a stage between the warps:
+// about 1 us a stage with two CTAs on the SM, whatever the cache's type, of which
+// a third remains if every load, conversion and exponential is left out; a CTA
+// costs 6 us more at its ends.  Measured: 65 rows x 32 heads over a 1024 window
+// 15.8 us; eight sequences of 65 rows, 32 heads over 8 KV heads, 4096 window
+// 84 us (35 GFLOP: 0.42 PFLOP/s); 4 bits, 65 rows x 32 heads over 8192 slots
+// 29.6 us, eight ragged sequences up to 4096 slots 64.2 us.  Measured and not
+// kept: the whole ring in flight before a tile is announced (92 against 82 us:
+// each tile then waits for the slot of the one NT before it), weights in tensor
+// memory, 16 warps, one CTA walking several ranges.
 //
 // Masks are built as 64 bits a row and stage.  Products run over masked keys
 // too, with weight 0, so a non-finite V element there would reach every row
@@ -505,8 +520,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
                 }
             }
         } else {
-            // half the ring of younger copies stays in flight when a tile is announced:
-            // with all of it, each tile waited for the slot of the one NT before it
+            // half the ring of younger copies stays in flight when a tile is announced
             constexpr int LAG = L::NT / 2;
             const bf16 *k16 = static_cast<const bf16 *>(kc), *v16 = static_cast<const bf16 *>(vc);
             bool go = true;
@@ -976,8 +990,8 @@ struct CachePlan {
     bool deal;  // ranges dealt out by the sequences' lengths
 };
 
-// Key ranges: the count that makes (waves of CTAs) x (stages per CTA + the
-// fixed cost of a CTA, in stages) smallest, joining included.
+// Key ranges: the count that makes (waves of CTAs) x (64-key stages per CTA + 3,
+// the fixed cost of a CTA in stages) smallest, joining included.
 CachePlan cache_plan(medusa_dtype dtype, bool kv4, int B, int R, int H, int Hkv, int P_max, int window,
                      int sinks) {
     CachePlan p;
@@ -997,7 +1011,9 @@ CachePlan cache_plan(medusa_dtype dtype, bool kv4, int B, int R, int H, int Hkv,
     const long long ctas = (long long)B * Hkv * p.row_tiles;
     double best = 0;
     p.ns = 1;
-    for (int ns = 1; ns <= std::min(subs, 512); ++ns) {
+    // (more than four waves only add to the fixed cost)
+    const int most = std::min<long long>(subs, std::max<long long>(1, 4LL * slots / ctas));
+    for (int ns = 1; ns <= most; ++ns) {
         const int per = (subs + ns - 1) / ns;
         if ((subs + per - 1) / per != ns) continue;  // the same split as a smaller ns
         const double waves = (double)((ctas * ns + slots - 1) / slots);
@@ -1007,8 +1023,10 @@ CachePlan cache_plan(medusa_dtype dtype, bool kv4, int B, int R, int H, int Hkv,
             p.ns = ns;
         }
     }
-    // Lengths differ (behind a window they are about alike): the deal.  It costs
-    // 2 us at the start and in the join (a 65-row step over 1024 slots 15 -> 17).
+    // Sequences of different lengths (behind a window they are about alike): ranges
+    // dealt out by length.  Single tokens, eight sequences of 7.5k to 32k 4-bit slots:
+    // 75 -> 56 us.  It costs 1-2 us at the start and in the join (a 65-row step over
+    // a 1024 window 15.8 -> 17.2 us).
     p.deal = !simt && p.ns > 1 && B > 1 && B <= 32 && !p.window;
     return p;
 }

