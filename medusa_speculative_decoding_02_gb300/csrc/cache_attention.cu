@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kSimtThreads) cache_attn_simt_kernel(CacheAttn
 // What bounds it is neither the products (a stage's take 0.33 us of an SM at the
 // measured bf16 rate) nor the bytes, but passing a stage between the warps:
 // about 1 us a stage with two CTAs on the SM, whatever the cache's type, of which
-// a third remains if every load, conversion and exponential is left out; a CTA
+// two thirds remain if loads, conversions and exponentials are left out; a CTA
 // costs 6 us more at its ends.  Measured: 65 rows x 32 heads over a 1024 window
 // 15.8 us; eight sequences of 65 rows, 32 heads over 8 KV heads, 4096 window
 // 84 us (35 GFLOP: 0.42 PFLOP/s); 4 bits, 65 rows x 32 heads over 8192 slots

@@ -8,21 +8,24 @@
 // from rot on stay.  K goes to k_out or straight into its cache slot, where V
 // is copied as well.
 //
-// Each vector is held by dh/8 lanes with eight elements each: one or two
-// 16-byte loads a lane, the sum of squares by shuffles inside the group, the
-// partner half of a pair by one shuffle per element.
+// Each vector is held by dh/8 lanes with four pairs each, both members of a pair
+// in one lane: two pieces of four elements, rot/2 apart or, interleaved, next to
+// each other.  A lane thus needs four angles and no exchange but the sum of
+// squares (with 16-byte loads, eight shuffles fetched the partners and a lane kept
+// eight sines and cosines: 38.5 against 31.3 us at the prompt below).
 //
 // Angles: p * inv_freq reaches 10^5 turns at far positions, where fp32 has no
 // fraction left.  inv_freq becomes a 64-bit fixed-point number of turns per
 // position, modulo one (turns_per_position); p times that, modulo 2^64, is the
 // fraction of a turn to 2^-33 at every p.  Integers throughout: this GPU does
 // two fp64 products a cycle and SM, and the same in fp64 cost 2.4 us at 65
-// rows.  Sine and cosine are taken in fp32 on [-1/2, 1/2] turn.  A lane meets
-// the same eight angles in every vector of the row and keeps their sines and
-// cosines in registers.
+// rows.  Sine and cosine are taken in fp32 on [-1/2, 1/2] turn.
 //
-// Bound by the bytes of q, K and V read and written once; the loads of a row
-// are issued before its angles are computed.
+// Bound by issue and, close behind, by the bytes of q, K and V read and written
+// once; the loads of a row are issued before its angles are computed.  6626 rows
+// of 32 + 8 + 8 vectors of 128 (160 MB) take 31.3 us, 5.1 TB/s; one row a CTA took
+// 41.2 (40.7 M instructions where four rows a CTA had 29.8 M).  65 rows of 32 + 32
+// + 32 vectors 3.0 us, eight rows of 32 + 8 1.9 us: latency of two rounds of loads.
 #include <algorithm>
 
 #include "common.cuh"
@@ -34,13 +37,14 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kMaxRot = 128;
+constexpr int kManyRows = 4, kManyPasses = 3;  // rows and passes of a CTA where there are many
 
 struct RopeArgs {
     const void *q, *k, *v;  // v: only with caches
     long long q_stride, k_stride, v_stride;
     const void *qw, *kw;    // [dh] or null (ones)
     float eps;
-    int norm, interleaved;
+    int norm;
     const int32_t *pos;
     const float *inv_freq;
     int rot;
@@ -54,30 +58,35 @@ struct RopeArgs {
     int *status;
 };
 
+// Four elements of a vector, the unit of a lane's loads and stores.
 template <typename T>
-__device__ __forceinline__ void widen8(const uint4 (&w)[8 / Vec16<T>::N], float (&x)[8]) {
-    constexpr int N = Vec16<T>::N;
+using Piece = typename std::conditional<sizeof(T) == 2, uint2, uint4>::type;
+
+__device__ __forceinline__ uint2 ld_piece(const bf16 *p) {
+    uint2 r;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint4 ld_piece(const float *p) { return ld_stream16(p); }
+
+// element i of the lane's eight (lo: the first four, hi: the others)
+__device__ __forceinline__ void widen(const uint2 &lo, const uint2 &hi, float (&x)[8]) {
+    x[0] = bf_lo(lo.x), x[1] = bf_hi(lo.x), x[2] = bf_lo(lo.y), x[3] = bf_hi(lo.y);
+    x[4] = bf_lo(hi.x), x[5] = bf_hi(hi.x), x[6] = bf_lo(hi.y), x[7] = bf_hi(hi.y);
+}
+__device__ __forceinline__ void widen(const uint4 &lo, const uint4 &hi, float (&x)[8]) {
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-    for (int u = 0; u < 8 / N; ++u) {
-        float f[N];
-        Vec16<T>::widen(w[u], f);
-#pragma unroll
-        for (int e = 0; e < N; ++e) x[u * N + e] = f[e];
-    }
+    for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(w[e]);
 }
 
-__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
-    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void store4(float *p, float a, float b, float c, float d) {
+    *reinterpret_cast<float4 *>(p) = make_float4(a, b, c, d);
 }
-__device__ __forceinline__ void store8(bf16 *p, const float (&x)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const __nv_bfloat162 t = __floats2bfloat162_rn(x[2 * u], x[2 * u + 1]);
-        w[u] = *reinterpret_cast<const uint32_t *>(&t);
-    }
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ void store4(bf16 *p, float a, float b, float c, float d) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(a, b), u = __floats2bfloat162_rn(c, d);
+    *reinterpret_cast<uint2 *>(p) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&t), *reinterpret_cast<const uint32_t *>(&u));
 }
 
 // f / (2 pi) modulo one in units of 2^-64, for finite f: with f = m 2^e (m a
@@ -105,37 +114,44 @@ __device__ __forceinline__ uint64_t turns_per_position(float f) {
     return f < 0.f ? 0 - step : step;
 }
 
-// grid (R, vector groups, B); a CTA takes NP * 256 / (dh/8) vectors of its row: H queries, then Hkv keys, then (with caches) Hkv values
-template <typename T, int DH, int NP>
+// grid (row groups, vector groups, B).  A CTA takes NP * 256 / (dh/8) vectors (H
+// queries, then Hkv keys, then, with caches, Hkv values) of each of NR rows: what
+// comes before the first vector, some 300 instructions a warp, is then done once
+// for the four rows, and the angles of all of them by all warps at once.  IL:
+// interleaved pairs.
+template <typename T, int DH, int NP, int NR, bool IL>
 __global__ void __launch_bounds__(kRopeThreads, NP == 1 ? 1 : sizeof(T) == 2 ? 4 : 2) qk_norm_rope_kernel(RopeArgs a) {
     pdl_enter();
     constexpr int LPV = DH / 8;                  // lanes per vector
     constexpr int VPP = kRopeThreads / LPV;      // vectors per pass
-    // (cos, sin) of pair j at cs_at(j): the lanes of a vector then read
-    // consecutive words
-    __shared__ float2 cs[kMaxRot / 2];
-    auto cs_at = [](int j) { return (j & 7) * (kMaxRot / 16) + (j >> 3); };
-    const int tid = threadIdx.x, sub = tid % LPV, e0 = sub * 8;
-    const int b = blockIdx.z, i = blockIdx.x;
-    const long long row = (long long)b * a.R + i;
+    __shared__ __align__(16) float cosine[NR][kMaxRot / 2], sine[NR][kMaxRot / 2];
+    const int tid = threadIdx.x, sub = tid % LPV;
+    const int b = blockIdx.z, i0 = blockIdx.x * NR;
     const int half = a.rot / 2;
-    constexpr int W = 8 / Vec16<T>::N;           // 16-byte words of a lane's elements
-    // everything the row's loads and angles depend on, in one round of loads
+    // The lane's pairs are 4 sub .. 4 sub + 3, if there are as many: its pieces
+    // begin at elements e_lo and e_hi (rot is a multiple of 16).
+    const bool turned = 4 * sub < half;
+    const int e_lo = IL || !turned ? 8 * sub : 4 * sub, e_hi = IL || !turned ? 8 * sub + 4 : 4 * sub + half;
+    // the angle a thread computes: pair j of row i0 + jr
+    constexpr int TPR = NR == 1 ? kRopeThreads : kMaxRot / 2;
+    const int j = tid % TPR, jr = NR == 1 ? 0 : tid / TPR;
+    // everything the rows' loads and angles depend on, in one round of loads
     const int n_rows = a.n_rows ? a.n_rows[b] : a.R;
     T *const kc = a.kc ? static_cast<T *>(a.kc[b]) : nullptr;
     T *const vc = a.kc ? static_cast<T *>(a.vc[b]) : nullptr;
     const int P = a.kc ? a.prefix_len[b] : 0;
-    const int pos = a.pos[row];
-    const float freq = tid < half ? a.inv_freq[tid] : 0.f;
-    uint4 wraw[2][W];
+    const bool angle = j < half && jr < NR && i0 + jr < a.R;
+    const int pos = angle ? a.pos[(long long)b * a.R + i0 + jr] : 0;
+    const float freq = angle ? a.inv_freq[j] : 0.f;
+    Piece<T> wraw[2][2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const T *w = static_cast<const T *>(k ? a.kw : a.qw);
-#pragma unroll
-        for (int c = 0; c < W; ++c)
-            wraw[k][c] = w ? *reinterpret_cast<const uint4 *>(w + e0 + c * Vec16<T>::N) : make_uint4(0, 0, 0, 0);
+        wraw[k][0] = w ? *reinterpret_cast<const Piece<T> *>(w + e_lo) : Piece<T>{};
+        wraw[k][1] = w ? *reinterpret_cast<const Piece<T> *>(w + e_hi) : Piece<T>{};
     }
-    if (i >= n_rows) return;                     // uniform over the CTA
+    const int rows = min(NR, min(n_rows, a.R) - i0);
+    if (rows <= 0) return;                       // uniform over the CTA
     T *krow, *vrow = nullptr;
     if (a.kc) {
         const bool bad_ptr =
@@ -145,125 +161,125 @@ __global__ void __launch_bounds__(kRopeThreads, NP == 1 ? 1 : sizeof(T) == 2 ? 4
             if (tid == 0) set_status(a.status, bad_ptr ? MEDUSA_DEV_BAD_CACHE : MEDUSA_DEV_BAD_PREFIX);
             return;
         }
-        krow = kc + (size_t)(P + i) * a.Hkv * DH;
-        vrow = vc + (size_t)(P + i) * a.Hkv * DH;
+        krow = kc + (size_t)(P + i0) * a.Hkv * DH;
+        vrow = vc + (size_t)(P + i0) * a.Hkv * DH;
     } else {
-        krow = static_cast<T *>(a.k_out) + row * a.Hkv * DH;
+        krow = static_cast<T *>(a.k_out) + ((long long)b * a.R + i0) * a.Hkv * DH;
     }
     const int nq = a.H, nqk = a.H + a.Hkv, nv = nqk + (a.kc ? a.Hkv : 0);
     const int v0 = blockIdx.y * (VPP * NP) + tid / LPV;
     // the row's vectors, as if each kind went on from the one before
-    const T *const qrow = static_cast<const T *>(a.q) + row * a.q_stride + e0;
-    const T *const kin = static_cast<const T *>(a.k) + row * a.k_stride - (long long)nq * DH + e0;
-    const T *const vin = static_cast<const T *>(a.v) + row * a.v_stride - (long long)nqk * DH + e0;
-    uint4 raw[NP][W];
+    const long long row = (long long)b * a.R + i0;
+    const T *qin = static_cast<const T *>(a.q) + row * a.q_stride;
+    const T *kin = static_cast<const T *>(a.k) + row * a.k_stride - (long long)nq * DH;
+    const T *vin = static_cast<const T *>(a.v) + row * a.v_stride - (long long)nqk * DH;
+    T *qout = static_cast<T *>(a.q_out) + row * nq * DH;
+    T *kout = krow - (long long)nq * DH;
+    T *vout = vrow - (long long)nqk * DH;
+    Piece<T> raw[NP][2];
+    auto load = [&] {
 #pragma unroll
-    for (int n = 0; n < NP; ++n) {
-        const int v = v0 + n * VPP;
-        const T *src = (v < nq ? qrow : v < nqk ? kin : vin) + v * DH;
-#pragma unroll
-        for (int c = 0; c < W; ++c)
-            raw[n][c] = v < nv ? ld_stream16(src + c * Vec16<T>::N) : make_uint4(0, 0, 0, 0);
-    }
-    if (tid < half) {
+        for (int n = 0; n < NP; ++n) {
+            const int v = v0 + n * VPP;
+            const T *src = (v < nq ? qin : v < nqk ? kin : vin) + v * DH;
+            raw[n][0] = v < nv ? ld_piece(src + e_lo) : Piece<T>{};
+            raw[n][1] = v < nv ? ld_piece(src + e_hi) : Piece<T>{};
+        }
+    };
+    load();
+    if (angle) {
         // fraction of a turn, in [-1/2, 1/2)
         const int64_t frac = (int64_t)((uint64_t)(int64_t)pos * turns_per_position(freq));
         float s, c;
         sincospif((float)frac * 0x1p-63f, &s, &c);
         if (!(fabsf(freq) < INFINITY)) s = c = NAN;
-        cs[cs_at(tid)] = make_float2(c, s);
+        cosine[jr][j] = c;
+        sine[jr][j] = s;
     }
     __syncthreads();
-    // this lane's cosines and sines, by pairs of elements; y = x cos + o sin, o
-    // the partner element, so the first of a pair takes -sin
-    const bool turned = e0 < a.rot;  // rot is a multiple of 16: the same for all eight
-    const int lane = tid & 31;
-    const int partner = e0 < half ? lane + half / 8 : turned ? lane - half / 8 : lane;
-    float2 c2[4], s2[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        c2[e] = make_float2(1.f, 1.f);
-        s2[e] = make_float2(0.f, 0.f);
-        if (turned && a.interleaved) {
-            const float2 t = cs[cs_at(e0 / 2 + e)];
-            c2[e] = make_float2(t.x, t.x);
-            s2[e] = make_float2(-t.y, t.y);
-        } else if (turned) {
-            const int j = (e0 < half ? e0 : e0 - half) + 2 * e;
-            const float2 t = cs[cs_at(j)], u = cs[cs_at(j + 1)];
-            c2[e] = make_float2(t.x, u.x);
-            s2[e] = e0 < half ? make_float2(-t.y, -u.y) : make_float2(t.y, u.y);
+#pragma unroll 1
+    for (int r = 0; r < rows; ++r) {
+        float4 c4 = make_float4(1.f, 1.f, 1.f, 1.f), s4 = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (turned) {
+            c4 = *reinterpret_cast<const float4 *>(&cosine[r][4 * sub]);
+            s4 = *reinterpret_cast<const float4 *>(&sine[r][4 * sub]);
         }
-    }
-    T *const qout = static_cast<T *>(a.q_out) + row * nq * DH + e0;
-    T *const kout = krow - (long long)nq * DH + e0;
-    T *const vout = vrow - (long long)nqk * DH + e0;
+        const float2 c2[2] = {make_float2(c4.x, c4.y), make_float2(c4.z, c4.w)};
+        const float2 s2[2] = {make_float2(s4.x, s4.y), make_float2(s4.z, s4.w)};
+        const float2 m2[2] = {make_float2(-s4.x, -s4.y), make_float2(-s4.z, -s4.w)};
 #pragma unroll
-    for (int n = 0; n < NP; ++n) {
-        const int v = v0 + n * VPP;
-        T *dst = (v < nq ? qout : v < nqk ? kout : vout) + v * DH;
-        if (__all_sync(0xffffffffu, v >= nqk)) {  // values (or past the end): copied
-            if (v < nv)
+        for (int n = 0; n < NP; ++n) {
+            const int v = v0 + n * VPP;
+            T *dst = (v < nq ? qout : v < nqk ? kout : vout) + v * DH;
+            if (v >= nqk && v < nv) {  // values: copied
+                *reinterpret_cast<Piece<T> *>(dst + e_lo) = raw[n][0];
+                *reinterpret_cast<Piece<T> *>(dst + e_hi) = raw[n][1];
+            }
+            if (__all_sync(0xffffffffu, v >= nqk)) continue;
+            // u, w: the first and second elements of the four pairs
+            float x[8];
+            widen(raw[n][0], raw[n][1], x);
+            float2 u[2], w[2];
 #pragma unroll
-                for (int c = 0; c < W; ++c)
-                    *reinterpret_cast<uint4 *>(dst + c * Vec16<T>::N) = raw[n][c];
-            continue;
-        }
-        float x[8];
-        widen8<T>(raw[n], x);
-        float2 x2[4], o2[4];
+            for (int e = 0; e < 2; ++e) {
+                u[e] = IL ? make_float2(x[4 * e], x[4 * e + 2]) : make_float2(x[2 * e], x[2 * e + 1]);
+                w[e] = IL ? make_float2(x[4 * e + 1], x[4 * e + 3]) : make_float2(x[2 * e + 4], x[2 * e + 5]);
+            }
+            if (a.norm) {  // uniform: the shuffles run in every lane
+                float2 q2 = __fmul2_rn(u[0], u[0]);
+                q2 = __ffma2_rn(u[1], u[1], q2);
+                q2 = __ffma2_rn(w[0], w[0], q2);
+                q2 = __ffma2_rn(w[1], w[1], q2);
+                float ss = q2.x + q2.y;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x2[e] = make_float2(x[2 * e], x[2 * e + 1]);
-        if (a.norm) {  // uniform: the shuffles run in every lane
-            float2 q2 = __fmul2_rn(x2[0], x2[0]);
+                for (int o = LPV / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                const float inv = rsqrtf(fmaf(ss, 1.f / DH, a.eps));  // within 2 units in the last place
+                const float2 i2 = make_float2(inv, inv);
+                const bool is_q = v < nq;
+                if (is_q ? a.qw : a.kw) {
+                    float f[8];
+                    widen(is_q ? wraw[0][0] : wraw[1][0], is_q ? wraw[0][1] : wraw[1][1], f);
 #pragma unroll
-            for (int e = 1; e < 4; ++e) q2 = __ffma2_rn(x2[e], x2[e], q2);
-            float ss = q2.x + q2.y;
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 fu = IL ? make_float2(f[4 * e], f[4 * e + 2]) : make_float2(f[2 * e], f[2 * e + 1]);
+                        const float2 fw = IL ? make_float2(f[4 * e + 1], f[4 * e + 3]) : make_float2(f[2 * e + 4], f[2 * e + 5]);
+                        u[e] = __fmul2_rn(u[e], __fmul2_rn(i2, fu));
+                        w[e] = __fmul2_rn(w[e], __fmul2_rn(i2, fw));
+                    }
+                } else {
 #pragma unroll
-            for (int o = LPV / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float inv = rsqrtf(fmaf(ss, 1.f / DH, a.eps));  // within 2 units in the last place
-            const float2 i2 = make_float2(inv, inv);
-            const bool is_q = v < nq;
-            if (is_q ? a.qw : a.kw) {
-                uint4 ww[W];
-                float wf[8];
+                    for (int e = 0; e < 2; ++e) {
+                        u[e] = __fmul2_rn(u[e], i2);
+                        w[e] = __fmul2_rn(w[e], i2);
+                    }
+                }
+            }
+            if (turned) {  // (the other elements stay what they are: inf * 0 is not 0)
 #pragma unroll
-                for (int c = 0; c < W; ++c) ww[c] = is_q ? wraw[0][c] : wraw[1][c];
-                widen8<T>(ww, wf);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    x2[e] = __fmul2_rn(x2[e], __fmul2_rn(i2, make_float2(wf[2 * e], wf[2 * e + 1])));
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x2[e] = __fmul2_rn(x2[e], i2);
+                for (int e = 0; e < 2; ++e) {
+                    const float2 t = __ffma2_rn(w[e], m2[e], __fmul2_rn(u[e], c2[e]));
+                    w[e] = __ffma2_rn(u[e], s2[e], __fmul2_rn(w[e], c2[e]));
+                    u[e] = t;
+                }
+            }
+            if (v < nqk) {
+                if (IL) {
+                    store4(dst + e_lo, u[0].x, w[0].x, u[0].y, w[0].y);
+                    store4(dst + e_hi, u[1].x, w[1].x, u[1].y, w[1].y);
+                } else {
+                    store4(dst + e_lo, u[0].x, u[0].y, u[1].x, u[1].y);
+                    store4(dst + e_hi, w[0].x, w[0].y, w[1].x, w[1].y);
+                }
             }
         }
-        if (a.interleaved) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o2[e] = make_float2(x2[e].y, x2[e].x);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                o2[e] = make_float2(__shfl_sync(0xffffffffu, x2[e].x, partner),
-                                    __shfl_sync(0xffffffffu, x2[e].y, partner));
-        }
-        if (a.rot < DH && !turned) {  // unchanged, whatever they hold (inf * 0 is not 0)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o2[e] = make_float2(0.f, 0.f);
-        }
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 t = __ffma2_rn(o2[e], s2[e], __fmul2_rn(x2[e], c2[e]));
-            y[2 * e] = t.x;
-            y[2 * e + 1] = t.y;
-        }
-        if (v < nqk)
-            store8(dst, y);
-        else if (v < nv)  // a warp with a key and a value
-#pragma unroll
-            for (int c = 0; c < W; ++c)
-                *reinterpret_cast<uint4 *>(dst + c * Vec16<T>::N) = raw[n][c];
+        if (NR == 1 || r + 1 == rows) break;
+        qin += a.q_stride;
+        kin += a.k_stride;
+        vin += a.v_stride;
+        qout += nq * DH;
+        kout += a.Hkv * DH;
+        vout += a.Hkv * DH;
+        load();
     }
 }
 
@@ -288,7 +304,6 @@ cudaError_t launch_qk_norm_rope(medusa_dtype dtype, const void *q, const void *k
     a.kw = k_weight;
     a.eps = eps;
     a.norm = norm;
-    a.interleaved = interleaved;
     a.pos = pos;
     a.inv_freq = inv_freq;
     a.rot = rot;
@@ -306,19 +321,23 @@ cudaError_t launch_qk_norm_rope(medusa_dtype dtype, const void *q, const void *k
     const int nv = H + Hkv + (k_cache ? Hkv : 0);
     const long long rows = (long long)B * R;
     const int vpp = kRopeThreads / (dh / 8);
-    // With few rows one pass per CTA puts more CTAs to work; with enough of them
-    // four passes share a row's angles and keep four loads a lane in flight.
+    // With few rows one row and pass per CTA puts more CTAs to work; with enough of
+    // them four passes keep four loads a lane in flight, over four rows.
     const int passes = (nv + vpp - 1) / vpp;
     const bool many = rows * passes >= 16LL * device_sm_count();
-    auto pick = [&](auto one, auto four) { return many ? four : one; };
-    auto kern =
-        dtype == MEDUSA_F32
-            ? (dh == 128 ? pick(qk_norm_rope_kernel<float, 128, 1>, qk_norm_rope_kernel<float, 128, 4>)
-                         : pick(qk_norm_rope_kernel<float, 64, 1>, qk_norm_rope_kernel<float, 64, 4>))
-            : (dh == 128 ? pick(qk_norm_rope_kernel<bf16, 128, 1>, qk_norm_rope_kernel<bf16, 128, 4>)
-                         : pick(qk_norm_rope_kernel<bf16, 64, 1>, qk_norm_rope_kernel<bf16, 64, 4>));
-    const int per_cta = many ? 4 : 1;
-    cudaError_t e = launch_pdl(kern, dim3(R, (passes + per_cta - 1) / per_cta, B),
+    auto of = [&](auto t, auto il) {
+        using T = decltype(t);
+        constexpr bool IL = decltype(il)::value;
+        return dh == 128 ? (many ? qk_norm_rope_kernel<T, 128, kManyPasses, kManyRows, IL>
+                                 : qk_norm_rope_kernel<T, 128, 1, 1, IL>)
+                         : (many ? qk_norm_rope_kernel<T, 64, kManyPasses, kManyRows, IL>
+                                 : qk_norm_rope_kernel<T, 64, 1, 1, IL>);
+    };
+    auto kern = dtype == MEDUSA_F32 ? (interleaved ? of(float{}, std::true_type{}) : of(float{}, std::false_type{}))
+                                    : (interleaved ? of(bf16{}, std::true_type{}) : of(bf16{}, std::false_type{}));
+    const int per_cta = many ? kManyPasses : 1;
+    cudaError_t e = launch_pdl(kern, dim3(many ? (R + kManyRows - 1) / kManyRows : R,
+                                    (passes + per_cta - 1) / per_cta, B),
                                dim3(kRopeThreads), 0, stream, a);
     note_launch();
     return e;
