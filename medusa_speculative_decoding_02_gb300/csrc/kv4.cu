@@ -1,12 +1,16 @@
 // kv4.cu -- rows into and out of the 4-bit cache (layout: kv4.cuh).
 //
-// kv4_append_kernel: one thread per block of 16 elements of K or V (kItems
-// blocks a CTA's width apart, their loads issued together): it picks the scale
-// and the codes and stores eight bytes of codes and one scale byte.
+// kv4_append_kernel: one thread per block of 16 elements of K or V: it picks the
+// scale and the codes and stores eight bytes of codes and one scale byte.
 // Consecutive threads take consecutive blocks of a sequence's rows, K's then
 // V's, so both stores of a warp are contiguous.  kv4_unpack_kernel is the
-// inverse.  Both are bound by the bytes they move (per element 2 or 4 bytes on
-// the wide side and 9/16 on the narrow one).
+// inverse.  They move 2 or 4 bytes an element on the wide side and 9/16 on the
+// narrow one, and are bound by issue (append) and by the latency of two dependent
+// rounds of loads (unpack).  Four ragged bf16 prompts of up to 4001 rows of 8 x 128
+// elements, appended and read back (115 MB): 25.0 us, 4.6 TB/s; 65 rows of 32 x
+// 128: 4.4 us.  Two blocks a thread gained nothing there and took 5.5 us at the 65
+// rows; with divisions by 6 and by the blocks of a slot, and the largest magnitude
+// taken element by element, the prompts took 27.5 us.
 #include <algorithm>
 
 #include "kv4.cuh"
@@ -17,7 +21,6 @@ namespace medusa {
 namespace {
 
 constexpr int kKv4Threads = 256;
-constexpr int kItems = 2;
 
 struct Kv4Args {
     const void *k, *v;        // wide rows (append: in; unpack: out)
@@ -27,6 +30,7 @@ struct Kv4Args {
     const int32_t *prefix_len;
     const int32_t *n_rows;    // or null: all R
     int R, Hkv, dh, P_max;
+    unsigned per_magic, per_shift;  // division by the blocks of a slot (K and V)
     int *status;
 };
 
@@ -40,7 +44,7 @@ struct Kv4Block {
     int e;  // block within the row
     __device__ __forceinline__ Kv4Block(const Kv4Args &a, int b, unsigned idx, int live) {
         const unsigned per = (unsigned)(a.Hkv * a.dh / 16);  // blocks of a K row, and of a V row
-        const unsigned i = idx / (2 * per);
+        const unsigned i = __umulhi(idx, a.per_magic) >> a.per_shift;
         unsigned blk = idx - i * (2 * per);
         const bool is_v = blk >= per;
         if (is_v) blk -= per;
@@ -69,91 +73,77 @@ __device__ __forceinline__ int kv4_live_rows(const Kv4Args &a, int b) {
     return a.n_rows ? min(a.R, a.n_rows[b]) : a.R;
 }
 
-// grid (blocks of a sequence over kItems * 256, B)
+// grid (blocks of a sequence over 256, B)
 template <typename T>
 __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(Kv4Args a) {
     pdl_enter();
     constexpr int N = Vec16<T>::N, V = 16 / N;
     const int b = blockIdx.y;
-    const int live = kv4_live_rows(a, b);
-    const unsigned first = blockIdx.x * (kItems * kKv4Threads) + threadIdx.x;
-    uint4 raw[kItems][V];
+    const Kv4Block<T> k(a, b, blockIdx.x * kKv4Threads + threadIdx.x, kv4_live_rows(a, b));
+    if (!k.row) return;
+    uint4 raw[V];
 #pragma unroll
-    for (int u = 0; u < kItems; ++u) {
-        const Kv4Block<T> k(a, b, first + u * kKv4Threads, live);
-        if (k.row)
+    for (int c = 0; c < V; ++c) raw[c] = ld_stream16(k.wide + c * N);
+    float x[16];
 #pragma unroll
-            for (int c = 0; c < V; ++c) raw[u][c] = ld_stream16(k.wide + c * N);
+    for (int c = 0; c < V; ++c) {
+        float f[N];
+        Vec16<T>::widen(raw[c], f);
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[c * N + j] = f[j];
     }
-#pragma unroll
-    for (int u = 0; u < kItems; ++u) {
-        const Kv4Block<T> k(a, b, first + u * kKv4Threads, live);
-        if (!k.row) return;  // the blocks after it lie further on
-        float x[16];
+    // the largest magnitude, by its bits: infinities and NaNs come out on top
+    uint32_t top = 0;
+    if constexpr (sizeof(T) == 2) {
 #pragma unroll
         for (int c = 0; c < V; ++c) {
-            float f[N];
-            Vec16<T>::widen(raw[u][c], f);
+            const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
 #pragma unroll
-            for (int j = 0; j < N; ++j) x[c * N + j] = f[j];
+            for (int j = 0; j < 4; ++j) top = __vmaxu2(top, w[j] & 0x7fff7fffu);
         }
-        // the largest magnitude, by its bits: infinities and NaNs come out on top
-        uint32_t top = 0;
+        top = max(top & 0xffff0000u, top << 16);
+    } else {
 #pragma unroll
         for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
-        uint32_t sb = kE4m3Nan, lo = 0, hi = 0;
-        if (top < 0x7f800000u) {
-            sb = kv4_scale_byte(__uint_as_float(top));
-            if (sb) {
-                const float s = e4m3_value(sb);
-                lo = kv4_codes(x, s, T());
-                hi = kv4_codes(x + 8, s, T());
-            }
-        }
-        *reinterpret_cast<uint2 *>(k.row + k.e * 8) = make_uint2(lo, hi);
-        k.row[kv4_code_bytes(a.Hkv, a.dh) + k.e] = (uint8_t)sb;
     }
+    uint32_t sb = kE4m3Nan, lo = 0, hi = 0;
+    if (top < 0x7f800000u) {
+        sb = kv4_scale_byte(__uint_as_float(top));
+        if (sb) {
+            const float s = e4m3_value(sb);
+            lo = kv4_codes(x, s, T());
+            hi = kv4_codes(x + 8, s, T());
+        }
+    }
+    *reinterpret_cast<uint2 *>(k.row + k.e * 8) = make_uint2(lo, hi);
+    k.row[kv4_code_bytes(a.Hkv, a.dh) + k.e] = (uint8_t)sb;
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kKv4Threads) kv4_unpack_kernel(Kv4Args a) {
     pdl_enter();
     const int b = blockIdx.y;
-    const int live = kv4_live_rows(a, b);
-    const unsigned first = blockIdx.x * (kItems * kKv4Threads) + threadIdx.x;
-    uint2 codes[kItems];
-    uint32_t scale[kItems];
+    const Kv4Block<T> k(a, b, blockIdx.x * kKv4Threads + threadIdx.x, kv4_live_rows(a, b));
+    if (!k.row) return;
+    const uint2 codes = *reinterpret_cast<const uint2 *>(k.row + k.e * 8);
+    const __half s = e4m3_half(k.row[kv4_code_bytes(a.Hkv, a.dh) + k.e]);
+    float x[2][8];
+    kv4_widen(codes.x, s, x[0]);
+    kv4_widen(codes.y, s, x[1]);
 #pragma unroll
-    for (int u = 0; u < kItems; ++u) {
-        const Kv4Block<T> k(a, b, first + u * kKv4Threads, live);
-        if (k.row) {
-            codes[u] = *reinterpret_cast<const uint2 *>(k.row + k.e * 8);
-            scale[u] = k.row[kv4_code_bytes(a.Hkv, a.dh) + k.e];
-        }
-    }
+    for (int h = 0; h < 2; ++h) {
+        T *dst = k.wide + 8 * h;
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float4 *>(dst) = make_float4(x[h][0], x[h][1], x[h][2], x[h][3]);
+            *reinterpret_cast<float4 *>(dst + 4) = make_float4(x[h][4], x[h][5], x[h][6], x[h][7]);
+        } else {
+            uint32_t w[4];
 #pragma unroll
-    for (int u = 0; u < kItems; ++u) {
-        const Kv4Block<T> k(a, b, first + u * kKv4Threads, live);
-        if (!k.row) return;
-        const __half s = e4m3_half(scale[u]);
-        float x[2][8];
-        kv4_widen(codes[u].x, s, x[0]);
-        kv4_widen(codes[u].y, s, x[1]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            T *dst = k.wide + 8 * h;
-            if constexpr (sizeof(T) == 4) {
-                *reinterpret_cast<float4 *>(dst) = make_float4(x[h][0], x[h][1], x[h][2], x[h][3]);
-                *reinterpret_cast<float4 *>(dst + 4) = make_float4(x[h][4], x[h][5], x[h][6], x[h][7]);
-            } else {
-                uint32_t w[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const __nv_bfloat162 p = __floats2bfloat162_rn(x[h][2 * c], x[h][2 * c + 1]);
-                    w[c] = *reinterpret_cast<const uint32_t *>(&p);
-                }
-                *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int c = 0; c < 4; ++c) {
+                const __nv_bfloat162 p = __floats2bfloat162_rn(x[h][2 * c], x[h][2 * c + 1]);
+                w[c] = *reinterpret_cast<const uint32_t *>(&p);
             }
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
 }
@@ -179,8 +169,16 @@ cudaError_t launch_kv4_rows(medusa_dtype dtype, bool append, const void *k, cons
     a.dh = dh;
     a.P_max = P_max;
     a.status = static_cast<int *>(ws);
+    // i / d = (i m) >> (32 + s) for all i < 2^30, with 2^s the power of two below d
+    // and m = 2^(32 + s) / d + 1: m is too large by less than one, so i m / 2^(32 + s)
+    // by less than i / 2^(32 + s) < 1 / d
+    const unsigned d = 2u * (unsigned)(Hkv * dh / 16);
+    unsigned s = 0;
+    while ((2u << s) < d) ++s;
+    a.per_shift = s;
+    a.per_magic = (unsigned)((1ull << (32 + s)) / d + 1);
     const unsigned blocks = (unsigned)R * (unsigned)(2 * Hkv * dh / 16);  // < 2^30
-    const unsigned gx = (blocks + kItems * kKv4Threads - 1) / (kItems * kKv4Threads);
+    const unsigned gx = (blocks + kKv4Threads - 1) / kKv4Threads;
     auto kern = append ? (dtype == MEDUSA_F32 ? kv4_append_kernel<float> : kv4_append_kernel<bf16>)
                        : (dtype == MEDUSA_F32 ? kv4_unpack_kernel<float> : kv4_unpack_kernel<bf16>);
     cudaError_t e = launch_pdl(kern, dim3(gx, B), dim3(kKv4Threads), 0, stream, a);

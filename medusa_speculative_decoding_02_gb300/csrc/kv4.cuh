@@ -70,11 +70,11 @@ __device__ __forceinline__ __half e4m3_half(uint32_t byte) {
 }
 
 // Scale byte of a block whose largest magnitude is `amax` (finite): the e4m3
-// nearest to amax / 6.  The conversion of the rounded quotient can be off by
+// nearest to amax / 6.  The conversion of the rounded product can be off by
 // one step next to a midpoint m; comparing amax with 6 m, which is exact
 // (m has five significant bits), puts it right.
 __device__ __forceinline__ uint32_t kv4_scale_byte(float amax) {
-    uint32_t c = __nv_cvt_float_to_fp8(amax / 6.f, __NV_SATFINITE, __NV_E4M3);
+    uint32_t c = __nv_cvt_float_to_fp8(amax * (1.f / 6.f), __NV_SATFINITE, __NV_E4M3);
     const float v = e4m3_value(c);
     if (c > 0) {
         const float lo6 = 3.f * (e4m3_value(c - 1) + v);  // six times the midpoint below
@@ -99,10 +99,13 @@ __device__ __forceinline__ uint32_t kv4_code(float x, float s) {
 
 // The codes of eight elements.  For bf16 elements the hardware's conversion of
 // y = x * (1/s) serves: a bf16 x (eight bits) is either exactly a midpoint
-// times s (seven bits at most) or off it by a relative 2^-8, and y, off by
-// 2^-23, is rounded to 16 bits first, which puts the exact ties back on the
-// midpoints and moves nothing across one.  fp32 elements can lie closer to a
-// midpoint than that, so they are compared (14 instructions each against 4).
+// times s (seven bits at most) or off it by a relative 2^-8, at least 2^-10 of y
+// as the midpoints begin at 1/4; y, off by a relative 2^-22, is rounded to a
+// multiple of 2^-13 first (by adding and taking away 3 * 2^9), which puts the exact
+// ties back on the midpoints and moves nothing across one.  The sign is kept, so
+// that a negative x near 0 gives -0; a -0 itself became +0 in the first product.
+// fp32 elements can lie closer to a midpoint, so they are compared (14
+// instructions each against 3).
 __device__ __forceinline__ uint32_t kv4_codes(const float *x, float s, float) {
     uint32_t w = 0;
 #pragma unroll
@@ -110,12 +113,18 @@ __device__ __forceinline__ uint32_t kv4_codes(const float *x, float s, float) {
     return w;
 }
 __device__ __forceinline__ uint32_t kv4_codes(const float *x, float s, bf16) {
-    const float inv = 1.f / s;
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));  // within one unit in the last place
+    const float2 i2 = make_float2(inv, inv), zero = make_float2(0.f, 0.f), big = make_float2(1536.f, 1536.f),
+                 less = make_float2(-1536.f, -1536.f);
     float y[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        // (the + 0 makes a -0 a +0)
-        y[j] = __uint_as_float((__float_as_uint(fmaf(x[j], inv, 0.f)) + 0x80u) & 0xffffff00u);
+    for (int j = 0; j < 8; j += 2) {
+        const float2 q = __ffma2_rn(make_float2(x[j], x[j + 1]), i2, zero);
+        const float2 r = __fadd2_rn(__fadd2_rn(q, big), less);
+        y[j] = copysignf(r.x, q.x);
+        y[j + 1] = copysignf(r.y, q.y);
+    }
     uint32_t w;
     asm("{\n.reg .b8 b0, b1, b2, b3;\n"
         "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
