@@ -695,7 +695,8 @@ MEDUSA_API medusa_status medusa_tree_attention_window(
  *       (window = 0: the whole prefix); q and out are dtype.  The values
  *       enter the products exactly; bf16 q is scaled by a power of two for
  *       each row into fp16, where its elements keep their eight bits down to
- *       2^-14 of the row's largest.
+ *       2^-14 of the row's largest, and weights below 2^-32 of the row's
+ *       largest so far may be dropped.
  * A prefix outside 0..P_max or a bad cache pointer sets the status and leaves
  * that sequence untouched (attention: zeros).  Requirements: dh in {64,128};
  * append and unpack: R <= 65535; attention and commit: R <= 256.  Workspace of

@@ -31,9 +31,11 @@
 //
 // Bound by the bytes for a bf16 cache: eight sequences x 32 KV heads x 8192 slots
 // (1.07 GB) in 148 us, 7.2 TB/s; eight single tokens behind a 2047 window (69 MB)
-// in 11.3 us, 6.1 TB/s.  A 4-bit cache takes about 380 instructions a tile of 16
-// keys, of which 64 conversions, 64 products with scales and 16 matrix
-// instructions, so it is bound by issue: 186 MB in 46.8 us, 4.0 TB/s.
+// in 16.4 us with a cold L2, 11.3 us with the rows in it, of which the second launch,
+// the join, is 2-3 us.  A 4-bit cache takes some 330 instructions a tile of 16 keys, of
+// which 64 conversions, 64 products with scales and 16 matrix instructions, and is
+// bound by issue and the latency of that chain (57 % of the issue slots at 12 warps
+// an SM): 186 MB in 46.9 us, 4.0 TB/s.
 #include "cache_attention.cuh"
 
 namespace medusa {

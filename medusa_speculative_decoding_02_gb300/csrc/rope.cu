@@ -23,9 +23,10 @@
 //
 // Bound by issue and, close behind, by the bytes of q, K and V read and written
 // once; the loads of a row are issued before its angles are computed.  6626 rows
-// of 32 + 8 + 8 vectors of 128 (160 MB) take 31.3 us, 5.1 TB/s; one row a CTA took
-// 41.2 (40.7 M instructions where four rows a CTA had 29.8 M).  65 rows of 32 + 32
-// + 32 vectors 3.0 us, eight rows of 32 + 8 1.9 us: latency of two rounds of loads.
+// of 32 + 8 + 8 vectors of 128 (159 MB) take 32.9 us, 4.8 TB/s (31.4 us back to
+// back); one row a CTA took 41.2 (40.7 M instructions a launch where four rows a
+// CTA had 29.8 M).  65 rows of 32 + 32 + 32 vectors take 3.0 us, eight rows of
+// 32 + 8 1.9 us: the latency of two rounds of loads.
 #include <algorithm>
 
 #include "common.cuh"
@@ -321,8 +322,10 @@ cudaError_t launch_qk_norm_rope(medusa_dtype dtype, const void *q, const void *k
     const int nv = H + Hkv + (k_cache ? Hkv : 0);
     const long long rows = (long long)B * R;
     const int vpp = kRopeThreads / (dh / 8);
-    // With few rows one row and pass per CTA puts more CTAs to work; with enough of
-    // them four passes keep four loads a lane in flight, over four rows.
+    // With few rows one row and pass per CTA puts more CTAs to work (65 rows of 96
+    // vectors: 3.0 us); with enough of them three passes over four rows share what
+    // comes before the first vector (the prompt above: 31.4 us; with two passes
+    // 39.1, with two rows 31.8).
     const int passes = (nv + vpp - 1) / vpp;
     const bool many = rows * passes >= 16LL * device_sm_count();
     auto of = [&](auto t, auto il) {
