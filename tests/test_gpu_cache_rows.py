@@ -1,15 +1,16 @@
-"""Attention over the caches at the row counts where its kernels change (rows a
-KV head has: up to 8, up to 16, more) against a 64-bit reference, with the
-tolerances of test_gpu_cache_ops."""
+"""The cache operators at the sizes where their kernels change, against a 64-bit
+reference with the tolerances of test_gpu_cache_ops: attention by the rows a
+KV head has (up to 8, up to 16, more), rotation of many rows, 4-bit rows of every
+size of element."""
 import math
 
-import numpy as np
 import pytest
 import torch
 
 import cache_ops_ref as ref
 import medusa_speculative_decoding_02_gb300 as m
-from test_gpu_cache_ops import BF, attn_inputs, call_attn, check_attn, dev, status  # noqa: F401 (dev: fixture)
+from test_gpu_cache_ops import (BF, attn_inputs, call_attn, check_attn, check_rope, dev, inv_freqs, np64,  # noqa: F401
+                                randn, status)
 
 pytestmark = pytest.mark.gpu
 
@@ -189,3 +190,97 @@ def test_single_tokens_on_a_side_stream_replayed_and_repeated(dev, kv4, window):
     g.replay()
     torch.cuda.synchronize()
     check_attn(out, a, window, 3 if window else 0, kv4=kv4)
+
+
+# Enough rows that a CTA takes several of them, numbers of rows that do not fill
+# the last CTA, vectors that fill one group of passes, more, and a part.
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("B,R,H,Hkv,dh,rot,rows", [
+    (2, 1303, 3, 1, 64, 64, [1303, 1102]), (3, 822, 3, 1, 128, 32, [821, 1, 0]),
+    (1, 701, 40, 5, 128, 96, [698]), (1, 2500, 1, 1, 64, 0, [2500])])
+def test_rotation_of_many_rows(dev, dtype, inter, B, R, H, Hkv, dh, rot, rows):
+    """Slices of a projection, ragged, with norms: to dense outputs, in place, and
+    with K and V into their slots; rows past a sequence's stay as they were."""
+    g = torch.Generator().manual_seed(R)
+    qkv = randn(g, B, R, H + 2 * Hkv, dh, dtype=dtype)
+    q, k, v = qkv[:, :, :H], qkv[:, :, H:H + Hkv], qkv[:, :, H + Hkv:]
+    qw, kw = (1 + 0.3 * randn(g, dh)).to(dtype), (1 + 0.3 * randn(g, dh)).to(dtype)
+    pos = torch.randint(0, 100000, (B, R), generator=g, dtype=torch.int32)
+    f, x = inv_freqs(rot), qkv.to(dev)
+    dq, dk, dv = x[:, :, :H], x[:, :, H:H + Hkv], x[:, :, H + Hkv:]
+    kw_ = dict(q_weight=qw.to(dev), k_weight=kw.to(dev), eps=1e-5, interleaved=inter,
+               n_rows=torch.tensor(rows, dtype=torch.int32, device=dev))
+    out = tuple(torch.full((B, R, h, dh), 7.0, dtype=dtype, device=dev) for h in (H, Hkv))
+    qo, ko = m.qk_norm_rope(dq, dk, pos.to(dev), f.to(dev), out=out, **kw_)
+    check_rope(qo, q, pos, f, qw, 1e-5, True, inter, rows)
+    check_rope(ko, k, pos, f, kw, 1e-5, True, inter, rows)
+    prefix = [5 + 3 * b for b in range(B)]
+    P = torch.tensor(prefix, dtype=torch.int32, device=dev)
+    kc = [torch.full((max(prefix) + R, Hkv, dh), 3.0, dtype=dtype, device=dev) for _ in range(B)]
+    vc = [c.clone() for c in kc]
+    ws = m.new_workspace(256)
+    q2 = m.qk_norm_rope_append(dq, dk, dv, pos.to(dev), f.to(dev), m.cache_pointers(kc, dev),
+                               m.cache_pointers(vc, dev), P, max(prefix), ws=ws, **kw_)
+    qd, kd = dq.contiguous(), dk.contiguous()
+    m.qk_norm_rope(qd, kd, pos.to(dev), f.to(dev), out=(qd, kd), **kw_)
+    for b, r in enumerate(rows):
+        p = prefix[b]
+        assert (qo[b, r:] == 7).all() and (ko[b, r:] == 7).all()
+        assert torch.equal(q2[b, :r], qo[b, :r]) and torch.equal(kc[b][p:p + r], ko[b, :r])
+        assert torch.equal(vc[b][p:p + r], dv[b, :r])
+        for c in (kc[b], vc[b]):
+            assert (c[:p] == 3).all() and (c[p + r:] == 3).all()
+        assert torch.equal(qd[b, :r], qo[b, :r]) and torch.equal(kd[b, :r], ko[b, :r])
+        assert torch.equal(qd[b, r:], dq[b, r:]) and torch.equal(kd[b, r:], dk[b, r:])
+    assert status(ws) == "ok"
+
+
+def test_rotation_of_many_rows_leaves_bad_sequences_alone(dev):
+    B, R, H, dh = 3, 900, 2, 64
+    g = torch.Generator().manual_seed(2)
+    x = randn(g, B, R, H, dh, dtype=BF).to(dev)
+    pos, f = torch.zeros(B, R, dtype=torch.int32, device=dev), inv_freqs(64).to(dev)
+    kc = [torch.zeros(R + 9, H, dh, dtype=BF, device=dev) for _ in range(B)]
+    vc = [c.clone() for c in kc]
+    for P, bad, name in (([4, 10, 9], 1, "bad prefix"), ([4, -1, 9], 1, "bad prefix"), ([4, 5, 9], 2, "bad cache")):
+        ws = m.new_workspace(256)
+        kp = m.cache_pointers(kc, dev)
+        if name == "bad cache":
+            kp[bad] = 0
+        for c in kc + vc:
+            c.zero_()
+        out = torch.full((B, R, H, dh), 7.0, dtype=BF, device=dev)
+        m.qk_norm_rope_append(x, x, x, pos, f, kp, m.cache_pointers(vc, dev),
+                              torch.tensor(P, dtype=torch.int32, device=dev), 9, norm=False, out=out, ws=ws)
+        assert status(ws) == name and (out[bad] == 7).all() and not kc[bad].any() and not vc[bad].any()
+        for b in {0, 1, 2} - {bad}:
+            assert torch.equal(out[b], x[b]) and torch.equal(vc[b][P[b]:P[b] + R], x[b])
+
+
+@pytest.mark.parametrize("Hkv,dh", [(1, 64), (3, 64), (5, 128), (7, 128)])
+def test_4bit_rows_of_every_size_of_element(dev, Hkv, dh):
+    """Blocks from the smallest to the largest bf16 magnitudes, ties and values next
+    to ties, bit for bit, rows of an odd number of blocks."""
+    g = torch.Generator().manual_seed(Hkv)
+    R = 301
+    x = randn(g, 1, R, Hkv, dh)
+    x *= torch.pow(2.0, torch.randint(-20, 20, (1, R, Hkv, dh // 16), generator=g).float()).repeat_interleave(16, 3)
+    k = x.to(BF)
+    # the midpoints between codes times a scale, a step above and below, both signs
+    s = torch.tensor([2.0 ** -6, 0.3125, 1.0, 1.875, 448.0])
+    mid = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    row = 0
+    for sc in s:
+        for e in (-1, 0, 1):
+            t = ((mid * sc).to(BF).view(torch.int16) + e).view(BF)
+            k[0, row, 0, :16] = torch.cat([(6 * sc).to(BF)[None], t, -t, torch.tensor([-0.0], dtype=BF)])
+            row += 1
+    kd = k.to(dev)
+    cap = [torch.zeros(R, m.kv4_row_bytes(Hkv, dh), dtype=torch.uint8, device=dev) for _ in range(2)]
+    P = torch.zeros(1, dtype=torch.int32, device=dev)
+    m.kv4_append(kd, -kd, m.cache_pointers(cap[:1], dev), m.cache_pointers(cap[1:], dev), P, 0,
+                 ws=m.new_workspace(256))
+    used = Hkv * dh * 9 // 16
+    for c, y in zip(cap, (k, -k)):
+        assert (c.cpu().numpy()[:, :used] == ref.pack_rows(np64(y)[0])[:, :used]).all()
