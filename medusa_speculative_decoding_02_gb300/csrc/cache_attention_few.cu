@@ -3,10 +3,10 @@
 //
 // Such a call reads the cache once and computes little, and the 128-row tiles
 // of the other kernel spend their time on passing stages between warps.  Here
-// every warp is on its own: it takes 16 keys at a time from global memory into
-// registers, already in the lane layout of the matrix instruction, so that
-// neither shared memory nor a barrier lies between the cache and the product
-// until the warps of a CTA join at the end.
+// every warp is on its own: it copies 16 keys at a time into a ring of its own and
+// reads them from there in the lane layout of a matrix instruction whose operands
+// are registers, so that no barrier lies between the cache and the product until
+// the warps of a CTA join at the end.
 //
 // Keys are the 16 rows of the instruction, query rows its 8 columns:
 //     S^T = K Q^T   (16 keys x 8 rows, over dh in steps of 16)
