@@ -599,9 +599,10 @@ def _ws_args(ws, dev: int):
 def _rows(t: torch.Tensor, name: str):
     """Row stride in elements of [B,R,heads,dh] rows: heads and dh dense, all
     rows evenly apart (a dense tensor, or a slice of a wider projection)."""
-    if t.dim() != 4:
+    shape = t.shape
+    if len(shape) != 4:
         raise ValueError(f"{name} must be [B,R,heads,dh]")
-    B, R, H, dh = t.shape
+    B, R, H, dh = shape
     if t.is_contiguous():
         return H * dh
     s = t.stride()
@@ -634,10 +635,11 @@ def _new(stream, like: torch.Tensor, shape=None, dtype=None):
 
 
 def _rope_args(q, k, q_weight, k_weight, dev):
-    if k.dtype is not q.dtype or k.get_device() != dev or k.dim() != 4 or q.dim() != 4 \
-            or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3]:
+    qs, ks = q.shape, k.shape
+    if k.dtype is not q.dtype or k.get_device() != dev or len(ks) != 4 or len(qs) != 4 \
+            or ks[0] != qs[0] or ks[1] != qs[1] or ks[3] != qs[3]:
         raise ValueError("q must be [B,R,H,dh] and k [B,R,Hkv,dh] of the same dtype and device")
-    dh = q.shape[3]
+    dh = qs[3]
     return (None if q_weight is None else _vec(q_weight, dh, q.dtype, dev, "q_weight"),
             None if k_weight is None else _vec(k_weight, dh, q.dtype, dev, "k_weight"))
 

@@ -4,6 +4,7 @@ KV head has (up to 8, up to 16, more), rotation of many rows, 4-bit rows of ever
 size of element."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -284,3 +285,41 @@ def test_4bit_rows_of_every_size_of_element(dev, Hkv, dh):
     used = Hkv * dh * 9 // 16
     for c, y in zip(cap, (k, -k)):
         assert (c.cpu().numpy()[:, :used] == ref.pack_rows(np64(y)[0])[:, :used]).all()
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+@pytest.mark.parametrize("R", [1, 17])
+def test_slots_past_four_gigabytes(dev, kv4, R):
+    """Rows written and read behind byte 2^32 of a cache: what the same calls give
+    in a small one (a window without sinks only sees differences of positions)."""
+    B, H, dh, window, near = 1, 256, 128, 100, 150
+    row = m.kv4_row_bytes(H, dh) if kv4 else H * dh * 2
+    P = 2 ** 32 // row + 300
+    g = torch.Generator().manual_seed(R)
+    q = randn(g, B, R, H, dh, dtype=BF).to(dev)
+    k, v = (randn(g, B, near + R, H, dh, dtype=BF).to(dev) for _ in range(2))
+    mask, depth = ref.tree(B, R, np.random.RandomState(R))
+    outs, stored = [], []
+    for prefix in (near, P):
+        slots = prefix + near + R
+        c = [m.kv4_cache(slots, H, dh, device=dev) if kv4
+             else torch.zeros(slots, H, dh, dtype=BF, device=dev) for _ in range(2)]
+        kp, vp = m.cache_pointers(c[:1], dev), m.cache_pointers(c[1:], dev)
+        start = torch.tensor([prefix - near], dtype=torch.int32, device=dev)
+        n = torch.tensor([prefix], dtype=torch.int32, device=dev)
+        if kv4:
+            m.kv4_append(k, v, kp, vp, start, prefix)
+            back = m.kv4_unpack(kp, vp, start, prefix, near + R, H, dh)
+        else:
+            m.qk_norm_rope_append(k, k, v, torch.zeros(B, near + R, dtype=torch.int32, device=dev),
+                                  inv_freqs(dh).to(dev), kp, vp, start, prefix, norm=False)
+            back = (c[0][prefix - near:prefix + R][None], c[1][prefix - near:prefix + R][None])
+        fn = m.tree_attention_kv4 if kv4 else m.tree_attention_window
+        outs.append(fn(q, kp, vp, n, prefix, mask.to(dev), H, depth=depth.to(dev), window=window))
+        stored.append([x.clone() for x in back])
+        assert prefix == near or (prefix - near) * row > 2 ** 32
+        del c, back
+    assert torch.equal(outs[0], outs[1]) and outs[0].any() and torch.isfinite(outs[0]).all()
+    for x, y in zip(*stored):
+        assert torch.equal(x, y) and x.any()
+    torch.cuda.empty_cache()
