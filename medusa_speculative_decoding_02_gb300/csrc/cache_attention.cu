@@ -422,7 +422,11 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
     volatile int *o_started = failed + 1;                        // O holds something before stage 0
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(sm + L::WORDS + 8);
     int *warp_depth = reinterpret_cast<int *>(sm + L::WORDS + 16);       // [4]
-    uint32_t *bad_keys = reinterpret_cast<uint32_t *>(sm + L::WORDS + 32);  // [2]
+    // Keys of a stage whose V is not finite, a pair of words for each parity of the
+    // stage: a warp may mark the next stage's keys while thread 0 still clears
+    // this one's.  The pair's next use, two stages on, follows thread 0's arrival
+    // on bar_sfree after the clearing.
+    uint32_t *bad_keys = reinterpret_cast<uint32_t *>(sm + L::WORDS + 32);  // [2][2]
 
     const int g = blockIdx.x / a.row_tiles, rt = blockIdx.x - g * a.row_tiles;
     const int R = a.R, G = a.H / a.Hkv, M = R * G;
@@ -471,7 +475,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
         tc::mbar_init(bar_drain, 1);
         *failed = 0;
         *o_started = 0;
-        bad_keys[0] = bad_keys[1] = 0;
+        bad_keys[0] = bad_keys[1] = bad_keys[2] = bad_keys[3] = 0;
         tc::fence_mbarrier_init();
     }
     if (warp == 8) tc::tmem_alloc(tmem_holder, 256);
@@ -794,6 +798,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
             if (masked) {
                 // ---- infinities and NaNs in V of a stage that some row does not see
                 unsigned char *vt = slot_of(v_tile(j, nsub));
+                uint32_t *bad_now = bad_keys + 2 * (j & 1);
                 if (!dead) dead = !wait_full(v_tile(j, nsub));
                 // thread t scans half a key row: 128-byte rows t, t + 128, ... of the tile
                 bool bad = false;
@@ -806,7 +811,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
                             if (pair_bad<KV4>(w.x) || pair_bad<KV4>(w.y) || pair_bad<KV4>(w.z) ||
                                 pair_bad<KV4>(w.w)) {
                                 bad = true;
-                                atomicOr(bad_keys + ((row & 63) >> 5), 1u << (row & 31));
+                                atomicOr(bad_now + ((row & 63) >> 5), 1u << (row & 31));
                             }
                         }
                 if (softmax_any(bad)) {
@@ -825,7 +830,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
                     if (!dead && rows_live) {
 #pragma unroll 1
                         for (int key = 0; key < kSub; ++key) {
-                            if (!((bad_keys[key >> 5] >> (key & 31)) & 1u)) continue;
+                            if (!((bad_now[key >> 5] >> (key & 31)) & 1u)) continue;
                             const float p = half_of_pair<KV4>(*reinterpret_cast<const uint16_t *>(
                                 p_row + tc::sw128(tid, key >> 3) + (key & 7) * 2), 0);
 #pragma unroll 1
@@ -848,7 +853,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
                                 uint16_t *e = reinterpret_cast<uint16_t *>(vt + row * 128) + c;
                                 if (pair_bad<KV4>(*e)) *e = 0;
                             }
-                    if (tid == 0) bad_keys[0] = bad_keys[1] = 0;
+                    if (tid == 0) bad_now[0] = bad_now[1] = 0;
                     tc::fence_proxy_async_smem();
                 }
             }

@@ -1,0 +1,65 @@
+"""The cache operators where two stages, two streams or the ends of a type meet,
+against a 64-bit reference with the tolerances of test_gpu_cache_ops."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import cache_ops_ref as ref
+import medusa_speculative_decoding_02_gb300 as m
+from test_gpu_cache_ops import BF, attn_inputs, call_attn, check_attn, dev  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def pack_mask(bits):
+    """bool [B,R,R] as the words of anc_mask, int64 [B,R,W]."""
+    B, R = bits.shape[:2]
+    full = np.zeros((B, R, (R + 63) // 64 * 64), bool)
+    full[..., :R] = bits
+    return torch.from_numpy(np.packbits(full, axis=-1, bitorder="little").view(np.int64))
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("R,G,prefix", [(32, 1, 50), (24, 1, 45), (129, 1, 0), (200, 1, 40), (256, 1, 0),
+                                        (65, 4, 40), (150, 2, 17)])
+def test_infinities_in_adjacent_stages(dev, kv4, dh, R, G, prefix):
+    """Whole V rows that are not finite in several adjacent stages of 64 keys, all
+    partly visible: even rows see the first stage's, odd rows a single one of the
+    second or the third (or none).  More than 16 rows a KV head and at most six
+    stages: one CTA works through all of them."""
+    B, Hkv = 2, 4
+    a = attn_inputs(B, R, G * Hkv, Hkv, dh, [prefix] * B, BF, kv4, dev, seed=R + prefix, slack=0)
+    rs = np.random.RandomState(R)
+    stage = (prefix + np.arange(R)) // 64
+    stages = sorted(set(stage))
+    assert len(stages) >= 2
+    first = np.flatnonzero(stage == stages[0])[:32]
+    single = [np.flatnonzero(stage == s)[-1] for s in stages[1:3]]
+    bits = rs.rand(B, R, R) < 0.3
+    bits[:, :, first] = False
+    bits[:, :, single] = False
+    bits[:, 0::2, first[0]] = True
+    for i, t in enumerate(single):
+        bits[:, 1 + 2 * i::2 * (len(single) + 1), t] = True
+    a["mask"] = pack_mask(bits)
+    for b in range(B):
+        for t in [*first, *single]:
+            s, value = prefix + int(t), math.nan if kv4 or t in first else -math.inf
+            if kv4:
+                a["vc"][b][s, Hkv * dh // 2:Hkv * dh // 2 + Hkv * dh // 16] = 0x7f
+            else:
+                a["vc"][b][s] = value
+            a["vs"][b][s] = value
+    ws = m.new_workspace(m.tree_attention_window_workspace_size(m.BF16, B, R, G * Hkv, Hkv, dh, prefix,
+                                                                kv4=kv4))
+    assert ws.numel() == m.WS_HEADER  # a single range
+    got = call_attn(a, 0, 0, Hkv, kv4, dev, ws=ws)
+    check_attn(got, a, 0, 0, kv4=kv4)
+    plain = torch.from_numpy(~bits[:, :, [*first, *single]].any(2)).to(dev)
+    assert plain.any() and torch.isfinite(got[plain]).all()
+    for _ in range(30):
+        again = call_attn(a, 0, 0, Hkv, kv4, dev, ws=ws)
+        assert torch.equal(torch.nan_to_num(again, 7.0, 8.0, 9.0), torch.nan_to_num(got, 7.0, 8.0, 9.0))
