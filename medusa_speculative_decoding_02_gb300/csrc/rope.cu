@@ -63,12 +63,22 @@ struct RopeArgs {
 template <typename T>
 using Piece = typename std::conditional<sizeof(T) == 2, uint2, uint4>::type;
 
+// Plain loads that leave no line in L1: outputs may be the inputs (q_out = q), and
+// the read-only path is for data that nothing writes during the kernel.  Every
+// piece is read by the lane that overwrites it, before it does.
 __device__ __forceinline__ uint2 ld_piece(const bf16 *p) {
     uint2 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p) : "memory");
     return r;
 }
-__device__ __forceinline__ uint4 ld_piece(const float *p) { return ld_stream16(p); }
+__device__ __forceinline__ uint4 ld_piece(const float *p) {
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p)
+                 : "memory");
+    return r;
+}
 
 // element i of the lane's eight (lo: the first four, hi: the others)
 __device__ __forceinline__ void widen(const uint2 &lo, const uint2 &hi, float (&x)[8]) {
