@@ -601,6 +601,9 @@ MEDUSA_API void medusa_step_destroy(medusa_step_exec *exec);
  * for the pairs (a, b) = (j, j + rot/2), or (2j, 2j+1) if interleaved;
  * elements from rot on are not rotated.  Angles are exact to about 2^-25 of a
  * turn at every position.
+ * The mean is taken in fp32: elements up to 2^60 in magnitude (past it the sum
+ * may be infinite, and the vector then comes out as zeros), and with eps = 0 a
+ * root mean square of at least 2^-60.
  *
  *   q [B,R,H,dh], k [B,R,Hkv,dh] dtype; consecutive rows lie q_stride and
  *            k_stride elements apart (H*dh and Hkv*dh when dense; more when

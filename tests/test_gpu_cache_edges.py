@@ -8,7 +8,7 @@ import torch
 
 import cache_ops_ref as ref
 import medusa_speculative_decoding_02_gb300 as m
-from test_gpu_cache_ops import BF, attn_inputs, call_attn, check_attn, dev  # noqa: F401
+from test_gpu_cache_ops import BF, attn_inputs, call_attn, check_attn, check_rope, dev, inv_freqs, randn  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +63,34 @@ def test_infinities_in_adjacent_stages(dev, kv4, dh, R, G, prefix):
     for _ in range(30):
         again = call_attn(a, 0, 0, Hkv, kv4, dev, ws=ws)
         assert torch.equal(torch.nan_to_num(again, 7.0, 8.0, 9.0), torch.nan_to_num(got, 7.0, 8.0, 9.0))
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("R", [20, 3000])
+def test_norms_over_the_whole_range_of_the_type(dev, dtype, dh, inter, R):
+    """Rows of every magnitude that the header allows: with eps 0 from 2^-60 to 2^60,
+    with an eps every smaller one as well; infinities and NaNs stay in their vector."""
+    g = torch.Generator().manual_seed(dh)
+    for eps, least in ((0.0, -57), (1e-30, -110), (1e-6, -110)):
+        size = torch.linspace(least, 57, R).round()
+        q = randn(g, 1, R, 3, dh).double() * torch.exp2(size.double())[None, :, None, None]
+        q[0, :, 1] = randn(g, R, dh)  # an ordinary vector beside
+        q[0, 9, 2] = 0
+        q[0, 9, 2, 5] = 2.0 ** 60
+        q = q.to(dtype)
+        pos, f = torch.arange(R, dtype=torch.int32)[None], inv_freqs(dh)
+        w = (1 + 0.3 * randn(g, dh)).to(dtype)
+        qo, ko = m.qk_norm_rope(q.to(dev), q.to(dev), pos.to(dev), f.to(dev), q_weight=w.to(dev), eps=eps,
+                                interleaved=inter)
+        check_rope(qo, q, pos, f, w, eps, True, inter)
+        check_rope(ko, q, pos, f, None, eps, True, inter)
+    bad = q.clone()
+    bad[0, 8, 0, 1], bad[0, 8, 2, 3] = math.inf, math.nan
+    got, _ = m.qk_norm_rope(bad.to(dev), q.to(dev), pos.to(dev), f.to(dev), q_weight=w.to(dev), eps=eps,
+                            interleaved=inter)
+    assert torch.isnan(got[0, 8, 0, 1]) and torch.isnan(got[0, 8, 2]).all()
+    rest = torch.ones(1, R, 3, dtype=torch.bool, device=dev)
+    rest[0, 8, 0] = rest[0, 8, 2] = False
+    assert torch.equal(got[rest], qo[rest])
