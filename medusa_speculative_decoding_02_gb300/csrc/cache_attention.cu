@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
             tc::mbar_arrive(bar_q);
         }
         // ---- what this row sees, in numbered keys
-        const int my_depth = a.window ? row_depth(a, b, r) : 0;
+        const int my_depth = row_depth(a, b, r);
         int dmax = 0;
         uint64_t am[4] = {0, 0, 0, 0};
         const int x_tree = run.n_sink + P - run.lo;  // number of tree slot 0
@@ -1062,7 +1062,7 @@ cudaError_t launch_cache_attention(medusa_dtype dtype, bool kv4, const void *q,
     a.vc = v_cache;
     a.prefix_len = prefix_len;
     a.anc_mask = anc_mask;
-    a.depth = p.window ? depth : nullptr;
+    a.depth = window ? depth : nullptr;  // checked also where no slot falls out of the window
     a.B = B;
     a.R = R;
     a.H = H;

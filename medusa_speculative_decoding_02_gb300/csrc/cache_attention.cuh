@@ -15,9 +15,9 @@ struct CacheAttnArgs {
     const void *const *vc;
     const int32_t *prefix_len;
     const uint64_t *anc_mask;
-    const int32_t *depth;  // null without a window
+    const int32_t *depth;  // null in calls without a window
     int B, R, H, Hkv, P_max;
-    int window, sinks;
+    int window, sinks;     // 0, 0 where no slot falls out of the window
     int ns, row_tiles;
     float scale_log2;
     uint32_t wait_polls;   // poll limit of the tensor-core path's waits

@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<KV4, NQ>) cache_attn_few
         uint64_t am = 0;
         int win = 0, far = 0;
         if (tid < M) {
-            const int r = tid / G, d = a.window ? row_depth(a, b, r) : 0;
+            const int r = tid / G, d = row_depth(a, b, r);
             am = a.anc_mask[(size_t)b * R + r];  // R <= 16: one word
             if (a.window) {
                 far = max(0, P + d - a.window + 1 - run.lo);

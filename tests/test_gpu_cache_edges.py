@@ -8,7 +8,8 @@ import torch
 
 import cache_ops_ref as ref
 import medusa_speculative_decoding_02_gb300 as m
-from test_gpu_cache_ops import BF, attn_inputs, call_attn, check_attn, check_rope, dev, inv_freqs, randn  # noqa: F401
+from test_gpu_cache_ops import (BF, attn_inputs, call_attn, check_attn, check_rope, dev, inv_freqs, randn,  # noqa: F401
+                                status)
 
 pytestmark = pytest.mark.gpu
 
@@ -94,3 +95,24 @@ def test_norms_over_the_whole_range_of_the_type(dev, dtype, dh, inter, R):
     rest = torch.ones(1, R, 3, dtype=torch.bool, device=dev)
     rest[0, 8, 0] = rest[0, 8, 2] = False
     assert torch.equal(got[rest], qo[rest])
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("kv4", [False, True])
+@pytest.mark.parametrize("R", [3, 20])
+def test_bad_depth_is_reported_behind_every_window(dev, dtype, kv4, R):
+    """A window that no slot falls out of does not use the depths, and reports a bad
+    one all the same; without a window they are not looked at."""
+    a = attn_inputs(2, R, 2, 1, 64, [30, 20], dtype, kv4, dev, seed=3)
+    want = call_attn(a, 0, 0, 1, kv4, dev)
+    fn = m.tree_attention_kv4 if kv4 else m.tree_attention_window
+    args = (a["q"].to(dev), m.cache_pointers(a["kc"], dev), m.cache_pointers(a["vc"], dev),
+            torch.tensor(a["prefix"], dtype=torch.int32, device=dev), a["P_max"], a["mask"].to(dev), 1)
+    for bad in (-1, R):
+        depth = a["depth"].clone()
+        depth[1, R - 1] = bad
+        for window, word in ((0, "ok"), (a["P_max"] + R, "bad depth"), (2 ** 31 - 1, "bad depth")):
+            ws = m.new_workspace(1 << 22)
+            got = fn(*args, depth=depth.to(dev), window=window, ws=ws)
+            assert status(ws) == word, window
+            assert torch.equal(got, want)
