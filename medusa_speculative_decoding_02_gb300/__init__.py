@@ -590,6 +590,13 @@ def _dense(t, shape, dtype, dev: int, name: str):
     return t.data_ptr()
 
 
+def _ints(*values):
+    """Refuses integers past 32 bits, which the foreign call would take modulo 2^32."""
+    for x in values:
+        if not -0x80000000 <= x <= 0x7fffffff:
+            raise ValueError(f"{x} does not fit in 32 bits")
+
+
 def _ws_args(ws, dev: int):
     if ws.get_device() != dev or ws.dtype is not torch.uint8 or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous uint8 tensor on the same device")
@@ -680,6 +687,7 @@ def qk_norm_rope_append(q, k, v, pos, inv_freq, k_ptrs, v_ptrs, prefix_len, P_ma
     qw, kw = _rope_args(q, k, q_weight, k_weight, dev)
     if v.dtype is not k.dtype or v.shape != k.shape or v.get_device() != dev:
         raise ValueError("v must have k's shape, dtype and device")
+    _ints(P_max)
     B, R, H, dh = q.shape
     half = inv_freq.numel()
     if out is None:
@@ -700,6 +708,7 @@ def qk_norm_rope_append(q, k, v, pos, inv_freq, k_ptrs, v_ptrs, prefix_len, P_ma
 
 def kv4_row_bytes(Hkv: int, dh: int) -> int:
     """Bytes of one slot of a 4-bit cache (one of K and V)."""
+    _ints(Hkv, dh)
     return int(lib().medusa_kv4_row_bytes(int(Hkv), int(dh)))
 
 
@@ -719,6 +728,7 @@ def kv4_append(k, v, k_ptrs, v_ptrs, prefix_len, P_max: int, n_rows=None, ws=Non
     dev, st = _launch_on(k, stream)
     if v.dtype is not k.dtype or v.shape != k.shape or v.get_device() != dev:
         raise ValueError("v must have k's shape, dtype and device")
+    _ints(P_max)
     ks, vs = _rows(k, "k"), _rows(v, "v")
     B, R, Hkv, dh = k.shape
     if ws is None:
@@ -736,6 +746,7 @@ def kv4_unpack(k_ptrs, v_ptrs, prefix_len, P_max: int, R: int, Hkv: int, dh: int
     """The values of slots prefix_len[b] + i, i < R, of 4-bit caches: (k, v)
     [B,R,Hkv,dh].  Rows i >= n_rows[b] are left as ``out`` has them."""
     dev, st = _launch_on(k_ptrs, stream)
+    _ints(P_max, R, Hkv, dh)
     B = k_ptrs.numel()
     shape = (B, R, Hkv, dh)
     if out is None:
@@ -757,6 +768,7 @@ def commit_kv4(k_ptrs, v_ptrs, prefix_len, path, accept_len, R: int, Hkv: int, d
                new_prefix_len=None, ws=None, stream=None):
     """commit_kv on 4-bit caches; returns new_prefix_len = P_b + L + 1."""
     dev, st = _launch_on(path, stream)
+    _ints(R, Hkv, dh)
     B, K1 = path.shape
     if new_prefix_len is None:
         new_prefix_len = _new(stream, prefix_len)
@@ -775,6 +787,7 @@ def tree_attention_window_workspace_size(dtype: int, B: int, R: int, H: int, Hkv
                                          P_max: int, window: int = 0, sinks: int = 0,
                                          kv4: bool = False) -> int:
     """Workspace of tree_attention_window, or with kv4 of tree_attention_kv4."""
+    _ints(B, R, H, Hkv, dh, P_max, window, sinks)
     fn = (lib().medusa_tree_attention_kv4_workspace_size if kv4
           else lib().medusa_tree_attention_window_workspace_size)
     return int(fn(dtype, B, R, H, Hkv, dh, int(P_max), int(window), int(sinks)))
@@ -789,6 +802,7 @@ def _cache_attention(kv4, q, k_ptrs, v_ptrs, prefix_len, P_max, anc_mask, Hkv, d
     B, R, H, dh = q.shape
     if Hkv is None:
         Hkv = H
+    _ints(P_max, window, sinks, Hkv)
     if out is None:
         out = _new(stream, q)
     if ws is None:
