@@ -670,8 +670,7 @@ medusa_status check_kv4_rows(const char *who, medusa_dtype dtype, const void *k,
                              int64_t k_stride, int64_t v_stride, const void *k_cache,
                              const void *v_cache, const int32_t *prefix_len, int P_max, int B,
                              int R, int Hkv, int dh, const void *ws, size_t ws_bytes) {
-    // rows are the grid's second dimension
-    if (medusa_status s = check_heads_shape(who, dtype, B, R, 65535, Hkv, Hkv, dh)) return s;
+    if (medusa_status s = check_heads_shape(who, dtype, B, R, kKv4MaxRows, Hkv, Hkv, dh)) return s;
     if (!k || !v) return fail(MEDUSA_ERR_INVALID_ARG, "%s: NULL pointer", who);
     if (!aligned16(k) || !aligned16(v))
         return fail(MEDUSA_ERR_INVALID_ARG, "%s: tensor pointers must be 16-byte aligned", who);

@@ -171,13 +171,14 @@ cudaError_t launch_kv4_rows(medusa_dtype dtype, bool append, const void *k, cons
     a.status = static_cast<int *>(ws);
     // i / d = (i m) >> (32 + s) for all i < 2^30, with 2^s the power of two below d
     // and m = 2^(32 + s) / d + 1: m is too large by less than one, so i m / 2^(32 + s)
-    // by less than i / 2^(32 + s) < 1 / d
+    // by less than i / 2^(32 + s) < 1 / d (i < 2^30 < 2^(32 + s) / d, as d <= 2^(s + 1))
     const unsigned d = 2u * (unsigned)(Hkv * dh / 16);
     unsigned s = 0;
     while ((2u << s) < d) ++s;
     a.per_shift = s;
     a.per_magic = (unsigned)((1ull << (32 + s)) / d + 1);
-    const unsigned blocks = (unsigned)R * (unsigned)(2 * Hkv * dh / 16);  // < 2^30
+    static_assert(2ll * kKv4MaxRows * 1024 * 128 / 16 < 1 << 30, "blocks of a sequence (1024 heads of 128)");
+    const unsigned blocks = (unsigned)R * (unsigned)(2 * Hkv * dh / 16);
     const unsigned gx = (blocks + kKv4Threads - 1) / kKv4Threads;
     auto kern = append ? (dtype == MEDUSA_F32 ? kv4_append_kernel<float> : kv4_append_kernel<bf16>)
                        : (dtype == MEDUSA_F32 ? kv4_unpack_kernel<float> : kv4_unpack_kernel<bf16>);

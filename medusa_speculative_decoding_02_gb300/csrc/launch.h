@@ -118,7 +118,10 @@ cudaError_t launch_commit_kv(size_t elt, void *const *k_cache, void *const *v_ca
                              int32_t *new_prefix_len, void *ws, cudaStream_t stream);
 
 // K/V rows into the 4-bit cache (append) or back out of it (k, v are then
-// the destinations); strides in elements between rows.
+// the destinations); strides in elements between rows.  The limit of R keeps the
+// blocks of a sequence below 2^30 at every size of a row, for the division in
+// launch_kv4_rows.
+constexpr int kKv4MaxRows = 65535;
 cudaError_t launch_kv4_rows(medusa_dtype dtype, bool append, const void *k, const void *v,
                             long long k_stride, long long v_stride, void *const *k_cache,
                             void *const *v_cache, const int32_t *prefix_len, int P_max,

@@ -30,3 +30,23 @@ def test_integers_past_32_bits_are_refused(kv4):
         with pytest.raises(ValueError):
             m._ints(0, bad)
     m._ints(2 ** 31 - 1, -2 ** 31)
+
+
+def test_rows_of_the_4bit_calls_stay_in_the_division():
+    """launch_kv4_rows divides a block's index by the blocks of a slot as a product
+    and a shift: right up to the last index of the largest call of every size."""
+    import numpy as np
+    rows = 65535
+    for dh in (64, 128):
+        for Hkv in [*range(1, 1024, 7), 512, 1024]:
+            d = 2 * Hkv * dh // 16
+            s = 0
+            while (2 << s) < d:
+                s += 1
+            magic = (1 << (32 + s)) // d + 1
+            assert magic < 1 << 32
+            blocks = rows * d
+            assert blocks <= (1 << 30) - 256  # the last CTA's threads past the end included
+            r = np.unique(np.r_[np.arange(3), np.linspace(3, rows, 97).astype(np.uint64)]).astype(np.uint64)
+            for i in (r * np.uint64(d), r * np.uint64(d) + np.uint64(d - 1)):
+                assert ((i * np.uint64(magic) >> np.uint64(32 + s)) == i // np.uint64(d)).all(), (dh, Hkv)

@@ -8,7 +8,7 @@ import torch
 
 import cache_ops_ref as ref
 import medusa_speculative_decoding_02_gb300 as m
-from test_gpu_cache_ops import (BF, attn_inputs, call_attn, check_attn, check_rope, dev, inv_freqs, randn,  # noqa: F401
+from test_gpu_cache_ops import (BF, attn_inputs, call_attn, check_attn, check_rope, dev, inv_freqs, np64, randn,  # noqa: F401
                                 status)
 
 pytestmark = pytest.mark.gpu
@@ -116,3 +116,25 @@ def test_bad_depth_is_reported_behind_every_window(dev, dtype, kv4, R):
             got = fn(*args, depth=depth.to(dev), window=window, ws=ws)
             assert status(ws) == word, window
             assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+def test_4bit_rows_up_to_the_largest_call(dev, dtype):
+    """65535 rows, and a ragged sequence beside: every slot is written and read."""
+    B, R, Hkv, dh = 2, 65535, 1, 64
+    g = torch.Generator().manual_seed(1)
+    k, v = randn(g, B, R, Hkv, dh, dtype=dtype, std=3.0), randn(g, B, R, Hkv, dh, dtype=dtype)
+    rows = [R, 65000]
+    kc = [torch.zeros(R, m.kv4_row_bytes(Hkv, dh), dtype=torch.uint8, device=dev) for _ in range(B)]
+    vc = [c.clone() for c in kc]
+    kp, vp = m.cache_pointers(kc, dev), m.cache_pointers(vc, dev)
+    P = torch.zeros(B, dtype=torch.int32, device=dev)
+    n = torch.tensor(rows, dtype=torch.int32, device=dev)
+    m.kv4_append(k.to(dev), v.to(dev), kp, vp, P, 0, n_rows=n)
+    ko, vo = m.kv4_unpack(kp, vp, P, 0, R, Hkv, dh, dtype=dtype, n_rows=n)
+    used = Hkv * dh // 2 + Hkv * dh // 16
+    for b, r in enumerate(rows):
+        for x, c, y in ((k, kc, ko), (v, vc, vo)):
+            want = ref.pack_rows(np64(x)[b, :r])
+            assert (c[b].cpu().numpy()[:r, :used] == want[:, :used]).all() and not c[b][r:].any()
+            assert (np64(y)[b, :r] == ref.unpack_rows(want, Hkv, dh)).all()
