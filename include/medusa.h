@@ -693,17 +693,20 @@ MEDUSA_API medusa_status medusa_tree_attention_window(
  *   medusa_kv4_unpack   the values of slots prefix_len[b] + i into dense
  *       k_out, v_out [B,R,Hkv,dh] dtype
  *   n_rows [B] int32 (device) or NULL: rows i >= n_rows[b] are left alone
- *   medusa_commit_kv4   medusa_commit_kv on these rows
+ *   medusa_commit_kv4   medusa_commit_kv on these rows.  Like that call it takes
+ *       no P_max: it refuses a negative prefix, and the caller sees to it that
+ *       the cache has prefix_len[b] + R slots
  *   medusa_tree_attention_kv4   medusa_tree_attention_window on these rows
  *       (window = 0: the whole prefix); q and out are dtype.  The values
  *       enter the products exactly; bf16 q is scaled by a power of two for
  *       each row into fp16, where its elements keep their eight bits down to
  *       2^-14 of the row's largest, and weights below 2^-32 of the row's
  *       largest so far may be dropped.
- * A prefix outside 0..P_max or a bad cache pointer sets the status and leaves
- * that sequence untouched (attention: zeros).  Requirements: dh in {64,128};
- * append and unpack: R <= 65535; attention and commit: R <= 256.  Workspace of
- * append, unpack and commit: MEDUSA_WS_HEADER bytes.
+ * A prefix outside 0..P_max (commit: below 0) or a bad cache pointer sets the
+ * status and leaves that sequence untouched (attention: zeros; commit:
+ * new_prefix_len = prefix_len).  Requirements: dh in {64,128}; append and
+ * unpack: R <= 65535; attention and commit: R <= 256.  Workspace of append,
+ * unpack and commit: MEDUSA_WS_HEADER bytes.
  * ---------------------------------------------------------------------- */
 MEDUSA_API size_t medusa_kv4_row_bytes(int Hkv, int dh);
 

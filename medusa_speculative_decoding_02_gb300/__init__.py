@@ -766,7 +766,8 @@ def kv4_unpack(k_ptrs, v_ptrs, prefix_len, P_max: int, R: int, Hkv: int, dh: int
 
 def commit_kv4(k_ptrs, v_ptrs, prefix_len, path, accept_len, R: int, Hkv: int, dh: int,
                new_prefix_len=None, ws=None, stream=None):
-    """commit_kv on 4-bit caches; returns new_prefix_len = P_b + L + 1."""
+    """commit_kv on 4-bit caches, which must have P_b + R slots; returns
+    new_prefix_len = P_b + L + 1."""
     dev, st = _launch_on(path, stream)
     _ints(R, Hkv, dh)
     B, K1 = path.shape

@@ -138,3 +138,44 @@ def test_4bit_rows_up_to_the_largest_call(dev, dtype):
             want = ref.pack_rows(np64(x)[b, :r])
             assert (c[b].cpu().numpy()[:r, :used] == want[:, :used]).all() and not c[b][r:].any()
             assert (np64(y)[b, :r] == ref.unpack_rows(want, Hkv, dh)).all()
+
+
+def test_commit_of_4bit_rows_leaves_bad_sequences_alone(dev):
+    """A negative prefix, a missing or unaligned cache and a path outside the tree:
+    the status says so, the others are committed."""
+    B, R, Hkv, dh = 3, 9, 1, 64
+    g = torch.Generator().manual_seed(4)
+    x = randn(g, B, R, Hkv, dh, dtype=BF).to(dev)
+    base = torch.tensor([4, 2, 0], dtype=torch.int32, device=dev)
+    path = torch.tensor([[0, 2, 5, 8], [0, 3, -1, -1], [0, 1, 4, -1]], dtype=torch.int32, device=dev)
+    acc = torch.tensor([3, 1, 2], dtype=torch.int32, device=dev)
+    for fault, word in (("prefix", "bad prefix"), ("hole", "bad cache"), ("odd", "bad cache"),
+                        ("path", "bad path"), ("length", "bad path")):
+        kc = [torch.zeros(4 + R, m.kv4_row_bytes(Hkv, dh), dtype=torch.uint8, device=dev) for _ in range(B)]
+        vc = [c.clone() for c in kc]
+        kp, vp = m.cache_pointers(kc, dev), m.cache_pointers(vc, dev)
+        m.kv4_append(x, -x, kp, vp, base, 4)
+        before = [c.clone() for c in kc + vc]
+        P, pth, n = base.clone(), path.clone(), acc.clone()
+        if fault == "prefix":
+            P[1] = -1
+        elif fault == "hole":
+            vp[1] = 0
+        elif fault == "odd":
+            kp[1] += 8
+        elif fault == "path":
+            pth[1, 1] = R
+        else:
+            n[1] = 4
+        ws = m.new_workspace(256)
+        new = m.commit_kv4(kp, vp, P, pth, n, R, Hkv, dh, ws=ws)
+        assert status(ws) == word, fault
+        assert new.tolist() == [8, int(P[1]), 3]
+        for c, old in zip(kc + vc, before):
+            b = [i for i in range(B) if c is kc[i] or c is vc[i]][0]
+            p, L = int(base[b]), int(acc[b])
+            if b == 1:
+                assert torch.equal(c, old)
+            else:
+                for q in range(L + 1):
+                    assert torch.equal(c[p + q], old[p + int(path[b, q])])
