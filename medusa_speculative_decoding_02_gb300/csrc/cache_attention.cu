@@ -251,7 +251,7 @@ constexpr int kSub = 64, kTcThreads = 288;
 constexpr uint32_t kDrainPolls = 1u << 16;
 constexpr int kAhead = 4;  // 4-bit tiles held in a loader's registers
 
-template <int DH, bool KV4>
+template <int DH>
 struct CacheSmem {
     static constexpr int NB = DH / 64;
     static constexpr int TILE = NB * kSub * 128;
@@ -410,7 +410,7 @@ __device__ __forceinline__ void store_regs_kv4(const Kv4Regs<DH> &r, unsigned ch
 template <int DH, bool KV4, bool DEAL>
 __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnArgs a) {
     pdl_enter();
-    using L = CacheSmem<DH, KV4>;
+    using L = CacheSmem<DH>;
     extern __shared__ __align__(1024) unsigned char sm[];
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BAR), *empty = full + L::NT;
     // p and o have a barrier for each P buffer: a warp may be a stage ahead of
@@ -1099,8 +1099,7 @@ cudaError_t launch_cache_attention(medusa_dtype dtype, bool kv4, const void *q,
                              : pick(cache_attn_tc_kernel<64, true, false>, cache_attn_tc_kernel<64, true, true>))
                 : (dh == 128 ? pick(cache_attn_tc_kernel<128, false, false>, cache_attn_tc_kernel<128, false, true>)
                              : pick(cache_attn_tc_kernel<64, false, false>, cache_attn_tc_kernel<64, false, true>));
-        const int smem = kv4 ? (dh == 128 ? CacheSmem<128, true>::TOTAL : CacheSmem<64, true>::TOTAL)
-                             : (dh == 128 ? CacheSmem<128, false>::TOTAL : CacheSmem<64, false>::TOTAL);
+        const int smem = dh == 128 ? CacheSmem<128>::TOTAL : CacheSmem<64>::TOTAL;
         if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
             return e;
         e = launch_pdl(kern, grid, dim3(kTcThreads), (size_t)smem, stream, a);
