@@ -179,3 +179,51 @@ def test_commit_of_4bit_rows_leaves_bad_sequences_alone(dev):
             else:
                 for q in range(L + 1):
                     assert torch.equal(c[p + q], old[p + int(path[b, q])])
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("kv4", [False, True])
+@pytest.mark.parametrize("R,prefix", [(6, 100), (6, 3000), (30, 100), (30, 3000)])
+def test_queries_that_are_not_finite_stay_in_their_rows(dev, dtype, kv4, R, prefix):
+    a = attn_inputs(1, R, 2, 1, 64, [prefix], dtype, kv4, dev, seed=7)
+    a["q"][0, 1, 0, 3], a["q"][0, 3, 1, 0], a["q"][0, 4, 0] = math.inf, math.nan, -math.inf
+    for window, sinks in ((0, 0), (40, 3)):
+        got = call_attn(a, window, sinks, 1, kv4, dev)
+        check_attn(got, a, window, sinks, kv4=kv4)
+        for r, h in ((1, 0), (3, 1), (4, 0)):
+            assert not torch.isfinite(got[0, r, h]).any()
+            assert torch.isfinite(got[0, r, 1 - h]).all()
+        assert torch.isfinite(got[0, [0, 2, 5]]).all()
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+@pytest.mark.parametrize("R", [1, 17])
+def test_calls_at_the_same_time_on_two_streams(dev, kv4, R):
+    """Each stream with a workspace of its own, the caches shared; and calls whose
+    workspace and outputs are made by the call and dropped at once."""
+    a = attn_inputs(4, R, 8, 2, 128, [3000, 100, 0, 1700], BF, kv4, dev, seed=R)
+    fn = m.tree_attention_kv4 if kv4 else m.tree_attention_window
+    kp, vp = m.cache_pointers(a["kc"], dev), m.cache_pointers(a["vc"], dev)
+    P = torch.tensor(a["prefix"], dtype=torch.int32, device=dev)
+    mask, depth = a["mask"].to(dev), a["depth"].to(dev)
+    qs = [a["q"].to(dev), (a["q"] * -0.5).to(dev)]
+    kinds = ((0, 0), (700, 9))
+
+    def call(i, stream=None, ws=None):
+        window, sinks = kinds[i]
+        return fn(qs[i], kp, vp, P, a["P_max"], mask, 2, depth=depth, window=window, sinks=sinks, ws=ws,
+                  stream=stream)
+
+    want = [call(0), call(1)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    spaces = [m.new_workspace(1 << 26) for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for n in range(40):
+        for i in range(2):
+            call(i, streams[i])  # dropped: its memory goes to the next call of this stream
+            outs.append((i, call(i, streams[i], spaces[i])))
+    torch.cuda.synchronize()
+    for i, got in outs:
+        assert torch.equal(got, want[i])
+    assert [status(ws) for ws in spaces] == ["ok", "ok"]
