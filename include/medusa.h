@@ -653,7 +653,9 @@ MEDUSA_API medusa_status medusa_qk_norm_rope_append(
  * not grow with the prefix: only sinks + window - 1 + R slots are read.
  * Query head h reads KV head h / (H / Hkv).  A row that sees nothing gets
  * zeros.  What slots hold that a row does not see (infinities and NaNs
- * included) does not change that row.
+ * included) does not change that row.  Softmax weights over a bf16 cache are
+ * rounded to bf16 for the product with V (2^-8 of a weight at most); scores,
+ * maxima, sums and outputs before their last rounding are fp32.
  *
  *   q, out   [B,R,H,dh] dtype; caches [>= P_b+R, Hkv, dh] dtype
  *   depth    [B,R] int32 from medusa_build_tree; outside 0..R-1:

@@ -229,12 +229,14 @@ __global__ void __launch_bounds__(kSimtThreads) cache_attn_simt_kernel(CacheAttn
 //
 // What bounds it is neither the products (a stage's take 0.33 us of an SM at the
 // measured bf16 rate) nor the bytes, but passing a stage between the warps:
-// about 1 us a stage with two CTAs on the SM, whatever the cache's type, of which
-// two thirds remain if loads, conversions and exponentials are left out; a CTA
-// costs 6 us more at its ends.  Measured: 65 rows x 32 heads over a 1024 window
-// 16.1 us; eight sequences of 65 rows, 32 heads over 8 KV heads, 4096 window
-// 85.8 us (35 GFLOP: 0.41 PFLOP/s); 4 bits, 65 rows x 32 heads over 8192 slots
-// 29.7 us, eight ragged sequences up to 4096 slots 64.6 us.  Measured and not
+// about 1 us a stage with two CTAs on the SM, whatever the cache's type; a CTA
+// costs 6 us more at its ends.  Without the loads and conversions after the first
+// ring 0.80-0.85 of a call's time remains, without the exponentials 0.91-0.94,
+// without both 0.72-0.79 (the last three cases here).  Measured: 65 rows x 32
+// heads over a 1024 window 16.1 us; eight sequences of 65 rows, 32 heads over 8 KV
+// heads, 4096 window 85.3 us (35 GFLOP: 0.41 PFLOP/s); 4 bits, 65 rows x 32 heads
+// over 8192 slots 29.8 us, eight ragged sequences up to 4096 slots 65.2 us.
+// Measured and not
 // kept: the whole ring in flight before a tile is announced (92 against 82 us:
 // each tile then waits for the slot of the one NT before it), weights in tensor
 // memory, 16 warps, one CTA walking several ranges, and the rows behind the last
@@ -771,7 +773,10 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
                     for (int e = 0; e < 8; e += 2) {
                         const float2 t = __ffma2_rn(make_float2(x[c * 8 + e], x[c * 8 + e + 1]), sc2, nm2);
                         const float p0 = ex2_approx(t.x), p1 = ex2_approx(t.y);
-                        // rounded for the product only; the sum adds the fp32 weights
+                        // Rounded for the product only, whose operands have 16 bits:
+                        // to bf16 beside a bf16 V (fp16 has not its range, and both
+                        // operands are of one type), at most 2^-8 of a weight; the
+                        // sum adds the fp32 weights.
                         pk[e / 2] = pack_weights<KV4>(p0, p1);
                         ls[(e / 2) & 1] = __fadd2_rn(ls[(e / 2) & 1], make_float2(p0, p1));
                     }
@@ -997,8 +1002,11 @@ struct CachePlan {
     bool deal;  // ranges dealt out by the sequences' lengths
 };
 
-// Key ranges: the count that makes (waves of CTAs) x (64-key stages per CTA + 3,
-// the fixed cost of a CTA in stages) smallest, joining included.
+// Key ranges: the count that makes (waves of CTAs) x (stages per CTA + 3)
+// smallest, joining included.  The 3 stands for the fixed cost of a CTA in all three
+// kernels: over 42 shapes of them every choice from 3 to 8 gave the same times
+// within 1 %, 1 and 2 the few-row kernel up to 20 % more (eight single tokens over
+// 4000 slots 18.9 against 15.7 us).
 CachePlan cache_plan(medusa_dtype dtype, bool kv4, int B, int R, int H, int Hkv, int P_max, int window,
                      int sinks) {
     CachePlan p;

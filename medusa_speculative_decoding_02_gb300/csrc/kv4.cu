@@ -7,10 +7,11 @@
 // inverse.  They move 2 or 4 bytes an element on the wide side and 9/16 on the
 // narrow one, and are bound by issue (append) and by the latency of two dependent
 // rounds of loads (unpack).  Four ragged bf16 prompts of up to 4001 rows of 8 x 128
-// elements, appended and read back (115 MB): 25.0 us, 4.6 TB/s; 65 rows of 32 x
-// 128: 4.4 us.  Two blocks a thread gained nothing there and took 5.5 us at the 65
-// rows; with divisions by 6 and by the blocks of a slot, and the largest magnitude
-// taken element by element, the prompts took 27.5 us.
+// elements (58 MB each way): append 13.6 us, 4.2 TB/s, unpack 11.2 us, 5.2 TB/s
+// (fp32, 103 MB: 27.0 and 24.8 us); 65 rows of 32 x 128: 2.2 and 2.1 us.  Two
+// blocks a thread gained nothing on the prompts and took 5.5 us for both calls at
+// the 65 rows; with divisions by 6 and by the blocks of a slot, and the largest
+// magnitude taken element by element, both calls took 27.5 us on the prompts.
 #include <algorithm>
 
 #include "kv4.cuh"

@@ -16,21 +16,25 @@
 //
 // Angles: p * inv_freq reaches 10^5 turns at far positions, where fp32 has no
 // fraction left.  inv_freq becomes a 64-bit fixed-point number of turns per
-// position, modulo one (turns_per_position); p times that, modulo 2^64, is the
-// fraction of a turn to 2^-33 at every p.  Integers throughout: this GPU does
-// two fp64 products a cycle and SM, and the same in fp64 cost 2.4 us at 65
-// rows.  Sine and cosine are taken in fp32 on [-1/2, 1/2] turn.
+// position, modulo one (turns_per_position, the argument reduction of Payne and
+// Hanek: only those bits of 1/(2 pi) are multiplied that reach the fraction); p
+// times that, modulo 2^64, is the fraction of a turn to 2^-33 at every p.
+// Integers throughout: this GPU does two fp64 products a cycle and SM, and the
+// same in fp64 cost 2.4 us at 65 rows.  Sine and cosine are taken in fp32 on
+// [-1/2, 1/2] turn.
 //
 // Squares are summed in fp32, which holds for elements up to 2^60.  Taking vectors
 // beyond it again, scaled by a power of two, was measured and not kept: the test in
-// every pass, on a kernel bound by issue, made the prompt below 32.8-34.8 us of 31.6.
+// every pass, on a kernel bound by issue, took the prompt below from 31.6 us to
+// 32.8-34.8.
 //
 // Bound by issue and, close behind, by the bytes of q, K and V read and written
-// once; the loads of a row are issued before its angles are computed.  6626 rows
-// of 32 + 8 + 8 vectors of 128 (159 MB) take 32.9 us, 4.8 TB/s (31.4 us back to
-// back); one row a CTA took 41.2 (40.7 M instructions a launch where four rows a
-// CTA had 29.8 M).  65 rows of 32 + 32 + 32 vectors take 3.0 us, eight rows of
-// 32 + 8 1.9 us: the latency of two rounds of loads.
+// once; the loads of a row are issued before its angles are computed.  6481 rows
+// of 32 + 8 + 8 vectors of 128 (159 MB) take 32.9 us, 4.8 TB/s (31.5 us back to
+// back; fp32, 319 MB, 55.4 us, 5.8 TB/s); one row a CTA took 41.2 (40.7 M
+// instructions a launch where four rows a CTA had 29.8 M).  65 rows of 32 + 32 +
+// 32 vectors take 2.9 us, eight rows of 32 + 8 1.9 us: the latency of two rounds
+// of loads.
 #include <algorithm>
 
 #include "common.cuh"
@@ -337,7 +341,7 @@ cudaError_t launch_qk_norm_rope(medusa_dtype dtype, const void *q, const void *k
     const long long rows = (long long)B * R;
     const int vpp = kRopeThreads / (dh / 8);
     // With few rows one row and pass per CTA puts more CTAs to work (65 rows of 96
-    // vectors: 3.0 us); with enough of them three passes over four rows share what
+    // vectors: 2.9 us); with enough of them three passes over four rows share what
     // comes before the first vector (the prompt above: 31.4 us; with two passes
     // 39.1, with two rows 31.8).
     const int passes = (nv + vpp - 1) / vpp;
