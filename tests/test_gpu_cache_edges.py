@@ -70,7 +70,7 @@ def test_infinities_in_adjacent_stages(dev, kv4, dh, R, G, prefix):
 @pytest.mark.parametrize("dh", [64, 128])
 @pytest.mark.parametrize("inter", [False, True])
 @pytest.mark.parametrize("R", [20, 3000])
-def test_norms_over_the_whole_range_of_the_type(dev, dtype, dh, inter, R):
+def test_norms_over_the_stated_range(dev, dtype, dh, inter, R):
     """Rows of every magnitude that the header allows: with eps 0 from 2^-60 to 2^60,
     with an eps every smaller one as well; infinities and NaNs stay in their vector."""
     g = torch.Generator().manual_seed(dh)
