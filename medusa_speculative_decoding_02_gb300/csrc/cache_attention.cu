@@ -236,12 +236,11 @@ __global__ void __launch_bounds__(kSimtThreads) cache_attn_simt_kernel(CacheAttn
 // heads over a 1024 window 16.1 us; eight sequences of 65 rows, 32 heads over 8 KV
 // heads, 4096 window 85.3 us (35 GFLOP: 0.41 PFLOP/s); 4 bits, 65 rows x 32 heads
 // over 8192 slots 29.8 us, eight ragged sequences up to 4096 slots 65.2 us.
-// Measured and not
-// kept: the whole ring in flight before a tile is announced (92 against 82 us:
-// each tile then waits for the slot of the one NT before it), weights in tensor
-// memory, 16 warps, one CTA walking several ranges, and the rows behind the last
-// whole tile (260 rows are two tiles and four) on the few-row kernel, launched to
-// overlap this one (5 us less to 7 us more).
+// Measured and not kept: the whole ring in flight before a tile is announced (92
+// against 82 us: each tile then waits for the slot of the one NT before it),
+// weights in tensor memory, 16 warps, one CTA walking several ranges, and the rows
+// behind the last whole tile (260 rows are two tiles and four) on the few-row
+// kernel, launched to overlap this one (5 us less to 7 us more).
 //
 // Masks are built as 64 bits a row and stage.  Products run over masked keys
 // too, with weight 0, so a non-finite V element there would reach every row
