@@ -100,12 +100,13 @@ enum {
                                       path entry outside [0, R)              */
     MEDUSA_DEV_BAD_CACHE = 8,      /* a cache pointer NULL or not 16-byte
                                       aligned                                 */
-    MEDUSA_DEV_DRAIN_TIMEOUT = 9   /* after a timeout, the drain of the CTA's
+    MEDUSA_DEV_DRAIN_TIMEOUT = 9,  /* after a timeout, the drain of the CTA's
                                       own MMAs also gave up; the tensor memory
                                       was freed with an MMA possibly still in
                                       flight, so this call's outputs and later
                                       tensor-core results on the device are
                                       suspect.  Overrides an earlier code.    */
+    MEDUSA_DEV_BAD_PAGE = 10       /* a page number outside [0, n_pages)      */
 };
 
 /* Limits. */
@@ -114,6 +115,9 @@ enum {
 #define MEDUSA_MAX_TREE_ROWS 256  /* R = n + 1                                 */
 #define MEDUSA_MAX_BATCH 8        /* B for medusa_heads                        */
 #define MEDUSA_WS_HEADER 256      /* bytes of workspace before any scratch     */
+#define MEDUSA_MIN_PAGE 16        /* slots of a page: a power of two in        */
+#define MEDUSA_MAX_PAGE 1024      /* MEDUSA_MIN_PAGE..MEDUSA_MAX_PAGE          */
+#define MEDUSA_MAX_VOCAB (1 << 24) /* V for medusa_token_logprobs              */
 
 typedef void *medusa_stream;      /* cudaStream_t */
 
@@ -740,6 +744,115 @@ MEDUSA_API medusa_status medusa_tree_attention_kv4(
     const int32_t *prefix_len, int P_max, const uint64_t *anc_mask, const int32_t *depth,
     int window, int sinks, int B, int R, int H, int Hkv, int dh, float scale, void *out, void *ws,
     size_t ws_bytes, medusa_stream stream);
+
+/* ------------------------------------------------------------------------
+ * 11. A cache in pages.
+ *
+ * The caches of the calls above are one piece a sequence.  Here all sequences
+ * share a pool of pages: K's (and V's) is [n_pages,page,Hkv,dh] dtype, and slot
+ * j of sequence b is row j % page of page page_table[b][j / page].
+ *
+ *   k_pages, v_pages  the pools (16-byte aligned)
+ *   n_pages, page     pages of a pool; slots of a page, a power of two in
+ *                     16..1024; n_pages * page < 2^31
+ *   page_table [B,table_stride] int32 (device); a call reads the entries of
+ *                     the slots it needs.  Sequences may share pages that are
+ *                     only read; a slot that a call writes belongs to one
+ *                     sequence
+ *   prefix_len [B]    int32 (device), 0 <= P_b <= P_max
+ *   P_max             table_stride * page >= P_max + R
+ * A page number outside 0..n_pages-1 sets MEDUSA_DEV_BAD_PAGE; nothing outside
+ * the pools is read or written.  A prefix outside 0..P_max sets
+ * MEDUSA_DEV_BAD_PREFIX.
+ *
+ *   medusa_paged_append   rows k, v [B,R,Hkv,dh] dtype (k_stride, v_stride
+ *       elements apart, as in medusa_qk_norm_rope) into slots prefix_len[b] + i;
+ *       rows i >= n_rows[b] (int32 [B] or NULL) are left alone, and so are rows
+ *       whose page is bad and sequences whose prefix is
+ *   medusa_commit_paged   medusa_commit_kv on pages; a sequence that fails a
+ *       device check (a bad page among its path's included) is left untouched
+ *       and gets new_prefix_len = prefix_len
+ *   medusa_chunk_attention_paged   attention of R new rows a sequence, whose own
+ *       slots P_b .. P_b+R-1 hold their K and V already (a piece of a prompt;
+ *       with R = 1 plain decoding): row i sees slots 0 .. P_b + i.  n_rows [B]
+ *       int32 or NULL: rows i >= n_rows[b] are not read and their outputs are
+ *       left as they were
+ *   medusa_tree_attention_paged   medusa_tree_attention on pages: row i sees the
+ *       prefix and the tree slots of its ancestors
+ *         q, out [B,R,H,dh] dtype; query head h reads KV head h / (H / Hkv)
+ *       What slots hold that a row does not see (infinities and NaNs included)
+ *       does not change that row.  Slots of a bad page are not seen.  A row that
+ *       sees nothing gets zeros, and so does a sequence with a bad prefix.
+ *       Softmax weights over a bf16 cache are rounded to bf16 for the product
+ *       with V (2^-8 of a weight at most); scores, maxima, sums and outputs
+ *       before their last rounding are fp32.
+ * Requirements: dh in {64,128}; H <= 1024, a multiple of Hkv; R <= 2^20 (tree
+ * and commit: 256); P_max <= 2^29; scale > 0; K <= 8.  Workspace of append and
+ * commit: MEDUSA_WS_HEADER bytes; of both attentions
+ * medusa_paged_attention_workspace_size(...).
+ * ---------------------------------------------------------------------- */
+MEDUSA_API medusa_status medusa_paged_append(medusa_dtype dtype, const void *k, const void *v,
+                                             int64_t k_stride, int64_t v_stride, void *k_pages,
+                                             void *v_pages, int n_pages, int page,
+                                             const int32_t *page_table, int table_stride,
+                                             const int32_t *prefix_len, int P_max,
+                                             const int32_t *n_rows, int B, int R, int Hkv, int dh,
+                                             void *ws, size_t ws_bytes, medusa_stream stream);
+
+MEDUSA_API medusa_status medusa_commit_paged(medusa_dtype dtype, void *k_pages, void *v_pages,
+                                             int n_pages, int page, const int32_t *page_table,
+                                             int table_stride, const int32_t *prefix_len, int P_max,
+                                             const int32_t *path, const int32_t *accept_len, int B,
+                                             int K, int R, int Hkv, int dh, int32_t *new_prefix_len,
+                                             void *ws, size_t ws_bytes, medusa_stream stream);
+
+MEDUSA_API size_t medusa_paged_attention_workspace_size(medusa_dtype dtype, int B, int R, int H,
+                                                        int Hkv, int dh, int P_max);
+
+MEDUSA_API medusa_status medusa_chunk_attention_paged(
+    medusa_dtype dtype, const void *q, const void *k_pages, const void *v_pages, int n_pages, int page,
+    const int32_t *page_table, int table_stride, const int32_t *prefix_len, int P_max,
+    const int32_t *n_rows, int B, int R, int H, int Hkv, int dh, float scale, void *out, void *ws,
+    size_t ws_bytes, medusa_stream stream);
+
+MEDUSA_API medusa_status medusa_tree_attention_paged(
+    medusa_dtype dtype, const void *q, const void *k_pages, const void *v_pages, int n_pages, int page,
+    const int32_t *page_table, int table_stride, const int32_t *prefix_len, int P_max,
+    const uint64_t *anc_mask, int B, int R, int H, int Hkv, int dh, float scale, void *out, void *ws,
+    size_t ws_bytes, medusa_stream stream);
+
+/* ------------------------------------------------------------------------
+ * 12. Log probabilities of given tokens.
+ *
+ * What a client is told about tokens beside the tokens: of the verification rows
+ * along the accepted path, or of a prompt's rows.  (The ranks of the true tokens
+ * under a head's logits, counted over a text, are the table of
+ * medusa_build_tree_static.)  For row x of V logits, p = softmax(x / temperature):
+ *     logp     ln p_t of the row's token t
+ *     entropy  -sum_i p_i ln p_i, in nats
+ *     rank     how many tokens come before t in the order "larger logit first,
+ *              equal logits -> smaller id" (0: t is the row's argmax)
+ *     top_ids, top_logp   the first `top` tokens of that order, and their ln p
+ *
+ *   logits [N,V] dtype, consecutive rows `stride` >= V elements apart (any
+ *            alignment but the first row's 16 bytes)
+ *   tokens [N] int32; -1: no token is asked for (logp 0, rank -1).  Other ids
+ *            outside [0, V) set MEDUSA_DEV_BAD_TOKEN and count as -1
+ *   logp, entropy [N] fp32, rank [N] int32, top_ids [N,top] int32, top_logp
+ *            [N,top] fp32 (NULL with top = 0)
+ * A logit of -inf is a token of probability zero (logp -inf; nothing in the
+ * entropy).  Where every logit is -inf, logp is -inf and the entropy 0.  A row
+ * that holds a NaN or +inf has NaN in logp, entropy and top_logp; a NaN comes
+ * behind all numbers in the order, has rank -1 itself and no place among the
+ * alternatives (a place that no number fills has id -1).
+ * Requirements: N >= 1; 1 <= V <= 2^24; top in 0..min(V, 16); temperature in
+ * 1e-30..1e30.  Workspace: MEDUSA_WS_HEADER bytes (the status word).
+ * ---------------------------------------------------------------------- */
+MEDUSA_API medusa_status medusa_token_logprobs(medusa_dtype dtype, const void *logits, int64_t stride,
+                                               const int32_t *tokens, int N, int V, int top,
+                                               float temperature, float *logp, float *entropy,
+                                               int32_t *rank, int32_t *top_ids, float *top_logp,
+                                               void *ws, size_t ws_bytes, medusa_stream stream);
 
 #ifdef __cplusplus
 }

@@ -9,7 +9,8 @@ the compiled library is missing, importing the calls fails loudly.
 Public calls (same names as the C ABI in include/medusa.h):
     heads, heads_lm, heads_sample, heads_noalloc, build_tree, build_tree_static, tree_attention, evaluate_posterior,
     speculative_posterior, commit_kv, evaluate_posterior_commit, qk_norm_rope, qk_norm_rope_append,
-    tree_attention_window, kv4_append, kv4_unpack, commit_kv4, tree_attention_kv4
+    tree_attention_window, kv4_append, kv4_unpack, commit_kv4, tree_attention_kv4, paged_append,
+    commit_paged, chunk_attention_paged, tree_attention_paged, token_logprobs
 plus workspace-size queries, device-status helpers, launch_count,
 ``StepExecutor`` (medusa_step_create / medusa_step_run: the whole step, input
 copies included, issued by one native call), and ``StepGraph``, which
@@ -42,7 +43,7 @@ STATUS = {0: "MEDUSA_OK", 1: "MEDUSA_ERR_INVALID_ARG", 2: "MEDUSA_ERR_UNSUPPORTE
           6: "MEDUSA_ERR_DEVICE_CHECK"}
 DEVICE_STATUS = {0: "ok", 1: "bad token", 2: "bad parent", 3: "bad prefix", 4: "bad score",
                  5: "bad depth", 6: "timeout", 7: "bad path", 8: "bad cache",
-                 9: "drain timeout"}
+                 9: "drain timeout", 10: "bad page"}
 
 EXPORTS = ("medusa_status_string", "medusa_last_error", "medusa_launch_count",
            "medusa_wait_budget", "medusa_set_wait_budget",
@@ -59,7 +60,9 @@ EXPORTS = ("medusa_status_string", "medusa_last_error", "medusa_launch_count",
            "medusa_qk_norm_rope", "medusa_qk_norm_rope_append",
            "medusa_tree_attention_window_workspace_size", "medusa_tree_attention_window",
            "medusa_kv4_row_bytes", "medusa_kv4_append", "medusa_kv4_unpack", "medusa_commit_kv4",
-           "medusa_tree_attention_kv4_workspace_size", "medusa_tree_attention_kv4")
+           "medusa_tree_attention_kv4_workspace_size", "medusa_tree_attention_kv4",
+           "medusa_paged_append", "medusa_commit_paged", "medusa_paged_attention_workspace_size",
+           "medusa_chunk_attention_paged", "medusa_tree_attention_paged", "medusa_token_logprobs")
 
 
 class _Copy(ctypes.Structure):
@@ -145,7 +148,14 @@ def lib() -> ctypes.CDLL:
         "medusa_kv4_append": ([I, P, P, I64, I64, P, P, P, I, P, I, I, I, I, P, S, P], I),
         "medusa_kv4_unpack": ([I, P, P, P, I, P, I, I, I, I, P, P, P, S, P], I),
         "medusa_commit_kv4": ([P, P, P, P, P, I, I, I, I, I, P, P, S, P], I),
+        "medusa_paged_append": ([I, P, P, I64, I64, P, P, I, I, P, I, P, I, P, I, I, I, I, P, S, P], I),
+        "medusa_commit_paged": ([I, P, P, I, I, P, I, P, I, P, P, I, I, I, I, I, P, P, S, P], I),
+        "medusa_paged_attention_workspace_size": ([I] * 7, S),
+        "medusa_token_logprobs": ([I, P, I64, P, I, I, I, F, P, P, P, P, P, P, S, P], I),
     }
+    for kind in ("chunk", "tree"):
+        sig[f"medusa_{kind}_attention_paged"] = ([I, P, P, P, I, I, P, I, P, I, P, I, I, I, I, I, F, P,
+                                                  P, S, P], I)
     for kind in ("window", "kv4"):
         sig[f"medusa_tree_attention_{kind}_workspace_size"] = ([I] * 9, S)
         sig[f"medusa_tree_attention_{kind}"] = ([I, P, P, P, P, I, P, P, I, I, I, I, I, I, I, F, P, P,
@@ -837,6 +847,176 @@ def tree_attention_kv4(q, k_ptrs, v_ptrs, prefix_len, P_max: int, anc_mask, Hkv=
     """tree_attention_window over 4-bit caches (kv4_cache, kv4_append)."""
     return _cache_attention(True, q, k_ptrs, v_ptrs, prefix_len, P_max, anc_mask, Hkv, depth, window,
                             sinks, scale, out, ws, stream)
+
+
+# ------------------------------------------ paged cache, log probabilities ---
+
+def _pages(k_pages, v_pages, page_table, B: int, Hkv: int, dh: int, dtype, dev: int):
+    """The cache arguments of a call on pages."""
+    ks, ts = k_pages.shape, page_table.shape
+    if len(ks) != 4 or ks[2] != Hkv or ks[3] != dh:
+        raise ValueError(f"the pools must be [pages,page,{Hkv},{dh}], got {tuple(ks)}")
+    if len(ts) != 2 or ts[0] != B:
+        raise ValueError(f"page_table must be [{B},pages], got {tuple(ts)}")
+    _ints(ks[0], ts[1])
+    return (_dense(k_pages, ks, dtype, dev, "k_pages"), _dense(v_pages, ks, dtype, dev, "v_pages"), ks[0],
+            ks[1], _vec(page_table, B * ts[1], _INT, dev, "page_table"), ts[1])
+
+
+def paged_append(k, v, k_pages, v_pages, page_table, prefix_len, P_max: int, n_rows=None, ws=None,
+                 stream=None):
+    """Rows k, v [B,R,Hkv,dh] into slots prefix_len[b] + i of a cache in pages: pools
+    [pages,page,Hkv,dh], slot j of sequence b in row j % page of page
+    page_table[b, j // page].  Rows i >= n_rows[b] are left alone."""
+    dt = _dtype(k)
+    dev, st = _launch_on(k, stream)
+    if v.dtype is not k.dtype or v.shape != k.shape or v.get_device() != dev:
+        raise ValueError("v must have k's shape, dtype and device")
+    _ints(P_max)
+    ks, vs = _rows(k, "k"), _rows(v, "v")
+    B, R, Hkv, dh = k.shape
+    cache = _pages(k_pages, v_pages, page_table, B, Hkv, dh, k.dtype, dev)
+    if ws is None:
+        ws = _scratch(WS_HEADER, k.device, stream)
+    ws_ptr, ws_n = _ws_args(ws, dev)
+    _check(lib().medusa_paged_append(
+        dt, k.data_ptr(), v.data_ptr(), ks, vs, *cache, _vec(prefix_len, B, _INT, dev, "prefix_len"), P_max,
+        None if n_rows is None else _vec(n_rows, B, _INT, dev, "n_rows"), B, R, Hkv, dh, ws_ptr, ws_n,
+        st))
+
+
+def commit_paged(k_pages, v_pages, page_table, prefix_len, P_max: int, path, accept_len, R: int,
+                 new_prefix_len=None, ws=None, stream=None):
+    """commit_kv on a cache in pages; returns new_prefix_len = P_b + L + 1."""
+    dt = _dtype(k_pages)
+    dev, st = _launch_on(path, stream)
+    _ints(P_max, R)
+    B, K1 = path.shape
+    cache = _pages(k_pages, v_pages, page_table, B, *k_pages.shape[2:], k_pages.dtype, dev)
+    if new_prefix_len is None:
+        new_prefix_len = _new(stream, prefix_len)
+    if ws is None:
+        ws = _scratch(WS_HEADER, path.device, stream)
+    ws_ptr, ws_n = _ws_args(ws, dev)
+    _check(lib().medusa_commit_paged(
+        dt, *cache, _vec(prefix_len, B, _INT, dev, "prefix_len"), P_max,
+        _vec(path, B * K1, _INT, dev, "path"), _vec(accept_len, B, _INT, dev, "accept_len"), B, K1 - 1, R,
+        *k_pages.shape[2:], _vec(new_prefix_len, B, _INT, dev, "new_prefix_len"), ws_ptr, ws_n, st))
+    return new_prefix_len
+
+
+def paged_attention_workspace_size(dtype: int, B: int, R: int, H: int, Hkv: int, dh: int,
+                                   P_max: int) -> int:
+    """Workspace of chunk_attention_paged and of tree_attention_paged."""
+    _ints(B, R, H, Hkv, dh, P_max)
+    return int(lib().medusa_paged_attention_workspace_size(dtype, B, R, H, Hkv, dh, int(P_max)))
+
+
+def _paged_attention(fn, q, k_pages, v_pages, page_table, prefix_len, P_max, last, scale, out, ws, stream,
+                     dt, dev, st):
+    if len(q.shape) != 4 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous [B,R,H,dh]")
+    B, R, H, dh = q.shape
+    if len(k_pages.shape) != 4:
+        raise ValueError("the pools must be [pages,page,Hkv,dh]")
+    Hkv = k_pages.shape[2]
+    _ints(P_max)
+    cache = _pages(k_pages, v_pages, page_table, B, Hkv, dh, q.dtype, dev)
+    if out is None:
+        out = _new(stream, q)
+    if ws is None:
+        ws = _scratch(paged_attention_workspace_size(dt, B, R, H, Hkv, dh, P_max), q.device, stream)
+    ws_ptr, ws_n = _ws_args(ws, dev)
+    _check(fn(dt, q.data_ptr(), *cache, _vec(prefix_len, B, _INT, dev, "prefix_len"), P_max, last, B, R, H,
+              Hkv, dh, dh ** -0.5 if scale is None else scale, _dense(out, q.shape, q.dtype, dev, "out"),
+              ws_ptr, ws_n, st))
+    return out
+
+
+def chunk_attention_paged(q, k_pages, v_pages, page_table, prefix_len, P_max: int, n_rows=None,
+                          scale=None, out=None, ws=None, stream=None):
+    """Attention of a chunk of new tokens over a cache in pages (see paged_append),
+    which holds their K and V already: row i of q [B,R,H,dh] sees slots
+    0 .. prefix_len[b] + i.  A piece of a prompt, or with R = 1 plain decoding.
+    Rows i >= n_rows[b] are left as ``out`` has them."""
+    dt = _dtype(q)
+    dev, st = _launch_on(q, stream)
+    last = None if n_rows is None else _vec(n_rows, q.shape[0], _INT, dev, "n_rows")
+    return _paged_attention(lib().medusa_chunk_attention_paged, q, k_pages, v_pages, page_table, prefix_len,
+                            P_max, last, scale, out, ws, stream, dt, dev, st)
+
+
+def tree_attention_paged(q, k_pages, v_pages, page_table, prefix_len, P_max: int, anc_mask, scale=None,
+                         out=None, ws=None, stream=None):
+    """tree_attention over a cache in pages (see paged_append); query head h reads KV
+    head h // (H // Hkv)."""
+    dt = _dtype(q)
+    dev, st = _launch_on(q, stream)
+    B, R = q.shape[:2]
+    mask = _vec(anc_mask, B * R * ((R + 63) // 64), torch.int64, dev, "anc_mask")
+    return _paged_attention(lib().medusa_tree_attention_paged, q, k_pages, v_pages, page_table, prefix_len,
+                            P_max, mask, scale, out, ws, stream, dt, dev, st)
+
+
+@dataclass
+class TokenLogprobs:
+    logp: torch.Tensor      # fp32 [...]
+    entropy: torch.Tensor   # fp32 [...], nats
+    rank: torch.Tensor      # int32 [...]
+    top_ids: torch.Tensor   # int32 [..., top]
+    top_logp: torch.Tensor  # fp32 [..., top]
+
+
+def token_logprobs(logits, tokens, top: int = 0, temperature: float = 1.0,
+                   out: Optional[TokenLogprobs] = None, ws=None, stream=None) -> TokenLogprobs:
+    """ln p of the given tokens under softmax(logits / temperature), their ranks (0: the
+    argmax), each row's entropy and its ``top`` most probable tokens, in one pass
+    over the logits [..., V] (rows evenly apart); tokens int32 [...], -1 for none."""
+    dt = _dtype(logits)
+    dev, st = _launch_on(logits, stream)
+    shape, V = logits.shape[:-1], logits.shape[-1]
+    N = tokens.numel()
+    if tokens.shape != shape:
+        raise ValueError(f"tokens must be {tuple(shape)}, got {tuple(tokens.shape)}")
+    _ints(N, V, top)
+    step = _row_step(logits, "logits")
+    if out is None:
+        f32, more = torch.float32, (*shape, top)
+        out = TokenLogprobs(_new(stream, logits, shape, f32), _new(stream, logits, shape, f32),
+                            _new(stream, logits, shape, _INT), _new(stream, logits, more, _INT),
+                            _new(stream, logits, more, f32))
+    if ws is None:
+        ws = _scratch(WS_HEADER, logits.device, stream)
+    ws_ptr, ws_n = _ws_args(ws, dev)
+    _check(lib().medusa_token_logprobs(
+        dt, logits.data_ptr(), step, _vec(tokens, N, _INT, dev, "tokens"), N, V, top, temperature,
+        _vec(out.logp, N, torch.float32, dev, "logp"), _vec(out.entropy, N, torch.float32, dev, "entropy"),
+        _vec(out.rank, N, _INT, dev, "rank"),
+        _vec(out.top_ids, N * top, _INT, dev, "top_ids") if top else None,
+        _vec(out.top_logp, N * top, torch.float32, dev, "top_logp") if top else None, ws_ptr, ws_n, st))
+    return out
+
+
+def _row_step(t: torch.Tensor, name: str) -> int:
+    """Elements between the rows of a tensor whose last dimension is dense and whose
+    rows are evenly apart."""
+    V = t.shape[-1]
+    if t.is_contiguous():
+        return V
+    s, n = t.stride(), t.shape
+    if s[-1] != 1 and V > 1:
+        raise ValueError(f"{name}: the last dimension must be dense")
+    step = None  # of the innermost dimension that has more than one row
+    rows = 1
+    for d in range(len(n) - 2, -1, -1):
+        if n[d] == 1:
+            continue
+        if step is None:
+            step = s[d]
+        elif s[d] != step * rows:
+            raise ValueError(f"{name}: rows must be evenly apart")
+        rows *= n[d]
+    return V if step is None else step
 
 
 # ------------------------------------------------------------- step graph ---

@@ -870,3 +870,183 @@ medusa_status medusa_tree_attention_kv4(
 }
 
 }  // extern "C"
+
+// ------------------------------------------------- paged cache, log probs ---
+
+namespace {
+
+constexpr int kMaxChunkRows = 1 << 20;  // rows times query heads of a KV head stay below 2^30
+
+medusa_status check_pages(const char *who, const void *k_pages, const void *v_pages, int n_pages,
+                          int page, const int32_t *page_table, int table_stride,
+                          const int32_t *prefix_len, int P_max, int R, PagedCache &cache) {
+    if (!k_pages || !v_pages || !page_table || !prefix_len)
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+    if (!aligned16(k_pages) || !aligned16(v_pages))
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: the pools must be 16-byte aligned", who);
+    if (page < MEDUSA_MIN_PAGE || page > MEDUSA_MAX_PAGE || (page & (page - 1)))
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: page=%d must be a power of two in %d..%d", who, page,
+                    MEDUSA_MIN_PAGE, MEDUSA_MAX_PAGE);
+    if (n_pages < 1 || (long long)n_pages * page > 0x7fffffffLL)
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: n_pages=%d pages of %d slots (1 to 2^31 - 1 slots)",
+                    who, n_pages, page);
+    if (P_max < 0 || P_max > kMaxPrefix)
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: P_max=%d outside 0..%d", who, P_max, kMaxPrefix);
+    if (table_stride < 1 || (long long)table_stride * page < (long long)P_max + R)
+        return fail(MEDUSA_ERR_INVALID_ARG,
+                    "%s: table_stride=%d pages of %d slots do not hold P_max + R = %lld slots", who,
+                    table_stride, page, (long long)P_max + R);
+    cache.table = page_table;
+    cache.stride = table_stride;
+    cache.n_pages = n_pages;
+    cache.shift = 0;
+    while ((1 << cache.shift) < page) ++cache.shift;
+    return MEDUSA_OK;
+}
+
+medusa_status paged_attention(const char *who, medusa_dtype dtype, const void *q,
+                              const void *k_pages, const void *v_pages, int n_pages, int page,
+                              const int32_t *page_table, int table_stride, const int32_t *prefix_len,
+                              int P_max, const uint64_t *anc_mask, const int32_t *n_rows, int max_rows,
+                              int B, int R, int H, int Hkv, int dh, float scale, void *out, void *ws,
+                              size_t ws_bytes, medusa_stream stream) {
+    if (medusa_status s = check_heads_shape(who, dtype, B, R, max_rows, H, Hkv, dh)) return s;
+    if (!q || !out) return fail(MEDUSA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+    PagedCache cache;
+    if (medusa_status s = check_pages(who, k_pages, v_pages, n_pages, page, page_table, table_stride,
+                                      prefix_len, P_max, R, cache))
+        return s;
+    if (!(scale > 0.f) || !(scale < 1e30f))
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: scale must be positive and finite", who);
+    if (!aligned16(q) || !aligned16(out))
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: tensor pointers must be 16-byte aligned", who);
+    if (medusa_status s = check_ws(
+            ws, ws_bytes, paged_attention_workspace_bytes(dtype, B, R, H, Hkv, dh, P_max), who))
+        return s;
+    cudaError_t e = launch_paged_attention(dtype, q, k_pages, v_pages, cache, prefix_len, P_max,
+                                           anc_mask, n_rows, B, R, H, Hkv, dh, scale, out, ws,
+                                           static_cast<cudaStream_t>(stream));
+    if (e) return cuda_fail(e, who);
+    return MEDUSA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+medusa_status medusa_paged_append(medusa_dtype dtype, const void *k, const void *v, int64_t k_stride,
+                                  int64_t v_stride, void *k_pages, void *v_pages, int n_pages,
+                                  int page, const int32_t *page_table, int table_stride,
+                                  const int32_t *prefix_len, int P_max, const int32_t *n_rows, int B,
+                                  int R, int Hkv, int dh, void *ws, size_t ws_bytes,
+                                  medusa_stream stream) {
+    const NvtxRange range("medusa_paged_append");
+    const char *who = "medusa_paged_append";
+    if (medusa_status s = check_heads_shape(who, dtype, B, R, kMaxChunkRows, Hkv, Hkv, dh)) return s;
+    if (!k || !v) return fail(MEDUSA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+    if (!aligned16(k) || !aligned16(v))
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: tensor pointers must be 16-byte aligned", who);
+    if (medusa_status s = check_row_stride(who, "k_stride", dtype, k_stride, Hkv, dh)) return s;
+    if (medusa_status s = check_row_stride(who, "v_stride", dtype, v_stride, Hkv, dh)) return s;
+    PagedCache cache;
+    if (medusa_status s = check_pages(who, k_pages, v_pages, n_pages, page, page_table, table_stride,
+                                      prefix_len, P_max, R, cache))
+        return s;
+    if (medusa_status s = check_ws(ws, ws_bytes, MEDUSA_WS_HEADER, who)) return s;
+    cudaError_t e = launch_paged_append(dtype == MEDUSA_BF16 ? 2 : 4, k, v, k_stride, v_stride,
+                                        k_pages, v_pages, cache, prefix_len, P_max, n_rows, B, R,
+                                        Hkv, dh, ws, static_cast<cudaStream_t>(stream));
+    if (e) return cuda_fail(e, who);
+    return MEDUSA_OK;
+}
+
+medusa_status medusa_commit_paged(medusa_dtype dtype, void *k_pages, void *v_pages, int n_pages,
+                                  int page, const int32_t *page_table, int table_stride,
+                                  const int32_t *prefix_len, int P_max, const int32_t *path,
+                                  const int32_t *accept_len, int B, int K, int R, int Hkv, int dh,
+                                  int32_t *new_prefix_len, void *ws, size_t ws_bytes,
+                                  medusa_stream stream) {
+    const NvtxRange range("medusa_commit_paged");
+    const char *who = "medusa_commit_paged";
+    if (medusa_status s = check_heads_shape(who, dtype, B, R, MEDUSA_MAX_TREE_ROWS, Hkv, Hkv, dh))
+        return s;
+    PagedCache cache;
+    if (medusa_status s = check_pages(who, k_pages, v_pages, n_pages, page, page_table, table_stride,
+                                      prefix_len, P_max, R, cache))
+        return s;
+    if (!path || !accept_len || !new_prefix_len)
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+    if (new_prefix_len == prefix_len)
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: new_prefix_len must not alias prefix_len", who);
+    if (K < 0 || K > MEDUSA_MAX_HEADS)
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: K=%d outside 0..%d", who, K, MEDUSA_MAX_HEADS);
+    if (medusa_status s = check_ws(ws, ws_bytes, MEDUSA_WS_HEADER, who)) return s;
+    cudaError_t e = launch_commit_paged(dtype == MEDUSA_BF16 ? 2 : 4, k_pages, v_pages, cache,
+                                        prefix_len, P_max, path, accept_len, B, K, R, Hkv, dh,
+                                        new_prefix_len, ws, static_cast<cudaStream_t>(stream));
+    if (e) return cuda_fail(e, who);
+    return MEDUSA_OK;
+}
+
+size_t medusa_paged_attention_workspace_size(medusa_dtype dtype, int B, int R, int H, int Hkv, int dh,
+                                             int P_max) {
+    if (!is_dtype(dtype) || B < 1 || B > 65535 || R < 1 || R > kMaxChunkRows || Hkv < 1 || H < Hkv ||
+        H > 1024 || H % Hkv || (dh != 64 && dh != 128) || P_max < 0 || P_max > kMaxPrefix)
+        return 0;
+    return paged_attention_workspace_bytes(dtype, B, R, H, Hkv, dh, P_max);
+}
+
+medusa_status medusa_chunk_attention_paged(
+    medusa_dtype dtype, const void *q, const void *k_pages, const void *v_pages, int n_pages, int page,
+    const int32_t *page_table, int table_stride, const int32_t *prefix_len, int P_max,
+    const int32_t *n_rows, int B, int R, int H, int Hkv, int dh, float scale, void *out, void *ws,
+    size_t ws_bytes, medusa_stream stream) {
+    const NvtxRange range("medusa_chunk_attention_paged");
+    return paged_attention("medusa_chunk_attention_paged", dtype, q, k_pages, v_pages, n_pages, page,
+                           page_table, table_stride, prefix_len, P_max, nullptr, n_rows,
+                           kMaxChunkRows, B, R, H, Hkv, dh, scale, out, ws, ws_bytes, stream);
+}
+
+medusa_status medusa_tree_attention_paged(
+    medusa_dtype dtype, const void *q, const void *k_pages, const void *v_pages, int n_pages, int page,
+    const int32_t *page_table, int table_stride, const int32_t *prefix_len, int P_max,
+    const uint64_t *anc_mask, int B, int R, int H, int Hkv, int dh, float scale, void *out, void *ws,
+    size_t ws_bytes, medusa_stream stream) {
+    const NvtxRange range("medusa_tree_attention_paged");
+    const char *who = "medusa_tree_attention_paged";
+    if (!anc_mask) return fail(MEDUSA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+    return paged_attention(who, dtype, q, k_pages, v_pages, n_pages, page, page_table, table_stride,
+                           prefix_len, P_max, anc_mask, nullptr, MEDUSA_MAX_TREE_ROWS, B, R, H, Hkv,
+                           dh, scale, out, ws, ws_bytes, stream);
+}
+
+medusa_status medusa_token_logprobs(medusa_dtype dtype, const void *logits, int64_t stride,
+                                    const int32_t *tokens, int N, int V, int top, float temperature,
+                                    float *logp, float *entropy, int32_t *rank, int32_t *top_ids,
+                                    float *top_logp, void *ws, size_t ws_bytes, medusa_stream stream) {
+    const NvtxRange range("medusa_token_logprobs");
+    const char *who = "medusa_token_logprobs";
+    if (!is_dtype(dtype)) return fail(MEDUSA_ERR_INVALID_ARG, "%s: unknown dtype %d", who, (int)dtype);
+    if (!logits || !tokens || !logp || !entropy || !rank || (top > 0 && (!top_ids || !top_logp)))
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+    if (!aligned16(logits))
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: logits must be 16-byte aligned", who);
+    if (N < 1) return fail(MEDUSA_ERR_INVALID_ARG, "%s: N=%d", who, N);
+    if (V < 1 || V > MEDUSA_MAX_VOCAB)
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: V=%d outside 1..%d", who, V, MEDUSA_MAX_VOCAB);
+    if (stride < V || stride > (int64_t)1 << 40)
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: stride=%lld below V=%d", who, (long long)stride, V);
+    if (top < 0 || top > MEDUSA_MAX_TOP_S || top > V)
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: top=%d outside 0..min(V, %d)", who, top,
+                    MEDUSA_MAX_TOP_S);
+    if (!(temperature > 1e-30f) || !(temperature < 1e30f))
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: temperature must be in 1e-30..1e30", who);
+    if (medusa_status s = check_ws(ws, ws_bytes, MEDUSA_WS_HEADER, who)) return s;
+    cudaError_t e = launch_token_logprobs(dtype, logits, stride, tokens, N, V, top, temperature, logp,
+                                          entropy, rank, top_ids, top_logp, ws,
+                                          static_cast<cudaStream_t>(stream));
+    if (e) return cuda_fail(e, who);
+    return MEDUSA_OK;
+}
+
+}  // extern "C"

@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kSimtThreads) cache_attn_simt_kernel(CacheAttn
     const bool live = m < M;
     const int r = live ? m / G : 0, h = g * G + (live ? m - r * G : 0);
     CacheItem it;
-    find_item<false, kKeys>(a, [&](int P) { return KeyRun(P, R, a.window, a.sinks).len; }, it);
+    find_item<false, kKeys>(a, [&](int P, int) { return KeyRun(P, R, a.window, a.sinks).len; }, it);
     const int b = it.b, P = it.P, kbeg = it.kbeg, kend = it.kend;
     const void *kc = it.kc, *vc = it.vc;
     const KeyRun run(P, R, a.window, a.sinks);
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
     const int R = a.R, G = a.H / a.Hkv, M = R * G;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     CacheItem it;
-    if (!find_item<DEAL>(a, [&](int P) { return KeyRun(P, R, a.window, a.sinks).len; }, it)) return;
+    if (!find_item<DEAL>(a, [&](int P, int) { return KeyRun(P, R, a.window, a.sinks).len; }, it)) return;
     const int b = it.b, P = it.P, kbeg = it.kbeg, kend = it.kend;
     const void *kc = it.kc, *vc = it.vc;
     const KeyRun run(P, R, a.window, a.sinks);
@@ -914,8 +914,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
 template <typename T, int DH>
 __global__ void __launch_bounds__(256)
 cache_attn_combine_kernel(const float *__restrict__ part_o, const float2 *__restrict__ part_ml,
-                          const int *__restrict__ starts, int B, int R, int H, int ns,
-                          T *__restrict__ out) {
+                          const int *__restrict__ starts, const int32_t *__restrict__ n_rows, int B,
+                          int R, int H, int ns, T *__restrict__ out) {
     pdl_enter();
     constexpr int PER = DH / 32, AHEAD = 8;
     const int lane = threadIdx.x & 31;
@@ -923,7 +923,9 @@ cache_attn_combine_kernel(const float *__restrict__ part_o, const float2 *__rest
     if (item >= (long long)B * H * R) return;
     const int r = (int)(item % R);
     const long long bh = item / R;
-    const int b = (int)(bh / H), first_range = starts ? starts[b] : b * ns;
+    const int b = (int)(bh / H);
+    if (n_rows && r >= n_rows[b]) return;
+    const int first_range = starts ? starts[b] : b * ns;
     const int NS = starts ? starts[b + 1] - first_range : ns;
     const size_t ml_step = (size_t)H * R, step = ml_step * DH;
     const float2 *ml = part_ml + first_range * ml_step + (bh % H) * R + r;
@@ -993,8 +995,6 @@ cache_attn_combine_kernel(const float *__restrict__ part_o, const float2 *__rest
 
 // ------------------------------------------------------------------- host ---
 
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
 struct CachePlan {
     int row_tiles, ns, window, sinks;
     bool few;   // at most kFewRows rows a KV head
@@ -1063,7 +1063,7 @@ cudaError_t launch_cache_attention(medusa_dtype dtype, bool kv4, const void *q,
                                    int Hkv, int dh, float scale, void *out, void *ws,
                                    cudaStream_t stream) {
     const CachePlan p = cache_plan(dtype, kv4, B, R, H, Hkv, P_max, window, sinks);
-    CacheAttnArgs a;
+    CacheAttnArgs a = {};
     a.q = q;
     a.kc = k_cache;
     a.vc = v_cache;
@@ -1113,17 +1113,22 @@ cudaError_t launch_cache_attention(medusa_dtype dtype, bool kv4, const void *q,
     }
     note_launch();
     if (e || p.ns == 1) return e;
-    const unsigned blocks = (unsigned)(((long long)B * H * R + 7) / 8);
+    return launch_cache_combine(a, dtype, dh, stream);
+}
+
+cudaError_t launch_cache_combine(const CacheAttnArgs &a, medusa_dtype dtype, int dh, cudaStream_t stream) {
+    const unsigned blocks = (unsigned)(((long long)a.B * a.H * a.R + 7) / 8);
     const float *po = a.part_o;
     const float2 *pm = a.part_ml;
-    if (f32)
+    cudaError_t e;
+    if (dtype == MEDUSA_F32)
         e = launch_pdl(dh == 128 ? cache_attn_combine_kernel<float, 128> : cache_attn_combine_kernel<float, 64>,
-                       dim3(blocks), dim3(256), 0, stream, po, pm, (const int *)a.starts, B, R, H, p.ns,
-                       static_cast<float *>(out));
+                       dim3(blocks), dim3(256), 0, stream, po, pm, (const int *)a.starts, a.n_rows, a.B, a.R,
+                       a.H, a.ns, static_cast<float *>(a.out));
     else
         e = launch_pdl(dh == 128 ? cache_attn_combine_kernel<bf16, 128> : cache_attn_combine_kernel<bf16, 64>,
-                       dim3(blocks), dim3(256), 0, stream, po, pm, (const int *)a.starts, B, R, H, p.ns,
-                       static_cast<bf16 *>(out));
+                       dim3(blocks), dim3(256), 0, stream, po, pm, (const int *)a.starts, a.n_rows, a.B, a.R,
+                       a.H, a.ns, static_cast<bf16 *>(a.out));
     note_launch();
     return e;
 }

@@ -4,6 +4,7 @@
 
 #include "kv4.cuh"
 #include "launch.h"
+#include "paged.cuh"
 
 namespace medusa {
 
@@ -26,6 +27,10 @@ struct CacheAttnArgs {
     int *starts;           // [B + 1] first range of each sequence, where they are dealt out
     void *out;
     int *status;
+    // Calls over a paged cache: kc and vc are null, window and sinks 0.
+    const void *kp, *vp;    // pools of K and V
+    PageMap map;
+    const int32_t *n_rows;  // rows of each sequence, or null: all R
 };
 
 // A sequence's visible slots, numbered without a gap.
@@ -50,14 +55,21 @@ __device__ __forceinline__ int row_depth(const CacheAttnArgs &a, int b, int t) {
     return d;
 }
 
+// rows of sequence b
+__device__ __forceinline__ int live_rows(const CacheAttnArgs &a, int b) {
+    return a.n_rows ? max(0, min(a.R, a.n_rows[b])) : a.R;
+}
+
 // Sequence b's prefix and caches, checked; false (and the status set) when
 // the sequence cannot run.
+template <bool PAGED>
 __device__ __forceinline__ bool sequence_ok(const CacheAttnArgs &a, int b, int &P, const void *&kc,
                                             const void *&vc) {
     P = a.prefix_len[b];
-    kc = a.kc[b];
-    vc = a.vc[b];
-    if (!kc || !vc || ((reinterpret_cast<uintptr_t>(kc) | reinterpret_cast<uintptr_t>(vc)) & 15u)) {
+    kc = PAGED ? a.kp : a.kc[b];
+    vc = PAGED ? a.vp : a.vc[b];
+    if (!PAGED && (!kc || !vc ||
+                   ((reinterpret_cast<uintptr_t>(kc) | reinterpret_cast<uintptr_t>(vc)) & 15u))) {
         set_status(a.status, MEDUSA_DEV_BAD_CACHE);
         return false;
     }
@@ -82,17 +94,17 @@ constexpr int kRangeUnit = 64;
 // is cut into ns ranges of its own length.  With DEAL (B <= 32) the B * ns
 // ranges are dealt out by the sequences' lengths: the shortest range size with
 // which all of them together need no more.  The first CTA leaves the first
-// numbers of the sequences' ranges for the join.  `len(P)`: numbered keys of a
-// prefix of P slots.  Called by whole warps; false: no item for this CTA.
-template <bool DEAL, int UNIT = kRangeUnit, typename Len>
+// numbers of the sequences' ranges for the join.  `len(P, b)`: numbered keys of
+// sequence b, whose prefix has P slots.  Called by whole warps; false: no item for this CTA.
+template <bool DEAL, int UNIT = kRangeUnit, bool PAGED = false, typename Len>
 __device__ __forceinline__ bool find_item(const CacheAttnArgs &a, Len len, CacheItem &it) {
     const int idx = blockIdx.z * a.ns + blockIdx.y, lane = threadIdx.x & 31;
     it.range = idx;
     if constexpr (!DEAL) {
         it.b = blockIdx.z;
-        const bool ok = sequence_ok(a, it.b, it.P, it.kc, it.vc);
+        const bool ok = sequence_ok<PAGED>(a, it.b, it.P, it.kc, it.vc);
         if (!ok) it.P = 0;
-        const int n = ok ? len(it.P) : 0;
+        const int n = ok ? len(it.P, it.b) : 0;
         const int size = ((n + UNIT - 1) / UNIT + a.ns - 1) / a.ns * UNIT;
         it.kbeg = blockIdx.y * size;
         it.kend = min(it.kbeg + size, n);
@@ -101,8 +113,8 @@ __device__ __forceinline__ bool find_item(const CacheAttnArgs &a, Len len, Cache
     int P = 0, units = 0;
     const void *kc = nullptr, *vc = nullptr;
     if (lane < a.B) {
-        if (sequence_ok(a, lane, P, kc, vc))
-            units = (len(P) + UNIT - 1) / UNIT;
+        if (sequence_ok<PAGED>(a, lane, P, kc, vc))
+            units = (len(P, lane) + UNIT - 1) / UNIT;
         else
             P = 0;
     }
@@ -135,7 +147,7 @@ __device__ __forceinline__ bool find_item(const CacheAttnArgs &a, Len len, Cache
     it.kc = reinterpret_cast<const void *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(kc), b));
     it.vc = reinterpret_cast<const void *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(vc), b));
     it.kbeg = (idx - __shfl_sync(0xffffffffu, end - n, b)) * size * UNIT;
-    it.kend = min(it.kbeg + size * UNIT, len(it.P));
+    it.kend = min(it.kbeg + size * UNIT, len(it.P, b));
     return true;
 }
 
@@ -180,5 +192,11 @@ __device__ __forceinline__ uint32_t pack_weights(float a, float b) {
 constexpr int kFewRows = 16;
 int cache_few_ctas_per_sm(bool kv4, int rows);
 cudaError_t launch_cache_attention_few(const CacheAttnArgs &a, bool kv4, int dh, cudaStream_t stream);
+
+// Joins the ranges of a call (a.part_o, a.part_ml, a.starts) into a.out; rows behind
+// a sequence's a.n_rows are left alone.
+cudaError_t launch_cache_combine(const CacheAttnArgs &a, medusa_dtype dtype, int dh, cudaStream_t stream);
+
+inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace medusa

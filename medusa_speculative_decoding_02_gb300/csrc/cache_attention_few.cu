@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<KV4, NQ>) cache_attn_few
     // that a tile's slots are consecutive.
     auto pad16 = [](int n) { return (n + 15) & ~15; };
     CacheItem it;
-    if (!find_item<DEAL>(a, [&](int P) {
+    if (!find_item<DEAL>(a, [&](int P, int) {
             const KeyRun r(P, R, a.window, a.sinks);
             return r.len - r.n_sink + pad16(r.n_sink);
         }, it))

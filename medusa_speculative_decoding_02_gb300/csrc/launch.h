@@ -148,4 +148,36 @@ cudaError_t launch_cache_attention(medusa_dtype dtype, bool kv4, const void *q,
                                    int Hkv, int dh, float scale, void *out, void *ws,
                                    cudaStream_t stream);
 
+// A cache in pages, as the calls name it: page numbers of B sequences, `stride` of
+// them each, into pools of n_pages pages of 2^shift rows.
+struct PagedCache {
+    const int32_t *table;
+    int stride, n_pages, shift;
+};
+
+// elt = bytes per element
+cudaError_t launch_paged_append(size_t elt, const void *k, const void *v, long long k_stride,
+                                long long v_stride, void *k_pages, void *v_pages,
+                                const PagedCache &cache, const int32_t *prefix_len, int P_max,
+                                const int32_t *n_rows, int B, int R, int Hkv, int dh, void *ws,
+                                cudaStream_t stream);
+cudaError_t launch_commit_paged(size_t elt, void *k_pages, void *v_pages, const PagedCache &cache,
+                                const int32_t *prefix_len, int P_max, const int32_t *path,
+                                const int32_t *accept_len, int B, int K, int R, int Hkv, int dh,
+                                int32_t *new_prefix_len, void *ws, cudaStream_t stream);
+
+// anc_mask == nullptr: causal rows (with n_rows or all R), otherwise a tree's.
+size_t paged_attention_workspace_bytes(medusa_dtype dtype, int B, int R, int H, int Hkv, int dh,
+                                       int P_max);
+cudaError_t launch_paged_attention(medusa_dtype dtype, const void *q, const void *k_pages,
+                                   const void *v_pages, const PagedCache &cache,
+                                   const int32_t *prefix_len, int P_max, const uint64_t *anc_mask,
+                                   const int32_t *n_rows, int B, int R, int H, int Hkv, int dh,
+                                   float scale, void *out, void *ws, cudaStream_t stream);
+
+cudaError_t launch_token_logprobs(medusa_dtype dtype, const void *logits, long long stride,
+                                  const int32_t *tokens, int N, int V, int top, float temperature,
+                                  float *logp, float *entropy, int32_t *rank, int32_t *top_ids,
+                                  float *top_logp, void *ws, cudaStream_t stream);
+
 }  // namespace medusa

@@ -1,0 +1,314 @@
+// paged_attention.cu -- attention over a cache in pages: a chunk of new tokens
+// (row i of sequence b sees slots 0 .. P + i) or a candidate tree (row i sees the
+// prefix and the slots of its ancestors).
+//
+// Query head h reads KV head h / G (G = H / Hkv).  The rows of a tile are rows that
+// share a KV head, row r * G + g being new row r and query head hk * G + g.  A
+// tile's keys are split into ranges where there are few tiles (find_item), which
+// cache_attn_combine_kernel joins.  A slot whose page number is outside the pool is
+// not seen (and the status is set).  A row that sees nothing gets zeros; rows behind
+// a sequence's n_rows are neither read nor written.
+#include <algorithm>
+
+#include "cache_attention.cuh"
+
+namespace medusa {
+
+namespace {
+
+// ------------------------------------------------------------- CUDA cores ---
+//
+// fp32.  128 threads, 32 rows and 64 keys at a time: thread (ty, tx) of 8 x 16 scores rows
+// 4 ty .. +3 against keys tx, tx + 16, .. and owns columns 4 tx + 64 c .. +3 of
+// those rows' outputs.  The running maximum and sum of a row live in its 16 threads.
+constexpr int kRows = 32, kKeys = 64, kSimtThreads = 128;
+
+template <int DH>
+struct SimtSmem {
+    static constexpr int LD = DH + 4, LP = kKeys + 4;
+    static constexpr int TOTAL = ((kRows + 2 * kKeys) * LD + kRows * LP) * 4 + kKeys * 4;
+};
+
+template <typename T, int DH>
+__global__ void __launch_bounds__(kSimtThreads, 2) paged_attn_simt_kernel(CacheAttnArgs a) {
+    pdl_enter();
+    using L = SimtSmem<DH>;
+    constexpr int LD = L::LD, LP = L::LP, C = DH / 64;
+    extern __shared__ __align__(16) float sf[];
+    float *qs = sf, *ks = qs + kRows * LD, *vs = ks + kKeys * LD, *ps = vs + kKeys * LD;
+    int *key_ok = reinterpret_cast<int *>(ps + kRows * LP);  // the key's page is in the pool
+    const int g = blockIdx.x / a.row_tiles, rt = a.row_tiles - 1 - (blockIdx.x - g * a.row_tiles);
+    const int R = a.R, G = a.H / a.Hkv;
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    CacheItem it;
+    find_item<false, kKeys, true>(a, [&](int P, int b) {
+        const int n = live_rows(a, b);
+        return n == 0 ? 0 : P + (a.anc_mask ? n : min(n, (rt * kRows + kRows - 1) / G + 1));
+    }, it);
+    const int b = it.b, P = it.P, kbeg = it.kbeg, kend = it.kend;
+    const int M = live_rows(a, b) * G;
+    if (rt * kRows >= M) return;  // uniform over the CTA
+    int row[4], head[4];
+    bool live[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int m = rt * kRows + ty * 4 + i;
+        live[i] = m < M;
+        row[i] = live[i] ? m / G : 0;
+        head[i] = g * G + (live[i] ? m - row[i] * G : 0);
+    }
+    auto out_row = [&](int i) {
+        return static_cast<T *>(a.out) + (((size_t)b * R + row[i]) * a.H + head[i]) * DH;
+    };
+    auto part_row = [&](int i) { return ((size_t)it.range * a.H + head[i]) * R + row[i]; };
+    auto store4 = [&](T *p, float4 v) {
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float4 *>(p) = v;
+        } else {
+            *reinterpret_cast<uint2 *>(p) = make_uint2(pack_weights<false>(v.x, v.y), pack_weights<false>(v.z, v.w));
+        }
+    };
+    if (kbeg >= kend) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (!live[i]) continue;
+            if (a.ns == 1) {
+#pragma unroll
+                for (int c = 0; c < C; ++c) store4(out_row(i) + tx * 4 + 64 * c, make_float4(0.f, 0.f, 0.f, 0.f));
+            } else if (tx == 0) {
+                a.part_ml[part_row(i)] = make_float2(-INFINITY, 0.f);
+            }
+        }
+        return;
+    }
+    auto put = [&](float *dst, const T *src) {  // 16 bytes, widened
+        constexpr int N = Vec16<T>::N;
+        float f[N];
+        Vec16<T>::widen(*reinterpret_cast<const uint4 *>(src), f);
+#pragma unroll
+        for (int e = 0; e < N; e += 4)
+            *reinterpret_cast<float4 *>(dst + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+    };
+    constexpr int N = Vec16<T>::N, VR = DH / N;  // vectors a row
+    for (int e = tid; e < kRows * VR; e += kSimtThreads) {
+        const int lr = e / VR, c = (e - lr * VR) * N, m = rt * kRows + lr;
+        const int r = m < M ? m / G : 0, h = g * G + (m < M ? m - r * G : 0);
+        put(qs + lr * LD + c, static_cast<const T *>(a.q) + (((size_t)b * R + r) * a.H + h) * DH + c);
+    }
+    float acc[4][C][4], m_run[4], l_run[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m_run[i] = -INFINITY;
+        l_run[i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][c][e] = 0.f;
+    }
+    const int W = (R + 63) / 64;
+    const T *kp = static_cast<const T *>(a.kp), *vp = static_cast<const T *>(a.vp);
+    // slots below this are seen by every row of the tile
+    const int all = a.anc_mask ? P : P + rt * kRows / G + 1;
+    for (int k0 = kbeg; k0 < kend; k0 += kKeys) {
+        __syncthreads();
+        bool bad = false;
+        for (int e = tid; e < kKeys * VR; e += kSimtThreads) {
+            const int kk = e / VR, c = (e - kk * VR) * N, slot = k0 + kk;
+            bool ok = slot < kend;
+            if (ok) {
+                const int page = a.map.page_of(b, slot);
+                if (a.map.good(page)) {
+                    const size_t at = (a.map.row(page, slot) * a.Hkv + g) * DH + c;
+                    put(ks + kk * LD + c, kp + at);
+                    put(vs + kk * LD + c, vp + at);
+                } else {
+                    ok = false;
+                    set_status(a.status, MEDUSA_DEV_BAD_PAGE);
+                }
+            }
+            if (!ok) {
+                bad = true;
+#pragma unroll
+                for (int x = 0; x < N; x += 4)
+                    *reinterpret_cast<float4 *>(ks + kk * LD + c + x) =
+                        *reinterpret_cast<float4 *>(vs + kk * LD + c + x) = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            if (c == 0) key_ok[kk] = ok;
+        }
+        const bool masked = __syncthreads_or(bad) || k0 + kKeys > all;
+        float s[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < DH; c += 4) {
+            float4 q[4], k[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4 *>(qs + (ty * 4 + i) * LD + c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const float4 *>(ks + (tx + 16 * j) * LD + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    s[i][j] = fmaf(q[i].x, k[j].x, fmaf(q[i].y, k[j].y, fmaf(q[i].z, k[j].z, fmaf(q[i].w, k[j].w, s[i][j]))));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float cm = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                bool see = true;
+                if (masked) {
+                    const int kk = tx + 16 * j, slot = k0 + kk, t = slot - P;
+                    see = live[i] && key_ok[kk];
+                    if (see && t >= 0)
+                        see = a.anc_mask ? (a.anc_mask[((size_t)b * R + row[i]) * W + (t >> 6)] >> (t & 63)) & 1u
+                                         : t <= row[i];
+                }
+                s[i][j] = see ? s[i][j] * a.scale_log2 : -INFINITY;
+                cm = fmaxf(cm, s[i][j]);
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, o));
+            const float m_new = fmaxf(m_run[i], cm);
+            const float mu = m_new == -INFINITY ? 0.f : m_new;
+            const float alpha = m_run[i] == m_new ? 1.f : exp2f(m_run[i] - mu);
+            m_run[i] = m_new;
+            l_run[i] *= alpha;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p = exp2f(s[i][j] - mu);
+                l_run[i] += p;
+                ps[(ty * 4 + i) * LP + tx + 16 * j] = p;
+            }
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][c][e] *= alpha;
+        }
+        __syncwarp();  // a row's 16 threads are in one warp
+#pragma unroll 2
+        for (int kk = 0; kk < kKeys; kk += 4) {
+            float4 p[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4 *>(ps + (ty * 4 + i) * LP + kk);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const float4 v = *reinterpret_cast<const float4 *>(vs + (kk + u) * LD + tx * 4 + 64 * c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float w = u == 0 ? p[i].x : u == 1 ? p[i].y : u == 2 ? p[i].z : p[i].w;
+                        // a key the row does not see adds nothing, whatever V holds
+                        if (!masked || w != 0.f) {
+                            acc[i][c][0] = fmaf(w, v.x, acc[i][c][0]);
+                            acc[i][c][1] = fmaf(w, v.y, acc[i][c][1]);
+                            acc[i][c][2] = fmaf(w, v.z, acc[i][c][2]);
+                            acc[i][c][3] = fmaf(w, v.w, acc[i][c][3]);
+                        }
+                    }
+                }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], o);
+        if (!live[i]) continue;
+        const float inv = a.ns > 1 ? 1.f : l_run[i] == 0.f ? 0.f : 1.f / l_run[i];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const float4 v = make_float4(acc[i][c][0] * inv, acc[i][c][1] * inv, acc[i][c][2] * inv, acc[i][c][3] * inv);
+            if (a.ns == 1)
+                store4(out_row(i) + tx * 4 + 64 * c, v);
+            else
+                *reinterpret_cast<float4 *>(a.part_o + part_row(i) * DH + tx * 4 + 64 * c) = v;
+        }
+        if (a.ns > 1 && tx == 0) a.part_ml[part_row(i)] = make_float2(m_run[i], l_run[i]);
+    }
+}
+
+// ------------------------------------------------------------------- host ---
+
+struct PagedPlan {
+    int row_tiles, ns;
+};
+
+// Key ranges: the count that makes (waves of CTAs) x (stages per CTA + 3) smallest.
+PagedPlan paged_plan(medusa_dtype dtype, int B, int R, int H, int Hkv, int P_max) {
+    PagedPlan p;
+    const int M = R * (H / Hkv);
+    const int slots = 2 * device_sm_count();
+    p.row_tiles = (M + kRows - 1) / kRows;
+    const int subs = (P_max + R + kKeys - 1) / kKeys;
+    const long long ctas = (long long)B * Hkv * p.row_tiles;
+    double best = 0;
+    p.ns = 1;
+    const int most = std::min<long long>(subs, std::max<long long>(1, 4LL * slots / ctas));
+    for (int ns = 1; ns <= most; ++ns) {
+        const int per = (subs + ns - 1) / ns;
+        if ((subs + per - 1) / per != ns) continue;
+        const double waves = (double)((ctas * ns + slots - 1) / slots);
+        const double cost = waves * (per + 3) + (ns > 1 ? 3.0 + 0.05 * ns : 0.0);
+        if (ns == 1 || cost < best) {
+            best = cost;
+            p.ns = ns;
+        }
+    }
+    return p;
+}
+
+}  // namespace
+
+size_t paged_attention_workspace_bytes(medusa_dtype dtype, int B, int R, int H, int Hkv, int dh,
+                                       int P_max) {
+    const PagedPlan p = paged_plan(dtype, B, R, H, Hkv, P_max);
+    if (p.ns == 1) return MEDUSA_WS_HEADER;
+    const size_t rows = (size_t)B * H * p.ns * R;
+    return MEDUSA_WS_HEADER + align256(rows * dh * sizeof(float)) + align256(rows * sizeof(float2));
+}
+
+cudaError_t launch_paged_attention(medusa_dtype dtype, const void *q, const void *k_pages,
+                                   const void *v_pages, const PagedCache &cache,
+                                   const int32_t *prefix_len, int P_max, const uint64_t *anc_mask,
+                                   const int32_t *n_rows, int B, int R, int H, int Hkv, int dh,
+                                   float scale, void *out, void *ws, cudaStream_t stream) {
+    const PagedPlan p = paged_plan(dtype, B, R, H, Hkv, P_max);
+    CacheAttnArgs a = {};
+    a.q = q;
+    a.kp = k_pages;
+    a.vp = v_pages;
+    a.map = PageMap{cache.table, cache.stride, cache.n_pages, cache.shift};
+    a.prefix_len = prefix_len;
+    a.anc_mask = anc_mask;
+    a.n_rows = n_rows;
+    a.B = B;
+    a.R = R;
+    a.H = H;
+    a.Hkv = Hkv;
+    a.P_max = P_max;
+    a.ns = p.ns;
+    a.row_tiles = p.row_tiles;
+    a.scale_log2 = scale * kLog2e;
+    const size_t rows = (size_t)B * H * p.ns * R;
+    char *w = static_cast<char *>(ws) + MEDUSA_WS_HEADER;
+    a.part_o = reinterpret_cast<float *>(w);
+    a.part_ml = reinterpret_cast<float2 *>(w + align256(rows * dh * sizeof(float)));
+    a.out = out;
+    a.status = static_cast<int *>(ws);
+    const bool f32 = dtype == MEDUSA_F32;
+    auto kern = f32 ? (dh == 128 ? paged_attn_simt_kernel<float, 128> : paged_attn_simt_kernel<float, 64>)
+                    : (dh == 128 ? paged_attn_simt_kernel<bf16, 128> : paged_attn_simt_kernel<bf16, 64>);
+    const int smem = dh == 128 ? SimtSmem<128>::TOTAL : SimtSmem<64>::TOTAL;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e) return e;
+    e = launch_pdl(kern, dim3(Hkv * p.row_tiles, p.ns, B), dim3(kSimtThreads), (size_t)smem, stream, a);
+    note_launch();
+    if (e || p.ns == 1) return e;
+    return launch_cache_combine(a, dtype, dh, stream);
+}
+
+}  // namespace medusa
