@@ -1,5 +1,6 @@
 // cache_attention_few.cu -- attention over the caches for few rows: plain
-// decoding, where a KV head has at most 16 rows (R * H / Hkv).
+// decoding, where a KV head has at most 16 rows (R * H / Hkv), over a cache in one
+// piece or in pages.
 //
 // Such a call reads the cache once and computes little, and the 128-row tiles
 // of the other kernel spend their time on passing stages between warps.  Here
@@ -274,8 +275,9 @@ struct FewSmem {
     static_assert(kFewCtas<KV4, NQ> * (TOTAL + 512 + 1024) <= 196 * 1024, "in the heads' carveout");
 };
 
-template <int DH, bool KV4, int NQ, bool DEAL>
+template <int DH, bool KV4, int NQ, bool DEAL, bool PAGED>
 __global__ void __launch_bounds__(kFewThreads, kFewCtas<KV4, NQ>) cache_attn_few_kernel(CacheAttnArgs a) {
+    static_assert(!(KV4 && PAGED), "pages hold bf16 rows");
     pdl_enter();
     using Tile = FewTile<DH, KV4>;
     using S = FewSmem<DH, KV4, NQ>;
@@ -286,20 +288,25 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<KV4, NQ>) cache_attn_few
     __shared__ int row_win[Q], row_far[Q];
 
     const int head = blockIdx.x;
-    const int R = a.R, G = a.H / a.Hkv, M = R * G;
+    const int R = a.R, G = a.H / a.Hkv;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     // The numbers here leave a gap after the sinks, up to a multiple of 16, so
     // that a tile's slots are consecutive.
     auto pad16 = [](int n) { return (n + 15) & ~15; };
     CacheItem it;
-    if (!find_item<DEAL>(a, [&](int P, int) {
+    if (!find_item<DEAL, kRangeUnit, PAGED>(a, [&](int P, int b) {
+            if constexpr (PAGED) {
+                const int n = live_rows(a, b);
+                return n ? P + n : 0;
+            }
             const KeyRun r(P, R, a.window, a.sinks);
             return r.len - r.n_sink + pad16(r.n_sink);
         }, it))
         return;
     const int b = it.b, P = it.P, kbeg = it.kbeg, kend = it.kend;
-    const KeyRun run(P, R, a.window, a.sinks);
-    const int n_pad = pad16(run.n_sink), last = P + R - 1;
+    const int rows = PAGED ? live_rows(a, b) : R, M = rows * G;
+    const KeyRun run(P, rows, PAGED ? 0 : a.window, PAGED ? 0 : a.sinks);
+    const int n_pad = pad16(run.n_sink), last = P + rows - 1;
     auto slot = [&](int x) { return x < n_pad ? x : x - n_pad + run.lo; };
     bf16 *out = static_cast<bf16 *>(a.out);
     auto out_row = [&](int m) { return out + (((size_t)b * R + m / G) * a.H + head * G + m % G) * DH; };
@@ -321,10 +328,30 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<KV4, NQ>) cache_attn_few
     char *ring = sm + warp * S::WARP;
     const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
     const typename Tile::Copy copy_tile(it, head, KV4 ? kv4_code_bytes(a.Hkv, DH) : 0, lane);
+    // In pages: a tile's 16 slots lie in one, whose number is read a tile before its
+    // copies.  A tile of a bad page copies rows of page 0 (bad_places: which ring
+    // places hold such), and no row sees its keys.
+    int page = 0;
+    uint32_t bad_places = 0;
+    auto look_up = [&](int x) {
+        if (PAGED && x < kend) page = a.map.page_of(b, x);
+    };
     auto copy = [&](int x, int place) {
-        if (x < kend) copy_tile(ring_at + place * Tile::BYTES, row_bytes, slot(x), last, lane);
+        if constexpr (PAGED) {
+            if (x < kend) {
+                const bool ok = a.map.good(page);
+                if (!ok) set_status(a.status, MEDUSA_DEV_BAD_PAGE);
+                bad_places = (bad_places & ~(1u << place)) | (ok ? 0u : 1u << place);
+                const int row = (int)a.map.row(ok ? page : 0, x);
+                copy_tile(ring_at + place * Tile::BYTES, row_bytes, row, row + min(last - x, 15), lane);
+            }
+            look_up(x + kStep);
+        } else if (x < kend) {
+            copy_tile(ring_at + place * Tile::BYTES, row_bytes, slot(x), last, lane);
+        }
         asm volatile("cp.async.commit_group;\n" ::: "memory");
     };
+    look_up(x_warp);
 #pragma unroll
     for (int i = 0; i < D - 1; ++i) copy(x_warp + i * kStep, i);
 
@@ -335,7 +362,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<KV4, NQ>) cache_attn_few
         int win = 0, far = 0;
         if (tid < M) {
             const int r = tid / G, d = row_depth(a, b, r);
-            am = a.anc_mask[(size_t)b * R + r];  // R <= 16: one word
+            // R <= 16: one word (a chunk's row sees the rows up to itself)
+            am = PAGED && !a.anc_mask ? (2ull << r) - 1 : a.anc_mask[(size_t)b * R + r];
             if (a.window) {
                 far = max(0, P + d - a.window + 1 - run.lo);
                 win = n_pad + far;
@@ -425,6 +453,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<KV4, NQ>) cache_attn_few
         __syncwarp();  // every lane's copies are there, and the tile before is read
         copy(x0 + (D - 1) * kStep, at == 0 ? D - 1 : at - 1);
         const Tile tl{ring + at * Tile::BYTES, place};
+        const bool bad_page = PAGED && (bad_places >> at) & 1u;
         at = at == D - 1 ? 0 : at + 1;
         // s[..][0], [1]: key g, rows 8n + 2t and + 1; s[..][2], [3]: key g + 8
         float s[NQ][4];
@@ -450,13 +479,13 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<KV4, NQ>) cache_attn_few
                 for (int e = 0; e < 4; ++e) s[n][e] += s2[n][e];
         }
         const bool masked =
-            !(x0 + 16 <= min(kend, x_tree) && (x0 >= x_all || x0 + 16 <= run.n_sink));
+            bad_page || !(x0 + 16 <= min(kend, x_tree) && (x0 >= x_all || x0 + 16 <= run.n_sink));
         if (masked) {
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (!sees(8 * n + 2 * t + (e & 1), x0 + g + 8 * (e >> 1))) s[n][e] = -INFINITY;
+                    if (bad_page || !sees(8 * n + 2 * t + (e & 1), x0 + g + 8 * (e >> 1))) s[n][e] = -INFINITY;
         }
         bool grew = false;
         float cm[NQ][2];
@@ -614,9 +643,10 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<KV4, NQ>) cache_attn_few
     }
 }
 
-template <int DH, bool KV4, int NQ>
+template <int DH, bool KV4, int NQ, bool PAGED = false>
 cudaError_t launch_few(const CacheAttnArgs &a, cudaStream_t stream) {
-    auto kern = a.starts ? cache_attn_few_kernel<DH, KV4, NQ, true> : cache_attn_few_kernel<DH, KV4, NQ, false>;
+    auto kern = a.starts ? cache_attn_few_kernel<DH, KV4, NQ, true, PAGED>
+                         : cache_attn_few_kernel<DH, KV4, NQ, false, PAGED>;
     constexpr int smem = FewSmem<DH, KV4, NQ>::TOTAL;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e) return e;
@@ -631,6 +661,9 @@ int cache_few_ctas_per_sm(bool kv4, int rows) {
 
 cudaError_t launch_cache_attention_few(const CacheAttnArgs &a, bool kv4, int dh, cudaStream_t stream) {
     const bool two = a.R * (a.H / a.Hkv) > 8;
+    if (a.kp && dh == 128)
+        return two ? launch_few<128, false, 2, true>(a, stream) : launch_few<128, false, 1, true>(a, stream);
+    if (a.kp) return two ? launch_few<64, false, 2, true>(a, stream) : launch_few<64, false, 1, true>(a, stream);
     if (kv4 && dh == 128) return two ? launch_few<128, true, 2>(a, stream) : launch_few<128, true, 1>(a, stream);
     if (kv4) return two ? launch_few<64, true, 2>(a, stream) : launch_few<64, true, 1>(a, stream);
     if (dh == 128) return two ? launch_few<128, false, 2>(a, stream) : launch_few<128, false, 1>(a, stream);

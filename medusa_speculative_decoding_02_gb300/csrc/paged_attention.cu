@@ -235,14 +235,17 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_attn_simt_kernel(CacheA
 
 struct PagedPlan {
     int row_tiles, ns;
+    bool few;   // at most kFewRows rows a KV head
+    bool deal;  // ranges dealt out by the sequences' lengths
 };
 
 // Key ranges: the count that makes (waves of CTAs) x (stages per CTA + 3) smallest.
 PagedPlan paged_plan(medusa_dtype dtype, int B, int R, int H, int Hkv, int P_max) {
     PagedPlan p;
     const int M = R * (H / Hkv);
-    const int slots = 2 * device_sm_count();
-    p.row_tiles = (M + kRows - 1) / kRows;
+    p.few = dtype == MEDUSA_BF16 && M <= kFewRows;
+    const int slots = (p.few ? cache_few_ctas_per_sm(false, M) : 2) * device_sm_count();
+    p.row_tiles = p.few ? 1 : (M + kRows - 1) / kRows;
     const int subs = (P_max + R + kKeys - 1) / kKeys;
     const long long ctas = (long long)B * Hkv * p.row_tiles;
     double best = 0;
@@ -258,6 +261,7 @@ PagedPlan paged_plan(medusa_dtype dtype, int B, int R, int H, int Hkv, int P_max
             p.ns = ns;
         }
     }
+    p.deal = p.few && p.ns > 1 && B > 1 && B <= 32;
     return p;
 }
 
@@ -268,7 +272,8 @@ size_t paged_attention_workspace_bytes(medusa_dtype dtype, int B, int R, int H, 
     const PagedPlan p = paged_plan(dtype, B, R, H, Hkv, P_max);
     if (p.ns == 1) return MEDUSA_WS_HEADER;
     const size_t rows = (size_t)B * H * p.ns * R;
-    return MEDUSA_WS_HEADER + align256(rows * dh * sizeof(float)) + align256(rows * sizeof(float2));
+    return MEDUSA_WS_HEADER + align256(rows * dh * sizeof(float)) + align256(rows * sizeof(float2)) +
+           (p.deal ? align256((B + 1) * sizeof(int)) : 0);
 }
 
 cudaError_t launch_paged_attention(medusa_dtype dtype, const void *q, const void *k_pages,
@@ -297,13 +302,23 @@ cudaError_t launch_paged_attention(medusa_dtype dtype, const void *q, const void
     char *w = static_cast<char *>(ws) + MEDUSA_WS_HEADER;
     a.part_o = reinterpret_cast<float *>(w);
     a.part_ml = reinterpret_cast<float2 *>(w + align256(rows * dh * sizeof(float)));
+    a.starts = p.deal ? reinterpret_cast<int *>(reinterpret_cast<char *>(a.part_ml) +
+                                                align256(rows * sizeof(float2)))
+                      : nullptr;
     a.out = out;
     a.status = static_cast<int *>(ws);
+    cudaError_t e;
+    if (p.few) {
+        e = launch_cache_attention_few(a, false, dh, stream);
+        note_launch();
+        if (e || p.ns == 1) return e;
+        return launch_cache_combine(a, dtype, dh, stream);
+    }
     const bool f32 = dtype == MEDUSA_F32;
     auto kern = f32 ? (dh == 128 ? paged_attn_simt_kernel<float, 128> : paged_attn_simt_kernel<float, 64>)
                     : (dh == 128 ? paged_attn_simt_kernel<bf16, 128> : paged_attn_simt_kernel<bf16, 64>);
     const int smem = dh == 128 ? SimtSmem<128>::TOTAL : SimtSmem<64>::TOTAL;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e) return e;
     e = launch_pdl(kern, dim3(Hkv * p.row_tiles, p.ns, B), dim3(kSimtThreads), (size_t)smem, stream, a);
     note_launch();
