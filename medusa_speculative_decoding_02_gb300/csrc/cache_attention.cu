@@ -249,7 +249,6 @@ __global__ void __launch_bounds__(kSimtThreads) cache_attn_simt_kernel(CacheAttn
 // product.  Every wait is bounded; on a timeout the CTA sets the status, waits
 // (bounded) for its products, frees its tensor memory and publishes nothing.
 constexpr int kSub = 64, kTcThreads = 288;
-constexpr uint32_t kDrainPolls = 1u << 16;
 constexpr int kAhead = 4;  // 4-bit tiles held in a loader's registers
 
 template <int DH>
@@ -294,23 +293,6 @@ __device__ __forceinline__ bool softmax_any(bool p) {
         : "r"((int)p)
         : "memory");
     return r != 0;
-}
-
-// Wait of a converged warp for a phase, giving up after `limit` polls or once
-// the CTA has failed.  The votes keep the loop free of divergence.
-__device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, uint32_t limit,
-                                             volatile int *failed) {
-    for (uint32_t i = 0; i < limit; ++i) {
-        if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
-        if (__any_sync(0xffffffffu, *failed)) return false;
-    }
-    *failed = 1;
-    return false;
-}
-
-// the lowest n bits (n may be negative or past 64)
-__device__ __forceinline__ uint64_t bits_below(int n) {
-    return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
 }
 
 // ---- loader, bf16 cache: 128 threads; thread t copies 16-byte column t % CPR

@@ -5,6 +5,7 @@
 #include "kv4.cuh"
 #include "launch.h"
 #include "paged.cuh"
+#include "tcgen05.cuh"
 
 namespace medusa {
 
@@ -185,6 +186,26 @@ __device__ __forceinline__ uint32_t pack_weights(float a, float b) {
     }
 }
 
+// polls after which the wait for a CTA's own products and copies gives up
+constexpr uint32_t kDrainPolls = 1u << 16;
+
+// Wait of a converged warp for a phase, giving up after `limit` polls or once
+// the CTA has failed.  The votes keep the loop free of divergence.
+__device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, uint32_t limit,
+                                             volatile int *failed) {
+    for (uint32_t i = 0; i < limit; ++i) {
+        if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, *failed)) return false;
+    }
+    *failed = 1;
+    return false;
+}
+
+// the lowest n bits (n may be negative or past 64)
+__device__ __forceinline__ uint64_t bits_below(int n) {
+    return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
+}
+
 // Kernel for few rows (cache_attention_few.cu): rows a KV head may have, and the
 // launch.  At 16 rows, eight sequences of 8192 slots and eight KV heads it takes
 // 47.2 us against 50.1 of the 128-row tiles (4 bits 32.5 against 42.5), at 1 row
@@ -192,6 +213,11 @@ __device__ __forceinline__ uint32_t pack_weights(float a, float b) {
 constexpr int kFewRows = 16;
 int cache_few_ctas_per_sm(bool kv4, int rows);
 cudaError_t launch_cache_attention_few(const CacheAttnArgs &a, bool kv4, int dh, cudaStream_t stream);
+
+// Kernel for more rows over a cache in pages (paged_attention_tc.cu), on 256-row
+// tiles and 128-key stages.
+constexpr int kPagedTileRows = 256, kPagedStage = 128;
+cudaError_t launch_paged_attention_tc(const CacheAttnArgs &a, int dh, cudaStream_t stream);
 
 // Joins the ranges of a call (a.part_o, a.part_ml, a.starts) into a.out; rows behind
 // a sequence's a.n_rows are left alone.

@@ -59,6 +59,7 @@
 #include "launch.h"
 #include "philox.cuh"
 #include "tcgen05.cuh"
+#include "tensor_map.h"
 #include "topk.cuh"
 
 namespace medusa {
@@ -528,24 +529,6 @@ heads_tc_kernel(const __grid_constant__ TcMaps maps, const TcArgs a) {
 
 // ------------------------------------------------------------- host ---
 
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encoder() {
-    static EncodeTiled fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                             cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return static_cast<EncodeTiled>(nullptr);
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return fn;
-}
-
 // Tensor maps are plain host-side descriptors; encoding them costs host time
 // only, so the last few are kept by (address, shape, box).
 struct MapKey {
@@ -571,7 +554,7 @@ bool encode_rows(CUtensorMap *out, const void *base, uint64_t rows, uint64_t col
             *out = e.second;
             return true;
         }
-    EncodeTiled fn = encoder();
+    EncodeTiled fn = tensor_map_encoder();
     if (!fn) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)kKb, rows, cols / kKb};
     const cuuint64_t strides[2] = {cols * 2, (cuuint64_t)kKb * 2};

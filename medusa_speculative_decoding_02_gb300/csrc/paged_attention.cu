@@ -8,6 +8,9 @@
 // cache_attn_combine_kernel joins.  A slot whose page number is outside the pool is
 // not seen (and the status is set).  A row that sees nothing gets zeros; rows behind
 // a sequence's n_rows are neither read nor written.
+//
+// Three kernels: fp32 on the CUDA cores here, bf16 with at most 16 rows a KV head in
+// cache_attention_few.cu, bf16 with more in paged_attention_tc.cu.
 #include <algorithm>
 
 #include "cache_attention.cuh"
@@ -29,7 +32,7 @@ struct SimtSmem {
     static constexpr int TOTAL = ((kRows + 2 * kKeys) * LD + kRows * LP) * 4 + kKeys * 4;
 };
 
-template <typename T, int DH>
+template <int DH>
 __global__ void __launch_bounds__(kSimtThreads, 2) paged_attn_simt_kernel(CacheAttnArgs a) {
     pdl_enter();
     using L = SimtSmem<DH>;
@@ -58,16 +61,10 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_attn_simt_kernel(CacheA
         head[i] = g * G + (live[i] ? m - row[i] * G : 0);
     }
     auto out_row = [&](int i) {
-        return static_cast<T *>(a.out) + (((size_t)b * R + row[i]) * a.H + head[i]) * DH;
+        return static_cast<float *>(a.out) + (((size_t)b * R + row[i]) * a.H + head[i]) * DH;
     };
     auto part_row = [&](int i) { return ((size_t)it.range * a.H + head[i]) * R + row[i]; };
-    auto store4 = [&](T *p, float4 v) {
-        if constexpr (sizeof(T) == 4) {
-            *reinterpret_cast<float4 *>(p) = v;
-        } else {
-            *reinterpret_cast<uint2 *>(p) = make_uint2(pack_weights<false>(v.x, v.y), pack_weights<false>(v.z, v.w));
-        }
-    };
+    auto store4 = [&](float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; };
     if (kbeg >= kend) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -81,19 +78,14 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_attn_simt_kernel(CacheA
         }
         return;
     }
-    auto put = [&](float *dst, const T *src) {  // 16 bytes, widened
-        constexpr int N = Vec16<T>::N;
-        float f[N];
-        Vec16<T>::widen(*reinterpret_cast<const uint4 *>(src), f);
-#pragma unroll
-        for (int e = 0; e < N; e += 4)
-            *reinterpret_cast<float4 *>(dst + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+    auto put = [&](float *dst, const float *src) {
+        *reinterpret_cast<float4 *>(dst) = *reinterpret_cast<const float4 *>(src);
     };
-    constexpr int N = Vec16<T>::N, VR = DH / N;  // vectors a row
+    constexpr int VR = DH / 4;  // 16-byte vectors a row
     for (int e = tid; e < kRows * VR; e += kSimtThreads) {
-        const int lr = e / VR, c = (e - lr * VR) * N, m = rt * kRows + lr;
+        const int lr = e / VR, c = (e - lr * VR) * 4, m = rt * kRows + lr;
         const int r = m < M ? m / G : 0, h = g * G + (m < M ? m - r * G : 0);
-        put(qs + lr * LD + c, static_cast<const T *>(a.q) + (((size_t)b * R + r) * a.H + h) * DH + c);
+        put(qs + lr * LD + c, static_cast<const float *>(a.q) + (((size_t)b * R + r) * a.H + h) * DH + c);
     }
     float acc[4][C][4], m_run[4], l_run[4];
 #pragma unroll
@@ -106,14 +98,14 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_attn_simt_kernel(CacheA
             for (int e = 0; e < 4; ++e) acc[i][c][e] = 0.f;
     }
     const int W = (R + 63) / 64;
-    const T *kp = static_cast<const T *>(a.kp), *vp = static_cast<const T *>(a.vp);
+    const float *kp = static_cast<const float *>(a.kp), *vp = static_cast<const float *>(a.vp);
     // slots below this are seen by every row of the tile
     const int all = a.anc_mask ? P : P + rt * kRows / G + 1;
     for (int k0 = kbeg; k0 < kend; k0 += kKeys) {
         __syncthreads();
         bool bad = false;
         for (int e = tid; e < kKeys * VR; e += kSimtThreads) {
-            const int kk = e / VR, c = (e - kk * VR) * N, slot = k0 + kk;
+            const int kk = e / VR, c = (e - kk * VR) * 4, slot = k0 + kk;
             bool ok = slot < kend;
             if (ok) {
                 const int page = a.map.page_of(b, slot);
@@ -128,10 +120,8 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_attn_simt_kernel(CacheA
             }
             if (!ok) {
                 bad = true;
-#pragma unroll
-                for (int x = 0; x < N; x += 4)
-                    *reinterpret_cast<float4 *>(ks + kk * LD + c + x) =
-                        *reinterpret_cast<float4 *>(vs + kk * LD + c + x) = make_float4(0.f, 0.f, 0.f, 0.f);
+                store4(ks + kk * LD + c, make_float4(0.f, 0.f, 0.f, 0.f));
+                store4(vs + kk * LD + c, make_float4(0.f, 0.f, 0.f, 0.f));
             }
             if (c == 0) key_ok[kk] = ok;
         }
@@ -243,10 +233,12 @@ struct PagedPlan {
 PagedPlan paged_plan(medusa_dtype dtype, int B, int R, int H, int Hkv, int P_max) {
     PagedPlan p;
     const int M = R * (H / Hkv);
-    p.few = dtype == MEDUSA_BF16 && M <= kFewRows;
-    const int slots = (p.few ? cache_few_ctas_per_sm(false, M) : 2) * device_sm_count();
-    p.row_tiles = p.few ? 1 : (M + kRows - 1) / kRows;
-    const int subs = (P_max + R + kKeys - 1) / kKeys;
+    const bool simt = dtype == MEDUSA_F32;
+    p.few = !simt && M <= kFewRows;
+    const int rows = simt ? kRows : kPagedTileRows, sub = simt || p.few ? kKeys : kPagedStage;
+    const int slots = (p.few ? cache_few_ctas_per_sm(false, M) : simt ? 2 : 1) * device_sm_count();
+    p.row_tiles = p.few ? 1 : (M + rows - 1) / rows;
+    const int subs = (P_max + R + sub - 1) / sub;
     const long long ctas = (long long)B * Hkv * p.row_tiles;
     double best = 0;
     p.ns = 1;
@@ -261,7 +253,7 @@ PagedPlan paged_plan(medusa_dtype dtype, int B, int R, int H, int Hkv, int P_max
             p.ns = ns;
         }
     }
-    p.deal = p.few && p.ns > 1 && B > 1 && B <= 32;
+    p.deal = !simt && p.ns > 1 && B > 1 && B <= 32;
     return p;
 }
 
@@ -307,20 +299,17 @@ cudaError_t launch_paged_attention(medusa_dtype dtype, const void *q, const void
                       : nullptr;
     a.out = out;
     a.status = static_cast<int *>(ws);
+    a.wait_polls = wait_budget();
     cudaError_t e;
-    if (p.few) {
-        e = launch_cache_attention_few(a, false, dh, stream);
-        note_launch();
-        if (e || p.ns == 1) return e;
-        return launch_cache_combine(a, dtype, dh, stream);
+    if (dtype == MEDUSA_F32) {
+        auto kern = dh == 128 ? paged_attn_simt_kernel<128> : paged_attn_simt_kernel<64>;
+        const int smem = dh == 128 ? SimtSmem<128>::TOTAL : SimtSmem<64>::TOTAL;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e) return e;
+        e = launch_pdl(kern, dim3(Hkv * p.row_tiles, p.ns, B), dim3(kSimtThreads), (size_t)smem, stream, a);
+    } else {
+        e = p.few ? launch_cache_attention_few(a, false, dh, stream) : launch_paged_attention_tc(a, dh, stream);
     }
-    const bool f32 = dtype == MEDUSA_F32;
-    auto kern = f32 ? (dh == 128 ? paged_attn_simt_kernel<float, 128> : paged_attn_simt_kernel<float, 64>)
-                    : (dh == 128 ? paged_attn_simt_kernel<bf16, 128> : paged_attn_simt_kernel<bf16, 64>);
-    const int smem = dh == 128 ? SimtSmem<128>::TOTAL : SimtSmem<64>::TOTAL;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e) return e;
-    e = launch_pdl(kern, dim3(Hkv * p.row_tiles, p.ns, B), dim3(kSimtThreads), (size_t)smem, stream, a);
     note_launch();
     if (e || p.ns == 1) return e;
     return launch_cache_combine(a, dtype, dh, stream);

@@ -1,0 +1,634 @@
+// paged_attention_tc.cu -- attention over a cache in pages on the tensor cores:
+// prompt chunks and trees with more than 16 rows a KV head, bf16.
+//
+// One CTA an SM (twelve warps) works on up to 256 rows that share a KV head, in two
+// tiles A and B of 128 rows, over stages of 128 keys:
+//   warps 0-3, 4-7  softmax of tile A and of tile B: thread t owns row t, reads its 128
+//              scores from tensor memory, keeps the row's reference m and sum l in
+//              registers, and writes the weights P over the scores, as the bf16 A
+//              operand of the second product.
+//   warp 8     products: S = Q K^T (both operands in shared memory), O += P V (P in
+//              tensor memory).  The tiles take turns: while the softmax of one
+//              works, the products of the other run.
+//   warp 9     copies: K and V of a stage, one TMA box a page (and 64 columns),
+//              into a ring of tiles in the order of their use.
+//   warps 10-11  look for infinities and NaNs in the V of stages that some row
+//              does not see wholly, and clear them before the product.
+// With at most 128 rows the two tiles hold the same rows, A the even stages and B the
+// odd ones, so that the work still takes turns; their results are joined at the end.
+//
+// Tensor memory (512 columns): S / P of A, S / P of B, O of A, O of B.  The reference
+// m moves only when a stage's maximum exceeds it by 2^8, and O is then rescaled in
+// tensor memory.
+//
+// Masks are built as 128 bits a row and stage, in stages that a warp's rows do not
+// see wholly.  A weight of zero times an infinity in V would be a NaN in every row, so
+// such elements are cleared; a row that does see one adds it at the end, from the
+// cache itself.  Every wait is bounded; on a timeout the CTA sets the status, waits
+// (bounded) for its products and copies, frees its tensor memory and publishes
+// nothing.
+#include "cache_attention.cuh"
+#include "tensor_map.h"
+
+namespace medusa {
+
+namespace {
+
+constexpr int kThreads = 384, kCheckThreads = 64;
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;  // 256 * 216 + 128 * 72 = 384 * 168
+constexpr int kMaskedStages = 4;  // stages that hold new rows: at most 3 (255 keys apart)
+
+template <int DH>
+struct PagedSmem {
+    static constexpr int NB = DH / 64;
+    static constexpr int BLOCK = 128 * 128;          // 128 rows of 64 elements
+    static constexpr int TILE = NB * BLOCK;          // Q tile, K or V of a stage
+    static constexpr int NT = 4 * (128 / DH);        // ring
+    static constexpr int RING = 2 * TILE;
+    static constexpr int BAR = RING + NT * TILE;
+    // full[NT], empty[NT], q[2], s[2], p[2], o[2], drain, armed and clean[kMaskedStages]
+    static constexpr int WORDS = BAR + (2 * NT + 9 + 2 * kMaskedStages) * 8;
+    // failed, tmem, bad (a V element is not finite), pad; bad keys [kMaskedStages][4]
+    static constexpr int TOTAL = WORDS + 16 + kMaskedStages * 16;
+    // B's rows and their (m, l) for the join of the halves, in place of the Q tiles and
+    // the ring
+    static constexpr int LD = DH + 4;
+    static_assert(128 * (LD * 4 + 8) <= BAR, "the join fits before the barriers");
+    static_assert(TOTAL + 1024 <= 227 * 1024, "shared memory of an SM");
+};
+
+struct PagedMaps {
+    CUtensorMap k, v;
+};
+
+__device__ __forceinline__ bool pair_not_finite(uint4 w) {
+    return pair_bad<false>(w.x) || pair_bad<false>(w.y) || pair_bad<false>(w.z) || pair_bad<false>(w.w);
+}
+
+// 32 lanes x 128 consecutive 32-bit columns: four loads in flight, one wait
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
+    uint32_t r[128];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        uint32_t *q = r + 32 * h;
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+            "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+            : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]), "=r"(q[4]), "=r"(q[5]), "=r"(q[6]),
+              "=r"(q[7]), "=r"(q[8]), "=r"(q[9]), "=r"(q[10]), "=r"(q[11]), "=r"(q[12]), "=r"(q[13]),
+              "=r"(q[14]), "=r"(q[15]), "=r"(q[16]), "=r"(q[17]), "=r"(q[18]), "=r"(q[19]),
+              "=r"(q[20]), "=r"(q[21]), "=r"(q[22]), "=r"(q[23]), "=r"(q[24]), "=r"(q[25]),
+              "=r"(q[26]), "=r"(q[27]), "=r"(q[28]), "=r"(q[29]), "=r"(q[30]), "=r"(q[31])
+            : "r"(taddr + 32 * h));
+    }
+    // the wait names the registers, so no use can move above it
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 128; ++i) {
+        asm volatile("" : "+r"(r[i]));
+        v[i] = __uint_as_float(r[i]);
+    }
+}
+
+template <int DH, bool DEAL>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs a) {
+    pdl_enter();
+    using L = PagedSmem<DH>;
+    constexpr int NT = L::NT;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BAR), *empty = full + NT, *bar_q = empty + NT,
+             *bar_s = bar_q + 2, *bar_p = bar_q + 4, *bar_o = bar_q + 6, *bar_drain = bar_q + 8,
+             *armed = bar_q + 9, *clean = armed + kMaskedStages;
+    volatile int *failed = reinterpret_cast<volatile int *>(sm + L::WORDS);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(sm + L::WORDS + 4);
+    int *bad_v = reinterpret_cast<int *>(sm + L::WORDS + 8);
+    uint32_t *bad_keys = reinterpret_cast<uint32_t *>(sm + L::WORDS + 16);
+
+    const int g = blockIdx.x % a.Hkv, rt = a.row_tiles - 1 - (int)(blockIdx.x / a.Hkv);  // most keys first
+    const int R = a.R, G = a.H / a.Hkv;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const bool tree = a.anc_mask != nullptr;
+    const int m0 = rt * kPagedTileRows;
+    CacheItem it;
+    // slots that the last of the first `rows` rows sees (a tree's rows: all)
+    auto keys_of = [&](int P, int n, int rows) { return P + (tree ? n : min(n, (rows - 1) / G + 1)); };
+    if (!find_item<DEAL, kPagedStage, true>(a, [&](int P, int b) {
+            const int n = live_rows(a, b);
+            return n == 0 ? 0 : DEAL ? P + n : keys_of(P, n, m0 + kPagedTileRows);
+        }, it))
+        return;
+    const int b = it.b, P = it.P;
+    const int n = live_rows(a, b), M = n * G;
+    if (m0 >= M) return;  // uniform over the CTA
+    const int rows = min(kPagedTileRows, M - m0);
+    const bool split = rows <= 128;  // A and B are the same rows, by turns of the stages
+    const int kbeg = it.kbeg, kend = min(it.kend, keys_of(P, n, m0 + rows));
+
+    // row of a softmax thread
+    const int side = (warp >> 2) & 1, t = tid & 127;
+    const int m = m0 + (split ? 0 : side * 128) + t;
+    const bool live = tid < 256 && m < M;
+    const int r = live ? m / G : 0, h = g * G + (live ? m - r * G : 0);
+    const size_t prow = ((size_t)it.range * a.H + h) * R + r;
+    bf16 *dst = static_cast<bf16 *>(a.out) + (((size_t)b * R + r) * a.H + h) * DH;
+    auto publish_nothing = [&] {
+        if (!live || (split && side)) return;
+        if (a.ns == 1) {
+#pragma unroll
+            for (int c = 0; c < DH; c += 8) *reinterpret_cast<uint4 *>(dst + c) = make_uint4(0, 0, 0, 0);
+        } else {
+            a.part_ml[prow] = make_float2(-INFINITY, 0.f);
+        }
+    };
+    if (kbeg >= kend) {  // uniform over the CTA
+        publish_nothing();
+        return;
+    }
+    const int nsub = (kend - kbeg + kPagedStage - 1) / kPagedStage;
+    // stages of tile A that hold keys one of its rows sees (of B: all nsub)
+    const int nsub_a = split ? nsub
+                             : max(0, min(nsub, (keys_of(P, n, m0 + 128) - kbeg + kPagedStage - 1) / kPagedStage));
+    // the first stage that some row of the CTA does not see wholly
+    const int all = tree ? P : min(P + m0 / G + 1, kend);
+    const int j_masked = max(0, (all - kbeg) / kPagedStage);
+
+    if (tid == 0) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            tc::mbar_init(full + i, 1);
+            tc::mbar_init(empty + i, 1);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(bar_q + i, 128);
+            tc::mbar_init(bar_s + i, 1);
+            tc::mbar_init(bar_p + i, 128);
+            tc::mbar_init(bar_o + i, 1);
+        }
+        tc::mbar_init(bar_drain, 1);
+#pragma unroll
+        for (int i = 0; i < kMaskedStages; ++i) {
+            tc::mbar_init(armed + i, 1);
+            tc::mbar_init(clean + i, kCheckThreads);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) bad_keys[4 * i + w] = 0;
+        }
+        *failed = 0;
+        *bad_v = 0;
+        tc::fence_mbarrier_init();
+    }
+    if (warp == 8) tc::tmem_alloc(tmem_holder, 512);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_holder;
+
+    // The ring's tiles in the order of their use: K0 V0 K1 V1 .., or for halves K0 K1 V0 K2 V1 ..
+    auto k_tile = [&](int j) { return split ? (j == 0 ? 0 : 2 * j - 1) : 2 * j; };
+    auto v_tile = [&](int j) { return split ? min(2 * j + 2, 2 * nsub - 1) : 2 * j + 1; };
+    auto wait_full = [&](int i) {
+        return wait_or_fail(full + i % NT, (i / NT) & 1, a.wait_polls, failed);
+    };
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+        if (warp == 9) {
+            // -------------------------------------------------------- copies
+            const int box = min(1 << a.map.shift, 128);
+            // lane: one box of the tile (a box of 128 rows brings all columns)
+            const int per = box == 128 ? 1 : L::NB, boxes = box == 128 ? 1 : 128 / box * L::NB;
+            const int my = lane / per, half = lane % per;
+            const uint32_t to = half * L::BLOCK + my * box * 128;
+            const int rows_end = a.map.n_pages << a.map.shift;  // past the pool: zeros
+            const int n_tiles = 2 * nsub, end = P + n;
+            auto stage_of = [&](int i) {
+                return split ? (i == 0 ? 0 : i == n_tiles - 1 ? nsub - 1 : (i & 1) ? (i + 1) / 2 : i / 2 - 1) : i >> 1;
+            };
+            auto row_of = [&](int i) {  // the lane's pool row of tile i
+                const int slot = kbeg + stage_of(i) * kPagedStage + my * box;
+                if (lane >= boxes || slot >= end) return rows_end;
+                const int page = a.map.page_of(b, slot);
+                return a.map.good(page) ? (int)a.map.row(page, slot) : rows_end;
+            };
+            auto is_v = [&](int i) { return split ? (i > 0 && (i & 1) == 0) || i == n_tiles - 1 : (i & 1) == 1; };
+            int next = row_of(0), issued = 0;
+            for (int i = 0; i < n_tiles; ++i) {
+                const int row = next;
+                if (i + 1 < n_tiles) next = row_of(i + 1);
+                if (i >= NT && !wait_or_fail(empty + i % NT, (i / NT - 1) & 1, a.wait_polls, failed)) break;
+                if (lane == 0) tc::mbar_arrive_expect_tx(full + i % NT, L::TILE);
+                __syncwarp();
+                if (lane < boxes)
+                    tc::tma_load_3d(sm + L::RING + (i % NT) * L::TILE + to, is_v(i) ? &maps.v : &maps.k, 0, row,
+                                    g * L::NB + half, full + i % NT);
+                // (a phase of `full` can be told from the one two before it only by who knows
+                // which tile is in the slot: the checking warps wait from here on)
+                if (is_v(i) && stage_of(i) >= j_masked && lane == 0) tc::mbar_arrive(armed + (stage_of(i) - j_masked));
+                issued = i + 1;
+            }
+            // every copy has landed before the shared memory goes
+            for (int i = max(0, issued - NT); i < issued; ++i)
+                if (!__all_sync(0xffffffffu, tc::mbar_wait_bounded(full + i % NT, (i / NT) & 1, kDrainPolls)))
+                    *failed = 1;
+        } else if (warp == 8) {
+            // ------------------------------------------------------ products
+            // (the warp stays converged; one elected lane issues)
+            constexpr uint32_t id_s = tc::idesc_bf16(128, kPagedStage, 0), id_o = tc::idesc_bf16(128, DH, 1);
+            const uint64_t qd0 = tc::sdesc_sw128(tc::smem_addr(sm), 16, 1024);
+            const uint64_t kd0 = tc::sdesc_sw128(tc::smem_addr(sm + L::RING), 16, 1024);
+            const uint64_t vd0 = tc::sdesc_sw128(tc::smem_addr(sm + L::RING), L::BLOCK, 1024);
+            auto scores = [&](int x, int j, bool last) {  // S of tile x; `last`: K is free then
+                const int i = k_tile(j), slot = i % NT;
+                if (!wait_full(i)) return false;
+                tc::fence_after_sync();
+                if (tc::elect_one()) {
+                    const uint64_t kd = kd0 + (uint64_t)(slot * (L::TILE >> 4));
+                    const uint64_t qd = qd0 + (uint64_t)((split ? 0 : x) * (L::TILE >> 4));
+#pragma unroll
+                    for (int ks = 0; ks < DH / 16; ++ks) {
+                        const int o = ((ks >> 2) * L::BLOCK + (ks & 3) * 32) >> 4;
+                        tc::mma_bf16_ss(tmem + x * 128, qd + o, kd + o, id_s, ks > 0);
+                    }
+                    tc::mma_commit(bar_s + x);
+                    if (last) tc::mma_commit(empty + slot);
+                }
+                __syncwarp();
+                return true;
+            };
+            auto values = [&](int x, int j, int use, bool last) {  // O += P V, the tile's product `use`
+                const int i = v_tile(j), slot = i % NT;
+                if (!wait_full(i)) return false;
+                if (j >= j_masked && !wait_or_fail(clean + (j - j_masked), 0, a.wait_polls, failed)) return false;
+                if (!wait_or_fail(bar_p + x, use & 1, a.wait_polls, failed)) return false;
+                tc::fence_after_sync();
+                if (tc::elect_one()) {
+                    const uint64_t vd = vd0 + (uint64_t)(slot * (L::TILE >> 4));
+#pragma unroll
+                    for (int ks = 0; ks < kPagedStage / 16; ++ks)
+                        tc::mma_bf16_ts(tmem + 256 + x * DH, tmem + x * 128 + ks * 8, vd + ((ks * 16 * 128) >> 4),
+                                        id_o, use > 0 || ks > 0);
+                    tc::mma_commit(bar_o + x);
+                    if (last) tc::mma_commit(empty + slot);
+                }
+                __syncwarp();
+                return true;
+            };
+            bool go = wait_or_fail(bar_q, 0, a.wait_polls, failed);
+            if (split) {
+                go = go && scores(0, 0, true) && (nsub == 1 || scores(1, 1, true));
+                for (int j = 0; j < nsub && go; ++j)
+                    go = values(j & 1, j, j >> 1, true) && (j + 2 >= nsub || scores(j & 1, j + 2, true));
+            } else {
+                if (go && nsub_a > 0) go = scores(0, 0, false);
+                go = go && wait_or_fail(bar_q + 1, 0, a.wait_polls, failed) && scores(1, 0, true);
+                for (int j = 0; j < nsub && go; ++j) {
+                    if (j < nsub_a) go = values(0, j, j, false) && (j + 1 >= nsub_a || scores(0, j + 1, false));
+                    go = go && values(1, j, j, true) && (j + 1 >= nsub || scores(1, j + 1, true));
+                }
+            }
+            // every product issued above is done before the tensor memory is freed
+            if (tc::elect_one()) tc::mma_commit(bar_drain);
+            __syncwarp();
+            if (!__all_sync(0xffffffffu, tc::mbar_wait_bounded(bar_drain, 0, kDrainPolls))) {
+                *failed = 1;
+                if (lane == 0 && a.status) atomicExch(a.status, MEDUSA_DEV_DRAIN_TIMEOUT);
+            }
+        } else {
+            // --------------------------------------- V of masked stages: finite
+            const int c = tid - 320;
+            for (int j = j_masked; j < nsub; ++j) {
+                const int i = v_tile(j);
+                if (!wait_or_fail(armed + (j - j_masked), 0, a.wait_polls, failed) || !wait_full(i)) break;
+                unsigned char *vt = sm + L::RING + (i % NT) * L::TILE;
+#pragma unroll
+                for (int u = 0; u < 2 * L::NB; ++u) {
+                    const int row = c + u * 64;  // of 128-byte rows, 128 a column block
+                    uint4 w[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        w[e] = *reinterpret_cast<const uint4 *>(vt + row * 128 + (e ^ (row & 7)) * 16);
+                    bool bad = false;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) bad = bad || pair_not_finite(w[e]);
+                    if (bad) {
+                        *bad_v = 1;
+                        atomicOr(bad_keys + 4 * (j - j_masked) + ((row & 127) >> 5), 1u << (row & 31));
+#pragma unroll 1
+                        for (int e = 0; e < 64; ++e) {
+                            uint16_t *x = reinterpret_cast<uint16_t *>(vt + row * 128) + e;
+                            if (pair_bad<false>(*x)) *x = 0;
+                        }
+                    }
+                }
+                tc::fence_proxy_async_smem();
+                tc::mbar_arrive(clean + (j - j_masked));
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
+        // ------------------------------------------------------------ softmax
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t t_s = tmem + side * 128 + lane_base, t_o = tmem + 256 + side * DH + lane_base;
+        const int mw = m0 + (split ? 0 : side * 128) + (warp & 3) * 32;  // the warp's first row
+        const bool rows_live = mw < M;                                   // warp-uniform
+        // a masked score, -inf, times the scale has to stay -inf
+        const float row_scale = fmaxf(a.scale_log2, 0x1p-126f);
+        const bf16 *q_row = static_cast<const bf16 *>(a.q) + (((size_t)b * R + r) * a.H + h) * DH;
+        if (!split || side == 0) {
+            unsigned char *qt = sm + side * L::TILE;
+#pragma unroll
+            for (int c = 0; c < DH / 8; ++c) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (live) v = *reinterpret_cast<const uint4 *>(q_row + c * 8);
+                *reinterpret_cast<uint4 *>(qt + (c >> 3) * L::BLOCK + tc::sw128(t, c & 7)) = v;
+            }
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(bar_q + side);
+        }
+        // ---- what this row sees: slots below `mine` and the tree's bits from P on
+        const int mine = tree ? P : P + r + 1;
+        const int warp_all = tree ? P : P + mw / G + 1;  // slots that every row of the warp sees
+        uint64_t am[4] = {0, 0, 0, 0};
+        if (tree && live) {
+            const int W = (R + 63) / 64;
+            const uint64_t *mr = a.anc_mask + ((size_t)b * R + r) * W;
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                if (w < W) am[w] = mr[w];
+        }
+        // 64 keys from slot k0 on that this row sees
+        auto sees64 = [&](int k0) {
+            uint64_t vis = bits_below(mine - k0);
+            if (tree) {
+                const int t0 = k0 - P;  // tree slot of the first key
+                if (t0 > -64) {
+                    if (t0 < 0) {
+                        vis |= am[0] << -t0;
+                    } else {
+                        const int w = t0 >> 6, s = t0 & 63;
+                        const uint64_t lo = w == 0 ? am[0] : w == 1 ? am[1] : w == 2 ? am[2] : w == 3 ? am[3] : 0ull;
+                        const uint64_t hi = w == 0 ? am[1] : w == 1 ? am[2] : w == 2 ? am[3] : 0ull;
+                        vis |= (lo >> s) | (s ? hi << (64 - s) : 0ull);
+                    }
+                }
+            }
+            vis &= bits_below(kend - k0);
+            return live ? vis : 0ull;
+        };
+        const int box_log2 = min(a.map.shift, 7), boxes = 128 >> box_log2;
+        const int step = split ? 2 : 1, mine_n = side == 0 ? nsub_a : nsub;
+
+        float m_run = -INFINITY, l_run = 0.f;
+        bool dead = false;  // warp-uniform
+        int use = 0;
+        for (int j = split ? side : 0; j < mine_n && !dead; j += step, ++use) {
+            const int k0 = kbeg + j * kPagedStage;
+            // pages of the stage, one a lane
+            bool bad_page = false;
+            if (lane < boxes && k0 + (lane << box_log2) < kend)
+                bad_page = !a.map.good(a.map.page_of(b, k0 + (lane << box_log2)));
+            dead = !wait_or_fail(bar_s + side, use & 1, a.wait_polls, failed);
+            if (dead) break;
+            tc::fence_after_sync();
+            if (rows_live) {
+                float x[kPagedStage];
+                tmem_ld128(t_s, x);
+                const uint32_t bad_pages = __ballot_sync(0xffffffffu, bad_page);
+                if (k0 + kPagedStage > min(warp_all, kend) || bad_pages) {
+                    uint64_t vis[2] = {sees64(k0), sees64(k0 + 64)};
+                    if (bad_pages) {
+                        if (lane == 0) set_status(a.status, MEDUSA_DEV_BAD_PAGE);
+                        for (int e = 0; e < boxes; ++e)
+                            if ((bad_pages >> e) & 1u) {
+                                const int at = e << box_log2, to = at + (1 << box_log2);
+                                vis[0] &= ~(bits_below(to) & ~bits_below(at));
+                                vis[1] &= ~(bits_below(to - 64) & ~bits_below(at - 64));
+                            }
+                    }
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t v = (uint32_t)(vis[w >> 1] >> (32 * (w & 1)));
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[32 * w + e] = (v >> e) & 1u ? x[32 * w + e] : -INFINITY;
+                    }
+                }
+                float mx[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    mx[i] = max3f(x[i], x[i + 4], x[i + 8]);
+#pragma unroll
+                    for (int e = 12; e + 4 < kPagedStage; e += 8) mx[i] = max3f(mx[i], x[i + e], x[i + e + 4]);
+                    mx[i] = fmaxf(mx[i], x[i + kPagedStage - 4]);
+                }
+                const float cm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * row_scale;
+                bool grew = false;
+                float alpha = 1.f;
+                if (cm > m_run + kRescaleLog2) {  // m_run = -inf: the first visible key
+                    alpha = exp2f(m_run - cm);
+                    m_run = cm;
+                    l_run *= alpha;
+                    grew = true;
+                }
+                const float mu = m_run == -INFINITY ? 0.f : m_run;
+                // past 2^16 the scores are rounded before the difference, as the maximum
+                // was: the fused form keeps bits of the product that the maximum lost,
+                // and the largest weight would leave 1
+                float sc = row_scale;
+                if (__any_sync(0xffffffffu, fabsf(mu) > 65536.f)) {
+#pragma unroll
+                    for (int e = 0; e < kPagedStage; ++e) x[e] *= row_scale;
+                    sc = 1.f;
+                }
+                const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-mu, -mu);
+                float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float2 y = __ffma2_rn(make_float2(x[64 * c + 2 * e], x[64 * c + 2 * e + 1]), sc2, nm2);
+                        const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
+                        // Rounded to bf16 for the product only, whose operands are of one
+                        // 16-bit type, at most 2^-8 of a weight; the sum adds the fp32
+                        // weights.
+                        pk[e] = pack_weights<false>(p0, p1);
+                        ls[e & 1] = __fadd2_rn(ls[e & 1], make_float2(p0, p1));
+                    }
+                    tc::tmem_st32u(t_s + 32 * c, pk);
+                }
+                l_run += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+                if (__any_sync(0xffffffffu, grew && use > 0)) {
+                    dead = !wait_or_fail(bar_o + side, (use - 1) & 1, a.wait_polls, failed);
+                    tc::fence_after_sync();
+                    if (!dead) {
+#pragma unroll 1
+                        for (int c = 0; c < DH; c += 32) {
+                            float ov[32];
+                            tc::tmem_ld32(t_o + c, ov);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) ov[e] *= alpha;
+                            tc::tmem_st32(t_o + c, ov);
+                        }
+                    }
+                }
+                tc::tmem_wait_st();
+            }
+            if (!dead) {
+                tc::fence_before_sync();
+                tc::mbar_arrive(bar_p + side);
+            }
+        }
+        // ---- the last product, then the row
+        if (!dead && use > 0) dead = !wait_or_fail(bar_o + side, (use - 1) & 1, a.wait_polls, failed);
+        tc::fence_after_sync();
+        // what V's infinities and NaNs add to 32 columns of the row, from the cache
+        auto add_not_finite = [&](int c0, float (&ov)[32]) {
+#pragma unroll 1
+            for (int j = j_masked; j < nsub; ++j) {
+                if (split && (j & 1) != side) continue;
+#pragma unroll 1
+                for (int key = 0; key < kPagedStage; ++key) {
+                    if (!((bad_keys[4 * (j - j_masked) + (key >> 5)] >> (key & 31)) & 1u)) continue;
+                    const int slot = kbeg + j * kPagedStage + key;
+                    if (!((sees64(slot & ~63) >> (slot & 63)) & 1ull)) continue;
+                    const int page = a.map.page_of(b, slot);
+                    if (!a.map.good(page)) continue;
+                    const size_t at = (a.map.row(page, slot) * a.Hkv + g) * DH;
+                    const bf16 *kr = static_cast<const bf16 *>(a.kp) + at;
+                    const bf16 *vr = static_cast<const bf16 *>(a.vp) + at;
+                    float s = 0.f;
+#pragma unroll 1
+                    for (int c = 0; c < DH; ++c) s = fmaf(__bfloat162float(q_row[c]), __bfloat162float(kr[c]), s);
+                    const float p = exp2f(s * row_scale - m_run);
+                    if (p == 0.f) continue;
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const float v = __bfloat162float(vr[c0 + c]);
+                        if (!isfinite(v)) ov[c] += p * v;
+                    }
+                }
+            }
+        };
+        const bool odd_v = *reinterpret_cast<volatile int *>(bad_v) != 0;
+        float *join = reinterpret_cast<float *>(sm) + t * L::LD;
+        float2 *join_ml = reinterpret_cast<float2 *>(sm + 128 * L::LD * 4) + t;
+        const bool none = use == 0;  // no stage was this half's
+        if (split) {
+            // B's half goes through shared memory: every product has read its operands
+            asm volatile("barrier.cta.sync 1, 256;\n" ::: "memory");
+            if (side == 1 && !dead && rows_live && !none) {
+#pragma unroll 1
+                for (int c = 0; c < DH; c += 32) {
+                    float ov[32];
+                    tc::tmem_ld32(t_o + c, ov);
+                    if (odd_v && live) add_not_finite(c, ov);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4 *>(join + c + e) = make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+                }
+            }
+            if (side == 1) *join_ml = make_float2(m_run, l_run);
+            asm volatile("barrier.cta.sync 1, 256;\n" ::: "memory");
+            dead = __any_sync(0xffffffffu, dead || *failed);  // the other half's wait as well
+        }
+        if (dead) {
+            publish_nothing();
+        } else if (rows_live && !(split && side)) {
+            // weights of the halves: 2^(m - top)
+            float fa = 1.f, fb = 0.f, top = m_run, l = l_run;
+            if (split) {
+                const float mb = join_ml->x, lb = join_ml->y;
+                top = fmaxf(m_run, mb);
+                const float mu = top == -INFINITY ? 0.f : top;
+                fa = exp2f(m_run - mu);
+                fb = exp2f(mb - mu);
+                // (also with a factor of 0: a row of NaN scores has m = -inf, l = NaN)
+                l = fa * l_run + fb * lb;
+            }
+            const float inv = a.ns > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+            fa *= inv;
+            fb *= inv;
+#pragma unroll 1
+            for (int c = 0; c < DH; c += 32) {
+                float ov[32];
+                if (none) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) ov[e] = 0.f;
+                } else {
+                    tc::tmem_ld32(t_o + c, ov);
+                }
+                if (!live) continue;
+                if (odd_v) add_not_finite(c, ov);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) ov[e] *= fa;
+                if (fb != 0.f) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 o = *reinterpret_cast<const float4 *>(join + c + e);
+                        ov[e] = fmaf(fb, o.x, ov[e]);
+                        ov[e + 1] = fmaf(fb, o.y, ov[e + 1]);
+                        ov[e + 2] = fmaf(fb, o.z, ov[e + 2]);
+                        ov[e + 3] = fmaf(fb, o.w, ov[e + 3]);
+                    }
+                }
+                if (a.ns == 1) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        *reinterpret_cast<uint4 *>(dst + c + e) =
+                            make_uint4(pack_weights<false>(ov[e], ov[e + 1]), pack_weights<false>(ov[e + 2], ov[e + 3]),
+                                       pack_weights<false>(ov[e + 4], ov[e + 5]), pack_weights<false>(ov[e + 6], ov[e + 7]));
+                } else {
+                    float *po = a.part_o + prow * DH + c;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4 *>(po + e) = make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+                }
+            }
+            if (live && a.ns > 1) a.part_ml[prow] = make_float2(top, l);
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (tid == 0 && *failed) set_status(a.status, MEDUSA_DEV_TIMEOUT);
+    if (warp == 8) tc::tmem_dealloc(tmem, 512);
+}
+
+// A pool as [Hkv dh / 64][rows][64] for boxes of `box` rows (all of a head's columns
+// where a box is a whole stage), 128-byte swizzle, zeros past the rows.
+bool encode_pool(CUtensorMap *map, const void *pool, const CacheAttnArgs &a, int dh) {
+    EncodeTiled fn = tensor_map_encoder();
+    if (!fn) return false;
+    const uint32_t box_rows = a.map.shift >= 7 ? 128u : 1u << a.map.shift;
+    const cuuint64_t cols = (cuuint64_t)a.Hkv * dh;
+    const cuuint64_t dims[3] = {64, (cuuint64_t)a.map.n_pages << a.map.shift, cols / 64};
+    const cuuint64_t strides[2] = {cols * 2, 128};
+    const cuuint32_t box[3] = {64, box_rows, box_rows == 128 ? (cuuint32_t)dh / 64 : 1u};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(pool), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DH>
+cudaError_t launch(const PagedMaps &maps, const CacheAttnArgs &a, cudaStream_t stream) {
+    auto kern = a.starts ? paged_attn_tc_kernel<DH, true> : paged_attn_tc_kernel<DH, false>;
+    constexpr int smem = PagedSmem<DH>::TOTAL;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e) return e;
+    return launch_pdl(kern, dim3(a.Hkv * a.row_tiles, a.ns, a.B), dim3(kThreads), (size_t)smem, stream, maps, a);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_attention_tc(const CacheAttnArgs &a, int dh, cudaStream_t stream) {
+    PagedMaps maps;
+    if (!encode_pool(&maps.k, a.kp, a, dh) || !encode_pool(&maps.v, a.vp, a, dh)) {
+        set_last_error("tensor maps of the pools could not be made (cuTensorMapEncodeTiled failed)");
+        return cudaErrorInvalidValue;
+    }
+    return dh == 128 ? launch<128>(maps, a, stream) : launch<64>(maps, a, stream);
+}
+
+}  // namespace medusa
