@@ -276,11 +276,6 @@ __device__ __forceinline__ int tile_stage(int i, int n) {
 __device__ __forceinline__ int k_tile(int j) { return j == 0 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ int v_tile(int j, int n) { return min(2 * j + 2, 2 * n - 1); }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool ok) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
-                 "r"(ok ? 16 : 0));
-}
-
 // barrier of the 128 softmax threads that also ORs a predicate
 __device__ __forceinline__ bool softmax_any(bool p) {
     int r;

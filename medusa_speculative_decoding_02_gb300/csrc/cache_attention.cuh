@@ -186,6 +186,12 @@ __device__ __forceinline__ uint32_t pack_weights(float a, float b) {
     }
 }
 
+// 16 bytes into shared memory, zeros unless `ok`
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
+                 "r"(ok ? 16 : 0));
+}
+
 // polls after which the wait for a CTA's own products and copies gives up
 constexpr uint32_t kDrainPolls = 1u << 16;
 

@@ -10,10 +10,9 @@
 //   warp 8     products: S = Q K^T (both operands in shared memory), O += P V (P in
 //              tensor memory).  The tiles take turns: while the softmax of one
 //              works, the products of the other run.
-//   warp 9     copies: K and V of a stage, one TMA box a page (and 64 columns),
-//              into a ring of tiles in the order of their use.
-//   warps 10-11  look for infinities and NaNs in the V of stages that some row
-//              does not see wholly, and clear them before the product.
+//   warps 9, 10  copies: K and V of a stage, one TMA box a page (and 64 columns),
+//              into a ring each.
+//   warp 11    nothing (register budgets are by four warps).
 // With at most 128 rows the two tiles hold the same rows, A the even stages and B the
 // odd ones, so that the work still takes turns; their results are joined at the end.
 //
@@ -23,8 +22,9 @@
 //
 // Masks are built as 128 bits a row and stage, in stages that a warp's rows do not
 // see wholly.  A weight of zero times an infinity in V would be a NaN in every row, so
-// such elements are cleared; a row that does see one adds it at the end, from the
-// cache itself.  Every wait is bounded; on a timeout the CTA sets the status, waits
+// the softmax warps (of B, or of the stage's half) look for such elements before those
+// stages and clear them; a row that does see one adds it at the end, from the cache
+// itself.  Every wait is bounded; on a timeout the CTA sets the status, waits
 // (bounded) for its products and copies, frees its tensor memory and publishes
 // nothing.
 #include "cache_attention.cuh"
@@ -34,7 +34,7 @@ namespace medusa {
 
 namespace {
 
-constexpr int kThreads = 384, kCheckThreads = 64;
+constexpr int kThreads = 384;
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;  // 256 * 216 + 128 * 72 = 384 * 168
 constexpr int kMaskedStages = 4;  // stages that hold new rows: at most 3 (255 keys apart)
 
@@ -43,11 +43,11 @@ struct PagedSmem {
     static constexpr int NB = DH / 64;
     static constexpr int BLOCK = 128 * 128;          // 128 rows of 64 elements
     static constexpr int TILE = NB * BLOCK;          // Q tile, K or V of a stage
-    static constexpr int NT = 4 * (128 / DH);        // ring
+    static constexpr int NK = 2 * (128 / DH), NT = 2 * NK;  // stages in the rings of K and of V
     static constexpr int RING = 2 * TILE;
     static constexpr int BAR = RING + NT * TILE;
-    // full[NT], empty[NT], q[2], s[2], p[2], o[2], drain, armed and clean[kMaskedStages]
-    static constexpr int WORDS = BAR + (2 * NT + 9 + 2 * kMaskedStages) * 8;
+    // full[NT], empty[NT], q[2], s[2], o[2], p[2][2], drain, armed and clean[kMaskedStages]
+    static constexpr int WORDS = BAR + (2 * NT + 11 + 2 * kMaskedStages) * 8;
     // failed, tmem, bad (a V element is not finite), pad; bad keys [kMaskedStages][4]
     static constexpr int TOTAL = WORDS + 16 + kMaskedStages * 16;
     // B's rows and their (m, l) for the join of the halves, in place of the Q tiles and
@@ -96,11 +96,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs a) {
     pdl_enter();
     using L = PagedSmem<DH>;
-    constexpr int NT = L::NT;
+    constexpr int NK = L::NK, NT = 2 * NK;
     extern __shared__ __align__(1024) unsigned char sm[];
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BAR), *empty = full + NT, *bar_q = empty + NT,
-             *bar_s = bar_q + 2, *bar_p = bar_q + 4, *bar_o = bar_q + 6, *bar_drain = bar_q + 8,
-             *armed = bar_q + 9, *clean = armed + kMaskedStages;
+             *bar_s = bar_q + 2, *bar_o = bar_q + 4, *bar_p = bar_q + 6, *bar_drain = bar_q + 10,
+             *armed = bar_q + 11, *clean = armed + kMaskedStages;
     volatile int *failed = reinterpret_cast<volatile int *>(sm + L::WORDS);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(sm + L::WORDS + 4);
     int *bad_v = reinterpret_cast<int *>(sm + L::WORDS + 8);
@@ -130,16 +130,38 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
     const int side = (warp >> 2) & 1, t = tid & 127;
     const int m = m0 + (split ? 0 : side * 128) + t;
     const bool live = tid < 256 && m < M;
-    const int r = live ? m / G : 0, h = g * G + (live ? m - r * G : 0);
-    const size_t prow = ((size_t)it.range * a.H + h) * R + r;
-    bf16 *dst = static_cast<bf16 *>(a.out) + (((size_t)b * R + r) * a.H + h) * DH;
+    const int r = live ? m / G : 0;
+    const int mw = m0 + (split ? 0 : side * 128) + (warp & 3) * 32;  // the warp's first row
+    // row of q and out, and of the partial results, in rows of DH elements
+    auto row_at = [&](int r, int gq) { return ((size_t)b * R + r) * a.H + g * G + gq; };
+    auto part_at = [&](int r, int gq) { return ((size_t)it.range * a.H + g * G + gq) * R + r; };
     auto publish_nothing = [&] {
         if (!live || (split && side)) return;
         if (a.ns == 1) {
+            bf16 *dst = static_cast<bf16 *>(a.out) + row_at(r, m - r * G) * DH;
 #pragma unroll
             for (int c = 0; c < DH; c += 8) *reinterpret_cast<uint4 *>(dst + c) = make_uint4(0, 0, 0, 0);
         } else {
-            a.part_ml[prow] = make_float2(-INFINITY, 0.f);
+            a.part_ml[part_at(r, m - r * G)] = make_float2(-INFINITY, 0.f);
+        }
+    };
+    // The warp's 32 rows in pieces of 16 bytes, kCols pieces a row: f(row of the 32,
+    // piece, new row, query head of the group) for the lane's of each kPass rows,
+    // so that a warp's accesses to global memory are whole rows.
+    constexpr int kCols = DH / 8, kPass = 32 / kCols;
+    auto for_rows = [&](auto f) {
+        const int first = mw + lane / kCols;
+        int rr = first / G, gg = first - rr * G;
+        const int dr = kPass / G, dg = kPass - dr * G;
+#pragma unroll 4
+        for (int i = 0; i < 32; i += kPass) {
+            f(i + lane / kCols, lane % kCols, rr, gg);
+            rr += dr;
+            gg += dg;
+            if (gg >= G) {
+                gg -= G;
+                ++rr;
+            }
         }
     };
     if (kbeg >= kend) {  // uniform over the CTA
@@ -164,14 +186,15 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(bar_q + i, 128);
             tc::mbar_init(bar_s + i, 1);
-            tc::mbar_init(bar_p + i, 128);
+            tc::mbar_init(bar_p + 2 * i, 128);
+            tc::mbar_init(bar_p + 2 * i + 1, 128);
             tc::mbar_init(bar_o + i, 1);
         }
         tc::mbar_init(bar_drain, 1);
 #pragma unroll
         for (int i = 0; i < kMaskedStages; ++i) {
             tc::mbar_init(armed + i, 1);
-            tc::mbar_init(clean + i, kCheckThreads);
+            tc::mbar_init(clean + i, 128);
 #pragma unroll
             for (int w = 0; w < 4; ++w) bad_keys[4 * i + w] = 0;
         }
@@ -180,21 +203,30 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
         tc::fence_mbarrier_init();
     }
     if (warp == 8) tc::tmem_alloc(tmem_holder, 512);
+    if (warp < 8 && !(split && side)) {  // Q: rows that are not there are zeros
+        const uint32_t qt = tc::smem_addr(sm + side * L::TILE);
+        const bf16 *q = static_cast<const bf16 *>(a.q);
+        for_rows([&](int i, int c, int rr, int gg) {
+            const bool ok = mw + i < M;
+            cp_async16(qt + (c >> 3) * L::BLOCK + tc::sw128((warp & 3) * 32 + i, c & 7),
+                       ok ? q + row_at(rr, gg) * DH + c * 8 : q, ok);
+        });
+        asm volatile("cp.async.commit_group;\n" ::: "memory");
+    }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_holder;
 
-    // The ring's tiles in the order of their use: K0 V0 K1 V1 .., or for halves K0 K1 V0 K2 V1 ..
-    auto k_tile = [&](int j) { return split ? (j == 0 ? 0 : 2 * j - 1) : 2 * j; };
-    auto v_tile = [&](int j) { return split ? min(2 * j + 2, 2 * nsub - 1) : 2 * j + 1; };
-    auto wait_full = [&](int i) {
-        return wait_or_fail(full + i % NT, (i / NT) & 1, a.wait_polls, failed);
+    // place of stage j's K or V among the slots, a ring for each
+    auto slot_of = [&](int j, bool vs) { return (vs ? NK : 0) + j % NK; };
+    auto wait_full = [&](int j, bool vs) {
+        return wait_or_fail(full + slot_of(j, vs), (j / NK) & 1, a.wait_polls, failed);
     };
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
-        if (warp == 9) {
+        if (warp == 9 || warp == 10) {
             // -------------------------------------------------------- copies
             const int box = min(1 << a.map.shift, 128);
             // lane: one box of the tile (a box of 128 rows brings all columns)
@@ -202,35 +234,32 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
             const int my = lane / per, half = lane % per;
             const uint32_t to = half * L::BLOCK + my * box * 128;
             const int rows_end = a.map.n_pages << a.map.shift;  // past the pool: zeros
-            const int n_tiles = 2 * nsub, end = P + n;
-            auto stage_of = [&](int i) {
-                return split ? (i == 0 ? 0 : i == n_tiles - 1 ? nsub - 1 : (i & 1) ? (i + 1) / 2 : i / 2 - 1) : i >> 1;
-            };
-            auto row_of = [&](int i) {  // the lane's pool row of tile i
-                const int slot = kbeg + stage_of(i) * kPagedStage + my * box;
+            const int end = P + n;
+            const bool vs = warp == 10;
+            auto row_of = [&](int j) {  // the lane's pool row of stage j
+                const int slot = kbeg + j * kPagedStage + my * box;
                 if (lane >= boxes || slot >= end) return rows_end;
                 const int page = a.map.page_of(b, slot);
                 return a.map.good(page) ? (int)a.map.row(page, slot) : rows_end;
             };
-            auto is_v = [&](int i) { return split ? (i > 0 && (i & 1) == 0) || i == n_tiles - 1 : (i & 1) == 1; };
+            const CUtensorMap *map = vs ? &maps.v : &maps.k;
             int next = row_of(0), issued = 0;
-            for (int i = 0; i < n_tiles; ++i) {
-                const int row = next;
-                if (i + 1 < n_tiles) next = row_of(i + 1);
-                if (i >= NT && !wait_or_fail(empty + i % NT, (i / NT - 1) & 1, a.wait_polls, failed)) break;
-                if (lane == 0) tc::mbar_arrive_expect_tx(full + i % NT, L::TILE);
+            for (; issued < nsub; ++issued) {
+                const int j = issued, i = slot_of(j, vs), row = next;
+                if (j + 1 < nsub) next = row_of(j + 1);
+                if (j >= NK && !wait_or_fail(empty + i, (j / NK - 1) & 1, a.wait_polls, failed)) break;
+                if (lane == 0) tc::mbar_arrive_expect_tx(full + i, L::TILE);
                 __syncwarp();
                 if (lane < boxes)
-                    tc::tma_load_3d(sm + L::RING + (i % NT) * L::TILE + to, is_v(i) ? &maps.v : &maps.k, 0, row,
-                                    g * L::NB + half, full + i % NT);
+                    tc::tma_load_3d(sm + L::RING + i * L::TILE + to, map, 0, row, g * L::NB + half, full + i);
                 // (a phase of `full` can be told from the one two before it only by who knows
-                // which tile is in the slot: the checking warps wait from here on)
-                if (is_v(i) && stage_of(i) >= j_masked && lane == 0) tc::mbar_arrive(armed + (stage_of(i) - j_masked));
-                issued = i + 1;
+                // which stage is in the slot: the checking warp waits from here on)
+                if (vs && j >= j_masked && lane == 0) tc::mbar_arrive(armed + (j - j_masked));
             }
             // every copy has landed before the shared memory goes
-            for (int i = max(0, issued - NT); i < issued; ++i)
-                if (!__all_sync(0xffffffffu, tc::mbar_wait_bounded(full + i % NT, (i / NT) & 1, kDrainPolls)))
+            for (int j = max(0, issued - NK); j < issued; ++j)
+                if (!__all_sync(0xffffffffu,
+                                tc::mbar_wait_bounded(full + slot_of(j, vs), (j / NK) & 1, kDrainPolls)))
                     *failed = 1;
         } else if (warp == 8) {
             // ------------------------------------------------------ products
@@ -240,8 +269,8 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
             const uint64_t kd0 = tc::sdesc_sw128(tc::smem_addr(sm + L::RING), 16, 1024);
             const uint64_t vd0 = tc::sdesc_sw128(tc::smem_addr(sm + L::RING), L::BLOCK, 1024);
             auto scores = [&](int x, int j, bool last) {  // S of tile x; `last`: K is free then
-                const int i = k_tile(j), slot = i % NT;
-                if (!wait_full(i)) return false;
+                const int slot = slot_of(j, false);
+                if (!wait_full(j, false)) return false;
                 tc::fence_after_sync();
                 if (tc::elect_one()) {
                     const uint64_t kd = kd0 + (uint64_t)(slot * (L::TILE >> 4));
@@ -258,21 +287,24 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
                 return true;
             };
             auto values = [&](int x, int j, int use, bool last) {  // O += P V, the tile's product `use`
-                const int i = v_tile(j), slot = i % NT;
-                if (!wait_full(i)) return false;
+                const int slot = slot_of(j, true);
+                if (!wait_full(j, true)) return false;
                 if (j >= j_masked && !wait_or_fail(clean + (j - j_masked), 0, a.wait_polls, failed)) return false;
-                if (!wait_or_fail(bar_p + x, use & 1, a.wait_polls, failed)) return false;
-                tc::fence_after_sync();
-                if (tc::elect_one()) {
-                    const uint64_t vd = vd0 + (uint64_t)(slot * (L::TILE >> 4));
+                const uint64_t vd = vd0 + (uint64_t)(slot * (L::TILE >> 4));
 #pragma unroll
-                    for (int ks = 0; ks < kPagedStage / 16; ++ks)
-                        tc::mma_bf16_ts(tmem + 256 + x * DH, tmem + x * 128 + ks * 8, vd + ((ks * 16 * 128) >> 4),
-                                        id_o, use > 0 || ks > 0);
-                    tc::mma_commit(bar_o + x);
-                    if (last) tc::mma_commit(empty + slot);
+                for (int half = 0; half < 2; ++half) {  // weights of 64 keys each
+                    if (!wait_or_fail(bar_p + 2 * x + half, use & 1, a.wait_polls, failed)) return false;
+                    tc::fence_after_sync();
+                    if (tc::elect_one()) {
+#pragma unroll
+                        for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+                            tc::mma_bf16_ts(tmem + 256 + x * DH, tmem + x * 128 + ks * 8,
+                                            vd + ((ks * 16 * 128) >> 4), id_o, use > 0 || ks > 0);
+                        if (half) tc::mma_commit(bar_o + x);
+                        if (half && last) tc::mma_commit(empty + slot);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
                 return true;
             };
             bool go = wait_or_fail(bar_q, 0, a.wait_polls, failed);
@@ -295,83 +327,35 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
                 *failed = 1;
                 if (lane == 0 && a.status) atomicExch(a.status, MEDUSA_DEV_DRAIN_TIMEOUT);
             }
-        } else {
-            // --------------------------------------- V of masked stages: finite
-            const int c = tid - 320;
-            for (int j = j_masked; j < nsub; ++j) {
-                const int i = v_tile(j);
-                if (!wait_or_fail(armed + (j - j_masked), 0, a.wait_polls, failed) || !wait_full(i)) break;
-                unsigned char *vt = sm + L::RING + (i % NT) * L::TILE;
-#pragma unroll
-                for (int u = 0; u < 2 * L::NB; ++u) {
-                    const int row = c + u * 64;  // of 128-byte rows, 128 a column block
-                    uint4 w[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        w[e] = *reinterpret_cast<const uint4 *>(vt + row * 128 + (e ^ (row & 7)) * 16);
-                    bool bad = false;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) bad = bad || pair_not_finite(w[e]);
-                    if (bad) {
-                        *bad_v = 1;
-                        atomicOr(bad_keys + 4 * (j - j_masked) + ((row & 127) >> 5), 1u << (row & 31));
-#pragma unroll 1
-                        for (int e = 0; e < 64; ++e) {
-                            uint16_t *x = reinterpret_cast<uint16_t *>(vt + row * 128) + e;
-                            if (pair_bad<false>(*x)) *x = 0;
-                        }
-                    }
-                }
-                tc::fence_proxy_async_smem();
-                tc::mbar_arrive(clean + (j - j_masked));
-            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
         // ------------------------------------------------------------ softmax
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + side * 128 + lane_base, t_o = tmem + 256 + side * DH + lane_base;
-        const int mw = m0 + (split ? 0 : side * 128) + (warp & 3) * 32;  // the warp's first row
-        const bool rows_live = mw < M;                                   // warp-uniform
+        const bool rows_live = mw < M;  // warp-uniform
         // a masked score, -inf, times the scale has to stay -inf
         const float row_scale = fmaxf(a.scale_log2, 0x1p-126f);
-        const bf16 *q_row = static_cast<const bf16 *>(a.q) + (((size_t)b * R + r) * a.H + h) * DH;
-        if (!split || side == 0) {
-            unsigned char *qt = sm + side * L::TILE;
-#pragma unroll
-            for (int c = 0; c < DH / 8; ++c) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (live) v = *reinterpret_cast<const uint4 *>(q_row + c * 8);
-                *reinterpret_cast<uint4 *>(qt + (c >> 3) * L::BLOCK + tc::sw128(t, c & 7)) = v;
-            }
+        if (!(split && side)) {
+            asm volatile("cp.async.wait_group 0;\n" ::: "memory");
             tc::fence_proxy_async_smem();
             tc::mbar_arrive(bar_q + side);
         }
         // ---- what this row sees: slots below `mine` and the tree's bits from P on
         const int mine = tree ? P : P + r + 1;
         const int warp_all = tree ? P : P + mw / G + 1;  // slots that every row of the warp sees
-        uint64_t am[4] = {0, 0, 0, 0};
-        if (tree && live) {
-            const int W = (R + 63) / 64;
-            const uint64_t *mr = a.anc_mask + ((size_t)b * R + r) * W;
-#pragma unroll
-            for (int w = 0; w < 4; ++w)
-                if (w < W) am[w] = mr[w];
-        }
         // 64 keys from slot k0 on that this row sees
         auto sees64 = [&](int k0) {
             uint64_t vis = bits_below(mine - k0);
-            if (tree) {
-                const int t0 = k0 - P;  // tree slot of the first key
-                if (t0 > -64) {
-                    if (t0 < 0) {
-                        vis |= am[0] << -t0;
-                    } else {
-                        const int w = t0 >> 6, s = t0 & 63;
-                        const uint64_t lo = w == 0 ? am[0] : w == 1 ? am[1] : w == 2 ? am[2] : w == 3 ? am[3] : 0ull;
-                        const uint64_t hi = w == 0 ? am[1] : w == 1 ? am[2] : w == 2 ? am[3] : 0ull;
-                        vis |= (lo >> s) | (s ? hi << (64 - s) : 0ull);
-                    }
+            if (tree && k0 + 64 > P && live) {
+                const int t0 = k0 - P, W = (R + 63) / 64;  // tree slot of the first key
+                const uint64_t *mr = a.anc_mask + ((size_t)b * R + r) * W;
+                if (t0 < 0) {
+                    vis |= mr[0] << -t0;
+                } else {
+                    const int w = t0 >> 6, s = t0 & 63;
+                    vis |= w < W ? mr[w] >> s : 0ull;
+                    if (s && w + 1 < W) vis |= mr[w + 1] << (64 - s);
                 }
             }
             vis &= bits_below(kend - k0);
@@ -389,6 +373,33 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
             bool bad_page = false;
             if (lane < boxes && k0 + (lane << box_log2) < kend)
                 bad_page = !a.map.good(a.map.page_of(b, k0 + (lane << box_log2)));
+            if (j >= j_masked && (split || side)) {
+                // ---- infinities and NaNs in V of a stage that some row does not see wholly
+                dead = !wait_or_fail(armed + (j - j_masked), 0, a.wait_polls, failed) || !wait_full(j, true);
+                if (dead) break;
+                unsigned char *vt = sm + L::RING + slot_of(j, true) * L::TILE;
+#pragma unroll
+                for (int u = 0; u < L::NB; ++u) {  // key t's 64 elements of a column block
+                    uint4 w[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        w[e] = *reinterpret_cast<const uint4 *>(vt + u * L::BLOCK + t * 128 + (e ^ (t & 7)) * 16);
+                    bool bad = false;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) bad = bad || pair_not_finite(w[e]);
+                    if (bad) {
+                        *bad_v = 1;
+                        atomicOr(bad_keys + 4 * (j - j_masked) + (t >> 5), 1u << (t & 31));
+#pragma unroll 1
+                        for (int e = 0; e < 64; ++e) {
+                            uint16_t *x = reinterpret_cast<uint16_t *>(vt + u * L::BLOCK + t * 128) + e;
+                            if (pair_bad<false>(*x)) *x = 0;
+                        }
+                    }
+                }
+                tc::fence_proxy_async_smem();
+                tc::mbar_arrive(clean + (j - j_masked));
+            }
             dead = !wait_or_fail(bar_s + side, use & 1, a.wait_polls, failed);
             if (dead) break;
             tc::fence_after_sync();
@@ -441,10 +452,23 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
                     for (int e = 0; e < kPagedStage; ++e) x[e] *= row_scale;
                     sc = 1.f;
                 }
+                if (__any_sync(0xffffffffu, grew && use > 0)) {
+                    dead = !wait_or_fail(bar_o + side, (use - 1) & 1, a.wait_polls, failed);
+                    if (dead) break;
+                    tc::fence_after_sync();
+#pragma unroll 1
+                    for (int c = 0; c < DH; c += 32) {
+                        float ov[32];
+                        tc::tmem_ld32(t_o + c, ov);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) ov[e] *= alpha;
+                        tc::tmem_st32(t_o + c, ov);
+                    }
+                }
                 const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-mu, -mu);
                 float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
+                for (int c = 0; c < 2; ++c) {  // the product begins with the first half
                     uint32_t pk[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
@@ -457,27 +481,15 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
                         ls[e & 1] = __fadd2_rn(ls[e & 1], make_float2(p0, p1));
                     }
                     tc::tmem_st32u(t_s + 32 * c, pk);
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                    tc::mbar_arrive(bar_p + 2 * side + c);
                 }
                 l_run += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
-                if (__any_sync(0xffffffffu, grew && use > 0)) {
-                    dead = !wait_or_fail(bar_o + side, (use - 1) & 1, a.wait_polls, failed);
-                    tc::fence_after_sync();
-                    if (!dead) {
-#pragma unroll 1
-                        for (int c = 0; c < DH; c += 32) {
-                            float ov[32];
-                            tc::tmem_ld32(t_o + c, ov);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) ov[e] *= alpha;
-                            tc::tmem_st32(t_o + c, ov);
-                        }
-                    }
-                }
-                tc::tmem_wait_st();
-            }
-            if (!dead) {
+            } else {
                 tc::fence_before_sync();
-                tc::mbar_arrive(bar_p + side);
+                tc::mbar_arrive(bar_p + 2 * side);
+                tc::mbar_arrive(bar_p + 2 * side + 1);
             }
         }
         // ---- the last product, then the row
@@ -485,6 +497,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
         tc::fence_after_sync();
         // what V's infinities and NaNs add to 32 columns of the row, from the cache
         auto add_not_finite = [&](int c0, float (&ov)[32]) {
+            const bf16 *q_row = static_cast<const bf16 *>(a.q) + row_at(r, m - r * G) * DH;
 #pragma unroll 1
             for (int j = j_masked; j < nsub; ++j) {
                 if (split && (j & 1) != side) continue;
@@ -550,43 +563,64 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
             const float inv = a.ns > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
             fa *= inv;
             fb *= inv;
+            // Rows go out through shared memory, whole rows of bf16 or halves of fp32 at a
+            // time: stored by their threads they took 10700 cycles a CTA (of 81000 for 32
+            // stages), and Q read by them 8200.  The place: the side's Q tile, whose last
+            // product is done, or (halves) one behind what they were joined in.
+            unsigned char *stage = sm + (split ? 3 : side) * L::TILE + (warp & 3) * 32 * DH * 2;
+            auto piece = [&](int row, int c) {
+                return reinterpret_cast<uint4 *>(stage + row * DH * 2 + ((c ^ (row & 7)) << 4));
+            };
+            const int passes = a.ns == 1 ? 1 : 2, wide = DH / passes;  // columns a pass
 #pragma unroll 1
-            for (int c = 0; c < DH; c += 32) {
-                float ov[32];
-                if (none) {
+            for (int pass = 0; pass < passes; ++pass) {
+#pragma unroll 1
+                for (int c = pass * wide; c < (pass + 1) * wide; c += 32) {
+                    float ov[32];
+                    if (none) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) ov[e] = 0.f;
-                } else {
-                    tc::tmem_ld32(t_o + c, ov);
-                }
-                if (!live) continue;
-                if (odd_v) add_not_finite(c, ov);
+                        for (int e = 0; e < 32; ++e) ov[e] = 0.f;
+                    } else {
+                        tc::tmem_ld32(t_o + c, ov);
+                    }
+                    if (odd_v && live) add_not_finite(c, ov);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) ov[e] *= fa;
-                if (fb != 0.f) {
+                    for (int e = 0; e < 32; ++e) ov[e] *= fa;
+                    if (fb != 0.f) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 o = *reinterpret_cast<const float4 *>(join + c + e);
-                        ov[e] = fmaf(fb, o.x, ov[e]);
-                        ov[e + 1] = fmaf(fb, o.y, ov[e + 1]);
-                        ov[e + 2] = fmaf(fb, o.z, ov[e + 2]);
-                        ov[e + 3] = fmaf(fb, o.w, ov[e + 3]);
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 o = *reinterpret_cast<const float4 *>(join + c + e);
+                            ov[e] = fmaf(fb, o.x, ov[e]);
+                            ov[e + 1] = fmaf(fb, o.y, ov[e + 1]);
+                            ov[e + 2] = fmaf(fb, o.z, ov[e + 2]);
+                            ov[e + 3] = fmaf(fb, o.w, ov[e + 3]);
+                        }
+                    }
+                    if (a.ns == 1) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            *piece(lane, (c + e) / 8) =
+                                make_uint4(pack_weights<false>(ov[e], ov[e + 1]), pack_weights<false>(ov[e + 2], ov[e + 3]),
+                                           pack_weights<false>(ov[e + 4], ov[e + 5]), pack_weights<false>(ov[e + 6], ov[e + 7]));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *piece(lane, (c - pass * wide + e) / 4) =
+                                make_uint4(__float_as_uint(ov[e]), __float_as_uint(ov[e + 1]), __float_as_uint(ov[e + 2]),
+                                           __float_as_uint(ov[e + 3]));
                     }
                 }
-                if (a.ns == 1) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        *reinterpret_cast<uint4 *>(dst + c + e) =
-                            make_uint4(pack_weights<false>(ov[e], ov[e + 1]), pack_weights<false>(ov[e + 2], ov[e + 3]),
-                                       pack_weights<false>(ov[e + 4], ov[e + 5]), pack_weights<false>(ov[e + 6], ov[e + 7]));
-                } else {
-                    float *po = a.part_o + prow * DH + c;
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<float4 *>(po + e) = make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
-                }
+                __syncwarp();
+                for_rows([&](int i, int c, int rr, int gg) {
+                    if (mw + i >= M) return;
+                    if (a.ns == 1)
+                        *reinterpret_cast<uint4 *>(static_cast<bf16 *>(a.out) + row_at(rr, gg) * DH + c * 8) = *piece(i, c);
+                    else
+                        *reinterpret_cast<uint4 *>(a.part_o + part_at(rr, gg) * DH + pass * wide + c * 4) = *piece(i, c);
+                });
+                __syncwarp();
             }
-            if (live && a.ns > 1) a.part_ml[prow] = make_float2(top, l);
+            if (live && a.ns > 1) a.part_ml[part_at(r, m - r * G)] = make_float2(top, l);
         }
     }
     tc::fence_before_sync();
