@@ -1,29 +1,53 @@
 // logprobs.cu -- log probabilities of given tokens, with their ranks, the entropy
-// of each row and its top alternatives.
+// of each row and its top alternatives, in one pass over the logits.
 //
-// Row x of V logits, temperature T, token t:
-//     logp = x_t / T - ln sum_i e^(x_i / T)
-//     entropy = -sum_i p_i ln p_i = ln S - ln2 A / S, from the shifted sums
-//         S = sum 2^(y - m), A = sum 2^(y - m) (y - m), y = x log2(e) / T
+// Row x of V logits, temperature T, token t, y = x log2(e) / T, m the row's largest y:
+//     S = sum 2^(y - m),  A = sum 2^(y - m) (y - m)
+//     logp = ln2 (y_t - m - log2 S)       entropy = ln2 (log2 S - A / S)
 //     rank = number of tokens before t in the order (larger logit, then smaller id)
 //     alternatives: the first `top` tokens of that order
+//
+// A CTA (eight warps that compute, one that copies) takes a row at a time, in chunks
+// of 1024 16-byte vectors that come by bulk copies into a ring of four; with few rows
+// a cluster of CTAs shares each row.  A thread keeps its own m, S and A and moves m
+// when a chunk's maximum (packed, NaNs kept) exceeds it; m in base 2 is rounded by a
+// product that is not fused, so that all sums are relative to the same number.  Ranks
+// are packed comparisons with the token's logit, "or equal" before its place.
+// Alternatives: the k-th largest of sixteen groups of threads' maxima over the first
+// chunk is at most the row's k-th largest logit, so only elements that reach it are
+// candidates (some tens); a candidate's place in the order is the number of better
+// ones among them.
+//
+// What this form does not take (a NaN, +inf or nothing above -1e29 in the row, the token
+// at -inf, more than kCandidates candidates because of ties, fewer possible tokens
+// than alternatives, temperatures below 1e-7) is done by slow_row, by plain passes over
+// the row: the results are the same by definition.
+#include <algorithm>
 #include <climits>
 
 #include "common.cuh"
 #include "launch.h"
+#include "tcgen05.cuh"
 
 namespace medusa {
 
 namespace {
 
-constexpr int kLpThreads = 512;
+constexpr int kConsumers = 256, kLpThreads = kConsumers + 32, kWarps = kConsumers / 32;
+constexpr int kChunk = 1024, kPer = kChunk / kConsumers;  // vectors of a chunk, of a thread
+constexpr int kRing = 4, kLpCtas = 3;
+constexpr int kCandidates = 1024, kGroups = 16;
+constexpr int kMaxCluster = 8;
+constexpr uint32_t kLpPolls = 1u << 20;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLowest = -1e30f, kNothing = -1e29f, kHighest = 1e30f;
+static_assert(kGroups >= MEDUSA_MAX_TOP_S, "a group for each alternative");
 
 struct LogprobArgs {
     const void *logits;
     long long stride;
     const int32_t *tokens;
-    int V, top;
+    int N, V, top;
     float inv_T, y_scale;  // 1 / T, log2(e) / T
     float *logp, *entropy;
     int32_t *rank;
@@ -32,58 +56,164 @@ struct LogprobArgs {
     int *status;
 };
 
+// What a CTA of a cluster knows of its part of a row.
+struct RowPart {
+    float m;       // largest logit (NaN if there is one)
+    float S, A;    // relative to m
+    int before, n; // tokens before the row's token; candidates (-1: too many)
+    float val[MEDUSA_MAX_TOP_S];
+    int id[MEDUSA_MAX_TOP_S];  // the part's first tokens
+};
+
+struct LpSmem {
+    static constexpr int RING = 0;
+    static constexpr int CAND = kRing * kChunk * 16;  // (logit, id)
+    static constexpr int PART = CAND + kCandidates * 8;
+    static constexpr int RED = PART + (int)(sizeof(RowPart) + 15) / 16 * 16;  // [4][kWarps]
+    static constexpr int GROUP = RED + 4 * kWarps * 4;                        // [kWarps][kGroups]
+    static constexpr int BAR = GROUP + kWarps * kGroups * 4;
+    static constexpr int WORDS = BAR + 2 * kRing * 8;  // candidates counted, failed
+    static constexpr int TOTAL = WORDS + 16;
+    static_assert(kLpCtas * (TOTAL + 1024) <= 228 * 1024, "CTAs of an SM");
+};
+
+__device__ __forceinline__ void consumers_sync() { asm volatile("barrier.cta.sync 1, 256;\n" ::: "memory"); }
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// Sixteen bytes of logits: the packed steps of a vector.
+template <typename T> struct Lp;
+template <> struct Lp<bf16> {
+    static constexpr int N = 8;
+    using Pair = __nv_bfloat162;
+    __device__ static __forceinline__ uint4 nothing() { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
+    __device__ static __forceinline__ Pair pair(uint32_t w) { return *reinterpret_cast<const Pair *>(&w); }
+    __device__ static __forceinline__ float top(const uint4 &v) {
+        const Pair p = __hmax2_nan(__hmax2_nan(pair(v.x), pair(v.y)), __hmax2_nan(pair(v.z), pair(v.w)));
+        return max_nan(__low2float(p), __high2float(p));
+    }
+    // elements above x (and equal to it)
+    template <bool EQUAL>
+    __device__ static __forceinline__ float above(const uint4 &v, float x) {
+        const Pair b = __float2bfloat162_rn(x);
+        auto c = [&](uint32_t w) { return EQUAL ? __hge2(pair(w), b) : __hgt2(pair(w), b); };
+        const Pair s = __hadd2(__hadd2(c(v.x), c(v.y)), __hadd2(c(v.z), c(v.w)));
+        return __low2float(s) + __high2float(s);
+    }
+    __device__ static __forceinline__ void add(const uint4 &v, float ys, float m2, float2 (&S)[2], float2 (&A)[2]) {
+        const Pair low = __float2bfloat162_rn(kLowest);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // (-inf is lifted: 0 * -inf would make A a NaN)
+            const Pair c = __hmax2(pair(w[i]), low);
+            const uint32_t u = *reinterpret_cast<const uint32_t *>(&c);
+            const float2 t = __ffma2_rn(make_float2(bf_lo(u), bf_hi(u)), make_float2(ys, ys), make_float2(-m2, -m2));
+            const float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+            S[i & 1] = __fadd2_rn(S[i & 1], p);
+            A[i & 1] = __ffma2_rn(p, t, A[i & 1]);
+        }
+    }
+};
+template <> struct Lp<float> {
+    static constexpr int N = 4;
+    __device__ static __forceinline__ uint4 nothing() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
+    __device__ static __forceinline__ float top(const uint4 &v) {
+        return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
+                       max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+    }
+    template <bool EQUAL>
+    __device__ static __forceinline__ float above(const uint4 &v, float x) {
+        auto c = [&](uint32_t w) {
+            const float f = __uint_as_float(w);
+            return (EQUAL ? f >= x : f > x) ? 1.f : 0.f;
+        };
+        return (c(v.x) + c(v.y)) + (c(v.z) + c(v.w));
+    }
+    __device__ static __forceinline__ void add(const uint4 &v, float ys, float m2, float2 (&S)[2], float2 (&A)[2]) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float2 f = make_float2(fmaxf(__uint_as_float(w[2 * i]), kLowest), fmaxf(__uint_as_float(w[2 * i + 1]), kLowest));
+            const float2 t = __ffma2_rn(f, make_float2(ys, ys), make_float2(-m2, -m2));
+            const float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+            S[i] = __fadd2_rn(S[i], p);
+            A[i] = __ffma2_rn(p, t, A[i]);
+        }
+    }
+};
+
+// Where a row's vectors lie: elements N i - off .. of whole 16-byte blocks i in [first,
+// last), the others at the row's ends one by one.
+template <typename T>
+struct RowShape {
+    const char *block;  // block 0: the 16 bytes that hold element 0
+    int off, first, last;
+    int left, edges;    // elements before block `first`; and all outside the whole blocks
+    __device__ __forceinline__ RowShape(const LogprobArgs &a, int row) {
+        constexpr int N = Lp<T>::N;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(static_cast<const T *>(a.logits) + (long long)row * a.stride);
+        block = reinterpret_cast<const char *>(at & ~(uintptr_t)15);
+        off = (int)(at & 15) / (int)sizeof(T);
+        first = off ? 1 : 0;
+        last = (off + a.V) / N;
+        left = off ? min(N - off, a.V) : 0;
+        if (last < first) last = first;
+        edges = a.V - (last - first) * N;
+    }
+    // id of the i-th of the edge elements
+    __device__ __forceinline__ int edge(int i) const { return i < left ? i : i + (last - first) * Lp<T>::N; }
+};
+
 template <typename F>
-__device__ __forceinline__ float block_fold(float v, float *s, F f) {
+__device__ __forceinline__ float fold_consumers(float v, float *s, F f) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
-    __syncthreads();
+    consumers_sync();
     if (lane == 0) s[warp] = v;
-    __syncthreads();
+    consumers_sync();
     v = s[0];
-    for (int w = 1; w < kLpThreads / 32; ++w) v = f(v, s[w]);
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) v = f(v, s[w]);
     return v;
 }
 
+// A row by the definition: a pass for the maximum, one for the sums, one for each
+// alternative.
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(LogprobArgs a) {
-    pdl_enter();
-    __shared__ float s_f[kLpThreads / 32];
-    __shared__ int s_i[kLpThreads / 32];
-    const int row = blockIdx.x, tid = threadIdx.x;
+__device__ __noinline__ void slow_row(const LogprobArgs &a, int row, int tok, float *s_f, int *s_i) {
+    const int tid = threadIdx.x;
     const T *x = static_cast<const T *>(a.logits) + (long long)row * a.stride;
     auto add = [](float p, float q) { return p + q; };
     auto larger = [](float p, float q) { return fmaxf(p, q); };
-    int tok = a.tokens[row];
-    if (tok >= a.V || tok < -1) {
-        if (tid == 0) set_status(a.status, MEDUSA_DEV_BAD_TOKEN);
-        tok = -1;
-    }
     const float xt = tok >= 0 ? Vec16<T>::load1(x + tok) : NAN;
-    float m = -INFINITY, nan = 0.f;
-    for (int i = tid; i < a.V; i += kLpThreads) {
+    float m = -INFINITY, odd = 0.f;
+    for (int i = tid; i < a.V; i += kConsumers) {
         const float f = Vec16<T>::load1(x + i);
         m = fmaxf(m, f);
-        if (!(f < INFINITY)) nan = 1.f;
+        if (!(f < INFINITY)) odd = 1.f;
     }
-    m = block_fold(m, s_f, larger);
-    const bool bad = block_fold(nan, s_f, larger) != 0.f;  // +inf or NaN in the row
+    m = fold_consumers(m, s_f, larger);
+    const bool bad = fold_consumers(odd, s_f, larger) != 0.f;  // +inf or NaN in the row
     float S = 0.f, A = 0.f, before = 0.f;
-    for (int i = tid; i < a.V; i += kLpThreads) {
+    for (int i = tid; i < a.V; i += kConsumers) {
         const float f = Vec16<T>::load1(x + i);
         const float t = fmaxf((f - m) * a.y_scale, -127.f), p = ex2_approx(t);
         S += p;
         A = fmaf(p, t, A);
         if (f > xt || (f == xt && i < tok)) before += 1.f;
     }
-    S = block_fold(S, s_f, add);
-    A = block_fold(A, s_f, add);
-    before = block_fold(before, s_f, add);
+    S = fold_consumers(S, s_f, add);
+    A = fold_consumers(A, s_f, add);
+    before = fold_consumers(before, s_f, add);
     const bool none = m == -INFINITY;  // nothing is possible
     const float ls = log2f(S);
-    auto logp_of = [&](float f) {
-        return bad ? NAN : none ? -INFINITY : ((f - m) * a.inv_T - ls * kLn2);
-    };
+    auto logp_of = [&](float f) { return bad ? NAN : none ? -INFINITY : (f - m) * a.inv_T - ls * kLn2; };
     if (tid == 0) {
         a.logp[row] = tok < 0 ? 0.f : logp_of(xt);
         a.rank[row] = tok < 0 || isnan(xt) ? -1 : (int)before;
@@ -96,7 +226,7 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(LogprobArgs 
         float bv = -INFINITY;
         int bi = INT_MAX;
         if (any)
-            for (int i = tid; i < a.V; i += kLpThreads) {
+            for (int i = tid; i < a.V; i += kConsumers) {
                 const float f = Vec16<T>::load1(x + i);
                 if (!isnan(f) && (k == 0 || better(lv, li, f, i)) && (bi == INT_MAX || better(f, i, bv, bi))) {
                     bv = f;
@@ -109,10 +239,10 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(LogprobArgs 
             const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
             if (better(ov, oi, bv, bi)) bv = ov, bi = oi;
         }
-        __syncthreads();
+        consumers_sync();
         if ((tid & 31) == 0) s_f[tid >> 5] = bv, s_i[tid >> 5] = bi;
-        __syncthreads();
-        for (int w = 0; w < kLpThreads / 32; ++w)
+        consumers_sync();
+        for (int w = 0; w < kWarps; ++w)
             if (better(s_f[w], s_i[w], bv, bi)) bv = s_f[w], bi = s_i[w];
         any = bi != INT_MAX;
         if (tid == 0) {
@@ -122,6 +252,397 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(LogprobArgs 
         lv = bv;
         li = bi;
     }
+}
+
+__device__ __forceinline__ void bulk_copy(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                     tc::smem_addr(dst)),
+                 "l"(src), "r"(bytes), "r"(tc::smem_addr(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;\n" ::: "memory");
+}
+// generic address of `p` in the shared memory of CTA `rank` of the cluster
+template <typename P>
+__device__ __forceinline__ const P *cluster_ptr(const P *p, uint32_t rank) {
+    uint64_t r;
+    asm("mapa.u64 %0, %1, %2;\n" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
+    return reinterpret_cast<const P *>(r);
+}
+
+// What the one pass holds for; otherwise slow_row.
+__device__ __forceinline__ bool fast_form(const LogprobArgs &a, float top, bool many, int n, int tok, float xt) {
+    return top >= kNothing && top <= kHighest && !many && n >= a.top && (tok < 0 || xt > -INFINITY) &&
+           a.y_scale <= 1e7f;
+}
+
+// ln p of logits of a row whose largest is `top`, with the sum relative to it
+struct LogP {
+    float y_scale, inv_T, t2, ls;
+    __device__ __forceinline__ LogP(const LogprobArgs &a, float top, float sum) {
+        y_scale = a.y_scale;
+        inv_T = a.inv_T;
+        t2 = __fmul_rn(top, a.y_scale);
+        ls = log2f(sum);
+    }
+    __device__ __forceinline__ float operator()(float f) const {
+        const float l = (fmaf(f, y_scale, -t2) - ls) * kLn2;
+        return l == -INFINITY && f > -INFINITY ? f * inv_T : l;
+    }
+};
+
+// grid: C CTAs (a cluster) a row; with C = 1 a CTA takes rows blockIdx.x, + gridDim.x, ..
+template <typename T, bool CLUSTER>
+__global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(LogprobArgs a, int C) {
+    pdl_enter();
+    constexpr int N = Lp<T>::N;
+    extern __shared__ __align__(128) unsigned char sm[];
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm + LpSmem::BAR), *empty = full + kRing;
+    float2 *cand = reinterpret_cast<float2 *>(sm + LpSmem::CAND);
+    RowPart *part = reinterpret_cast<RowPart *>(sm + LpSmem::PART);
+    float *red = reinterpret_cast<float *>(sm + LpSmem::RED), *group_max = reinterpret_cast<float *>(sm + LpSmem::GROUP);
+    int *n_cand = reinterpret_cast<int *>(sm + LpSmem::WORDS);
+    volatile int *failed = reinterpret_cast<volatile int *>(n_cand + 1);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank_in = CLUSTER ? (int)cluster_rank() : 0;
+    const int row0 = CLUSTER ? (int)blockIdx.x / C : blockIdx.x, row_step = CLUSTER ? a.N : gridDim.x;
+    if (tid == 0) {
+#pragma unroll
+        for (int i = 0; i < kRing; ++i) {
+            tc::mbar_init(full + i, 1);
+            tc::mbar_init(empty + i, kWarps);
+        }
+        *n_cand = 0;
+        *failed = 0;
+        tc::fence_mbarrier_init();
+    }
+    __syncthreads();
+    auto slice = [&](const RowShape<T> &s, int &lo, int &hi) {
+        const long long n = s.last - s.first;
+        lo = s.first + (int)(n * rank_in / C);
+        hi = s.first + (int)(n * (rank_in + 1) / C);
+    };
+    // a row's token (-1: none) and its logit
+    auto token_of = [&](int row) { return row < a.N ? a.tokens[row] : -1; };
+    auto logit_of = [&](int row, int tok) {
+        return tok >= 0 && tok < a.V
+                   ? Vec16<T>::load1(static_cast<const T *>(a.logits) + (long long)row * a.stride + tok)
+                   : INFINITY;
+    };
+
+    if (warp == kWarps) {
+        // ------------------------------------------------------------ copies
+        if (lane == 0) {
+            int it = 0;
+            bool go = true;
+            for (int row = row0; row < a.N && go; row += row_step) {
+                const RowShape<T> s(a, row);
+                int lo, hi;
+                slice(s, lo, hi);
+                for (int v = lo; v < hi; v += kChunk, ++it) {
+                    const int at = it % kRing;
+                    if (it >= kRing) {
+                        uint32_t i = 0;
+                        while (go && !tc::mbar_try_wait(empty + at, (it / kRing - 1) & 1))
+                            go = !*failed && ++i < kLpPolls;
+                        if (!go) {
+                            *failed = 1;
+                            break;
+                        }
+                    }
+                    const uint32_t bytes = (uint32_t)min(kChunk, hi - v) * 16;
+                    tc::mbar_arrive_expect_tx(full + at, bytes);
+                    bulk_copy(sm + LpSmem::RING + at * kChunk * 16, s.block + (size_t)v * 16, bytes, full + at);
+                }
+            }
+            // every copy has landed before the shared memory goes
+            for (int i = max(0, it - kRing); i < it; ++i)
+                if (!tc::mbar_wait_bounded(full + i % kRing, (i / kRing) & 1, kLpPolls)) *failed = 1;
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ rows
+        int it = 0, tok = token_of(row0);
+        float xt = logit_of(row0, tok);
+        for (int row = row0; row < a.N; row += row_step) {
+            // (the next row's token and logit are on their way while this row is done)
+            const int next_tok = CLUSTER ? -1 : token_of(row + row_step);
+            const RowShape<T> s(a, row);
+            int lo, hi;
+            slice(s, lo, hi);
+            if (tok >= a.V || tok < -1) {
+                if (tid == 0 && rank_in == 0) set_status(a.status, MEDUSA_DEV_BAD_TOKEN);
+                tok = -1;
+            }
+            const int tv = tok >= 0 ? (s.off + tok) / N : -1;  // the token's block
+            float m = -INFINITY, m2 = 0.f, before = 0.f;
+            float2 S[2] = {}, A[2] = {};
+            float T0 = kLowest;  // candidates reach it
+            auto grow = [&](float top) {  // the reference at least `top`
+                if (!(top <= m)) {        // (a NaN stays)
+                    const float n2 = __fmul_rn(top, a.y_scale), f = m < kNothing ? 0.f : exp2f(m2 - n2), d = m2 - n2;
+                    if (m < kNothing) {
+                        S[0] = S[1] = A[0] = A[1] = make_float2(0.f, 0.f);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            A[i] = make_float2(f * fmaf(S[i].x, d, A[i].x), f * fmaf(S[i].y, d, A[i].y));
+                            S[i] = make_float2(f * S[i].x, f * S[i].y);
+                        }
+                    }
+                    m = max_nan(m, top);
+                    m2 = n2;
+                }
+            };
+            auto candidate = [&](float f, int id) {
+                if (f >= T0) {
+                    const int at = atomicAdd(n_cand, 1);
+                    if (at < kCandidates) cand[at] = make_float2(f, __int_as_float(id));
+                }
+            };
+            for (int v0 = lo; v0 < hi; v0 += kChunk, ++it) {
+                const int at = it % kRing;
+                uint32_t polls = 0;
+                while (!tc::mbar_try_wait(full + at, (it / kRing) & 1))
+                    if (*failed || ++polls == kLpPolls) {
+                        *failed = 1;
+                        break;
+                    }
+                const uint4 *src = reinterpret_cast<const uint4 *>(sm + LpSmem::RING + at * kChunk * 16);
+                uint4 w[kPer];
+#pragma unroll
+                for (int u = 0; u < kPer; ++u)
+                    w[u] = v0 + u * kConsumers + tid < hi ? src[u * kConsumers + tid] : Lp<T>::nothing();
+                float vm[kPer], top = -INFINITY;
+#pragma unroll
+                for (int u = 0; u < kPer; ++u) {
+                    vm[u] = Lp<T>::top(w[u]);
+                    top = max_nan(top, vm[u]);
+                }
+                grow(top);
+                if (v0 == lo && a.top) {
+                    const float h = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                    if (lane < kGroups) group_max[warp * kGroups + lane] = h;
+                    consumers_sync();
+                    float mine = group_max[lane & 15];
+#pragma unroll
+                    for (int x = 1; x < kWarps; ++x) mine = fmaxf(mine, group_max[x * kGroups + (lane & 15)]);
+                    int place = 0;
+#pragma unroll
+                    for (int i = 0; i < kGroups; ++i) {
+                        const float o = __shfl_sync(0xffffffffu, mine, i);
+                        place += o > mine || (o == mine && i < (lane & 15));
+                    }
+                    const uint32_t who = __ballot_sync(0xffffffffu, place == a.top - 1);
+                    // (a NaN among them has no place: the row is not done here anyway)
+                    if (who) T0 = fmaxf(T0, __shfl_sync(0xffffffffu, mine, __ffs(who) - 1));
+                }
+#pragma unroll
+                for (int u = 0; u < kPer; ++u) {
+                    if (m >= kNothing) Lp<T>::add(w[u], a.y_scale, m2, S, A);
+                    const int v = v0 + u * kConsumers + tid;
+                    if (v > tv) {
+                        before += Lp<T>::template above<false>(w[u], xt);
+                    } else if (v < tv) {
+                        before += Lp<T>::template above<true>(w[u], xt);
+                    } else if (v < hi) {  // the token's block
+                        const T *e = reinterpret_cast<const T *>(s.block) + (size_t)v * N;
+                        for (int i = 0; i < N; ++i) {
+                            const float f = Vec16<T>::load1(e + i);
+                            before += f > xt || (f == xt && v * N + i < s.off + tok) ? 1.f : 0.f;
+                        }
+                    }
+                    if (a.top && vm[u] >= T0 && v < hi) {
+                        float f[N];
+                        Vec16<T>::widen(w[u], f);
+#pragma unroll
+                        for (int i = 0; i < N; ++i) candidate(f[i], v * N - s.off + i);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(empty + at);
+            }
+            if (rank_in == 0 && tid < s.edges) {  // the row's ends
+                const int id = s.edge(tid);
+                const float f = Vec16<T>::load1(static_cast<const T *>(a.logits) + (long long)row * a.stride + id);
+                grow(f);
+                if (m >= kNothing) {
+                    const float t = fmaf(fmaxf(f, kLowest), a.y_scale, -m2), p = ex2_approx(t);
+                    S[0].x += p;
+                    A[0].x = fmaf(p, t, A[0].x);
+                }
+                before += f > xt || (f == xt && id < tok) ? 1.f : 0.f;
+                if (a.top) candidate(f, id);
+            }
+            const float next_xt = CLUSTER ? 0.f : logit_of(row + row_step, next_tok);
+            // ---- the CTA's part: the reference first, then plain sums
+            float top = m;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (lane == 0) red[warp] = top;
+            consumers_sync();
+            top = red[0];
+#pragma unroll
+            for (int x = 1; x < kWarps; ++x) top = max_nan(top, red[x]);
+            float sum = 0.f, asum = 0.f;
+            if (m >= kNothing) {
+                const float d = m2 - __fmul_rn(top, a.y_scale), f = exp2f(d);
+                sum = (S[0].x + S[0].y) + (S[1].x + S[1].y);
+                asum = f * fmaf(sum, d, (A[0].x + A[0].y) + (A[1].x + A[1].y));
+                sum *= f;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                asum += __shfl_xor_sync(0xffffffffu, asum, o);
+                before += __shfl_xor_sync(0xffffffffu, before, o);
+            }
+            if (lane == 0) {
+                red[kWarps + warp] = sum;
+                red[2 * kWarps + warp] = asum;
+                red[3 * kWarps + warp] = before;
+            }
+            consumers_sync();
+            sum = red[kWarps];
+            asum = red[2 * kWarps];
+            before = red[3 * kWarps];
+#pragma unroll
+            for (int x = 1; x < kWarps; ++x) {
+                sum += red[kWarps + x];
+                asum += red[2 * kWarps + x];
+                before += red[3 * kWarps + x];
+            }
+            int n = *n_cand;
+            const bool many = n > kCandidates;
+            if (many) n = 0;
+            // places of the candidates in the order
+            auto place_of = [&](const float2 &c) {
+                int p = 0;
+                for (int i = 0; i < n; ++i) {
+                    const float2 o = cand[i];
+                    p += better(o.x, __float_as_int(o.y), c.x, __float_as_int(c.y));
+                }
+                return p;
+            };
+            if constexpr (CLUSTER) {
+                if (tid < a.top) part->id[tid] = INT_MAX;
+                consumers_sync();
+                for (int i = tid; i < n; i += kConsumers) {
+                    const float2 c = cand[i];
+                    const int p = place_of(c);
+                    if (p < a.top) {
+                        part->val[p] = c.x;
+                        part->id[p] = __float_as_int(c.y);
+                    }
+                }
+                if (tid == 0) {
+                    part->m = top;
+                    part->S = sum;
+                    part->A = asum;
+                    part->before = (int)before;
+                    part->n = many ? -1 : min(n, a.top);
+                }
+                break;  // (to the cluster's barriers, which are for all its warps)
+            } else {
+                if (fast_form(a, top, many, n, tok, xt)) {
+                    const LogP logp_of(a, top, sum);
+                    if (tid == 0) {
+                        a.logp[row] = tok < 0 ? 0.f : logp_of(xt);
+                        a.rank[row] = tok < 0 ? -1 : (int)before;
+                        a.entropy[row] = fmaxf(kLn2 * (logp_of.ls - asum / sum), 0.f);
+                    }
+                    if (a.top)
+                        for (int i = tid; i < n; i += kConsumers) {
+                            const float2 c = cand[i];
+                            const int p = place_of(c);
+                            if (p < a.top) {
+                                a.top_ids[(size_t)row * a.top + p] = __float_as_int(c.y);
+                                a.top_logp[(size_t)row * a.top + p] = logp_of(c.x);
+                            }
+                        }
+                } else {
+                    slow_row<T>(a, row, tok, red, reinterpret_cast<int *>(group_max));
+                }
+                consumers_sync();
+                if (tid == 0) *n_cand = 0;
+                consumers_sync();
+                tok = next_tok;
+                xt = next_xt;
+            }
+        }
+    }
+    if constexpr (CLUSTER) {
+        __syncthreads();
+        cluster_sync();  // every part is written
+        if (rank_in == 0 && warp < kWarps) {
+            const int row = row0;
+            int tok = a.tokens[row];
+            if (tok >= a.V || tok < -1) tok = -1;
+            const float xt = logit_of(row, tok);
+            const RowPart *p = cluster_ptr(part, lane < C ? lane : 0);
+            const bool mine = lane < C;
+            const float m = mine ? p->m : -INFINITY;
+            float top = m, sum = 0.f, asum = 0.f;
+            int before = mine ? p->before : 0, n = mine ? p->n : 0;
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+            top = __shfl_sync(0xffffffffu, top, 0);
+            if (mine && m >= kNothing) {
+                const float d = __fmul_rn(m, a.y_scale) - __fmul_rn(top, a.y_scale), f = exp2f(d);
+                sum = f * p->S;
+                asum = f * fmaf(p->S, d, p->A);
+            }
+            const bool many = __any_sync(0xffffffffu, n < 0);
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) {
+                sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                asum += __shfl_xor_sync(0xffffffffu, asum, o);
+                before += __shfl_xor_sync(0xffffffffu, before, o);
+                n += __shfl_xor_sync(0xffffffffu, n, o);
+            }
+            sum = __shfl_sync(0xffffffffu, sum, 0);
+            asum = __shfl_sync(0xffffffffu, asum, 0);
+            before = __shfl_sync(0xffffffffu, before, 0);
+            n = __shfl_sync(0xffffffffu, n, 0);
+            if (fast_form(a, top, many, n, tok, xt)) {
+                const LogP logp_of(a, top, sum);
+                if (tid == 0) {
+                    a.logp[row] = tok < 0 ? 0.f : logp_of(xt);
+                    a.rank[row] = tok < 0 ? -1 : before;
+                    a.entropy[row] = fmaxf(kLn2 * (logp_of.ls - asum / sum), 0.f);
+                }
+                // the parts' first tokens, gathered, then placed as the candidates are
+                if (tid < C * a.top) {
+                    const RowPart *q = cluster_ptr(part, tid / a.top);
+                    const int k = tid % a.top, id = q->id[k];
+                    cand[tid] = make_float2(id == INT_MAX ? -INFINITY : q->val[k], __int_as_float(id));
+                }
+                consumers_sync();
+                if (tid < C * a.top) {
+                    const float2 c = cand[tid];
+                    const int id = __float_as_int(c.y);
+                    int at = 0;
+                    for (int i = 0; i < C * a.top; ++i) at += better(cand[i].x, __float_as_int(cand[i].y), c.x, id);
+                    if (at < a.top && id != INT_MAX) {
+                        a.top_ids[(size_t)row * a.top + at] = id;
+                        a.top_logp[(size_t)row * a.top + at] = logp_of(c.x);
+                    }
+                }
+            } else {
+                slow_row<T>(a, row, tok, red, reinterpret_cast<int *>(group_max));
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // no CTA leaves while its part may be read
+    }
+    if (tid == 0 && *failed) set_status(a.status, MEDUSA_DEV_TIMEOUT);
 }
 
 }  // namespace
@@ -134,6 +655,7 @@ cudaError_t launch_token_logprobs(medusa_dtype dtype, const void *logits, long l
     a.logits = logits;
     a.stride = stride;
     a.tokens = tokens;
+    a.N = N;
     a.V = V;
     a.top = top;
     a.inv_T = 1.f / temperature;
@@ -144,8 +666,30 @@ cudaError_t launch_token_logprobs(medusa_dtype dtype, const void *logits, long l
     a.top_ids = top_ids;
     a.top_logp = top_logp;
     a.status = static_cast<int *>(ws);
-    auto kern = dtype == MEDUSA_F32 ? token_logprobs_kernel<float> : token_logprobs_kernel<bf16>;
-    cudaError_t e = launch_pdl(kern, dim3(N), dim3(kLpThreads), 0, stream, a);
+    // CTAs a row: as many as fit at once, none with less than a chunk
+    const int slots = kLpCtas * device_sm_count();
+    const int chunks = (int)(((long long)V * (dtype == MEDUSA_F32 ? 4 : 2) + kChunk * 16 - 1) / (kChunk * 16));
+    int C = 1;
+    while (C < kMaxCluster && (long long)N * C * 2 <= slots && 2 * C <= chunks) C *= 2;
+    auto kern = dtype == MEDUSA_F32
+                    ? (C > 1 ? token_logprobs_kernel<float, true> : token_logprobs_kernel<float, false>)
+                    : (C > 1 ? token_logprobs_kernel<bf16, true> : token_logprobs_kernel<bf16, false>);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LpSmem::TOTAL);
+    if (e) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(C > 1 ? N * C : std::min(N, slots));
+    cfg.blockDim = dim3(kLpThreads);
+    cfg.dynamicSmemBytes = LpSmem::TOTAL;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = C > 1 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kern, a, C);
     note_launch();
     return e;
 }
