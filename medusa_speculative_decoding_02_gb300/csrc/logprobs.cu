@@ -7,19 +7,21 @@
 //     rank = number of tokens before t in the order (larger logit, then smaller id)
 //     alternatives: the first `top` tokens of that order
 //
-// A CTA (eight warps that compute, one that copies) takes a row at a time, in chunks
-// of 1024 16-byte vectors that come by bulk copies into a ring of four; with few rows
-// a cluster of CTAs shares each row.  A thread keeps its own m, S and A and moves m
-// when a chunk's maximum (packed, NaNs kept) exceeds it; m in base 2 is rounded by a
-// product that is not fused, so that all sums are relative to the same number.  Ranks
-// are packed comparisons with the token's logit, "or equal" before its place.
-// Alternatives: the k-th largest of sixteen groups of threads' maxima over the first
-// chunk is at most the row's k-th largest logit, so only elements that reach it are
-// candidates (some tens); a candidate's place in the order is the number of better
-// ones among them.
+// A CTA (four warps that compute, one that copies) takes a row at a time, in chunks of
+// 512 16-byte vectors that come by bulk copies into a ring; with few rows a cluster of
+// CTAs shares each row.  A thread keeps its own m, S and A and moves m when a chunk's
+// maximum (packed, NaNs kept) exceeds it; m in base 2 is rounded by a product that is
+// not fused, so that all sums are relative to the same number.
+// Most vectors hold nothing above the token's logit nor among the alternatives: their
+// maximum says so.  In the others tokens before the row's own are counted ("or equal"
+// before its place), and what may hold alternatives is kept: the k-th largest of 32
+// groups of threads' maxima so far is at most the row's k-th largest logit (T0, looked
+// at again after 1, 2, 4, .. chunks).  At the row's end the elements that reach T0 are
+// the candidates (some tens), and a candidate's place in the order is the number of
+// better ones among them.
 //
 // What this form does not take (a NaN, +inf or nothing above -1e29 in the row, the token
-// at -inf, more than kCandidates candidates because of ties, fewer possible tokens
+// at -inf, too many candidates because of ties, fewer possible tokens
 // than alternatives, temperatures below 1e-7) is done by slow_row, by plain passes over
 // the row: the results are the same by definition.
 #include <algorithm>
@@ -33,15 +35,15 @@ namespace medusa {
 
 namespace {
 
-constexpr int kConsumers = 256, kLpThreads = kConsumers + 32, kWarps = kConsumers / 32;
-constexpr int kChunk = 1024, kPer = kChunk / kConsumers;  // vectors of a chunk, of a thread
-constexpr int kRing = 4, kLpCtas = 3;
-constexpr int kCandidates = 1024, kGroups = 16;
+constexpr int kConsumers = 128, kLpThreads = kConsumers + 32, kWarps = kConsumers / 32;
+constexpr int kChunk = 512, kPer = kChunk / kConsumers;  // vectors of a chunk, of a thread
+constexpr int kRing = 3, kLpCtas = 6;
+constexpr int kVectors = 256, kCandidates = 512;  // kept of a row
 constexpr int kMaxCluster = 8;
 constexpr uint32_t kLpPolls = 1u << 20;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -1e30f, kNothing = -1e29f, kHighest = 1e30f;
-static_assert(kGroups >= MEDUSA_MAX_TOP_S, "a group for each alternative");
+static_assert(32 >= MEDUSA_MAX_TOP_S && kMaxCluster * MEDUSA_MAX_TOP_S <= kConsumers, "groups, and parts' lists");
 
 struct LogprobArgs {
     const void *logits;
@@ -61,23 +63,37 @@ struct RowPart {
     float m;       // largest logit (NaN if there is one)
     float S, A;    // relative to m
     int before, n; // tokens before the row's token; candidates (-1: too many)
-    float val[MEDUSA_MAX_TOP_S];
-    int id[MEDUSA_MAX_TOP_S];  // the part's first tokens
+    uint64_t key[MEDUSA_MAX_TOP_S];  // the part's first tokens (0: none)
 };
 
 struct LpSmem {
     static constexpr int RING = 0;
-    static constexpr int CAND = kRing * kChunk * 16;  // (logit, id)
-    static constexpr int PART = CAND + kCandidates * 8;
+    static constexpr int VEC = kRing * kChunk * 16;  // vectors kept
+    static constexpr int CAND = VEC + kVectors * 16;  // candidates: see key_of
+    static constexpr int AT = CAND + kCandidates * 8; // the vectors' places
+    static constexpr int PART = AT + kVectors * 4;
     static constexpr int RED = PART + (int)(sizeof(RowPart) + 15) / 16 * 16;  // [4][kWarps]
-    static constexpr int GROUP = RED + 4 * kWarps * 4;                        // [kWarps][kGroups]
-    static constexpr int BAR = GROUP + kWarps * kGroups * 4;
-    static constexpr int WORDS = BAR + 2 * kRing * 8;  // candidates counted, failed
-    static constexpr int TOTAL = WORDS + 16;
+    static constexpr int GROUP = RED + 4 * kWarps * 4;                        // [2][kWarps][32]
+    static constexpr int BAR = GROUP + 2 * kWarps * 32 * 4;
+    static constexpr int WORDS = BAR + 2 * kRing * 8;  // vectors, candidates of even and odd rows; failed
+    static constexpr int TOTAL = WORDS + 32;
     static_assert(kLpCtas * (TOTAL + 1024) <= 228 * 1024, "CTAs of an SM");
 };
 
-__device__ __forceinline__ void consumers_sync() { asm volatile("barrier.cta.sync 1, 256;\n" ::: "memory"); }
+__device__ __forceinline__ void consumers_sync() { asm volatile("barrier.cta.sync 1, %0;\n" ::"n"(kConsumers) : "memory"); }
+
+// floats in order as unsigned numbers (a NaN: 0, below all)
+__device__ __forceinline__ uint32_t ordered(float f) {
+    const uint32_t u = __float_as_uint(f + 0.f);  // (-0 is 0)
+    return isnan(f) ? 0u : u ^ ((int)u < 0 ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t k) {
+    return __uint_as_float(k ^ ((int)k < 0 ? 0x80000000u : 0xffffffffu));
+}
+// a token in the order: the larger key comes first
+__device__ __forceinline__ uint64_t key_of(float f, int id) { return (uint64_t)ordered(f) << 32 | (uint32_t)~id; }
+__device__ __forceinline__ float key_logit(uint64_t k) { return unordered((uint32_t)(k >> 32)); }
+__device__ __forceinline__ int key_id(uint64_t k) { return (int)~(uint32_t)k; }
 
 __device__ __forceinline__ float max_nan(float a, float b) {
     float d;
@@ -89,6 +105,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 template <typename T> struct Lp;
 template <> struct Lp<bf16> {
     static constexpr int N = 8;
+    __device__ static __forceinline__ float value(bf16 x) { return __bfloat162float(x); }
     using Pair = __nv_bfloat162;
     __device__ static __forceinline__ uint4 nothing() { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
     __device__ static __forceinline__ Pair pair(uint32_t w) { return *reinterpret_cast<const Pair *>(&w); }
@@ -98,11 +115,11 @@ template <> struct Lp<bf16> {
     }
     // elements above x (and equal to it)
     template <bool EQUAL>
-    __device__ static __forceinline__ float above(const uint4 &v, float x) {
+    __device__ static __forceinline__ int above(const uint4 &v, float x) {
         const Pair b = __float2bfloat162_rn(x);
         auto c = [&](uint32_t w) { return EQUAL ? __hge2(pair(w), b) : __hgt2(pair(w), b); };
         const Pair s = __hadd2(__hadd2(c(v.x), c(v.y)), __hadd2(c(v.z), c(v.w)));
-        return __low2float(s) + __high2float(s);
+        return (int)(__low2float(s) + __high2float(s));
     }
     __device__ static __forceinline__ void add(const uint4 &v, float ys, float m2, float2 (&S)[2], float2 (&A)[2]) {
         const Pair low = __float2bfloat162_rn(kLowest);
@@ -121,16 +138,17 @@ template <> struct Lp<bf16> {
 };
 template <> struct Lp<float> {
     static constexpr int N = 4;
+    __device__ static __forceinline__ float value(float x) { return x; }
     __device__ static __forceinline__ uint4 nothing() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
     __device__ static __forceinline__ float top(const uint4 &v) {
         return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
                        max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
     }
     template <bool EQUAL>
-    __device__ static __forceinline__ float above(const uint4 &v, float x) {
+    __device__ static __forceinline__ int above(const uint4 &v, float x) {
         auto c = [&](uint32_t w) {
             const float f = __uint_as_float(w);
-            return (EQUAL ? f >= x : f > x) ? 1.f : 0.f;
+            return (EQUAL ? f >= x : f > x) ? 1 : 0;
         };
         return (c(v.x) + c(v.y)) + (c(v.z) + c(v.w));
     }
@@ -252,6 +270,7 @@ __device__ __noinline__ void slow_row(const LogprobArgs &a, int row, int tok, fl
         lv = bv;
         li = bi;
     }
+    consumers_sync();
 }
 
 __device__ __forceinline__ void bulk_copy(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
@@ -305,11 +324,13 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
     constexpr int N = Lp<T>::N;
     extern __shared__ __align__(128) unsigned char sm[];
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + LpSmem::BAR), *empty = full + kRing;
-    float2 *cand = reinterpret_cast<float2 *>(sm + LpSmem::CAND);
+    uint4 *kept = reinterpret_cast<uint4 *>(sm + LpSmem::VEC);
+    uint64_t *cand = reinterpret_cast<uint64_t *>(sm + LpSmem::CAND);
+    int *kept_at = reinterpret_cast<int *>(sm + LpSmem::AT);
     RowPart *part = reinterpret_cast<RowPart *>(sm + LpSmem::PART);
     float *red = reinterpret_cast<float *>(sm + LpSmem::RED), *group_max = reinterpret_cast<float *>(sm + LpSmem::GROUP);
-    int *n_cand = reinterpret_cast<int *>(sm + LpSmem::WORDS);
-    volatile int *failed = reinterpret_cast<volatile int *>(n_cand + 1);
+    int *counts = reinterpret_cast<int *>(sm + LpSmem::WORDS);
+    volatile int *failed = reinterpret_cast<volatile int *>(counts + 4);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank_in = CLUSTER ? (int)cluster_rank() : 0;
     const int row0 = CLUSTER ? (int)blockIdx.x / C : blockIdx.x, row_step = CLUSTER ? a.N : gridDim.x;
@@ -319,7 +340,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
             tc::mbar_init(full + i, 1);
             tc::mbar_init(empty + i, kWarps);
         }
-        *n_cand = 0;
+        counts[0] = counts[1] = counts[2] = counts[3] = 0;
         *failed = 0;
         tc::fence_mbarrier_init();
     }
@@ -369,9 +390,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
         __syncwarp();
     } else {
         // ------------------------------------------------------------ rows
-        int it = 0, tok = token_of(row0);
+        int it = 0, tok = token_of(row0), odd = 0, look = 0;
         float xt = logit_of(row0, tok);
-        for (int row = row0; row < a.N; row += row_step) {
+        for (int row = row0; row < a.N; row += row_step, odd ^= 1) {
             // (the next row's token and logit are on their way while this row is done)
             const int next_tok = CLUSTER ? -1 : token_of(row + row_step);
             const RowShape<T> s(a, row);
@@ -382,7 +403,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
                 tok = -1;
             }
             const int tv = tok >= 0 ? (s.off + tok) / N : -1;  // the token's block
-            float m = -INFINITY, m2 = 0.f, before = 0.f;
+            float m = -INFINITY, m2 = 0.f;
+            int before = 0;
             float2 S[2] = {}, A[2] = {};
             float T0 = kLowest;  // candidates reach it
             auto grow = [&](float top) {  // the reference at least `top`
@@ -401,10 +423,20 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
                     m2 = n2;
                 }
             };
+            // Counters of this row.  The row before has done with its own, and with what is
+            // kept, behind the first barrier of this row: of T0, or here.
+            int *n_kept = counts + 2 * odd, *n_cand = n_kept + 1;
+            auto other_counters = [&] {
+                if (tid == 0) counts[2 * (odd ^ 1)] = counts[2 * (odd ^ 1) + 1] = 0;
+            };
+            if (lo >= hi) {
+                consumers_sync();
+                other_counters();
+            }
             auto candidate = [&](float f, int id) {
                 if (f >= T0) {
                     const int at = atomicAdd(n_cand, 1);
-                    if (at < kCandidates) cand[at] = make_float2(f, __int_as_float(id));
+                    if (at < kCandidates) cand[at] = key_of(f, id);
                 }
             };
             for (int v0 = lo; v0 < hi; v0 += kChunk, ++it) {
@@ -427,43 +459,49 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
                     top = max_nan(top, vm[u]);
                 }
                 grow(top);
-                if (v0 == lo && a.top) {
-                    const float h = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                    if (lane < kGroups) group_max[warp * kGroups + lane] = h;
+                const int chunk = (v0 - lo) / kChunk;
+                if (a.top && (chunk & (chunk + 1)) == 0 && (chunk == 0 || v0 + kChunk < hi)) {
+                    // (two places by turns: a warp may be a look ahead of another)
+                    float *gm = group_max + look * kWarps * 32;
+                    look ^= 1;
+                    gm[warp * 32 + lane] = m;
                     consumers_sync();
-                    float mine = group_max[lane & 15];
+                    if (chunk == 0) other_counters();
+                    uint32_t mine = 0, best = 0;
 #pragma unroll
-                    for (int x = 1; x < kWarps; ++x) mine = fmaxf(mine, group_max[x * kGroups + (lane & 15)]);
-                    int place = 0;
-#pragma unroll
-                    for (int i = 0; i < kGroups; ++i) {
-                        const float o = __shfl_sync(0xffffffffu, mine, i);
-                        place += o > mine || (o == mine && i < (lane & 15));
+                    for (int x = 0; x < kWarps; ++x) mine = max(mine, ordered(gm[x * 32 + lane]));
+                    // (equal ones go at once: the bound may only be lower)
+                    for (int k = 0; k < a.top; ++k) {
+                        best = __reduce_max_sync(0xffffffffu, mine);
+                        if (mine == best) mine = 0;
                     }
-                    const uint32_t who = __ballot_sync(0xffffffffu, place == a.top - 1);
-                    // (a NaN among them has no place: the row is not done here anyway)
-                    if (who) T0 = fmaxf(T0, __shfl_sync(0xffffffffu, mine, __ffs(who) - 1));
+                    if (best) T0 = fmaxf(T0, unordered(best));
                 }
+                const float limit = a.top ? fminf(T0, xt) : xt;
+#pragma unroll
+                for (int u = 0; u < kPer; ++u)
+                    if (m >= kNothing) Lp<T>::add(w[u], a.y_scale, m2, S, A);
 #pragma unroll
                 for (int u = 0; u < kPer; ++u) {
-                    if (m >= kNothing) Lp<T>::add(w[u], a.y_scale, m2, S, A);
                     const int v = v0 + u * kConsumers + tid;
+                    if (!(vm[u] >= limit) || v >= hi) continue;
                     if (v > tv) {
                         before += Lp<T>::template above<false>(w[u], xt);
                     } else if (v < tv) {
                         before += Lp<T>::template above<true>(w[u], xt);
-                    } else if (v < hi) {  // the token's block
+                    } else {  // the token's block
                         const T *e = reinterpret_cast<const T *>(s.block) + (size_t)v * N;
                         for (int i = 0; i < N; ++i) {
                             const float f = Vec16<T>::load1(e + i);
-                            before += f > xt || (f == xt && v * N + i < s.off + tok) ? 1.f : 0.f;
+                            before += f > xt || (f == xt && v * N + i < s.off + tok);
                         }
                     }
-                    if (a.top && vm[u] >= T0 && v < hi) {
-                        float f[N];
-                        Vec16<T>::widen(w[u], f);
-#pragma unroll
-                        for (int i = 0; i < N; ++i) candidate(f[i], v * N - s.off + i);
+                    if (a.top && vm[u] >= T0) {
+                        const int at = atomicAdd(n_kept, 1);
+                        if (at < kVectors) {
+                            kept[at] = w[u];
+                            kept_at[at] = v * N - s.off;
+                        }
                     }
                 }
                 __syncwarp();
@@ -478,19 +516,26 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
                     S[0].x += p;
                     A[0].x = fmaf(p, t, A[0].x);
                 }
-                before += f > xt || (f == xt && id < tok) ? 1.f : 0.f;
+                before += f > xt || (f == xt && id < tok);
                 if (a.top) candidate(f, id);
             }
             const float next_xt = CLUSTER ? 0.f : logit_of(row + row_step, next_tok);
             // ---- the CTA's part: the reference first, then plain sums
-            float top = m;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+            float top;
+            asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;\n" : "=f"(top) : "f"(m));
             if (lane == 0) red[warp] = top;
             consumers_sync();
             top = red[0];
 #pragma unroll
             for (int x = 1; x < kWarps; ++x) top = max_nan(top, red[x]);
+            // the kept vectors' elements that reach T0
+            bool many = false;
+            if (a.top) {
+                const int n = *n_kept;
+                many = n > kVectors;
+                for (int i = tid; i < min(n, kVectors) * N; i += kConsumers)
+                    candidate(Lp<T>::value(reinterpret_cast<const T *>(kept)[i]), kept_at[i / N] + i % N);
+            }
             float sum = 0.f, asum = 0.f;
             if (m >= kNothing) {
                 const float d = m2 - __fmul_rn(top, a.y_scale), f = exp2f(d);
@@ -502,51 +547,46 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
             for (int o = 16; o > 0; o >>= 1) {
                 sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 asum += __shfl_xor_sync(0xffffffffu, asum, o);
-                before += __shfl_xor_sync(0xffffffffu, before, o);
             }
+            before = __reduce_add_sync(0xffffffffu, before);
             if (lane == 0) {
                 red[kWarps + warp] = sum;
                 red[2 * kWarps + warp] = asum;
-                red[3 * kWarps + warp] = before;
+                red[3 * kWarps + warp] = __int_as_float(before);
             }
             consumers_sync();
             sum = red[kWarps];
             asum = red[2 * kWarps];
-            before = red[3 * kWarps];
+            before = __float_as_int(red[3 * kWarps]);
 #pragma unroll
             for (int x = 1; x < kWarps; ++x) {
                 sum += red[kWarps + x];
                 asum += red[2 * kWarps + x];
-                before += red[3 * kWarps + x];
+                before += __float_as_int(red[3 * kWarps + x]);
             }
             int n = *n_cand;
-            const bool many = n > kCandidates;
+            many = many || n > kCandidates;
             if (many) n = 0;
             // places of the candidates in the order
-            auto place_of = [&](const float2 &c) {
+            auto place_of = [&](uint64_t c) {
                 int p = 0;
-                for (int i = 0; i < n; ++i) {
-                    const float2 o = cand[i];
-                    p += better(o.x, __float_as_int(o.y), c.x, __float_as_int(c.y));
-                }
+#pragma unroll 4
+                for (int i = 0; i < n; ++i) p += cand[i] > c;
                 return p;
             };
             if constexpr (CLUSTER) {
-                if (tid < a.top) part->id[tid] = INT_MAX;
+                if (tid < a.top) part->key[tid] = 0;
                 consumers_sync();
                 for (int i = tid; i < n; i += kConsumers) {
-                    const float2 c = cand[i];
+                    const uint64_t c = cand[i];
                     const int p = place_of(c);
-                    if (p < a.top) {
-                        part->val[p] = c.x;
-                        part->id[p] = __float_as_int(c.y);
-                    }
+                    if (p < a.top) part->key[p] = c;
                 }
                 if (tid == 0) {
                     part->m = top;
                     part->S = sum;
                     part->A = asum;
-                    part->before = (int)before;
+                    part->before = before;
                     part->n = many ? -1 : min(n, a.top);
                 }
                 break;  // (to the cluster's barriers, which are for all its warps)
@@ -555,24 +595,21 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
                     const LogP logp_of(a, top, sum);
                     if (tid == 0) {
                         a.logp[row] = tok < 0 ? 0.f : logp_of(xt);
-                        a.rank[row] = tok < 0 ? -1 : (int)before;
+                        a.rank[row] = tok < 0 ? -1 : before;
                         a.entropy[row] = fmaxf(kLn2 * (logp_of.ls - asum / sum), 0.f);
                     }
                     if (a.top)
                         for (int i = tid; i < n; i += kConsumers) {
-                            const float2 c = cand[i];
+                            const uint64_t c = cand[i];
                             const int p = place_of(c);
                             if (p < a.top) {
-                                a.top_ids[(size_t)row * a.top + p] = __float_as_int(c.y);
-                                a.top_logp[(size_t)row * a.top + p] = logp_of(c.x);
+                                a.top_ids[(size_t)row * a.top + p] = key_id(c);
+                                a.top_logp[(size_t)row * a.top + p] = logp_of(key_logit(c));
                             }
                         }
                 } else {
                     slow_row<T>(a, row, tok, red, reinterpret_cast<int *>(group_max));
                 }
-                consumers_sync();
-                if (tid == 0) *n_cand = 0;
-                consumers_sync();
                 tok = next_tok;
                 xt = next_xt;
             }
@@ -619,20 +656,15 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
                     a.entropy[row] = fmaxf(kLn2 * (logp_of.ls - asum / sum), 0.f);
                 }
                 // the parts' first tokens, gathered, then placed as the candidates are
-                if (tid < C * a.top) {
-                    const RowPart *q = cluster_ptr(part, tid / a.top);
-                    const int k = tid % a.top, id = q->id[k];
-                    cand[tid] = make_float2(id == INT_MAX ? -INFINITY : q->val[k], __int_as_float(id));
-                }
+                if (tid < C * a.top) cand[tid] = cluster_ptr(part, tid / a.top)->key[tid % a.top];
                 consumers_sync();
                 if (tid < C * a.top) {
-                    const float2 c = cand[tid];
-                    const int id = __float_as_int(c.y);
+                    const uint64_t c = cand[tid];
                     int at = 0;
-                    for (int i = 0; i < C * a.top; ++i) at += better(cand[i].x, __float_as_int(cand[i].y), c.x, id);
-                    if (at < a.top && id != INT_MAX) {
-                        a.top_ids[(size_t)row * a.top + at] = id;
-                        a.top_logp[(size_t)row * a.top + at] = logp_of(c.x);
+                    for (int i = 0; i < C * a.top; ++i) at += cand[i] > c;
+                    if (at < a.top && c) {
+                        a.top_ids[(size_t)row * a.top + at] = key_id(c);
+                        a.top_logp[(size_t)row * a.top + at] = logp_of(key_logit(c));
                     }
                 }
             } else {
