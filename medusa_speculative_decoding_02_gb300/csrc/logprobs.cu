@@ -9,16 +9,16 @@
 //
 // A CTA (four warps that compute, one that copies) takes a row at a time, in chunks of
 // 512 16-byte vectors that come by bulk copies into a ring; with few rows a cluster of
-// CTAs shares each row.  A thread keeps its own m, S and A and moves m when a chunk's
-// maximum (packed, NaNs kept) exceeds it; m in base 2 is rounded by a product that is
-// not fused, so that all sums are relative to the same number.
-// Most vectors hold nothing above the token's logit nor among the alternatives: their
-// maximum says so.  In the others tokens before the row's own are counted ("or equal"
-// before its place), and what may hold alternatives is kept: the k-th largest of 32
-// groups of threads' maxima so far is at most the row's k-th largest logit (T0, looked
-// at again after 1, 2, 4, .. chunks).  At the row's end the elements that reach T0 are
-// the candidates (some tens), and a candidate's place in the order is the number of
-// better ones among them.
+// CTAs shares each row.  A thread keeps its own reference, S and A, and moves the
+// reference when a chunk's maximum (packed, NaNs kept) exceeds it by 2^8; references in
+// base 2 are rounded by products that are not fused, so that all sums are relative
+// to the same number.
+// Ranks are packed comparisons with the token's logit, or up to its place with the
+// number below it.  Alternatives: the k-th largest of 32 groups of threads' maxima so
+// far is at most the row's k-th largest logit (T0, looked at again after 1, 2, 4, ..
+// chunks); vectors whose maximum reaches it are kept, at the row's end their elements that
+// do are the candidates (some tens), and a candidate's place in the order is the number
+// of better ones among them.
 //
 // What this form does not take (a NaN, +inf or nothing above -1e29 in the row, the token
 // at -inf, too many candidates because of ties, fewer possible tokens
@@ -42,7 +42,7 @@ constexpr int kVectors = 256, kCandidates = 512;  // kept of a row
 constexpr int kMaxCluster = 8;
 constexpr uint32_t kLpPolls = 1u << 20;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kLowest = -1e30f, kNothing = -1e29f, kHighest = 1e30f;
+constexpr float kLowest = -1e30f, kNothing = -1e29f, kHighest = 1e30f, kLag = 8.f;
 static_assert(32 >= MEDUSA_MAX_TOP_S && kMaxCluster * MEDUSA_MAX_TOP_S <= kConsumers, "groups, and parts' lists");
 
 struct LogprobArgs {
@@ -109,17 +109,34 @@ template <> struct Lp<bf16> {
     using Pair = __nv_bfloat162;
     __device__ static __forceinline__ uint4 nothing() { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
     __device__ static __forceinline__ Pair pair(uint32_t w) { return *reinterpret_cast<const Pair *>(&w); }
-    __device__ static __forceinline__ float top(const uint4 &v) {
-        const Pair p = __hmax2_nan(__hmax2_nan(pair(v.x), pair(v.y)), __hmax2_nan(pair(v.z), pair(v.w)));
-        return max_nan(__low2float(p), __high2float(p));
+    // the largest of a vector, in two halves, of two such, and as a number
+    using Top = Pair;
+    __device__ static __forceinline__ Top top(const uint4 &v) {
+        return __hmax2_nan(__hmax2_nan(pair(v.x), pair(v.y)), __hmax2_nan(pair(v.z), pair(v.w)));
     }
-    // elements above x (and equal to it)
-    template <bool EQUAL>
-    __device__ static __forceinline__ int above(const uint4 &v, float x) {
-        const Pair b = __float2bfloat162_rn(x);
-        auto c = [&](uint32_t w) { return EQUAL ? __hge2(pair(w), b) : __hgt2(pair(w), b); };
-        const Pair s = __hadd2(__hadd2(c(v.x), c(v.y)), __hadd2(c(v.z), c(v.w)));
-        return (int)(__low2float(s) + __high2float(s));
+    __device__ static __forceinline__ Top top(Top a, Top b) { return __hmax2_nan(a, b); }
+    __device__ static __forceinline__ float number(Top p) { return max_nan(__low2float(p), __high2float(p)); }
+    // how many elements of a chunk's vectors lie above a bound
+    using Bound = Pair;
+    __device__ static __forceinline__ Bound bound(float x) { return __float2bfloat162_rn(x); }
+    struct Count {
+        float2 all = make_float2(0.f, 0.f);
+        Pair n;
+        __device__ __forceinline__ void start() { n = __float2bfloat162_rn(0.f); }
+        __device__ __forceinline__ void add(const uint4 &v, Bound b) {
+            n = __hadd2(n, __hadd2(__hadd2(__hgt2(pair(v.x), b), __hgt2(pair(v.y), b)),
+                                   __hadd2(__hgt2(pair(v.z), b), __hgt2(pair(v.w), b))));
+        }
+        __device__ __forceinline__ void end() {  // (up to 16 in a half, and 2^24 in all, are exact)
+            const uint32_t u = *reinterpret_cast<const uint32_t *>(&n);
+            all = __fadd2_rn(all, make_float2(bf_lo(u), bf_hi(u)));
+        }
+        __device__ __forceinline__ int total() const { return (int)(all.x + all.y); }
+    };
+    // the largest number of the type below x
+    __device__ static __forceinline__ float below(float x) {
+        const uint32_t u = __float_as_uint(x);
+        return __uint_as_float(x == 0.f ? 0x80010000u : (int)u < 0 ? u + 0x10000u : u - 0x10000u);
     }
     __device__ static __forceinline__ void add(const uint4 &v, float ys, float m2, float2 (&S)[2], float2 (&A)[2]) {
         const Pair low = __float2bfloat162_rn(kLowest);
@@ -140,17 +157,28 @@ template <> struct Lp<float> {
     static constexpr int N = 4;
     __device__ static __forceinline__ float value(float x) { return x; }
     __device__ static __forceinline__ uint4 nothing() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
-    __device__ static __forceinline__ float top(const uint4 &v) {
+    using Top = float;
+    __device__ static __forceinline__ Top top(const uint4 &v) {
         return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
                        max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
     }
-    template <bool EQUAL>
-    __device__ static __forceinline__ int above(const uint4 &v, float x) {
-        auto c = [&](uint32_t w) {
-            const float f = __uint_as_float(w);
-            return (EQUAL ? f >= x : f > x) ? 1 : 0;
-        };
-        return (c(v.x) + c(v.y)) + (c(v.z) + c(v.w));
+    __device__ static __forceinline__ Top top(Top a, Top b) { return max_nan(a, b); }
+    __device__ static __forceinline__ float number(Top p) { return p; }
+    using Bound = float;
+    __device__ static __forceinline__ Bound bound(float x) { return x; }
+    struct Count {
+        int n = 0;
+        __device__ __forceinline__ void start() {}
+        __device__ __forceinline__ void add(const uint4 &v, Bound b) {
+            n += (__uint_as_float(v.x) > b) + (__uint_as_float(v.y) > b) + (__uint_as_float(v.z) > b) +
+                 (__uint_as_float(v.w) > b);
+        }
+        __device__ __forceinline__ void end() {}
+        __device__ __forceinline__ int total() const { return n; }
+    };
+    __device__ static __forceinline__ float below(float x) {
+        const uint32_t u = __float_as_uint(x);
+        return __uint_as_float(x == 0.f ? 0x80000001u : (int)u < 0 ? u + 1u : u - 1u);
     }
     __device__ static __forceinline__ void add(const uint4 &v, float ys, float m2, float2 (&S)[2], float2 (&A)[2]) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -402,24 +430,32 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
                 if (tid == 0 && rank_in == 0) set_status(a.status, MEDUSA_DEV_BAD_TOKEN);
                 tok = -1;
             }
-            const int tv = tok >= 0 ? (s.off + tok) / N : -1;  // the token's block
-            float m = -INFINITY, m2 = 0.f;
-            int before = 0;
+            // Tokens before the row's own: logits above xt, in the blocks up to the token's
+            // own xt too (above the number below it), less the equal ones in that block
+            // from the token on, which are counted back here.
+            const int tv = tok >= 0 ? (s.off + tok) / N : -1;
+            const typename Lp<T>::Bound after_it = Lp<T>::bound(xt), up_to_it = Lp<T>::bound(Lp<T>::below(xt));
+            typename Lp<T>::Count above;
+            bool not_before = false;
+            if (tid < N && tv >= lo && tv < hi && tv * N - s.off + tid >= tok)
+                not_before = logit_of(row, tv * N - s.off + tid) == xt;
+            // m: the thread's largest logit; m2: what its sums are relative to, in base 2
+            // (-inf: nothing summed yet), at most kLag below the largest
+            float m = -INFINITY, m2 = -INFINITY;
+            int before = not_before ? -1 : 0;
             float2 S[2] = {}, A[2] = {};
             float T0 = kLowest;  // candidates reach it
-            auto grow = [&](float top) {  // the reference at least `top`
-                if (!(top <= m)) {        // (a NaN stays)
-                    const float n2 = __fmul_rn(top, a.y_scale), f = m < kNothing ? 0.f : exp2f(m2 - n2), d = m2 - n2;
-                    if (m < kNothing) {
-                        S[0] = S[1] = A[0] = A[1] = make_float2(0.f, 0.f);
-                    } else {
+            auto grow = [&](float top) {
+                m = max_nan(m, top);
+                const float n2 = __fmul_rn(top, a.y_scale);
+                if (n2 > m2 + kLag && top >= kNothing) {  // m2 = -inf: the first possible token
+                    const float d = m2 - n2, f = exp2f(d);
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            A[i] = make_float2(f * fmaf(S[i].x, d, A[i].x), f * fmaf(S[i].y, d, A[i].y));
-                            S[i] = make_float2(f * S[i].x, f * S[i].y);
-                        }
+                    for (int i = 0; i < 2; ++i) {
+                        A[i] = f == 0.f ? make_float2(0.f, 0.f)
+                                        : make_float2(f * fmaf(S[i].x, d, A[i].x), f * fmaf(S[i].y, d, A[i].y));
+                        S[i] = make_float2(f * S[i].x, f * S[i].y);
                     }
-                    m = max_nan(m, top);
                     m2 = n2;
                 }
             };
@@ -452,12 +488,13 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
 #pragma unroll
                 for (int u = 0; u < kPer; ++u)
                     w[u] = v0 + u * kConsumers + tid < hi ? src[u * kConsumers + tid] : Lp<T>::nothing();
-                float vm[kPer], top = -INFINITY;
+                typename Lp<T>::Top vm[kPer], all;
 #pragma unroll
                 for (int u = 0; u < kPer; ++u) {
                     vm[u] = Lp<T>::top(w[u]);
-                    top = max_nan(top, vm[u]);
+                    all = u ? Lp<T>::top(all, vm[u]) : vm[u];
                 }
+                const float top = Lp<T>::number(all);
                 grow(top);
                 const int chunk = (v0 - lo) / kChunk;
                 if (a.top && (chunk & (chunk + 1)) == 0 && (chunk == 0 || v0 + kChunk < hi)) {
@@ -477,32 +514,24 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
                     }
                     if (best) T0 = fmaxf(T0, unordered(best));
                 }
-                const float limit = a.top ? fminf(T0, xt) : xt;
+                if (m2 > -INFINITY) {
 #pragma unroll
-                for (int u = 0; u < kPer; ++u)
-                    if (m >= kNothing) Lp<T>::add(w[u], a.y_scale, m2, S, A);
+                    for (int u = 0; u < kPer; ++u) Lp<T>::add(w[u], a.y_scale, m2, S, A);
+                }
+                above.start();
 #pragma unroll
-                for (int u = 0; u < kPer; ++u) {
-                    const int v = v0 + u * kConsumers + tid;
-                    if (!(vm[u] >= limit) || v >= hi) continue;
-                    if (v > tv) {
-                        before += Lp<T>::template above<false>(w[u], xt);
-                    } else if (v < tv) {
-                        before += Lp<T>::template above<true>(w[u], xt);
-                    } else {  // the token's block
-                        const T *e = reinterpret_cast<const T *>(s.block) + (size_t)v * N;
-                        for (int i = 0; i < N; ++i) {
-                            const float f = Vec16<T>::load1(e + i);
-                            before += f > xt || (f == xt && v * N + i < s.off + tok);
+                for (int u = 0; u < kPer; ++u) above.add(w[u], v0 + u * kConsumers + tid <= tv ? up_to_it : after_it);
+                above.end();
+                if (top >= T0 && a.top) {
+#pragma unroll
+                    for (int u = 0; u < kPer; ++u)
+                        if (Lp<T>::number(vm[u]) >= T0) {
+                            const int at = atomicAdd(n_kept, 1);
+                            if (at < kVectors) {
+                                kept[at] = w[u];
+                                kept_at[at] = (v0 + u * kConsumers + tid) * N - s.off;
+                            }
                         }
-                    }
-                    if (a.top && vm[u] >= T0) {
-                        const int at = atomicAdd(n_kept, 1);
-                        if (at < kVectors) {
-                            kept[at] = w[u];
-                            kept_at[at] = v * N - s.off;
-                        }
-                    }
                 }
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(empty + at);
@@ -511,7 +540,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
                 const int id = s.edge(tid);
                 const float f = Vec16<T>::load1(static_cast<const T *>(a.logits) + (long long)row * a.stride + id);
                 grow(f);
-                if (m >= kNothing) {
+                if (m2 > -INFINITY) {
                     const float t = fmaf(fmaxf(f, kLowest), a.y_scale, -m2), p = ex2_approx(t);
                     S[0].x += p;
                     A[0].x = fmaf(p, t, A[0].x);
@@ -537,7 +566,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
                     candidate(Lp<T>::value(reinterpret_cast<const T *>(kept)[i]), kept_at[i / N] + i % N);
             }
             float sum = 0.f, asum = 0.f;
-            if (m >= kNothing) {
+            if (m2 > -INFINITY) {
                 const float d = m2 - __fmul_rn(top, a.y_scale), f = exp2f(d);
                 sum = (S[0].x + S[0].y) + (S[1].x + S[1].y);
                 asum = f * fmaf(sum, d, (A[0].x + A[0].y) + (A[1].x + A[1].y));
@@ -548,7 +577,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
                 sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 asum += __shfl_xor_sync(0xffffffffu, asum, o);
             }
-            before = __reduce_add_sync(0xffffffffu, before);
+            before = __reduce_add_sync(0xffffffffu, before + above.total());
             if (lane == 0) {
                 red[kWarps + warp] = sum;
                 red[2 * kWarps + warp] = asum;
