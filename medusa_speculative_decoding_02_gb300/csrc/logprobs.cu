@@ -7,18 +7,22 @@
 //     rank = number of tokens before t in the order (larger logit, then smaller id)
 //     alternatives: the first `top` tokens of that order
 //
-// A CTA (four warps that compute, one that copies) takes a row at a time, in chunks of
-// 512 16-byte vectors that come by bulk copies into a ring; with few rows a cluster of
-// CTAs shares each row.  A thread keeps its own reference, S and A, and moves the
-// reference when a chunk's maximum (packed, NaNs kept) exceeds it by 2^8; references in
-// base 2 are rounded by products that are not fused, so that all sums are relative
-// to the same number.
-// Ranks are packed comparisons with the token's logit, or up to its place with the
-// number below it.  Alternatives: the k-th largest of 32 groups of threads' maxima so
-// far is at most the row's k-th largest logit (T0, looked at again after 1, 2, 4, ..
-// chunks); vectors whose maximum reaches it are kept, at the row's end their elements that
-// do are the candidates (some tens), and a candidate's place in the order is the number
-// of better ones among them.
+// A CTA takes a row at a time, in chunks of 1024 16-byte vectors; with few rows a
+// cluster of CTAs shares each row.
+//   warps 0-3  a thread keeps the largest logit of its vectors, and S and A relative to
+//              a reference of its own, which moves when a chunk's maximum (packed, NaNs
+//              kept) exceeds it by 2^8.  References in base 2 are rounded by products
+//              that are not fused, so that all sums are relative to the same number.
+//              Ranks are packed comparisons with the token's logit, or up to its place
+//              with the number below it.
+//   warp 4     bulk copies into a ring of three chunks
+//   warp 5     ends a row while the others are at the next: it joins the threads' sums,
+//              and finds the alternatives.  The k-th largest of 32 groups of threads'
+//              maxima (T0) is at most the row's k-th largest logit.  The few threads
+//              whose maximum reaches it have their vectors of that chunk read again
+//              (from L2; of the whole row where the largest of their other chunks
+//              reaches it as well), the elements that reach it are the candidates, and
+//              a candidate's place in the order is the number of better ones among them.
 //
 // What this form does not take (a NaN, +inf or nothing above -1e29 in the row, the token
 // at -inf, too many candidates because of ties, fewer possible tokens
@@ -35,15 +39,15 @@ namespace medusa {
 
 namespace {
 
-constexpr int kConsumers = 128, kLpThreads = kConsumers + 32, kWarps = kConsumers / 32;
-constexpr int kChunk = 512, kPer = kChunk / kConsumers;  // vectors of a chunk, of a thread
-constexpr int kRing = 3, kLpCtas = 6;
-constexpr int kVectors = 256, kCandidates = 512;  // kept of a row
-constexpr int kMaxCluster = 8;
+constexpr int kConsumers = 128, kWarps = kConsumers / 32, kLpThreads = kConsumers + 64;
+constexpr int kChunk = 1024, kPer = kChunk / kConsumers;  // vectors of a chunk, of a thread
+constexpr int kRing = 3, kLpCtas = 4;
+constexpr int kCandidates = 256;
+constexpr int kMaxCluster = 4;
 constexpr uint32_t kLpPolls = 1u << 20;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -1e30f, kNothing = -1e29f, kHighest = 1e30f, kLag = 8.f;
-static_assert(32 >= MEDUSA_MAX_TOP_S && kMaxCluster * MEDUSA_MAX_TOP_S <= kConsumers, "groups, and parts' lists");
+static_assert(kMaxCluster * MEDUSA_MAX_TOP_S <= kCandidates, "the parts' lists");
 
 struct LogprobArgs {
     const void *logits;
@@ -66,21 +70,39 @@ struct RowPart {
     uint64_t key[MEDUSA_MAX_TOP_S];  // the part's first tokens (0: none)
 };
 
+// A thread's share of a row: the largest logit of its vectors, the chunk that holds it,
+// the largest of the other chunks; its sums and their reference in base 2.
+struct Sums {
+    float m, other;
+    int chunk;
+    float m2, S, A;
+    int before;
+};
+
 struct LpSmem {
     static constexpr int RING = 0;
-    static constexpr int VEC = kRing * kChunk * 16;  // vectors kept
-    static constexpr int CAND = VEC + kVectors * 16;  // candidates: see key_of
-    static constexpr int AT = CAND + kCandidates * 8; // the vectors' places
-    static constexpr int PART = AT + kVectors * 4;
-    static constexpr int RED = PART + (int)(sizeof(RowPart) + 15) / 16 * 16;  // [4][kWarps]
-    static constexpr int GROUP = RED + 4 * kWarps * 4;                        // [2][kWarps][32]
-    static constexpr int BAR = GROUP + 2 * kWarps * 32 * 4;
-    static constexpr int WORDS = BAR + 2 * kRing * 8;  // vectors, candidates of even and odd rows; failed
+    static constexpr int CAND = kRing * kChunk * 16;  // candidates: see key_of
+    static constexpr int VECTORS = CAND + kCandidates * 8;  // that hold them
+    static constexpr int PART = VECTORS + kCandidates * 4;
+    static constexpr int SUMS = PART + (int)(sizeof(RowPart) + 15) / 16 * 16;  // of the threads
+    static constexpr int COLUMNS = SUMS + kConsumers * (int)sizeof(Sums);      // [kConsumers]
+    static constexpr int BAR = (COLUMNS + kConsumers * 4 + 7) / 8 * 8;
+    static constexpr int WORDS = BAR + 2 * kRing * 8;  // vectors; failed
     static constexpr int TOTAL = WORDS + 32;
     static_assert(kLpCtas * (TOTAL + 1024) <= 228 * 1024, "CTAs of an SM");
 };
 
-__device__ __forceinline__ void consumers_sync() { asm volatile("barrier.cta.sync 1, %0;\n" ::"n"(kConsumers) : "memory"); }
+// Barriers between the warps that sum and the one that ends rows: the sums of a row
+// are there, and they have been read.
+template <int ID>
+__device__ __forceinline__ void row_arrive() {
+    asm volatile("barrier.cta.arrive %0, %1;\n" ::"n"(ID), "n"(kConsumers + 32) : "memory");
+}
+template <int ID>
+__device__ __forceinline__ void row_sync() {
+    asm volatile("barrier.cta.sync %0, %1;\n" ::"n"(ID), "n"(kConsumers + 32) : "memory");
+}
+constexpr int kSummed = 1, kRead = 2;
 
 // floats in order as unsigned numbers (a NaN: 0, below all)
 __device__ __forceinline__ uint32_t ordered(float f) {
@@ -215,90 +237,66 @@ struct RowShape {
     __device__ __forceinline__ int edge(int i) const { return i < left ? i : i + (last - first) * Lp<T>::N; }
 };
 
-template <typename F>
-__device__ __forceinline__ float fold_consumers(float v, float *s, F f) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
-    consumers_sync();
-    if (lane == 0) s[warp] = v;
-    consumers_sync();
-    v = s[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) v = f(v, s[w]);
-    return v;
-}
-
-// A row by the definition: a pass for the maximum, one for the sums, one for each
-// alternative.
+// A row by the definition, by one warp: a pass for the maximum, one for the sums, one
+// for each alternative.
 template <typename T>
-__device__ __noinline__ void slow_row(const LogprobArgs &a, int row, int tok, float *s_f, int *s_i) {
-    const int tid = threadIdx.x;
+__device__ __noinline__ void slow_row(const LogprobArgs &a, int row, int tok) {
+    const int lane = threadIdx.x & 31;
     const T *x = static_cast<const T *>(a.logits) + (long long)row * a.stride;
-    auto add = [](float p, float q) { return p + q; };
-    auto larger = [](float p, float q) { return fmaxf(p, q); };
     const float xt = tok >= 0 ? Vec16<T>::load1(x + tok) : NAN;
-    float m = -INFINITY, odd = 0.f;
-    for (int i = tid; i < a.V; i += kConsumers) {
+    float m = -INFINITY;
+    bool bad = false;  // +inf or NaN in the row
+#pragma unroll 8
+    for (int i = lane; i < a.V; i += 32) {
         const float f = Vec16<T>::load1(x + i);
         m = fmaxf(m, f);
-        if (!(f < INFINITY)) odd = 1.f;
+        bad = bad || !(f < INFINITY);
     }
-    m = fold_consumers(m, s_f, larger);
-    const bool bad = fold_consumers(odd, s_f, larger) != 0.f;  // +inf or NaN in the row
-    float S = 0.f, A = 0.f, before = 0.f;
-    for (int i = tid; i < a.V; i += kConsumers) {
+    bad = __any_sync(0xffffffffu, bad);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float S = 0.f, A = 0.f;
+    int before = 0;
+#pragma unroll 8
+    for (int i = lane; i < a.V; i += 32) {
         const float f = Vec16<T>::load1(x + i);
         const float t = fmaxf((f - m) * a.y_scale, -127.f), p = ex2_approx(t);
         S += p;
         A = fmaf(p, t, A);
-        if (f > xt || (f == xt && i < tok)) before += 1.f;
+        before += f > xt || (f == xt && i < tok);
     }
-    S = fold_consumers(S, s_f, add);
-    A = fold_consumers(A, s_f, add);
-    before = fold_consumers(before, s_f, add);
+    S = warp_sum(S);
+    A = warp_sum(A);
+    before = __reduce_add_sync(0xffffffffu, before);
     const bool none = m == -INFINITY;  // nothing is possible
     const float ls = log2f(S);
     auto logp_of = [&](float f) { return bad ? NAN : none ? -INFINITY : (f - m) * a.inv_T - ls * kLn2; };
-    if (tid == 0) {
+    if (lane == 0) {
         a.logp[row] = tok < 0 ? 0.f : logp_of(xt);
-        a.rank[row] = tok < 0 || isnan(xt) ? -1 : (int)before;
+        a.rank[row] = tok < 0 || isnan(xt) ? -1 : before;
         a.entropy[row] = bad ? NAN : none ? 0.f : fmaxf(kLn2 * (ls - A / S), 0.f);
     }
-    float lv = INFINITY;  // the alternative before
-    int li = -1;
-    bool any = true;
+    uint64_t last = ~0ull;  // the alternative before
     for (int k = 0; k < a.top; ++k) {
-        float bv = -INFINITY;
-        int bi = INT_MAX;
-        if (any)
-            for (int i = tid; i < a.V; i += kConsumers) {
+        uint64_t best = 0;
+        if (last)
+#pragma unroll 8
+            for (int i = lane; i < a.V; i += 32) {
                 const float f = Vec16<T>::load1(x + i);
-                if (!isnan(f) && (k == 0 || better(lv, li, f, i)) && (bi == INT_MAX || better(f, i, bv, bi))) {
-                    bv = f;
-                    bi = i;
-                }
+                const uint64_t c = isnan(f) ? 0 : key_of(f, i);
+                if (c < last && c > best) best = c;
             }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-            const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
-            if (better(ov, oi, bv, bi)) bv = ov, bi = oi;
+            const uint64_t c = __shfl_xor_sync(0xffffffffu, (unsigned long long)best, o);
+            if (c > best) best = c;
         }
-        consumers_sync();
-        if ((tid & 31) == 0) s_f[tid >> 5] = bv, s_i[tid >> 5] = bi;
-        consumers_sync();
-        for (int w = 0; w < kWarps; ++w)
-            if (better(s_f[w], s_i[w], bv, bi)) bv = s_f[w], bi = s_i[w];
-        any = bi != INT_MAX;
-        if (tid == 0) {
-            a.top_ids[(size_t)row * a.top + k] = any ? bi : -1;
-            a.top_logp[(size_t)row * a.top + k] = any ? logp_of(bv) : NAN;
+        if (lane == 0) {
+            a.top_ids[(size_t)row * a.top + k] = best ? key_id(best) : -1;
+            a.top_logp[(size_t)row * a.top + k] = best ? logp_of(key_logit(best)) : NAN;
         }
-        lv = bv;
-        li = bi;
+        last = best;
     }
-    consumers_sync();
 }
 
 __device__ __forceinline__ void bulk_copy(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
@@ -313,9 +311,8 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;\n" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory"); }
 // generic address of `p` in the shared memory of CTA `rank` of the cluster
 template <typename P>
 __device__ __forceinline__ const P *cluster_ptr(const P *p, uint32_t rank) {
@@ -352,13 +349,12 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
     constexpr int N = Lp<T>::N;
     extern __shared__ __align__(128) unsigned char sm[];
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + LpSmem::BAR), *empty = full + kRing;
-    uint4 *kept = reinterpret_cast<uint4 *>(sm + LpSmem::VEC);
     uint64_t *cand = reinterpret_cast<uint64_t *>(sm + LpSmem::CAND);
-    int *kept_at = reinterpret_cast<int *>(sm + LpSmem::AT);
     RowPart *part = reinterpret_cast<RowPart *>(sm + LpSmem::PART);
-    float *red = reinterpret_cast<float *>(sm + LpSmem::RED), *group_max = reinterpret_cast<float *>(sm + LpSmem::GROUP);
-    int *counts = reinterpret_cast<int *>(sm + LpSmem::WORDS);
-    volatile int *failed = reinterpret_cast<volatile int *>(counts + 4);
+    Sums *sums = reinterpret_cast<Sums *>(sm + LpSmem::SUMS);
+    int *columns = reinterpret_cast<int *>(sm + LpSmem::COLUMNS);
+    int *vectors = reinterpret_cast<int *>(sm + LpSmem::VECTORS), *n_vec = reinterpret_cast<int *>(sm + LpSmem::WORDS);
+    volatile int *failed = reinterpret_cast<volatile int *>(n_vec + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank_in = CLUSTER ? (int)cluster_rank() : 0;
     const int row0 = CLUSTER ? (int)blockIdx.x / C : blockIdx.x, row_step = CLUSTER ? a.N : gridDim.x;
@@ -368,15 +364,18 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
             tc::mbar_init(full + i, 1);
             tc::mbar_init(empty + i, kWarps);
         }
-        counts[0] = counts[1] = counts[2] = counts[3] = 0;
         *failed = 0;
         tc::fence_mbarrier_init();
     }
     __syncthreads();
     auto slice = [&](const RowShape<T> &s, int &lo, int &hi) {
-        const long long n = s.last - s.first;
-        lo = s.first + (int)(n * rank_in / C);
-        hi = s.first + (int)(n * (rank_in + 1) / C);
+        lo = s.first;
+        hi = s.last;
+        if constexpr (CLUSTER) {
+            const int per = (hi - lo + C - 1) / C;
+            lo = min(lo + rank_in * per, hi);
+            hi = min(lo + per, hi);
+        }
     };
     // a row's token (-1: none) and its logit
     auto token_of = [&](int row) { return row < a.N ? a.tokens[row] : -1; };
@@ -416,37 +415,34 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
                 if (!tc::mbar_wait_bounded(full + i % kRing, (i / kRing) & 1, kLpPolls)) *failed = 1;
         }
         __syncwarp();
-    } else {
-        // ------------------------------------------------------------ rows
-        int it = 0, tok = token_of(row0), odd = 0, look = 0;
+    } else if (warp < kWarps) {
+        // -------------------------------------------------------------- sums
+        int it = 0, tok = token_of(row0), next_tok = CLUSTER ? -1 : token_of(row0 + row_step);
         float xt = logit_of(row0, tok);
-        for (int row = row0; row < a.N; row += row_step, odd ^= 1) {
-            // (the next row's token and logit are on their way while this row is done)
-            const int next_tok = CLUSTER ? -1 : token_of(row + row_step);
+        for (int row = row0; row < a.N; row += row_step) {
+            // (the next row's logit, and the token after it, are on their way while this row is
+            // done)
+            const float next_xt = CLUSTER ? 0.f : logit_of(row + row_step, next_tok);
+            const int tok_after = CLUSTER ? -1 : token_of(row + 2 * row_step);
             const RowShape<T> s(a, row);
             int lo, hi;
             slice(s, lo, hi);
-            if (tok >= a.V || tok < -1) {
-                if (tid == 0 && rank_in == 0) set_status(a.status, MEDUSA_DEV_BAD_TOKEN);
+            if (tok >= a.V || tok < 0) {
                 tok = -1;
+                xt = INFINITY;
             }
             // Tokens before the row's own: logits above xt, in the blocks up to the token's
-            // own xt too (above the number below it), less the equal ones in that block
-            // from the token on, which are counted back here.
+            // own xt too (above the number below it); the equal ones of that block from the
+            // token on are counted back at the row's end.
             const int tv = tok >= 0 ? (s.off + tok) / N : -1;
             const typename Lp<T>::Bound after_it = Lp<T>::bound(xt), up_to_it = Lp<T>::bound(Lp<T>::below(xt));
             typename Lp<T>::Count above;
-            bool not_before = false;
-            if (tid < N && tv >= lo && tv < hi && tv * N - s.off + tid >= tok)
-                not_before = logit_of(row, tv * N - s.off + tid) == xt;
-            // m: the thread's largest logit; m2: what its sums are relative to, in base 2
-            // (-inf: nothing summed yet), at most kLag below the largest
-            float m = -INFINITY, m2 = -INFINITY;
-            int before = not_before ? -1 : 0;
+            // m2: what the sums are relative to, in base 2 (-inf: nothing summed yet), at
+            // most kLag below the largest
+            float m = -INFINITY, other = -INFINITY, m2 = -INFINITY;
+            int before = 0, chunk = 0;
             float2 S[2] = {}, A[2] = {};
-            float T0 = kLowest;  // candidates reach it
             auto grow = [&](float top) {
-                m = max_nan(m, top);
                 const float n2 = __fmul_rn(top, a.y_scale);
                 if (n2 > m2 + kLag && top >= kNothing) {  // m2 = -inf: the first possible token
                     const float d = m2 - n2, f = exp2f(d);
@@ -457,22 +453,6 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
                         S[i] = make_float2(f * S[i].x, f * S[i].y);
                     }
                     m2 = n2;
-                }
-            };
-            // Counters of this row.  The row before has done with its own, and with what is
-            // kept, behind the first barrier of this row: of T0, or here.
-            int *n_kept = counts + 2 * odd, *n_cand = n_kept + 1;
-            auto other_counters = [&] {
-                if (tid == 0) counts[2 * (odd ^ 1)] = counts[2 * (odd ^ 1) + 1] = 0;
-            };
-            if (lo >= hi) {
-                consumers_sync();
-                other_counters();
-            }
-            auto candidate = [&](float f, int id) {
-                if (f >= T0) {
-                    const int at = atomicAdd(n_cand, 1);
-                    if (at < kCandidates) cand[at] = key_of(f, id);
                 }
             };
             for (int v0 = lo; v0 < hi; v0 += kChunk, ++it) {
@@ -488,32 +468,14 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
 #pragma unroll
                 for (int u = 0; u < kPer; ++u)
                     w[u] = v0 + u * kConsumers + tid < hi ? src[u * kConsumers + tid] : Lp<T>::nothing();
-                typename Lp<T>::Top vm[kPer], all;
+                typename Lp<T>::Top all = Lp<T>::top(w[0]);
 #pragma unroll
-                for (int u = 0; u < kPer; ++u) {
-                    vm[u] = Lp<T>::top(w[u]);
-                    all = u ? Lp<T>::top(all, vm[u]) : vm[u];
-                }
+                for (int u = 1; u < kPer; ++u) all = Lp<T>::top(all, Lp<T>::top(w[u]));
                 const float top = Lp<T>::number(all);
+                other = fmaxf(other, fminf(m, top));
+                if (top > m) chunk = (v0 - lo) / kChunk;
+                m = max_nan(m, top);
                 grow(top);
-                const int chunk = (v0 - lo) / kChunk;
-                if (a.top && (chunk & (chunk + 1)) == 0 && (chunk == 0 || v0 + kChunk < hi)) {
-                    // (two places by turns: a warp may be a look ahead of another)
-                    float *gm = group_max + look * kWarps * 32;
-                    look ^= 1;
-                    gm[warp * 32 + lane] = m;
-                    consumers_sync();
-                    if (chunk == 0) other_counters();
-                    uint32_t mine = 0, best = 0;
-#pragma unroll
-                    for (int x = 0; x < kWarps; ++x) mine = max(mine, ordered(gm[x * 32 + lane]));
-                    // (equal ones go at once: the bound may only be lower)
-                    for (int k = 0; k < a.top; ++k) {
-                        best = __reduce_max_sync(0xffffffffu, mine);
-                        if (mine == best) mine = 0;
-                    }
-                    if (best) T0 = fmaxf(T0, unordered(best));
-                }
                 if (m2 > -INFINITY) {
 #pragma unroll
                     for (int u = 0; u < kPer; ++u) Lp<T>::add(w[u], a.y_scale, m2, S, A);
@@ -522,17 +484,6 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
 #pragma unroll
                 for (int u = 0; u < kPer; ++u) above.add(w[u], v0 + u * kConsumers + tid <= tv ? up_to_it : after_it);
                 above.end();
-                if (top >= T0 && a.top) {
-#pragma unroll
-                    for (int u = 0; u < kPer; ++u)
-                        if (Lp<T>::number(vm[u]) >= T0) {
-                            const int at = atomicAdd(n_kept, 1);
-                            if (at < kVectors) {
-                                kept[at] = w[u];
-                                kept_at[at] = (v0 + u * kConsumers + tid) * N - s.off;
-                            }
-                        }
-                }
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(empty + at);
             }
@@ -546,163 +497,213 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
                     A[0].x = fmaf(p, t, A[0].x);
                 }
                 before += f > xt || (f == xt && id < tok);
-                if (a.top) candidate(f, id);
             }
-            const float next_xt = CLUSTER ? 0.f : logit_of(row + row_step, next_tok);
-            // ---- the CTA's part: the reference first, then plain sums
-            float top;
-            asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;\n" : "=f"(top) : "f"(m));
-            if (lane == 0) red[warp] = top;
-            consumers_sync();
-            top = red[0];
+            if (row != row0) row_sync<kRead>();  // the sums of the row before
+            sums[tid] = Sums{m, other, chunk, m2, (S[0].x + S[0].y) + (S[1].x + S[1].y), (A[0].x + A[0].y) + (A[1].x + A[1].y),
+                             before + above.total()};
+            row_arrive<kSummed>();
+            tok = next_tok;
+            next_tok = tok_after;
+            xt = next_xt;
+        }
+    } else {
+        // ----------------------------------------------------------- rows' ends
+        for (int row = row0; row < a.N; row += row_step) {
+            const RowShape<T> s(a, row);
+            int lo, hi;
+            slice(s, lo, hi);
+            int tok = token_of(row);
+            if (tok >= a.V || tok < -1) {
+                if (lane == 0 && rank_in == 0) set_status(a.status, MEDUSA_DEV_BAD_TOKEN);
+                tok = -1;
+            }
+            const float xt = logit_of(row, tok);
+            // equal logits of the token's block from the token on
+            const int tv = tok >= 0 ? (s.off + tok) / N : -1, beside = tv * N - s.off + lane;
+            const bool back = lane < N && tv >= lo && tv < hi && beside >= tok && logit_of(row, beside) == xt;
+            const bool at_edge = rank_in == 0 && lane < s.edges;
+            const float f_edge = at_edge ? logit_of(row, s.edge(lane)) : 0.f;
+            row_sync<kSummed>();
+            Sums x[kWarps];
 #pragma unroll
-            for (int x = 1; x < kWarps; ++x) top = max_nan(top, red[x]);
-            // the kept vectors' elements that reach T0
-            bool many = false;
-            if (a.top) {
-                const int n = *n_kept;
-                many = n > kVectors;
-                for (int i = tid; i < min(n, kVectors) * N; i += kConsumers)
-                    candidate(Lp<T>::value(reinterpret_cast<const T *>(kept)[i]), kept_at[i / N] + i % N);
-            }
+            for (int w = 0; w < kWarps; ++w) x[w] = sums[w * 32 + lane];
+            if (row + row_step < a.N) row_arrive<kRead>();
+            float top = max_nan(max_nan(x[0].m, x[1].m), max_nan(x[2].m, x[3].m));
+            static_assert(kWarps == 4, "four shares a lane");
+            if (at_edge) top = max_nan(top, f_edge);
+            asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;\n" : "=f"(top) : "f"(top));
+            const float t2 = __fmul_rn(top, a.y_scale);
             float sum = 0.f, asum = 0.f;
-            if (m2 > -INFINITY) {
-                const float d = m2 - __fmul_rn(top, a.y_scale), f = exp2f(d);
-                sum = (S[0].x + S[0].y) + (S[1].x + S[1].y);
-                asum = f * fmaf(sum, d, (A[0].x + A[0].y) + (A[1].x + A[1].y));
-                sum *= f;
-            }
+            int before = back ? -1 : 0;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                asum += __shfl_xor_sync(0xffffffffu, asum, o);
+            for (int w = 0; w < kWarps; ++w) {
+                before += x[w].before;
+                if (x[w].m2 > -INFINITY) {
+                    const float d = x[w].m2 - t2, f = exp2f(d);
+                    sum = fmaf(f, x[w].S, sum);
+                    asum = fmaf(f, fmaf(x[w].S, d, x[w].A), asum);
+                }
             }
-            before = __reduce_add_sync(0xffffffffu, before + above.total());
-            if (lane == 0) {
-                red[kWarps + warp] = sum;
-                red[2 * kWarps + warp] = asum;
-                red[3 * kWarps + warp] = __int_as_float(before);
-            }
-            consumers_sync();
-            sum = red[kWarps];
-            asum = red[2 * kWarps];
-            before = __float_as_int(red[3 * kWarps]);
+            sum = warp_sum(sum);
+            asum = warp_sum(asum);
+            before = __reduce_add_sync(0xffffffffu, before);
+            int n = 0;
+            if (a.top) {
+                float mine = -INFINITY;  // (NaNs are left out: such a row is not done here)
 #pragma unroll
-            for (int x = 1; x < kWarps; ++x) {
-                sum += red[kWarps + x];
-                asum += red[2 * kWarps + x];
-                before += __float_as_int(red[3 * kWarps + x]);
+                for (int w = 0; w < kWarps; ++w) mine = fmaxf(mine, x[w].m);
+                int place = 0;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float o = __shfl_sync(0xffffffffu, mine, i);
+                    place += o > mine || (o == mine && i < lane);
+                }
+                const uint32_t kth = __ballot_sync(0xffffffffu, place == a.top - 1);
+                const float T0 = fmaxf(kth ? __shfl_sync(0xffffffffu, mine, __ffs(kth) - 1) : kLowest, kLowest);
+                int n_col = 0;  // the threads that reach it
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const bool is = x[w].m >= T0;
+                    const uint32_t who = __ballot_sync(0xffffffffu, is);
+                    if (is) columns[n_col + __popc(who & ((1u << lane) - 1))] = w * 32 + lane + x[w].chunk * kChunk;
+                    n_col += __popc(who);
+                }
+                if (lane == 0) *n_vec = 0;
+                __syncwarp();
+                const uint4 *blocks = reinterpret_cast<const uint4 *>(s.block);
+                auto keep = [&](int v) {
+                    const int at = atomicAdd(n_vec, 1);
+                    if (at < kCandidates) vectors[at] = v;
+                };
+                constexpr int kAhead = 4;
+                for (int i0 = lane; i0 - lane < n_col * kPer; i0 += 32 * kAhead) {
+                    uint4 y[kAhead];
+                    int v[kAhead];
+#pragma unroll
+                    for (int q = 0; q < kAhead; ++q) {
+                        const int i = i0 + 32 * q;
+                        v[q] = i < n_col * kPer ? lo + columns[i / kPer] + i % kPer * kConsumers : hi;
+                        y[q] = v[q] < hi ? __ldg(blocks + v[q]) : Lp<T>::nothing();
+                    }
+#pragma unroll
+                    for (int q = 0; q < kAhead; ++q)
+                        if (Lp<T>::number(Lp<T>::top(y[q])) >= T0) keep(v[q]);
+                }
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+                    for (uint32_t who = __ballot_sync(0xffffffffu, x[w].other >= T0); who; who &= who - 1) {
+                        const int t = __ffs(who) - 1, done = __shfl_sync(0xffffffffu, x[w].chunk, t);
+                        for (int v = lo + w * 32 + t + lane * kConsumers; v < hi; v += 32 * kConsumers)
+                            if ((v - lo) / kChunk != done && Lp<T>::number(Lp<T>::top(__ldg(blocks + v))) >= T0) keep(v);
+                    }
+                __syncwarp();
+                // the candidates, numbered by the warp
+                auto candidates = [&](bool is, float f, int id) {
+                    const uint32_t who = __ballot_sync(0xffffffffu, is && f >= T0);
+                    const int at = n + __popc(who & ((1u << lane) - 1));
+                    if (is && f >= T0 && at < kCandidates) cand[at] = key_of(f, id);
+                    n += __popc(who);
+                };
+                const int nv = *n_vec;
+                if (nv > kCandidates) n = kCandidates + 1;
+                for (int i = lane; i - lane < nv * N && nv <= kCandidates; i += 32) {
+                    const bool is = i < nv * N;
+                    const int id = is ? vectors[i / N] * N - s.off + i % N : 0;
+                    candidates(is, is ? logit_of(row, id) : 0.f, id);
+                }
+                if (s.edges) candidates(at_edge, f_edge, s.edge(lane));
+                __syncwarp();
             }
-            int n = *n_cand;
-            many = many || n > kCandidates;
+            const bool many = n > kCandidates;
             if (many) n = 0;
             // places of the candidates in the order
-            auto place_of = [&](uint64_t c) {
+            auto place_of = [&](uint64_t c, int n) {
                 int p = 0;
 #pragma unroll 4
                 for (int i = 0; i < n; ++i) p += cand[i] > c;
                 return p;
             };
-            if constexpr (CLUSTER) {
-                if (tid < a.top) part->key[tid] = 0;
-                consumers_sync();
-                for (int i = tid; i < n; i += kConsumers) {
+            auto finish = [&](bool many, int n) {
+                if (!fast_form(a, top, many, n, tok, xt)) {
+                    slow_row<T>(a, row, tok);
+                    return;
+                }
+                const LogP logp_of(a, top, sum);
+                if (lane == 0) {
+                    a.logp[row] = tok < 0 ? 0.f : logp_of(xt);
+                    a.rank[row] = tok < 0 ? -1 : before;
+                    a.entropy[row] = fmaxf(kLn2 * (logp_of.ls - asum / sum), 0.f);
+                }
+                for (int i = lane; i < n; i += 32) {
                     const uint64_t c = cand[i];
-                    const int p = place_of(c);
+                    const int p = place_of(c, n);
+                    if (p < a.top && c) {
+                        a.top_ids[(size_t)row * a.top + p] = key_id(c);
+                        a.top_logp[(size_t)row * a.top + p] = logp_of(key_logit(c));
+                    }
+                }
+                __syncwarp();
+            };
+            if constexpr (CLUSTER) {
+                if (lane < a.top) part->key[lane] = 0;
+                __syncwarp();
+                for (int i = lane; i < n; i += 32) {
+                    const uint64_t c = cand[i];
+                    const int p = place_of(c, n);
                     if (p < a.top) part->key[p] = c;
                 }
-                if (tid == 0) {
+                if (lane == 0) {
                     part->m = top;
                     part->S = sum;
                     part->A = asum;
                     part->before = before;
                     part->n = many ? -1 : min(n, a.top);
                 }
-                break;  // (to the cluster's barriers, which are for all its warps)
-            } else {
-                if (fast_form(a, top, many, n, tok, xt)) {
-                    const LogP logp_of(a, top, sum);
-                    if (tid == 0) {
-                        a.logp[row] = tok < 0 ? 0.f : logp_of(xt);
-                        a.rank[row] = tok < 0 ? -1 : before;
-                        a.entropy[row] = fmaxf(kLn2 * (logp_of.ls - asum / sum), 0.f);
+                __syncwarp();
+                cluster_arrive();  // the part is written
+                cluster_wait();
+                if (rank_in == 0) {
+                    const RowPart *p = cluster_ptr(part, lane < C ? lane : 0);
+                    const bool mine = lane < C;
+                    const float m = mine ? p->m : -INFINITY;
+                    asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;\n" : "=f"(top) : "f"(m));
+                    sum = asum = 0.f;
+                    if (mine && m >= kNothing) {
+                        const float d = __fmul_rn(m, a.y_scale) - __fmul_rn(top, a.y_scale), f = exp2f(d);
+                        sum = f * p->S;
+                        asum = f * fmaf(p->S, d, p->A);
                     }
-                    if (a.top)
-                        for (int i = tid; i < n; i += kConsumers) {
-                            const uint64_t c = cand[i];
-                            const int p = place_of(c);
-                            if (p < a.top) {
-                                a.top_ids[(size_t)row * a.top + p] = key_id(c);
-                                a.top_logp[(size_t)row * a.top + p] = logp_of(key_logit(c));
-                            }
-                        }
-                } else {
-                    slow_row<T>(a, row, tok, red, reinterpret_cast<int *>(group_max));
+                    sum = warp_sum(sum);
+                    asum = warp_sum(asum);
+                    before = __reduce_add_sync(0xffffffffu, mine ? p->before : 0);
+                    n = mine ? p->n : 0;
+                    const bool over = __any_sync(0xffffffffu, n < 0);
+                    n = __reduce_add_sync(0xffffffffu, n);
+                    if (fast_form(a, top, over, n, tok, xt)) {
+                        // the parts' first tokens, gathered, then placed as the candidates are
+                        for (int i = lane; i < C * a.top; i += 32)
+                            cand[i] = cluster_ptr(part, i / a.top)->key[i % a.top];
+                        n = C * a.top;
+                        __syncwarp();
+                    }
+                    finish(over, n);
                 }
-                tok = next_tok;
-                xt = next_xt;
+                __syncwarp();
+            } else {
+                finish(many, n);
             }
         }
     }
     if constexpr (CLUSTER) {
-        __syncthreads();
-        cluster_sync();  // every part is written
-        if (rank_in == 0 && warp < kWarps) {
-            const int row = row0;
-            int tok = a.tokens[row];
-            if (tok >= a.V || tok < -1) tok = -1;
-            const float xt = logit_of(row, tok);
-            const RowPart *p = cluster_ptr(part, lane < C ? lane : 0);
-            const bool mine = lane < C;
-            const float m = mine ? p->m : -INFINITY;
-            float top = m, sum = 0.f, asum = 0.f;
-            int before = mine ? p->before : 0, n = mine ? p->n : 0;
-#pragma unroll
-            for (int o = 4; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-            top = __shfl_sync(0xffffffffu, top, 0);
-            if (mine && m >= kNothing) {
-                const float d = __fmul_rn(m, a.y_scale) - __fmul_rn(top, a.y_scale), f = exp2f(d);
-                sum = f * p->S;
-                asum = f * fmaf(p->S, d, p->A);
-            }
-            const bool many = __any_sync(0xffffffffu, n < 0);
-#pragma unroll
-            for (int o = 4; o > 0; o >>= 1) {
-                sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                asum += __shfl_xor_sync(0xffffffffu, asum, o);
-                before += __shfl_xor_sync(0xffffffffu, before, o);
-                n += __shfl_xor_sync(0xffffffffu, n, o);
-            }
-            sum = __shfl_sync(0xffffffffu, sum, 0);
-            asum = __shfl_sync(0xffffffffu, asum, 0);
-            before = __shfl_sync(0xffffffffu, before, 0);
-            n = __shfl_sync(0xffffffffu, n, 0);
-            if (fast_form(a, top, many, n, tok, xt)) {
-                const LogP logp_of(a, top, sum);
-                if (tid == 0) {
-                    a.logp[row] = tok < 0 ? 0.f : logp_of(xt);
-                    a.rank[row] = tok < 0 ? -1 : before;
-                    a.entropy[row] = fmaxf(kLn2 * (logp_of.ls - asum / sum), 0.f);
-                }
-                // the parts' first tokens, gathered, then placed as the candidates are
-                if (tid < C * a.top) cand[tid] = cluster_ptr(part, tid / a.top)->key[tid % a.top];
-                consumers_sync();
-                if (tid < C * a.top) {
-                    const uint64_t c = cand[tid];
-                    int at = 0;
-                    for (int i = 0; i < C * a.top; ++i) at += cand[i] > c;
-                    if (at < a.top && c) {
-                        a.top_ids[(size_t)row * a.top + at] = key_id(c);
-                        a.top_logp[(size_t)row * a.top + at] = logp_of(key_logit(c));
-                    }
-                }
-            } else {
-                slow_row<T>(a, row, tok, red, reinterpret_cast<int *>(group_max));
-            }
+        if (warp != kWarps + 1) {
+            cluster_arrive();
+            cluster_wait();
         }
         __syncwarp();
-        cluster_sync();  // no CTA leaves while its part may be read
+        cluster_arrive();  // no CTA leaves while its part may be read
+        cluster_wait();
     }
+    __syncthreads();
     if (tid == 0 && *failed) set_status(a.status, MEDUSA_DEV_TIMEOUT);
 }
 
@@ -738,7 +739,9 @@ cudaError_t launch_token_logprobs(medusa_dtype dtype, const void *logits, long l
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LpSmem::TOTAL);
     if (e) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(C > 1 ? N * C : std::min(N, slots));
+    // (as many rows for each CTA, rather than a last round of a few)
+    const int rounds = (N + slots - 1) / slots;
+    cfg.gridDim = dim3(C > 1 ? N * C : (N + rounds - 1) / rounds);
     cfg.blockDim = dim3(kLpThreads);
     cfg.dynamicSmemBytes = LpSmem::TOTAL;
     cfg.stream = stream;
