@@ -891,8 +891,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
 template <typename T, int DH>
 __global__ void __launch_bounds__(256)
 cache_attn_combine_kernel(const float *__restrict__ part_o, const float2 *__restrict__ part_ml,
-                          const int *__restrict__ starts, const int32_t *__restrict__ n_rows, int B,
-                          int R, int H, int ns, T *__restrict__ out) {
+                          const int *__restrict__ starts, int B, int R, int H, int ns,
+                          T *__restrict__ out) {
     pdl_enter();
     constexpr int PER = DH / 32, AHEAD = 8;
     const int lane = threadIdx.x & 31;
@@ -900,9 +900,7 @@ cache_attn_combine_kernel(const float *__restrict__ part_o, const float2 *__rest
     if (item >= (long long)B * H * R) return;
     const int r = (int)(item % R);
     const long long bh = item / R;
-    const int b = (int)(bh / H);
-    if (n_rows && r >= n_rows[b]) return;
-    const int first_range = starts ? starts[b] : b * ns;
+    const int b = (int)(bh / H), first_range = starts ? starts[b] : b * ns;
     const int NS = starts ? starts[b + 1] - first_range : ns;
     const size_t ml_step = (size_t)H * R, step = ml_step * DH;
     const float2 *ml = part_ml + first_range * ml_step + (bh % H) * R + r;
@@ -1090,22 +1088,17 @@ cudaError_t launch_cache_attention(medusa_dtype dtype, bool kv4, const void *q,
     }
     note_launch();
     if (e || p.ns == 1) return e;
-    return launch_cache_combine(a, dtype, dh, stream);
-}
-
-cudaError_t launch_cache_combine(const CacheAttnArgs &a, medusa_dtype dtype, int dh, cudaStream_t stream) {
-    const unsigned blocks = (unsigned)(((long long)a.B * a.H * a.R + 7) / 8);
+    const unsigned blocks = (unsigned)(((long long)B * H * R + 7) / 8);
     const float *po = a.part_o;
     const float2 *pm = a.part_ml;
-    cudaError_t e;
-    if (dtype == MEDUSA_F32)
+    if (f32)
         e = launch_pdl(dh == 128 ? cache_attn_combine_kernel<float, 128> : cache_attn_combine_kernel<float, 64>,
-                       dim3(blocks), dim3(256), 0, stream, po, pm, (const int *)a.starts, a.n_rows, a.B, a.R,
-                       a.H, a.ns, static_cast<float *>(a.out));
+                       dim3(blocks), dim3(256), 0, stream, po, pm, (const int *)a.starts, B, R, H, p.ns,
+                       static_cast<float *>(out));
     else
         e = launch_pdl(dh == 128 ? cache_attn_combine_kernel<bf16, 128> : cache_attn_combine_kernel<bf16, 64>,
-                       dim3(blocks), dim3(256), 0, stream, po, pm, (const int *)a.starts, a.n_rows, a.B, a.R,
-                       a.H, a.ns, static_cast<bf16 *>(a.out));
+                       dim3(blocks), dim3(256), 0, stream, po, pm, (const int *)a.starts, B, R, H, p.ns,
+                       static_cast<bf16 *>(out));
     note_launch();
     return e;
 }

@@ -225,10 +225,6 @@ cudaError_t launch_cache_attention_few(const CacheAttnArgs &a, bool kv4, int dh,
 constexpr int kPagedTileRows = 256, kPagedStage = 128;
 cudaError_t launch_paged_attention_tc(const CacheAttnArgs &a, int dh, cudaStream_t stream);
 
-// Joins the ranges of a call (a.part_o, a.part_ml, a.starts) into a.out; rows behind
-// a sequence's a.n_rows are left alone.
-cudaError_t launch_cache_combine(const CacheAttnArgs &a, medusa_dtype dtype, int dh, cudaStream_t stream);
-
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace medusa

@@ -5,7 +5,7 @@
 // Query head h reads KV head h / G (G = H / Hkv).  The rows of a tile are rows that
 // share a KV head, row r * G + g being new row r and query head hk * G + g.  A
 // tile's keys are split into ranges where there are few tiles (find_item), which
-// cache_attn_combine_kernel joins.  A slot whose page number is outside the pool is
+// paged_join_kernel joins.  A slot whose page number is outside the pool is
 // not seen (and the status is set).  A row that sees nothing gets zeros; rows behind
 // a sequence's n_rows are neither read nor written.
 //
@@ -221,6 +221,156 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_attn_simt_kernel(CacheA
     }
 }
 
+// ------------------------------------------------------------------- join ---
+
+// out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s over a row's key ranges.  An empty range
+// (l = 0) has no O row.  The O rows do not depend on the weights: the first of them are
+// on their way while those are computed.
+template <typename T>
+__device__ __forceinline__ void store_row4(T *dst, const float (&x)[4], float inv) {
+    if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float4 *>(dst) = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+    else
+        *reinterpret_cast<uint2 *>(dst) =
+            make_uint2(pack_weights<false>(x[0] * inv, x[1] * inv), pack_weights<false>(x[2] * inv, x[3] * inv));
+}
+__device__ __forceinline__ void add4(float (&acc)[4], float f, const float4 &x) {
+    acc[0] = fmaf(f, x.x, acc[0]);
+    acc[1] = fmaf(f, x.y, acc[1]);
+    acc[2] = fmaf(f, x.z, acc[2]);
+    acc[3] = fmaf(f, x.w, acc[3]);
+}
+
+// Many rows: eight lanes a row, so that many rows are on their way.
+template <typename T, int DH>
+__global__ void __launch_bounds__(128, 4) paged_join_rows_kernel(CacheAttnArgs a) {
+    pdl_enter();
+    constexpr int C = DH / 8, V = C / 4, AHEAD = 4;  // a lane's columns, vectors of them
+    const int lane = threadIdx.x & 31, c = lane & 7, R = a.R, H = a.H;
+    const int groups = (R + 3) / 4;
+    const long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (item >= (long long)a.B * H * groups) return;
+    const int r = (int)(item % groups) * 4 + (lane >> 3);
+    const int bh = (int)(item / groups), b = bh / H, h = bh - b * H;
+    const bool live = r < live_rows(a, b);
+    const int first = a.starts ? a.starts[b] : b * a.ns, NS = a.starts ? a.starts[b + 1] - first : a.ns;
+    const size_t step = (size_t)H * R, at = first * step + (size_t)h * R + (live ? r : 0);
+    const float4 *po = reinterpret_cast<const float4 *>(a.part_o + at * DH) + c * V;
+    float4 row[AHEAD][V];
+    auto load = [&](int s, float4 (&x)[V]) {
+        if (s < NS)
+#pragma unroll
+            for (int v = 0; v < V; ++v) x[v] = po[s * step * (DH / 4) + v];
+    };
+#pragma unroll
+    for (int s = 0; s < AHEAD; ++s) load(s, row[s]);
+    const float2 empty = make_float2(-INFINITY, 0.f);
+    auto ml = [&](int s) { return s < NS ? a.part_ml[at + s * step] : empty; };
+    const float2 mine = ml(c);  // of range c; ranges from 8 on are read again below
+    float M = mine.y != 0.f ? mine.x : -INFINITY;
+    for (int s = c + 8; s < NS; s += 8) {
+        const float2 x = ml(s);
+        if (x.y != 0.f) M = fmaxf(M, x.x);
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float mu = M == -INFINITY ? 0.f : M;
+    float L = 0.f, w = 0.f, acc[V][4];
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v][0] = acc[v][1] = acc[v][2] = acc[v][3] = 0.f;
+    for (int s0 = 0; s0 < NS; s0 += AHEAD) {
+        if ((s0 & 7) == 0) {
+            const float2 x = s0 == 0 ? mine : ml(s0 + c);
+            w = x.y != 0.f ? exp2f(x.x - mu) : 0.f;
+            if (x.y != 0.f) L = fmaf(w, x.y, L);
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const float f = __shfl_sync(0xffffffffu, w, (lane & 24) | ((s0 + i) & 7));
+            if (s0 + i < NS && f != 0.f) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) add4(acc[v], f, row[i][v]);
+            }
+            load(s0 + AHEAD + i, row[i]);
+        }
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (!live) return;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    T *dst = static_cast<T *>(a.out) + (((size_t)b * R + r) * H + h) * DH + c * C;
+#pragma unroll
+    for (int v = 0; v < V; ++v) store_row4(dst + 4 * v, acc[v], inv);
+}
+
+// Few rows: a CTA a row, its ranges dealt to groups of DH / 4 threads.  grid B * H * R
+template <typename T, int DH>
+__global__ void __launch_bounds__(256) paged_join_ranges_kernel(CacheAttnArgs a) {
+    pdl_enter();
+    constexpr int COLS = DH / 4, GROUPS = 256 / COLS, AHEAD = 4;
+    __shared__ float s_o[GROUPS][COLS][4];
+    const int tid = threadIdx.x, lane = tid & 31, c = tid % COLS, group = tid / COLS, R = a.R, H = a.H;
+    const int r = blockIdx.x % R, bh = blockIdx.x / R, b = bh / H, h = bh - b * H;
+    if (r >= live_rows(a, b)) return;  // uniform over the CTA
+    const int first = a.starts ? a.starts[b] : b * a.ns, NS = a.starts ? a.starts[b + 1] - first : a.ns;
+    const size_t step = (size_t)H * R, at = first * step + (size_t)h * R + r;
+    const float4 *po = reinterpret_cast<const float4 *>(a.part_o + at * DH) + c;
+    const float2 *ml = a.part_ml + at;
+    float4 row[AHEAD];
+    auto load = [&](int s, float4 &x) {
+        if (s < NS) x = po[s * step * (DH / 4)];
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) load(group + i * GROUPS, row[i]);
+    float M = -INFINITY;
+    for (int s = lane; s < NS; s += 32) {
+        const float2 x = ml[s * step];
+        if (x.y != 0.f) M = fmaxf(M, x.x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float mu = M == -INFINITY ? 0.f : M;
+    float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s = lane; s < NS; s += 32) {  // (every warp for itself; from the cache)
+        const float2 x = ml[s * step];
+        if (x.y != 0.f) L = fmaf(exp2f(x.x - mu), x.y, L);
+    }
+    L = warp_sum(L);
+    for (int s0 = group; s0 < NS; s0 += AHEAD * GROUPS)
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int s = s0 + i * GROUPS;
+            if (s < NS) {
+                const float2 x = ml[s * step];
+                const float f = x.y != 0.f ? exp2f(x.x - mu) : 0.f;
+                if (f != 0.f) add4(acc, f, row[i]);
+            }
+            load(s + AHEAD * GROUPS, row[i]);
+        }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s_o[group][c][e] = acc[e];
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int x = 1; x < GROUPS; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] += s_o[x][c][e];
+    store_row4(static_cast<T *>(a.out) + (((size_t)b * R + r) * H + h) * DH + c * 4, acc, L == 0.f ? 0.f : 1.f / L);
+}
+
+// Up to kJoinFewRows rows the time is the latency of a row's ranges, beyond it is how
+// many rows are on their way.
+constexpr int kJoinFewRows = 1024;
+
+template <typename T, int DH>
+cudaError_t launch_join(const CacheAttnArgs &a, cudaStream_t stream) {
+    const long long rows = (long long)a.B * a.H * a.R;
+    if (rows <= kJoinFewRows)
+        return launch_pdl(paged_join_ranges_kernel<T, DH>, dim3((unsigned)rows), dim3(256), 0, stream, a);
+    const long long warps = (long long)a.B * a.H * ((a.R + 3) / 4);
+    return launch_pdl(paged_join_rows_kernel<T, DH>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, stream, a);
+}
+
 // ------------------------------------------------------------------- host ---
 
 struct PagedPlan {
@@ -312,7 +462,10 @@ cudaError_t launch_paged_attention(medusa_dtype dtype, const void *q, const void
     }
     note_launch();
     if (e || p.ns == 1) return e;
-    return launch_cache_combine(a, dtype, dh, stream);
+    e = dtype == MEDUSA_F32 ? (dh == 128 ? launch_join<float, 128>(a, stream) : launch_join<float, 64>(a, stream))
+                            : (dh == 128 ? launch_join<bf16, 128>(a, stream) : launch_join<bf16, 64>(a, stream));
+    note_launch();
+    return e;
 }
 
 }  // namespace medusa

@@ -94,21 +94,53 @@ __device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
 template <int DH, bool DEAL>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs a) {
-    pdl_enter();
     using L = PagedSmem<DH>;
     constexpr int NK = L::NK, NT = 2 * NK;
     extern __shared__ __align__(1024) unsigned char sm[];
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BAR), *empty = full + NT, *bar_q = empty + NT,
              *bar_s = bar_q + 2, *bar_o = bar_q + 4, *bar_p = bar_q + 6, *bar_drain = bar_q + 10,
              *armed = bar_q + 11, *clean = armed + kMaskedStages;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     volatile int *failed = reinterpret_cast<volatile int *>(sm + L::WORDS);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(sm + L::WORDS + 4);
     int *bad_v = reinterpret_cast<int *>(sm + L::WORDS + 8);
     uint32_t *bad_keys = reinterpret_cast<uint32_t *>(sm + L::WORDS + 16);
 
-    const int g = blockIdx.x % a.Hkv, rt = a.row_tiles - 1 - (int)(blockIdx.x / a.Hkv);  // most keys first
+    // (done while the grid before ends, and by a warp that is free)
+    if (tid == kThreads - 1) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            tc::mbar_init(full + i, 1);
+            tc::mbar_init(empty + i, 1);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(bar_q + i, 128);
+            tc::mbar_init(bar_s + i, 1);
+            tc::mbar_init(bar_p + 2 * i, 128);
+            tc::mbar_init(bar_p + 2 * i + 1, 128);
+            tc::mbar_init(bar_o + i, 1);
+        }
+        tc::mbar_init(bar_drain, 1);
+#pragma unroll
+        for (int i = 0; i < kMaskedStages; ++i) {
+            tc::mbar_init(armed + i, 1);
+            tc::mbar_init(clean + i, 128);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) bad_keys[4 * i + w] = 0;
+        }
+        *failed = 0;
+        *bad_v = 0;
+        tc::fence_mbarrier_init();
+    }
+    if (warp == 9) tc::prefetch_tmap(&maps.k);
+    if (warp == 10) tc::prefetch_tmap(&maps.v);
+    pdl_enter();
+
+    // the longest first: a chunk's last rows see the most keys, a tree's last tile has the fewest rows
+    const int g = blockIdx.x % a.Hkv, rt_up = blockIdx.x / a.Hkv;
+    const int rt = a.anc_mask ? rt_up : a.row_tiles - 1 - rt_up;
     const int R = a.R, G = a.H / a.Hkv;
-    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const bool tree = a.anc_mask != nullptr;
     const int m0 = rt * kPagedTileRows;
     CacheItem it;
@@ -176,32 +208,22 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
     const int all = tree ? P : min(P + m0 / G + 1, kend);
     const int j_masked = max(0, (all - kbeg) / kPagedStage);
 
-    if (tid == 0) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            tc::mbar_init(full + i, 1);
-            tc::mbar_init(empty + i, 1);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(bar_q + i, 128);
-            tc::mbar_init(bar_s + i, 1);
-            tc::mbar_init(bar_p + 2 * i, 128);
-            tc::mbar_init(bar_p + 2 * i + 1, 128);
-            tc::mbar_init(bar_o + i, 1);
-        }
-        tc::mbar_init(bar_drain, 1);
-#pragma unroll
-        for (int i = 0; i < kMaskedStages; ++i) {
-            tc::mbar_init(armed + i, 1);
-            tc::mbar_init(clean + i, 128);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) bad_keys[4 * i + w] = 0;
-        }
-        *failed = 0;
-        *bad_v = 0;
-        tc::fence_mbarrier_init();
-    }
+    const int box = min(1 << a.map.shift, 128);
+    // lane: one box of the tile (a box of 128 rows brings all columns)
+    const int per = box == 128 ? 1 : L::NB, boxes = box == 128 ? 1 : 128 / box * L::NB;
+    const int my = lane / per, half = lane % per;
+    const uint32_t to = half * L::BLOCK + my * box * 128;
+    const int rows_end = a.map.n_pages << a.map.shift;  // past the pool: zeros
+    const int end = P + n;
+    const bool vs = warp == 10;
+    auto row_of = [&](int j) {  // the lane's pool row of stage j
+        const int slot = kbeg + j * kPagedStage + my * box;
+        if (lane >= boxes || slot >= end) return rows_end;
+        const int page = a.map.page_of(b, slot);
+        return a.map.good(page) ? (int)a.map.row(page, slot) : rows_end;
+    };
+    // (looked up before the barrier)
+    const int first_row = warp == 9 || warp == 10 ? row_of(0) : 0;
     if (warp == 8) tc::tmem_alloc(tmem_holder, 512);
     if (warp < 8 && !(split && side)) {  // Q: rows that are not there are zeros
         const uint32_t qt = tc::smem_addr(sm + side * L::TILE);
@@ -228,22 +250,8 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
         if (warp == 9 || warp == 10) {
             // -------------------------------------------------------- copies
-            const int box = min(1 << a.map.shift, 128);
-            // lane: one box of the tile (a box of 128 rows brings all columns)
-            const int per = box == 128 ? 1 : L::NB, boxes = box == 128 ? 1 : 128 / box * L::NB;
-            const int my = lane / per, half = lane % per;
-            const uint32_t to = half * L::BLOCK + my * box * 128;
-            const int rows_end = a.map.n_pages << a.map.shift;  // past the pool: zeros
-            const int end = P + n;
-            const bool vs = warp == 10;
-            auto row_of = [&](int j) {  // the lane's pool row of stage j
-                const int slot = kbeg + j * kPagedStage + my * box;
-                if (lane >= boxes || slot >= end) return rows_end;
-                const int page = a.map.page_of(b, slot);
-                return a.map.good(page) ? (int)a.map.row(page, slot) : rows_end;
-            };
             const CUtensorMap *map = vs ? &maps.v : &maps.k;
-            int next = row_of(0), issued = 0;
+            int next = first_row, issued = 0;
             for (; issued < nsub; ++issued) {
                 const int j = issued, i = slot_of(j, vs), row = next;
                 if (j + 1 < nsub) next = row_of(j + 1);
