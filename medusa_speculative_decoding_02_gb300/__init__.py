@@ -646,9 +646,11 @@ def _scratch(nbytes: int, device, stream):
 
 def _new(stream, like: torch.Tensor, shape=None, dtype=None):
     """An output tensor made on the launch stream."""
-    with _issue_on(stream):
-        return torch.empty(like.shape if shape is None else shape, dtype=dtype or like.dtype,
-                           device=like.device)
+    shape, dtype = like.shape if shape is None else shape, dtype or like.dtype
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _rope_args(q, k, q_weight, k_weight, dev):
