@@ -57,8 +57,23 @@ struct PagedSmem {
     static_assert(TOTAL + 1024 <= 227 * 1024, "shared memory of an SM");
 };
 
+// Division of numbers below 2^31 by d, as a product and a shift.  With 2^s the power of
+// two below d and m = 2^(32 + s) / d + 1, m is too large by less than one, so that
+// i m / 2^(32 + s) is by less than i / 2^(32 + s) < 1 / d (d <= 2^(s + 1)).
+struct Divisor {
+    unsigned magic, shift;  // magic 0: d = 1
+    __host__ explicit Divisor(unsigned d = 1) : magic(0), shift(0) {
+        while ((2u << shift) < d) ++shift;
+        if (d > 1) magic = (unsigned)((1ull << (32 + shift)) / d + 1);
+    }
+    __device__ __forceinline__ int operator()(int x) const {
+        return magic ? (int)(__umulhi((unsigned)x, magic) >> shift) : x;
+    }
+};
+
 struct PagedMaps {
     CUtensorMap k, v;
+    Divisor by_g, by_hkv;  // division by G and by the KV heads
 };
 
 __device__ __forceinline__ bool pair_not_finite(uint4 w) {
@@ -135,17 +150,20 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
     }
     if (warp == 9) tc::prefetch_tmap(&maps.k);
     if (warp == 10) tc::prefetch_tmap(&maps.v);
+    // (the copying warps do not wait for the others to be set up)
+    if (warp >= 9) asm volatile("barrier.cta.sync 3, 96;\n" ::: "memory");
     pdl_enter();
 
     // the longest first: a chunk's last rows see the most keys, a tree's last tile has the fewest rows
-    const int g = blockIdx.x % a.Hkv, rt_up = blockIdx.x / a.Hkv;
+    const int rt_up = maps.by_hkv(blockIdx.x), g = blockIdx.x - rt_up * a.Hkv;
     const int rt = a.anc_mask ? rt_up : a.row_tiles - 1 - rt_up;
     const int R = a.R, G = a.H / a.Hkv;
     const bool tree = a.anc_mask != nullptr;
     const int m0 = rt * kPagedTileRows;
     CacheItem it;
     // slots that the last of the first `rows` rows sees (a tree's rows: all)
-    auto keys_of = [&](int P, int n, int rows) { return P + (tree ? n : min(n, (rows - 1) / G + 1)); };
+    auto by_g = [&](int x) { return maps.by_g(x); };  // x / G
+    auto keys_of = [&](int P, int n, int rows) { return P + (tree ? n : min(n, by_g(rows - 1) + 1)); };
     if (!find_item<DEAL, kPagedStage, true>(a, [&](int P, int b) {
             const int n = live_rows(a, b);
             return n == 0 ? 0 : DEAL ? P + n : keys_of(P, n, m0 + kPagedTileRows);
@@ -162,7 +180,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
     const int side = (warp >> 2) & 1, t = tid & 127;
     const int m = m0 + (split ? 0 : side * 128) + t;
     const bool live = tid < 256 && m < M;
-    const int r = live ? m / G : 0;
+    const int r = live ? by_g(m) : 0;
     const int mw = m0 + (split ? 0 : side * 128) + (warp & 3) * 32;  // the warp's first row
     // row of q and out, and of the partial results, in rows of DH elements
     auto row_at = [&](int r, int gq) { return ((size_t)b * R + r) * a.H + g * G + gq; };
@@ -183,8 +201,8 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
     constexpr int kCols = DH / 8, kPass = 32 / kCols;
     auto for_rows = [&](auto f) {
         const int first = mw + lane / kCols;
-        int rr = first / G, gg = first - rr * G;
-        const int dr = kPass / G, dg = kPass - dr * G;
+        int rr = by_g(first), gg = first - rr * G;
+        const int dr = by_g(kPass), dg = kPass - dr * G;
 #pragma unroll 4
         for (int i = 0; i < 32; i += kPass) {
             f(i + lane / kCols, lane % kCols, rr, gg);
@@ -205,12 +223,18 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
     const int nsub_a = split ? nsub
                              : max(0, min(nsub, (keys_of(P, n, m0 + 128) - kbeg + kPagedStage - 1) / kPagedStage));
     // the first stage that some row of the CTA does not see wholly
-    const int all = tree ? P : min(P + m0 / G + 1, kend);
+    const int all = tree ? P : min(P + by_g(m0) + 1, kend);
     const int j_masked = max(0, (all - kbeg) / kPagedStage);
+
+    // place of stage j's K or V among the slots, a ring for each
+    auto slot_of = [&](int j, bool vs) { return (vs ? NK : 0) + j % NK; };
+    auto wait_full = [&](int j, bool vs) {
+        return wait_or_fail(full + slot_of(j, vs), (j / NK) & 1, a.wait_polls, failed);
+    };
 
     const int box = min(1 << a.map.shift, 128);
     // lane: one box of the tile (a box of 128 rows brings all columns)
-    const int per = box == 128 ? 1 : L::NB, boxes = box == 128 ? 1 : 128 / box * L::NB;
+    const int per = box == 128 ? 1 : L::NB, copy_boxes = box == 128 ? 1 : 128 / box * L::NB;
     const int my = lane / per, half = lane % per;
     const uint32_t to = half * L::BLOCK + my * box * 128;
     const int rows_end = a.map.n_pages << a.map.shift;  // past the pool: zeros
@@ -218,12 +242,29 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
     const bool vs = warp == 10;
     auto row_of = [&](int j) {  // the lane's pool row of stage j
         const int slot = kbeg + j * kPagedStage + my * box;
-        if (lane >= boxes || slot >= end) return rows_end;
+        if (lane >= copy_boxes || slot >= end) return rows_end;
         const int page = a.map.page_of(b, slot);
         return a.map.good(page) ? (int)a.map.row(page, slot) : rows_end;
     };
-    // (looked up before the barrier)
-    const int first_row = warp == 9 || warp == 10 ? row_of(0) : 0;
+    // The copies of stage j, whose row the lane has looked up; looks up the next stage's.
+    // -1: failed.
+    auto copy_stage = [&](int j, int row) {
+        const int i = slot_of(j, vs), next = j + 1 < nsub ? row_of(j + 1) : 0;
+        if (j >= NK && !wait_or_fail(empty + i, (j / NK - 1) & 1, a.wait_polls, failed)) return -1;
+        if (lane == 0) tc::mbar_arrive_expect_tx(full + i, L::TILE);
+        __syncwarp();
+        if (lane < copy_boxes)
+            tc::tma_load_3d(sm + L::RING + i * L::TILE + to, vs ? &maps.v : &maps.k, 0, row, g * L::NB + half, full + i);
+        // (a phase of `full` can be told from the one two before it only by who knows
+        // which stage is in the slot: the checking warps wait from here on)
+        if (vs && j >= j_masked && lane == 0) tc::mbar_arrive(armed + (j - j_masked));
+        return next;
+    };
+    int issued = 0, next = 0;
+    if (warp == 9 || warp == 10) {
+        next = copy_stage(0, row_of(0));
+        issued = 1;
+    }
     if (warp == 8) tc::tmem_alloc(tmem_holder, 512);
     if (warp < 8 && !(split && side)) {  // Q: rows that are not there are zeros
         const uint32_t qt = tc::smem_addr(sm + side * L::TILE);
@@ -240,29 +281,13 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_holder;
 
-    // place of stage j's K or V among the slots, a ring for each
-    auto slot_of = [&](int j, bool vs) { return (vs ? NK : 0) + j % NK; };
-    auto wait_full = [&](int j, bool vs) {
-        return wait_or_fail(full + slot_of(j, vs), (j / NK) & 1, a.wait_polls, failed);
-    };
-
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
         if (warp == 9 || warp == 10) {
             // -------------------------------------------------------- copies
-            const CUtensorMap *map = vs ? &maps.v : &maps.k;
-            int next = first_row, issued = 0;
             for (; issued < nsub; ++issued) {
-                const int j = issued, i = slot_of(j, vs), row = next;
-                if (j + 1 < nsub) next = row_of(j + 1);
-                if (j >= NK && !wait_or_fail(empty + i, (j / NK - 1) & 1, a.wait_polls, failed)) break;
-                if (lane == 0) tc::mbar_arrive_expect_tx(full + i, L::TILE);
-                __syncwarp();
-                if (lane < boxes)
-                    tc::tma_load_3d(sm + L::RING + i * L::TILE + to, map, 0, row, g * L::NB + half, full + i);
-                // (a phase of `full` can be told from the one two before it only by who knows
-                // which stage is in the slot: the checking warp waits from here on)
-                if (vs && j >= j_masked && lane == 0) tc::mbar_arrive(armed + (j - j_masked));
+                next = copy_stage(issued, next);
+                if (next < 0) break;
             }
             // every copy has landed before the shared memory goes
             for (int j = max(0, issued - NK); j < issued; ++j)
@@ -351,7 +376,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
         }
         // ---- what this row sees: slots below `mine` and the tree's bits from P on
         const int mine = tree ? P : P + r + 1;
-        const int warp_all = tree ? P : P + mw / G + 1;  // slots that every row of the warp sees
+        const int warp_all = tree ? P : P + by_g(mw) + 1;  // slots that every row of the warp sees
         // 64 keys from slot k0 on that this row sees
         auto sees64 = [&](int k0) {
             uint64_t vis = bits_below(mine - k0);
@@ -666,6 +691,8 @@ cudaError_t launch(const PagedMaps &maps, const CacheAttnArgs &a, cudaStream_t s
 
 cudaError_t launch_paged_attention_tc(const CacheAttnArgs &a, int dh, cudaStream_t stream) {
     PagedMaps maps;
+    maps.by_g = Divisor(a.H / a.Hkv);
+    maps.by_hkv = Divisor(a.Hkv);
     if (!encode_pool(&maps.k, a.kp, a, dh) || !encode_pool(&maps.v, a.vp, a, dh)) {
         set_last_error("tensor maps of the pools could not be made (cuTensorMapEncodeTiled failed)");
         return cudaErrorInvalidValue;
