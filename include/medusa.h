@@ -834,8 +834,8 @@ MEDUSA_API medusa_status medusa_tree_attention_paged(
  *              equal logits -> smaller id" (0: t is the row's argmax)
  *     top_ids, top_logp   the first `top` tokens of that order, and their ln p
  *
- *   logits [N,V] dtype, consecutive rows `stride` >= V elements apart (any
- *            alignment but the first row's 16 bytes)
+ *   logits [N,V] dtype, consecutive rows `stride` >= V elements apart, at any
+ *            alignment
  *   tokens [N] int32; -1: no token is asked for (logp 0, rank -1).  Other ids
  *            outside [0, V) set MEDUSA_DEV_BAD_TOKEN and count as -1
  *   logp, entropy [N] fp32, rank [N] int32, top_ids [N,top] int32, top_logp
@@ -845,7 +845,7 @@ MEDUSA_API medusa_status medusa_tree_attention_paged(
  * that holds a NaN or +inf has NaN in logp, entropy and top_logp; a NaN comes
  * behind all numbers in the order, has rank -1 itself and no place among the
  * alternatives (a place that no number fills has id -1).
- * Requirements: N >= 1; 1 <= V <= 2^24; top in 0..min(V, 16); temperature in
+ * Requirements: 1 <= N <= 2^30; 1 <= V <= 2^24; top in 0..min(V, 16); temperature in
  * 1e-30..1e30.  Workspace: MEDUSA_WS_HEADER bytes (the status word).
  * ---------------------------------------------------------------------- */
 MEDUSA_API medusa_status medusa_token_logprobs(medusa_dtype dtype, const void *logits, int64_t stride,

@@ -1029,9 +1029,9 @@ medusa_status medusa_token_logprobs(medusa_dtype dtype, const void *logits, int6
     if (!is_dtype(dtype)) return fail(MEDUSA_ERR_INVALID_ARG, "%s: unknown dtype %d", who, (int)dtype);
     if (!logits || !tokens || !logp || !entropy || !rank || (top > 0 && (!top_ids || !top_logp)))
         return fail(MEDUSA_ERR_INVALID_ARG, "%s: NULL pointer", who);
-    if (!aligned16(logits))
-        return fail(MEDUSA_ERR_INVALID_ARG, "%s: logits must be 16-byte aligned", who);
-    if (N < 1) return fail(MEDUSA_ERR_INVALID_ARG, "%s: N=%d", who, N);
+    if (reinterpret_cast<uintptr_t>(logits) % (dtype == MEDUSA_F32 ? 4 : 2))
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: logits must be aligned to their elements", who);
+    if (N < 1 || N > 1 << 30) return fail(MEDUSA_ERR_INVALID_ARG, "%s: N=%d outside 1..2^30", who, N);
     if (V < 1 || V > MEDUSA_MAX_VOCAB)
         return fail(MEDUSA_ERR_INVALID_ARG, "%s: V=%d outside 1..%d", who, V, MEDUSA_MAX_VOCAB);
     if (stride < V || stride > (int64_t)1 << 40)

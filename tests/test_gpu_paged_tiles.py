@@ -1,0 +1,208 @@
+"""Paged attention at the sizes where its kernels and their parts change: rows at the
+ends of tiles, ranges and joins of every kind, many sequences, bounded waits; and the
+log probabilities at every alignment of a row.  Tolerances as in test_gpu_paged and
+test_gpu_logprobs."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import cache_ops_ref
+import medusa_speculative_decoding_02_gb300 as m
+import paged_ref as ref
+import test_gpu_logprobs as tl
+from medusa_speculative_decoding_02_gb300 import build as mbuild
+from test_gpu_paged import BF, F32, Case, check, i32, status
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    mbuild.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    d = torch.device("cuda:0")
+    torch.cuda.set_device(d)
+    return d
+
+
+def workspace(c, H, dtype=BF):
+    return m.new_workspace(m.paged_attention_workspace_size(m.BF16 if dtype == BF else m.F32, c.B, c.R, H, c.Hkv,
+                                                            c.dh, c.P_max))
+
+
+@pytest.mark.parametrize("G", [1, 3, 4])
+@pytest.mark.parametrize("M", [16, 17, 32, 127, 128, 129, 136, 137, 255, 256, 257, 264, 265, 384, 385, 512, 513])
+def test_rows_where_tiles_change(dev, M, G):
+    """Rows a KV head around the few-row kernel's limit and the tiles of 128 and 256, in a
+    ragged batch whose second sequence ends somewhere inside."""
+    R = -(-M // G)
+    rows = (R, max(1, R - 2), min(R, 3))
+    c = Case(M + G, (130, 61, 0), rows, 2, 64, 32, BF, R=R, std=1.5)
+    q = c.randn(3, R, 2 * G, 64)
+    ws = workspace(c, 2 * G)
+    out = torch.full_like(q, 5.0).to(dev)
+    m.chunk_attention_paged(q.to(dev), *c.to(dev), n_rows=i32(*rows).to(dev), out=out, ws=ws)
+    check(out, q, c, lambda b: ref.causal(c.prefix[b], rows[b]))
+    for b in range(3):
+        assert (out[b, rows[b]:] == 5).all()
+    if R <= 256:
+        mask, _ = cache_ops_ref.tree(3, R, np.random.RandomState(M))
+        full = Case(M, (130, 61, 0), (R,) * 3, 2, 64, 32, BF)
+        got = m.tree_attention_paged(q.to(dev), *full.to(dev), mask.to(dev), ws=ws)
+        check(got, q, full, lambda b: ref.tree_sees(full.prefix[b], R, mask[b]))
+    assert status(ws) == "ok"
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("prefix,R,H,Hkv,dh", [
+    ((20000,), 1, 2, 1, 128), ((20000,), 1, 1, 1, 64), ((9000, 100, 5000), 1, 4, 2, 64), ((3000, 2000), 3, 8, 8, 128),
+    ((6000,), 40, 2, 1, 128), ((4000, 30), 70, 16, 16, 64), ((2500,), 600, 2, 1, 64)])
+def test_ranges_and_their_joins(dev, dtype, prefix, R, H, Hkv, dh):
+    """Few rows over long prefixes: from two ranges of keys to more than 32."""
+    c = Case(sum(prefix) + R, prefix, (R,) * len(prefix), Hkv, dh, 128, dtype, std=1.5)
+    q = c.randn(c.B, R, H, dh)
+    ws = workspace(c, H, dtype)
+    assert ws.numel() > m.WS_HEADER  # there are partial results
+    got = m.chunk_attention_paged(q.to(dev), *c.to(dev), ws=ws)
+    check(got, q, c, lambda b: ref.causal(prefix[b], R))
+    rows = [max(0, R - 1 - b) for b in range(c.B)]
+    out = torch.full_like(q, -3.0).to(dev)
+    m.chunk_attention_paged(q.to(dev), *c.to(dev), n_rows=i32(*rows).to(dev), out=out, ws=ws)
+    check(out, q, c, lambda b: ref.causal(prefix[b], rows[b]))
+    for b in range(c.B):
+        assert (out[b, rows[b]:] == -3).all()
+    assert status(ws) == "ok"
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,R", [(33, 1), (40, 20), (70, 2)])
+def test_many_sequences(dev, dtype, B, R):
+    """More sequences than ranges are dealt out to by their lengths."""
+    prefix = [(b * 37) % 700 for b in range(B)]
+    c = Case(B + R, prefix, (R,) * B, 1, 64, 16, dtype)
+    q = c.randn(B, R, 2, 64)
+    got = m.chunk_attention_paged(q.to(dev), *c.to(dev))
+    check(got, q, c, lambda b: ref.causal(prefix[b], R))
+
+
+@pytest.mark.parametrize("R,G", [(65, 4), (40, 2), (300, 1)])
+def test_infinities_and_bad_pages_over_ranges(dev, R, G):
+    """Non-finite V in the last tile, a bad page and a bad prefix at once, with the keys
+    in several ranges."""
+    c = Case(R, (3000, 700, 40), (R,) * 3, 1, 128, 16, BF)
+    q = c.randn(3, R, G, 128)
+    for b in range(3):
+        for j, x in ((R // 3, math.inf), (R - 2, math.nan)):
+            i, r = ref.spots(c.tab, b, 16, c.prefix[b] + j, 1)
+            c.vp[i, r, 0, 7 * b] = x
+    kp, vp, tab, pl, P_max = c.to(dev)
+    tab[0, 50] = -9
+    pl[2] = P_max + 1
+    ws = workspace(c, G)
+    got = m.chunk_attention_paged(q.to(dev), kp, vp, tab, pl, P_max, ws=ws)
+    assert (got[2] == 0).all() and status(ws) in ("bad page", "bad prefix")
+    two = Case.__new__(Case)
+    two.__dict__.update(c.__dict__, B=2)
+
+    def sees(b):
+        see = ref.causal(c.prefix[b], R)
+        if b == 0:
+            see[:, 800:816] = False
+        return see
+    check(got, q, two, sees)
+
+
+@pytest.mark.parametrize("R,H,Hkv,ns", [(65, 2, 2, True), (200, 4, 1, True), (512, 2, 2, False)])
+def test_waits_that_run_out(dev, R, H, Hkv, ns):
+    """With no polls every wait fails at once: the status says so, the rows are zeros, and
+    the same call on the same buffers is right afterwards."""
+    c = Case(R, (900 if ns else 0, 30), (R, R), Hkv, 128, 64, BF)
+    q = c.randn(2, R, H, 128)
+    args = c.to(dev)
+    ws = workspace(c, H)
+    budget = m.wait_budget()
+    try:
+        m.set_wait_budget(0)
+        out = torch.full_like(q, 9.0).to(dev)
+        m.chunk_attention_paged(q.to(dev), *args, out=out, ws=ws)
+        torch.cuda.synchronize()
+    finally:
+        m.set_wait_budget(budget)
+    assert status(ws) == "timeout" and (out == 0).all()
+    m.clear_device_status(ws)
+    m.chunk_attention_paged(q.to(dev), *args, out=out, ws=ws)
+    assert status(ws) == "ok"
+    check(out, q, c, lambda b: ref.causal(c.prefix[b], R))
+
+
+def test_one_page_and_shared_pages(dev):
+    """A pool of a single page, and two sequences that share the pages of their prefix."""
+    c = Case(1, (5,), (9,), 1, 64, 16, BF)
+    kp, vp = c.kp[c.tab[0, :1].long()].contiguous(), c.vp[c.tab[0, :1].long()].contiguous()
+    q = c.randn(1, 9, 2, 64)
+    one = Case.__new__(Case)
+    one.__dict__.update(c.__dict__, kp=kp, vp=vp, tab=torch.zeros((1, 1), dtype=torch.int32))
+    for n in (1, 9):
+        got = m.chunk_attention_paged(q[:, :n].contiguous().to(dev), kp.to(dev), vp.to(dev), one.tab.to(dev),
+                                      i32(5).to(dev), 5)
+        check(got, q[:, :n], one, lambda b: ref.causal(5, n))
+    c = Case(2, (64, 64), (30, 30), 2, 128, 16, BF)
+    c.tab[1, :4] = c.tab[0, :4]
+    q = c.randn(2, 30, 4, 128)
+    got = m.chunk_attention_paged(q.to(dev), *c.to(dev))
+    check(got, q, c, lambda b: ref.causal(64, 30))
+
+
+# -------------------------------------------------------- log probabilities ---
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [1, 2, 7, 8, 9, 15, 16, 17, 31, 4101, 16389])
+def test_logprobs_at_every_alignment(dev, dtype, V):
+    """Rows that begin and end anywhere in a 16-byte block; every place of the token."""
+    g = torch.Generator().manual_seed(V)
+    wide = (torch.randn((9, V + 13), generator=g) * 3).to(dtype)
+    top = min(V, 6)
+    for first in range(0, 9, 1 if V < 40 else 3):
+        x = wide[:, first:first + V]
+        tokens = torch.randint(0, V, (9,), generator=g, dtype=torch.int32)
+        tokens[0], tokens[1] = 0, V - 1
+        tl.check(m.token_logprobs(wide.to(dev)[:, first:first + V], tokens.to(dev), top), x, tokens, top, 1.0)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("N", [75, 76, 152, 153, 304, 305, 608, 609, 1400])
+def test_logprobs_where_clusters_change(dev, dtype, N):
+    """Rows shared by four CTAs, by two, a CTA each, several a CTA."""
+    g = torch.Generator().manual_seed(N)
+    V = 33000
+    x = tl.rows(g, N, V, dtype)
+    x[N // 2] = x[N // 2, 0]   # ties: too many candidates
+    x[N - 1, 3:] = -math.inf   # fewer possible tokens than alternatives
+    tokens = torch.randint(0, V, (N,), generator=g, dtype=torch.int32)
+    out = m.token_logprobs(x.to(dev), tokens.to(dev), 9, temperature=1.1)
+    keep = [0, 1, N // 2 - 1, N // 2, N - 2, N - 1] + list(range(3, N - 3, 97))
+    pick = m.TokenLogprobs(out.logp[keep], out.entropy[keep], out.rank[keep], out.top_ids[keep], out.top_logp[keep])
+    tl.check(pick, x[keep], tokens[keep], 9, 1.1)
+
+
+def test_logprobs_of_peaked_and_flat_rows(dev):
+    """Large maxima that come late, early, in every chunk; one thread with many of the best."""
+    V = 70000
+    x = torch.full((6, V), -20.0)
+    x[0, 69999] = 300.0
+    x[1, 0] = 300.0
+    x[2] = torch.arange(V).float() / 100
+    x[3, ::1024] = torch.arange(69).float() / 8 + 2      # the same thread in every chunk
+    x[4, 128 * 8 * torch.arange(60)] = 5.0
+    x[5] = torch.linspace(-4, 4, V).flip(0)
+    for dtype in (BF, F32):
+        y = x.to(dtype)
+        tokens = torch.tensor([5, 5, 69990, 2048, 1024, 69999], dtype=torch.int32)
+        tl.check(m.token_logprobs(y.to(dev), tokens.to(dev), 16), y, tokens, 16, 1.0)
+        big = y.repeat(120, 1)
+        out = m.token_logprobs(big.to(dev), tokens.repeat(120).to(dev), 16)
+        pick = slice(714, 720)
+        tl.check(m.TokenLogprobs(out.logp[pick], out.entropy[pick], out.rank[pick], out.top_ids[pick],
+                                 out.top_logp[pick]), y, tokens, 16, 1.0)

@@ -91,8 +91,9 @@ def test_attention_refuses_rows_and_masks(L):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(dtype=7), 1), (dict(x=None), 1), (dict(x=ODD), 1), (dict(t=None), 1), (dict(lp=None), 1),
+    (dict(dtype=7), 1), (dict(x=None), 1), (dict(x=P(4097)), 1), (dict(x=P(4098), dtype=m.F32), 1), (dict(t=None), 1), (dict(lp=None), 1),
     (dict(en=None), 1), (dict(rk=None), 1), (dict(ids=None), 1), (dict(tl=None), 1), (dict(N=0), 1),
+    (dict(N=(1 << 30) + 1), 1),
     (dict(V=0), 1), (dict(V=(1 << 24) + 1, step=1 << 25), 1), (dict(step=999), 1), (dict(step=1 << 41), 1),
     (dict(top=-1), 1), (dict(top=17), 1), (dict(V=4, top=5), 1), (dict(temp=0.0), 1), (dict(temp=-1.0), 1),
     (dict(temp=math.nan), 1), (dict(temp=math.inf), 1), (dict(temp=1e-31), 1), (dict(ws=None), 3),
