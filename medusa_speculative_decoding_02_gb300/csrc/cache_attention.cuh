@@ -32,6 +32,9 @@ struct CacheAttnArgs {
     const void *kp, *vp;    // pools of K and V
     PageMap map;
     const int32_t *n_rows;  // rows of each sequence, or null: all R
+    // On the tensor cores, ranges that are dealt out: their number (B to B * ns and more
+    // than B; grid.y).  A sequence that gets one is written without the join.
+    int ranges;
 };
 
 // A sequence's visible slots, numbered without a gap.
@@ -85,6 +88,7 @@ __device__ __forceinline__ bool sequence_ok(const CacheAttnArgs &a, int b, int &
 // number `range` of the B * ns; kend = 0: a range without keys.
 struct CacheItem {
     int b, range, kbeg, kend, P;
+    bool alone;  // DEAL: the sequence's only range
     const void *kc, *vc;
 };
 
@@ -119,10 +123,11 @@ __device__ __forceinline__ bool find_item(const CacheAttnArgs &a, Len len, Cache
         else
             P = 0;
     }
-    const int all = a.B * a.ns;
+    const int all = a.ranges ? a.ranges : a.B * a.ns;
     // (a range size that max / ns allows is enough for every sequence)
     int lo = max(1, (__reduce_add_sync(0xffffffffu, units) + all - 1) / all);
-    int size = max(1, (__reduce_max_sync(0xffffffffu, units) + a.ns - 1) / a.ns);
+    const int share = a.ranges ? a.ranges / a.B : a.ns;
+    int size = max(1, (__reduce_max_sync(0xffffffffu, units) + share - 1) / share);
     while (lo < size) {
         const int mid = (lo + size) >> 1;
         if (__reduce_add_sync(0xffffffffu, (units + mid - 1) / mid) <= all)
@@ -144,6 +149,7 @@ __device__ __forceinline__ bool find_item(const CacheAttnArgs &a, Len len, Cache
     const int b = __popc(__ballot_sync(0xffffffffu, idx >= end));
     if (b >= a.B) return false;
     it.b = b;
+    it.alone = __shfl_sync(0xffffffffu, n, b) == 1;
     it.P = __shfl_sync(0xffffffffu, P, b);
     it.kc = reinterpret_cast<const void *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(kc), b));
     it.vc = reinterpret_cast<const void *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(vc), b));

@@ -254,6 +254,7 @@ __global__ void __launch_bounds__(128, 4) paged_join_rows_kernel(CacheAttnArgs a
     const int bh = (int)(item / groups), b = bh / H, h = bh - b * H;
     const bool live = r < live_rows(a, b);
     const int first = a.starts ? a.starts[b] : b * a.ns, NS = a.starts ? a.starts[b + 1] - first : a.ns;
+    if (a.ranges && NS == 1) return;  // written already
     const size_t step = (size_t)H * R, at = first * step + (size_t)h * R + (live ? r : 0);
     const float4 *po = reinterpret_cast<const float4 *>(a.part_o + at * DH) + c * V;
     float4 row[AHEAD][V];
@@ -313,6 +314,7 @@ __global__ void __launch_bounds__(256) paged_join_ranges_kernel(CacheAttnArgs a)
     const int r = blockIdx.x % R, bh = blockIdx.x / R, b = bh / H, h = bh - b * H;
     if (r >= live_rows(a, b)) return;  // uniform over the CTA
     const int first = a.starts ? a.starts[b] : b * a.ns, NS = a.starts ? a.starts[b + 1] - first : a.ns;
+    if (a.ranges && NS == 1) return;  // written already
     const size_t step = (size_t)H * R, at = first * step + (size_t)h * R + r;
     const float4 *po = reinterpret_cast<const float4 *>(a.part_o + at * DH) + c;
     const float2 *ml = a.part_ml + at;
@@ -375,9 +377,12 @@ cudaError_t launch_join(const CacheAttnArgs &a, cudaStream_t stream) {
 
 struct PagedPlan {
     int row_tiles, ns;
-    bool few;   // at most kFewRows rows a KV head
-    bool deal;  // ranges dealt out by the sequences' lengths
+    int ranges;  // in all
+    bool few;    // at most kFewRows rows a KV head
+    bool deal;   // ranges dealt out by the sequences' lengths
 };
+
+constexpr int kLongStages = 64;
 
 // Key ranges: the count that makes (waves of CTAs) x (stages per CTA + 3) smallest.
 PagedPlan paged_plan(medusa_dtype dtype, int B, int R, int H, int Hkv, int P_max) {
@@ -404,6 +409,19 @@ PagedPlan paged_plan(medusa_dtype dtype, int B, int R, int H, int Hkv, int P_max
         }
     }
     p.deal = !simt && p.ns > 1 && B > 1 && B <= 32;
+    p.ranges = B * p.ns;
+    // One range a sequence, two tiles of rows a CTA and a wave of CTAs or less: the longest
+    // sequence would set the time, so where it is long half as many ranges again are dealt
+    // out, which the longer ones take.  Trees of 64 or 65 rows, 32 heads over 8, dh 128, half the
+    // sequences short: 8 of up to 8192 slots 91 -> 65 us and 16 of them 94 -> 74 (all
+    // equally long 94 -> 98, 101 -> 106), but 16 of up to 4096 53 -> 53 and 8 of up to
+    // 2048 30 -> 35; with one tile of rows a CTA (4 of 65 rows, 32 heads over 32), where
+    // the copies set the time, 71 -> 78.
+    if (!simt && !p.few && p.ns == 1 && B > 1 && B <= 32 && M > kPagedTileRows / 2 &&
+        subs >= kLongStages && ctas <= slots) {
+        p.deal = true;
+        p.ranges = B + (B + 1) / 2;
+    }
     return p;
 }
 
@@ -412,8 +430,8 @@ PagedPlan paged_plan(medusa_dtype dtype, int B, int R, int H, int Hkv, int P_max
 size_t paged_attention_workspace_bytes(medusa_dtype dtype, int B, int R, int H, int Hkv, int dh,
                                        int P_max) {
     const PagedPlan p = paged_plan(dtype, B, R, H, Hkv, P_max);
-    if (p.ns == 1) return MEDUSA_WS_HEADER;
-    const size_t rows = (size_t)B * H * p.ns * R;
+    if (p.ns == 1 && !p.deal) return MEDUSA_WS_HEADER;
+    const size_t rows = (size_t)p.ranges * H * R;
     return MEDUSA_WS_HEADER + align256(rows * dh * sizeof(float)) + align256(rows * sizeof(float2)) +
            (p.deal ? align256((B + 1) * sizeof(int)) : 0);
 }
@@ -440,7 +458,7 @@ cudaError_t launch_paged_attention(medusa_dtype dtype, const void *q, const void
     a.ns = p.ns;
     a.row_tiles = p.row_tiles;
     a.scale_log2 = scale * kLog2e;
-    const size_t rows = (size_t)B * H * p.ns * R;
+    const size_t rows = (size_t)p.ranges * H * R;
     char *w = static_cast<char *>(ws) + MEDUSA_WS_HEADER;
     a.part_o = reinterpret_cast<float *>(w);
     a.part_ml = reinterpret_cast<float2 *>(w + align256(rows * dh * sizeof(float)));
@@ -450,6 +468,7 @@ cudaError_t launch_paged_attention(medusa_dtype dtype, const void *q, const void
     a.out = out;
     a.status = static_cast<int *>(ws);
     a.wait_polls = wait_budget();
+    a.ranges = p.deal && !p.few ? p.ranges : 0;
     cudaError_t e;
     if (dtype == MEDUSA_F32) {
         auto kern = dh == 128 ? paged_attn_simt_kernel<128> : paged_attn_simt_kernel<64>;
@@ -461,7 +480,7 @@ cudaError_t launch_paged_attention(medusa_dtype dtype, const void *q, const void
         e = p.few ? launch_cache_attention_few(a, false, dh, stream) : launch_paged_attention_tc(a, dh, stream);
     }
     note_launch();
-    if (e || p.ns == 1) return e;
+    if (e || (p.ns == 1 && !p.deal)) return e;
     e = dtype == MEDUSA_F32 ? (dh == 128 ? launch_join<float, 128>(a, stream) : launch_join<float, 64>(a, stream))
                             : (dh == 128 ? launch_join<bf16, 128>(a, stream) : launch_join<bf16, 64>(a, stream));
     note_launch();

@@ -169,6 +169,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
             return n == 0 ? 0 : DEAL ? P + n : keys_of(P, n, m0 + kPagedTileRows);
         }, it))
         return;
+    const bool direct = DEAL ? it.alone : a.ns == 1;  // no join
     const int b = it.b, P = it.P;
     const int n = live_rows(a, b), M = n * G;
     if (m0 >= M) return;  // uniform over the CTA
@@ -187,7 +188,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
     auto part_at = [&](int r, int gq) { return ((size_t)it.range * a.H + g * G + gq) * R + r; };
     auto publish_nothing = [&] {
         if (!live || (split && side)) return;
-        if (a.ns == 1) {
+        if (direct) {
             bf16 *dst = static_cast<bf16 *>(a.out) + row_at(r, m - r * G) * DH;
 #pragma unroll
             for (int c = 0; c < DH; c += 8) *reinterpret_cast<uint4 *>(dst + c) = make_uint4(0, 0, 0, 0);
@@ -593,7 +594,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
                 // (also with a factor of 0: a row of NaN scores has m = -inf, l = NaN)
                 l = fa * l_run + fb * lb;
             }
-            const float inv = a.ns > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+            const float inv = !direct ? 1.f : l == 0.f ? 0.f : 1.f / l;
             fa *= inv;
             fb *= inv;
             // Rows go out through shared memory, whole rows of bf16 or halves of fp32 at a
@@ -604,7 +605,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
             auto piece = [&](int row, int c) {
                 return reinterpret_cast<uint4 *>(stage + row * DH * 2 + ((c ^ (row & 7)) << 4));
             };
-            const int passes = a.ns == 1 ? 1 : 2, wide = DH / passes;  // columns a pass
+            const int passes = direct ? 1 : 2, wide = DH / passes;  // columns a pass
 #pragma unroll 1
             for (int pass = 0; pass < passes; ++pass) {
 #pragma unroll 1
@@ -629,7 +630,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
                             ov[e + 3] = fmaf(fb, o.w, ov[e + 3]);
                         }
                     }
-                    if (a.ns == 1) {
+                    if (direct) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 8)
                             *piece(lane, (c + e) / 8) =
@@ -646,14 +647,14 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
                 __syncwarp();
                 for_rows([&](int i, int c, int rr, int gg) {
                     if (mw + i >= M) return;
-                    if (a.ns == 1)
+                    if (direct)
                         *reinterpret_cast<uint4 *>(static_cast<bf16 *>(a.out) + row_at(rr, gg) * DH + c * 8) = *piece(i, c);
                     else
                         *reinterpret_cast<uint4 *>(a.part_o + part_at(rr, gg) * DH + pass * wide + c * 4) = *piece(i, c);
                 });
                 __syncwarp();
             }
-            if (live && a.ns > 1) a.part_ml[part_at(r, m - r * G)] = make_float2(top, l);
+            if (live && !direct) a.part_ml[part_at(r, m - r * G)] = make_float2(top, l);
         }
     }
     tc::fence_before_sync();
@@ -684,7 +685,8 @@ cudaError_t launch(const PagedMaps &maps, const CacheAttnArgs &a, cudaStream_t s
     constexpr int smem = PagedSmem<DH>::TOTAL;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e) return e;
-    return launch_pdl(kern, dim3(a.Hkv * a.row_tiles, a.ns, a.B), dim3(kThreads), (size_t)smem, stream, maps, a);
+    const dim3 grid(a.Hkv * a.row_tiles, a.ranges ? a.ranges : a.ns, a.ranges ? 1 : a.B);
+    return launch_pdl(kern, grid, dim3(kThreads), (size_t)smem, stream, maps, a);
 }
 
 }  // namespace

@@ -206,3 +206,29 @@ def test_logprobs_of_peaked_and_flat_rows(dev):
         pick = slice(714, 720)
         tl.check(m.TokenLogprobs(out.logp[pick], out.entropy[pick], out.rank[pick], out.top_ids[pick],
                                  out.top_logp[pick]), y, tokens, 16, 1.0)
+
+
+@pytest.mark.parametrize("R,G,dh", [(65, 2, 64), (33, 4, 128)])
+def test_ranges_of_long_sequences(dev, R, G, dh):
+    """A wave of CTAs without ranges, some of whose sequences are long: those are shared
+    out, the others written without a join; some rows, a sequence or a prefix are missing."""
+    prefix = [8500, 3, 0, 500, 700, 60, 4100, 128, 1, 256] + [20] * 22
+    rows = [R, R, R - 5, 0, 1, R, R, R, R, R // 2] + [R] * 22
+    c = Case(R, prefix, rows, 4, dh, 64, BF, R=R, std=1.5)
+    q = c.randn(c.B, R, 4 * G, dh)
+    ws = workspace(c, 4 * G)
+    assert ws.numel() > m.WS_HEADER  # there are partial results
+    out = torch.full_like(q, 7.0).to(dev)
+    args = c.to(dev)
+    for _ in range(2):  # (the second time over the first one's partial results)
+        m.chunk_attention_paged(q.to(dev), *args, n_rows=i32(*rows).to(dev), out=out, ws=ws)
+        check(out, q, c, lambda b: ref.causal(prefix[b], rows[b]))
+        for b in range(c.B):
+            assert (out[b, rows[b]:] == 7).all()
+    assert status(ws) == "ok"
+    args[3][5] = -1
+    out.fill_(7.0)
+    m.chunk_attention_paged(q.to(dev), *args, n_rows=i32(*rows).to(dev), out=out, ws=ws)
+    assert (out[5] == 0).all() and status(ws) == "bad prefix"
+    five = rows[:5] + [0] + rows[6:]
+    check(out, q, c, lambda b: ref.causal(prefix[b], five[b]))
