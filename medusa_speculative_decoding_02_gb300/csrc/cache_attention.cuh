@@ -35,6 +35,7 @@ struct CacheAttnArgs {
     // On the tensor cores, ranges that are dealt out: their number (B to B * ns and more
     // than B; grid.y).  A sequence that gets one is written without the join.
     int ranges;
+    int cluster;  // the ns ranges are the CTAs of a cluster, which join them
 };
 
 // A sequence's visible slots, numbered without a gap.
@@ -192,6 +193,22 @@ __device__ __forceinline__ uint32_t pack_weights(float a, float b) {
     }
 }
 
+// Four columns of a row: scaled and stored; f times x added.
+template <typename T>
+__device__ __forceinline__ void store_row4(T *dst, const float (&x)[4], float inv) {
+    if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float4 *>(dst) = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+    else
+        *reinterpret_cast<uint2 *>(dst) =
+            make_uint2(pack_weights<false>(x[0] * inv, x[1] * inv), pack_weights<false>(x[2] * inv, x[3] * inv));
+}
+__device__ __forceinline__ void add4(float (&acc)[4], float f, const float4 &x) {
+    acc[0] = fmaf(f, x.x, acc[0]);
+    acc[1] = fmaf(f, x.y, acc[1]);
+    acc[2] = fmaf(f, x.z, acc[2]);
+    acc[3] = fmaf(f, x.w, acc[3]);
+}
+
 // 16 bytes into shared memory, zeros unless `ok`
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool ok) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
@@ -229,7 +246,9 @@ cudaError_t launch_cache_attention_few(const CacheAttnArgs &a, bool kv4, int dh,
 // Kernel for more rows over a cache in pages (paged_attention_tc.cu), on 256-row
 // tiles and 128-key stages.
 constexpr int kPagedTileRows = 256, kPagedStage = 128;
+constexpr int kClusterRanges = 8;  // ranges that a cluster joins
 cudaError_t launch_paged_attention_tc(const CacheAttnArgs &a, int dh, cudaStream_t stream);
+int paged_cluster_slots(int dh, int size);  // clusters of `size` CTAs that run at once (cached per device)
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 

@@ -127,6 +127,23 @@ __device__ __forceinline__ void pdl_enter() {
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 }
 
+// ------------------------------------------------------------- clusters ---
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory"); }
+// generic address of `p` in the shared memory of CTA `rank` of the cluster
+template <typename P>
+__device__ __forceinline__ const P *cluster_ptr(const P *p, uint32_t rank) {
+    uint64_t r;
+    asm("mapa.u64 %0, %1, %2;\n" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
+    return reinterpret_cast<const P *>(r);
+}
+
 // ------------------------------------------------------- device status ---
 
 __device__ __forceinline__ void set_status(int *status, int code) {

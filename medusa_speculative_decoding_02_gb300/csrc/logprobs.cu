@@ -306,21 +306,6 @@ __device__ __forceinline__ void bulk_copy(void *dst, const void *src, uint32_t b
                  : "memory");
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;\n" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory"); }
-// generic address of `p` in the shared memory of CTA `rank` of the cluster
-template <typename P>
-__device__ __forceinline__ const P *cluster_ptr(const P *p, uint32_t rank) {
-    uint64_t r;
-    asm("mapa.u64 %0, %1, %2;\n" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
-    return reinterpret_cast<const P *>(r);
-}
-
 // What the one pass holds for; otherwise slow_row.
 __device__ __forceinline__ bool fast_form(const LogprobArgs &a, float top, bool many, int n, int tok, float xt) {
     return top >= kNothing && top <= kHighest && !many && n >= a.top && (tok < 0 || xt > -INFINITY) &&
@@ -738,22 +723,11 @@ cudaError_t launch_token_logprobs(medusa_dtype dtype, const void *logits, long l
                     : (C > 1 ? token_logprobs_kernel<bf16, true> : token_logprobs_kernel<bf16, false>);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LpSmem::TOTAL);
     if (e) return e;
-    cudaLaunchConfig_t cfg = {};
     // (as many rows for each CTA, rather than a last round of a few)
     const int rounds = (N + slots - 1) / slots;
-    cfg.gridDim = dim3(C > 1 ? N * C : (N + rounds - 1) / rounds);
-    cfg.blockDim = dim3(kLpThreads);
-    cfg.dynamicSmemBytes = LpSmem::TOTAL;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = C;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = C > 1 ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, kern, a, C);
+    const dim3 grid(C > 1 ? N * C : (N + rounds - 1) / rounds), block(kLpThreads);
+    e = C > 1 ? launch_pdl_cluster(kern, grid, block, dim3(C), LpSmem::TOTAL, stream, a, C)
+              : launch_pdl(kern, grid, block, LpSmem::TOTAL, stream, a, C);
     note_launch();
     return e;
 }

@@ -226,20 +226,6 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_attn_simt_kernel(CacheA
 // out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s over a row's key ranges.  An empty range
 // (l = 0) has no O row.  The O rows do not depend on the weights: the first of them are
 // on their way while those are computed.
-template <typename T>
-__device__ __forceinline__ void store_row4(T *dst, const float (&x)[4], float inv) {
-    if constexpr (sizeof(T) == 4)
-        *reinterpret_cast<float4 *>(dst) = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-    else
-        *reinterpret_cast<uint2 *>(dst) =
-            make_uint2(pack_weights<false>(x[0] * inv, x[1] * inv), pack_weights<false>(x[2] * inv, x[3] * inv));
-}
-__device__ __forceinline__ void add4(float (&acc)[4], float f, const float4 &x) {
-    acc[0] = fmaf(f, x.x, acc[0]);
-    acc[1] = fmaf(f, x.y, acc[1]);
-    acc[2] = fmaf(f, x.z, acc[2]);
-    acc[3] = fmaf(f, x.w, acc[3]);
-}
 
 // Many rows: eight lanes a row, so that many rows are on their way.
 template <typename T, int DH>
@@ -377,15 +363,26 @@ cudaError_t launch_join(const CacheAttnArgs &a, cudaStream_t stream) {
 
 struct PagedPlan {
     int row_tiles, ns;
-    int ranges;  // in all
-    bool few;    // at most kFewRows rows a KV head
-    bool deal;   // ranges dealt out by the sequences' lengths
+    int ranges;    // in all
+    bool few;      // at most kFewRows rows a KV head
+    bool deal;     // ranges dealt out by the sequences' lengths
+    bool cluster;  // the ranges of a row are the CTAs of a cluster
 };
 
-constexpr int kLongStages = 64;
+constexpr int kLongStages = 64, kClusterStages = 16;
 
-// Key ranges: the count that makes (waves of CTAs) x (stages per CTA + 3) smallest.
-PagedPlan paged_plan(medusa_dtype dtype, int B, int R, int H, int Hkv, int P_max) {
+// Key ranges: the count that makes (waves of CTAs) x (stages per CTA + 3) smallest, with 3
+// stages (4 of one tile) for the join, 2 where a cluster of up to 8 CTAs joins its own ranges.
+//
+// Clusters are for at most 128 rows a KV head: 65 rows, 32 heads, prefix 1024 (3 ranges)
+// 14.3 -> 12.5 us, prefix 4096 (4) 18.5 -> 14.9, 17 rows 14.7 -> 10.9; 32 rows, 32 heads over
+// 8 (5) 14.1 -> 10.8.  Two tiles of rows are more than a few CTAs join as fast: 256 rows,
+// prefix 1024, in 2 ranges 15.6 -> 21.4, in 5 12.9 -> 13.8.  Clusters that do not all run
+// at once wait for one another: 24 of 6 CTAs (23 fit) 19.0 -> 24.3.  A batch's ranges are not
+// dealt out in clusters, so those are for up to kClusterStages stages a CTA: 3 x 65 rows, 8
+// heads, up to 3000 slots 19.1 -> 13.0; 4 x 65 up to 8000 (16 stages) 24.9 -> 22.1, equally
+// long 35.0 -> 30.2, but with one long sequence among short ones up to 11 stages more.
+PagedPlan paged_plan(medusa_dtype dtype, int B, int R, int H, int Hkv, int dh, int P_max) {
     PagedPlan p;
     const int M = R * (H / Hkv);
     const bool simt = dtype == MEDUSA_F32;
@@ -397,18 +394,23 @@ PagedPlan paged_plan(medusa_dtype dtype, int B, int R, int H, int Hkv, int P_max
     const long long ctas = (long long)B * Hkv * p.row_tiles;
     double best = 0;
     p.ns = 1;
+    p.cluster = false;
+    const bool split = !simt && !p.few && M <= kPagedTileRows / 2;
     const int most = std::min<long long>(subs, std::max<long long>(1, 4LL * slots / ctas));
     for (int ns = 1; ns <= most; ++ns) {
         const int per = (subs + ns - 1) / ns;
         if ((subs + per - 1) / per != ns) continue;
-        const double waves = (double)((ctas * ns + slots - 1) / slots);
-        const double cost = waves * (per + 3) + (ns > 1 ? 3.0 + 0.05 * ns : 0.0);
+        const bool cluster = split && ns > 1 && ns <= kClusterRanges && (B == 1 || per <= kClusterStages) &&
+                             ctas <= paged_cluster_slots(dh, ns);
+        const double waves = cluster ? 1.0 : (double)((ctas * ns + slots - 1) / slots);
+        const double cost = waves * (per + 3) + (cluster ? 2.0 : ns > 1 ? (split ? 4.0 : 3.0) + 0.05 * ns : 0.0);
         if (ns == 1 || cost < best) {
             best = cost;
             p.ns = ns;
+            p.cluster = cluster;
         }
     }
-    p.deal = !simt && p.ns > 1 && B > 1 && B <= 32;
+    p.deal = !simt && p.ns > 1 && !p.cluster && B > 1 && B <= 32;
     p.ranges = B * p.ns;
     // One range a sequence, two tiles of rows a CTA and a wave of CTAs or less: the longest
     // sequence would set the time, so where it is long half as many ranges again are dealt
@@ -429,8 +431,8 @@ PagedPlan paged_plan(medusa_dtype dtype, int B, int R, int H, int Hkv, int P_max
 
 size_t paged_attention_workspace_bytes(medusa_dtype dtype, int B, int R, int H, int Hkv, int dh,
                                        int P_max) {
-    const PagedPlan p = paged_plan(dtype, B, R, H, Hkv, P_max);
-    if (p.ns == 1 && !p.deal) return MEDUSA_WS_HEADER;
+    const PagedPlan p = paged_plan(dtype, B, R, H, Hkv, dh, P_max);
+    if (p.cluster || (p.ns == 1 && !p.deal)) return MEDUSA_WS_HEADER;
     const size_t rows = (size_t)p.ranges * H * R;
     return MEDUSA_WS_HEADER + align256(rows * dh * sizeof(float)) + align256(rows * sizeof(float2)) +
            (p.deal ? align256((B + 1) * sizeof(int)) : 0);
@@ -441,7 +443,7 @@ cudaError_t launch_paged_attention(medusa_dtype dtype, const void *q, const void
                                    const int32_t *prefix_len, int P_max, const uint64_t *anc_mask,
                                    const int32_t *n_rows, int B, int R, int H, int Hkv, int dh,
                                    float scale, void *out, void *ws, cudaStream_t stream) {
-    const PagedPlan p = paged_plan(dtype, B, R, H, Hkv, P_max);
+    const PagedPlan p = paged_plan(dtype, B, R, H, Hkv, dh, P_max);
     CacheAttnArgs a = {};
     a.q = q;
     a.kp = k_pages;
@@ -469,6 +471,7 @@ cudaError_t launch_paged_attention(medusa_dtype dtype, const void *q, const void
     a.status = static_cast<int *>(ws);
     a.wait_polls = wait_budget();
     a.ranges = p.deal && !p.few ? p.ranges : 0;
+    a.cluster = p.cluster;
     cudaError_t e;
     if (dtype == MEDUSA_F32) {
         auto kern = dh == 128 ? paged_attn_simt_kernel<128> : paged_attn_simt_kernel<64>;
@@ -480,7 +483,7 @@ cudaError_t launch_paged_attention(medusa_dtype dtype, const void *q, const void
         e = p.few ? launch_cache_attention_few(a, false, dh, stream) : launch_paged_attention_tc(a, dh, stream);
     }
     note_launch();
-    if (e || (p.ns == 1 && !p.deal)) return e;
+    if (e || p.cluster || (p.ns == 1 && !p.deal)) return e;
     e = dtype == MEDUSA_F32 ? (dh == 128 ? launch_join<float, 128>(a, stream) : launch_join<float, 64>(a, stream))
                             : (dh == 128 ? launch_join<bf16, 128>(a, stream) : launch_join<bf16, 64>(a, stream));
     note_launch();

@@ -30,6 +30,8 @@
 #include "cache_attention.cuh"
 #include "tensor_map.h"
 
+#include <atomic>
+
 namespace medusa {
 
 namespace {
@@ -49,11 +51,16 @@ struct PagedSmem {
     // full[NT], empty[NT], q[2], s[2], o[2], p[2][2], drain, armed and clean[kMaskedStages]
     static constexpr int WORDS = BAR + (2 * NT + 11 + 2 * kMaskedStages) * 8;
     // failed, tmem, bad (a V element is not finite), pad; bad keys [kMaskedStages][4]
-    static constexpr int TOTAL = WORDS + 16 + kMaskedStages * 16;
+    // CLUSTER: (m, l) of the rows of a range
+    static constexpr int PART_ML = (WORDS + 16 + kMaskedStages * 16 + 15) / 16 * 16;
+    static constexpr int TOTAL = PART_ML + 128 * 8;
     // B's rows and their (m, l) for the join of the halves, in place of the Q tiles and
     // the ring
     static constexpr int LD = DH + 4;
     static_assert(128 * (LD * 4 + 8) <= BAR, "the join fits before the barriers");
+    // CLUSTER: the range's rows, beside those
+    static constexpr int PART = 3 * TILE;
+    static_assert(128 * (LD * 4 + 8) <= PART && PART + 128 * LD * 4 <= BAR, "rows for the cluster");
     static_assert(TOTAL + 1024 <= 227 * 1024, "shared memory of an SM");
 };
 
@@ -106,7 +113,7 @@ __device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
     }
 }
 
-template <int DH, bool DEAL>
+template <int DH, bool DEAL, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs a) {
     using L = PagedSmem<DH>;
@@ -174,7 +181,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
     const int n = live_rows(a, b), M = n * G;
     if (m0 >= M) return;  // uniform over the CTA
     const int rows = min(kPagedTileRows, M - m0);
-    const bool split = rows <= 128;  // A and B are the same rows, by turns of the stages
+    const bool split = CLUSTER || rows <= 128;  // A and B are the same rows, by turns of the stages
     const int kbeg = it.kbeg, kend = min(it.kend, keys_of(P, n, m0 + rows));
 
     // row of a softmax thread
@@ -186,9 +193,13 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
     // row of q and out, and of the partial results, in rows of DH elements
     auto row_at = [&](int r, int gq) { return ((size_t)b * R + r) * a.H + g * G + gq; };
     auto part_at = [&](int r, int gq) { return ((size_t)it.range * a.H + g * G + gq) * R + r; };
+    float *const part_o = reinterpret_cast<float *>(sm + L::PART);  // CLUSTER: [128][LD]
+    float2 *const part_ml = reinterpret_cast<float2 *>(sm + L::PART_ML);
     auto publish_nothing = [&] {
         if (!live || (split && side)) return;
-        if (direct) {
+        if (CLUSTER) {
+            part_ml[t] = make_float2(-INFINITY, 0.f);
+        } else if (direct) {
             bf16 *dst = static_cast<bf16 *>(a.out) + row_at(r, m - r * G) * DH;
 #pragma unroll
             for (int c = 0; c < DH; c += 8) *reinterpret_cast<uint4 *>(dst + c) = make_uint4(0, 0, 0, 0);
@@ -215,8 +226,46 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
             }
         }
     };
+    // CLUSTER: the CTAs of the cluster hold a range of the same rows each, and take turns at
+    // joining them.  Rows of DH / 4 threads.
+    auto join_cluster = [&] {
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        constexpr int COLS = DH / 4;
+        if (tid < 256)
+            for (int i = blockIdx.y + a.ns * (tid / COLS); i < M; i += a.ns * (256 / COLS)) {
+                float2 ml[kClusterRanges];
+                float4 o[kClusterRanges];
+                float top = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int s = 0; s < kClusterRanges; ++s)
+                    if (s < a.ns) {
+                        ml[s] = *cluster_ptr(part_ml + i, s);
+                        o[s] = *reinterpret_cast<const float4 *>(cluster_ptr(part_o + i * L::LD + tid % COLS * 4, s));
+                    }
+#pragma unroll
+                for (int s = 0; s < kClusterRanges; ++s)
+                    if (s < a.ns && ml[s].y != 0.f) top = fmaxf(top, ml[s].x);
+                const float mu = top == -INFINITY ? 0.f : top;
+#pragma unroll
+                for (int s = 0; s < kClusterRanges; ++s)
+                    if (s < a.ns && ml[s].y != 0.f) {  // (an empty range has no row)
+                        const float f = exp2f(ml[s].x - mu);
+                        l = fmaf(f, ml[s].y, l);
+                        if (f != 0.f) add4(acc, f, o[s]);
+                    }
+                const int rr = by_g(i);
+                store_row4(static_cast<bf16 *>(a.out) + row_at(rr, i - rr * G) * DH + tid % COLS * 4, acc,
+                           l == 0.f ? 0.f : 1.f / l);
+            }
+        __syncwarp();
+        cluster_arrive();  // no CTA leaves while its rows may be read
+        cluster_wait();
+    };
     if (kbeg >= kend) {  // uniform over the CTA
         publish_nothing();
+        if constexpr (CLUSTER) join_cluster();
         return;
     }
     const int nsub = (kend - kbeg + kPagedStage - 1) / kPagedStage;
@@ -605,7 +654,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
             auto piece = [&](int row, int c) {
                 return reinterpret_cast<uint4 *>(stage + row * DH * 2 + ((c ^ (row & 7)) << 4));
             };
-            const int passes = direct ? 1 : 2, wide = DH / passes;  // columns a pass
+            const int passes = direct || CLUSTER ? 1 : 2, wide = DH / passes;  // columns a pass
 #pragma unroll 1
             for (int pass = 0; pass < passes; ++pass) {
 #pragma unroll 1
@@ -630,7 +679,12 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
                             ov[e + 3] = fmaf(fb, o.w, ov[e + 3]);
                         }
                     }
-                    if (direct) {
+                    if (CLUSTER) {
+                        float *dst = part_o + t * L::LD + c;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4 *>(dst + e) = make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+                    } else if (direct) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 8)
                             *piece(lane, (c + e) / 8) =
@@ -644,6 +698,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
                                            __float_as_uint(ov[e + 3]));
                     }
                 }
+                if (CLUSTER) continue;
                 __syncwarp();
                 for_rows([&](int i, int c, int rr, int gg) {
                     if (mw + i >= M) return;
@@ -654,13 +709,17 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
                 });
                 __syncwarp();
             }
-            if (live && !direct) a.part_ml[part_at(r, m - r * G)] = make_float2(top, l);
+            if (CLUSTER)
+                part_ml[t] = make_float2(top, l);
+            else if (live && !direct)
+                a.part_ml[part_at(r, m - r * G)] = make_float2(top, l);
         }
     }
     tc::fence_before_sync();
     __syncthreads();
     if (tid == 0 && *failed) set_status(a.status, MEDUSA_DEV_TIMEOUT);
     if (warp == 8) tc::tmem_dealloc(tmem, 512);
+    if constexpr (CLUSTER) join_cluster();
 }
 
 // A pool as [Hkv dh / 64][rows][64] for boxes of `box` rows (all of a head's columns
@@ -681,15 +740,46 @@ bool encode_pool(CUtensorMap *map, const void *pool, const CacheAttnArgs &a, int
 
 template <int DH>
 cudaError_t launch(const PagedMaps &maps, const CacheAttnArgs &a, cudaStream_t stream) {
-    auto kern = a.starts ? paged_attn_tc_kernel<DH, true> : paged_attn_tc_kernel<DH, false>;
+    auto kern = a.starts    ? paged_attn_tc_kernel<DH, true, false>
+                : a.cluster ? paged_attn_tc_kernel<DH, false, true>
+                            : paged_attn_tc_kernel<DH, false, false>;
     constexpr int smem = PagedSmem<DH>::TOTAL;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e) return e;
     const dim3 grid(a.Hkv * a.row_tiles, a.ranges ? a.ranges : a.ns, a.ranges ? 1 : a.B);
+    if (a.cluster)
+        return launch_pdl_cluster(kern, grid, dim3(kThreads), dim3(1, a.ns, 1), (size_t)smem, stream, maps, a);
     return launch_pdl(kern, grid, dim3(kThreads), (size_t)smem, stream, maps, a);
 }
 
 }  // namespace
+
+int paged_cluster_slots(int dh, int size) {
+    static std::atomic<int> known[64][2][kClusterRanges + 1];  // one more than the count
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::atomic<int> &k = known[dev][dh == 128][size];
+    if (int x = k.load(std::memory_order_relaxed)) return x - 1;
+    auto kern = dh == 128 ? paged_attn_tc_kernel<128, false, true> : paged_attn_tc_kernel<64, false, true>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1, size);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = dh == 128 ? PagedSmem<128>::TOTAL : PagedSmem<64>::TOTAL;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = attr.val.clusterDim.z = 1;
+    attr.val.clusterDim.y = size;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes) ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg)) {
+        cudaGetLastError();
+        return 0;
+    }
+    k.store(n + 1, std::memory_order_relaxed);
+    return n;
+}
 
 cudaError_t launch_paged_attention_tc(const CacheAttnArgs &a, int dh, cudaStream_t stream) {
     PagedMaps maps;

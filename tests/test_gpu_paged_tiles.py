@@ -64,7 +64,8 @@ def test_ranges_and_their_joins(dev, dtype, prefix, R, H, Hkv, dh):
     c = Case(sum(prefix) + R, prefix, (R,) * len(prefix), Hkv, dh, 128, dtype, std=1.5)
     q = c.randn(c.B, R, H, dh)
     ws = workspace(c, H, dtype)
-    assert ws.numel() > m.WS_HEADER  # there are partial results
+    # (partial results in the workspace, but for what clusters of CTAs join)
+    assert ws.numel() > m.WS_HEADER or (dtype == BF and 16 < R * H // Hkv <= 128)
     got = m.chunk_attention_paged(q.to(dev), *c.to(dev), ws=ws)
     check(got, q, c, lambda b: ref.causal(prefix[b], R))
     rows = [max(0, R - 1 - b) for b in range(c.B)]
@@ -232,3 +233,70 @@ def test_ranges_of_long_sequences(dev, R, G, dh):
     assert (out[5] == 0).all() and status(ws) == "bad prefix"
     five = rows[:5] + [0] + rows[6:]
     check(out, q, c, lambda b: ref.causal(prefix[b], five[b]))
+
+
+@pytest.mark.parametrize("P,R,H,Hkv,dh,B", [
+    (200, 17, 2, 2, 128, 1), (300, 33, 3, 1, 64, 1), (600, 65, 8, 8, 64, 1), (1000, 128, 1, 1, 128, 1),
+    (1500, 20, 32, 8, 128, 1), (1024, 65, 32, 32, 128, 1), (2048, 65, 40, 40, 128, 1), (5000, 65, 40, 40, 64, 1),
+    (1300, 60, 6, 3, 128, 5), (700, 18, 16, 16, 64, 2)])
+def test_ranges_in_clusters(dev, P, R, H, Hkv, dh, B):
+    """Few rows, whose ranges a cluster of CTAs joins: whole, empty and masked ranges, rows and
+    sequences that are missing, bad pages and prefixes, non-finite V, waits that run out."""
+    prefix, rows = ([P, 0, P // 2, 3, P - 1][:B], [R, R, R - 1, 0, 1][:B])
+    c = Case(P + R, prefix, rows, Hkv, dh, 16, BF, R=R, std=1.5)
+    q = c.randn(B, R, H, dh)
+    # (V that the last row alone sees)
+    i, r = ref.spots(c.tab, 0, 16, P + R - 1, 1)
+    c.vp[i, r, 0, 3] = math.inf
+    ws = m.new_workspace(m.paged_attention_workspace_size(m.BF16, B, R, H, Hkv, dh, P))
+    out = torch.full_like(q, 7.0).to(dev)
+    args, n = c.to(dev), i32(*rows).to(dev)
+
+    def call(expect="ok"):
+        m.chunk_attention_paged(q.to(dev), *args, n_rows=n, out=out, ws=ws)
+        assert status(ws) == expect
+        m.clear_device_status(ws)
+    for _ in range(2):
+        call()
+        check(out, q, c, lambda b: ref.causal(prefix[b], rows[b]))
+        for b in range(B):
+            assert (out[b, rows[b]:] == 7).all()
+    # a page in the middle that is not there
+    at = P // 32
+    args[2][0, at] = c.pages
+    call("bad page")
+
+    def sees(b):
+        see = ref.causal(prefix[b], rows[b])
+        if b == 0:
+            see[:, 16 * at:16 * at + 16] = False
+        return see
+    check(out, q, c, sees)
+    # no page is there
+    args[2][0] = -1
+    call("bad page")
+    assert (out[0] == 0).all()
+    args[2].copy_(c.tab)
+    args[3][0] = P + 1
+    call("bad prefix")
+    assert (out[0] == 0).all()
+    args[3][0] = P
+    budget = m.wait_budget()
+    try:
+        m.set_wait_budget(0)
+        call("timeout")
+    finally:
+        m.set_wait_budget(budget)
+    for b in range(B):
+        assert (out[b, :rows[b]] == 0).all()
+    call()
+    check(out, q, c, lambda b: ref.causal(prefix[b], rows[b]))
+    # n_rows: none, and the tree of the same rows
+    n.zero_()
+    out.fill_(7.0)
+    call()
+    assert (out == 7).all()
+    if B == 1:
+        mask, _ = cache_ops_ref.tree(1, R, np.random.RandomState(R))
+        got = m.tree_attention_paged(q.to(dev), *args, mask.to(dev), ws=ws)
+        check(got, q, c, lambda b: ref.tree_sees(P, R, mask[b]))
