@@ -22,16 +22,26 @@ struct AppendArgs {
     int *status;
 };
 
-// One warp a row of K or of V: its lanes copy 16-byte vectors, four loads ahead of
-// their stores; the page is looked up while they are on their way.
+// One warp a row of K or of V: its lanes copy 16-byte vectors, kAhead loads ahead of their
+// stores, the first of them before the row's place is known.
 // grid (2 R rows over 8 warps, B)
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(AppendArgs a) {
     pdl_enter();
+    constexpr int kAhead = 4;
     const int b = blockIdx.y, lane = threadIdx.x & 31;
     const int w = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
     const int i = w >> 1;
     const bool is_v = w & 1;
-    if (i >= a.R || (a.n_rows && i >= a.n_rows[b])) return;
+    if (i >= a.R || (a.n_rows && i >= a.n_rows[b])) return;  // (rows behind the last are not read)
+    const long long r = (long long)b * a.R + i;
+    const uint4 *src = is_v ? a.v + r * a.v_step : a.k + r * a.k_step;
+    uint4 x[kAhead];
+    auto load = [&](int c) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (c + 32 * u < a.row_vecs) x[u] = ld_stream16(src + c + 32 * u);
+    };
+    load(lane);
     const int P = a.prefix_len[b];
     if (P < 0 || P > a.P_max) {
         set_status(a.status, MEDUSA_DEV_BAD_PREFIX);
@@ -42,10 +52,14 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(AppendArgs
         set_status(a.status, MEDUSA_DEV_BAD_PAGE);
         return;
     }
-    const long long r = (long long)b * a.R + i;
-    const uint4 *src = is_v ? a.v + r * a.v_step : a.k + r * a.k_step;
     uint4 *dst = (is_v ? a.vp : a.kp) + a.map.row(page, P + i) * a.row_vecs;
-    for (int c = lane; c < a.row_vecs; c += 32) dst[c] = ld_stream16(src + c);
+    for (int c = lane; c < a.row_vecs;) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (c + 32 * u < a.row_vecs) dst[c + 32 * u] = x[u];
+        c += 32 * kAhead;
+        load(c);
+    }
 }
 
 struct PagedCommitArgs {
