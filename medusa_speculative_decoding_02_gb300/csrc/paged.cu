@@ -23,7 +23,10 @@ struct AppendArgs {
 };
 
 // One warp a row of K or of V: its lanes copy 16-byte vectors, kAhead loads ahead of their
-// stores, the first of them before the row's place is known.
+// stores, the first of them before the row's place is known (places first: 5.4 us for 8 x
+// 65 rows of 32 heads, 12.6 for four ragged prompts of up to 4001 rows of 8 heads, 66 MB;
+// as it is 5.1 and 12.0).  Bound by the bytes: 16 x 512 rows of 32 heads, bf16, 268 MB in
+// 41.6 us, 6.45 TB/s; small calls by the launch.
 // grid (2 R rows over 8 warps, B)
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(AppendArgs a) {
     pdl_enter();
@@ -73,7 +76,8 @@ struct PagedCommitArgs {
 
 // The commit of commit.cuh with a page looked up for every slot.  A thread owns
 // whole 16-byte columns and reads all rows of a column before it writes one, so
-// no barrier separates sources from targets.  grid (column blocks, B)
+// no barrier separates sources from targets.  Bound by the launch and two dependent
+// lookups: one sequence 2.2 us, 32 sequences of 32 heads 2.5.  grid (column blocks, B)
 __global__ void __launch_bounds__(kCommitThreads) paged_commit_kernel(PagedCommitArgs a) {
     pdl_enter();
     __shared__ size_t s_src[MEDUSA_MAX_HEADS + 1], s_dst[MEDUSA_MAX_HEADS + 1];

@@ -4,8 +4,8 @@
 //
 // Query head h reads KV head h / G (G = H / Hkv).  The rows of a tile are rows that
 // share a KV head, row r * G + g being new row r and query head hk * G + g.  A
-// tile's keys are split into ranges where there are few tiles (find_item), which
-// paged_join_kernel joins.  A slot whose page number is outside the pool is
+// tile's keys are split into ranges where there are few tiles (find_item), which a
+// cluster of CTAs or a second kernel joins.  A slot whose page number is outside the pool is
 // not seen (and the status is set).  A row that sees nothing gets zeros; rows behind
 // a sequence's n_rows are neither read nor written.
 //
@@ -21,41 +21,52 @@ namespace {
 
 // ------------------------------------------------------------- CUDA cores ---
 //
-// fp32.  128 threads, 32 rows and 64 keys at a time: thread (ty, tx) of 8 x 16 scores rows
-// 4 ty .. +3 against keys tx, tx + 16, .. and owns columns 4 tx + 64 c .. +3 of
-// those rows' outputs.  The running maximum and sum of a row live in its 16 threads.
-constexpr int kRows = 32, kKeys = 64, kSimtThreads = 128;
+// fp32.  ROWS rows and 32 keys at a time, four threads a row: thread (ty, tx) of ROWS / 4 x
+// 16 scores rows 4 ty .. +3 against keys tx and tx + 16, and owns columns 4 tx + 64 c .. +3
+// of those rows' outputs.  The running maximum and sum of a row live in its 16 threads.
+// K and V of the next keys are copied while these are at work.
+//
+// Bound by the reads of shared memory and their latency: the scores read 32 bytes a thread
+// for every 8 products.  8 sequences x 8 heads behind 2048 slots, dh 128: 64 rows 171 us
+// (26 TFLOP/s), 32 rows 114; a single 32 x 64 tile with copies between the stages took
+// 295 and 167.  Tiles of 64 rows lose where they are too few for the SMs (two trees of 65
+// rows behind 300 slots: 17.5 us for 14.4).
+constexpr int kKeys = 32;
 
-template <int DH>
+template <int DH, int ROWS>
 struct SimtSmem {
-    static constexpr int LD = DH + 4, LP = kKeys + 4;
-    static constexpr int TOTAL = ((kRows + 2 * kKeys) * LD + kRows * LP) * 4 + kKeys * 4;
+    static constexpr int LD = DH + 4, LP = kKeys + 4, TILE = 2 * kKeys * LD;  // K and V of a stage
+    static constexpr int WORDS = (ROWS * LD + 2 * TILE + ROWS * LP) * 4;
+    static constexpr int TOTAL = WORDS + (2 * kKeys + 2) * 4;
+    static_assert(2 * (TOTAL + 1024) <= 228 * 1024, "two CTAs an SM");
 };
 
-template <int DH>
-__global__ void __launch_bounds__(kSimtThreads, 2) paged_attn_simt_kernel(CacheAttnArgs a) {
+template <int DH, int ROWS>
+__global__ void __launch_bounds__(4 * ROWS, 2) paged_attn_simt_kernel(CacheAttnArgs a) {
     pdl_enter();
-    using L = SimtSmem<DH>;
-    constexpr int LD = L::LD, LP = L::LP, C = DH / 64;
+    using L = SimtSmem<DH, ROWS>;
+    constexpr int LD = L::LD, LP = L::LP, C = DH / 64, THREADS = 4 * ROWS;
     extern __shared__ __align__(16) float sf[];
-    float *qs = sf, *ks = qs + kRows * LD, *vs = ks + kKeys * LD, *ps = vs + kKeys * LD;
-    int *key_ok = reinterpret_cast<int *>(ps + kRows * LP);  // the key's page is in the pool
+    auto smem_at = [](const float *p) { return (uint32_t)__cvta_generic_to_shared(p); };
+    float *qs = sf, *tiles = qs + ROWS * LD, *ps = tiles + 2 * L::TILE;
+    int *key_ok = reinterpret_cast<int *>(sf + L::WORDS / 4);  // [2][kKeys]: the key's page is in the pool
+    int *bad_at = key_ok + 2 * kKeys;  // [2]: the stage, if it has keys whose page is not
     const int g = blockIdx.x / a.row_tiles, rt = a.row_tiles - 1 - (blockIdx.x - g * a.row_tiles);
     const int R = a.R, G = a.H / a.Hkv;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     CacheItem it;
-    find_item<false, kKeys, true>(a, [&](int P, int b) {
+    find_item<false, kRangeUnit, true>(a, [&](int P, int b) {
         const int n = live_rows(a, b);
-        return n == 0 ? 0 : P + (a.anc_mask ? n : min(n, (rt * kRows + kRows - 1) / G + 1));
+        return n == 0 ? 0 : P + (a.anc_mask ? n : min(n, (rt * ROWS + ROWS - 1) / G + 1));
     }, it);
     const int b = it.b, P = it.P, kbeg = it.kbeg, kend = it.kend;
     const int M = live_rows(a, b) * G;
-    if (rt * kRows >= M) return;  // uniform over the CTA
+    if (rt * ROWS >= M) return;  // uniform over the CTA
     int row[4], head[4];
     bool live[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int m = rt * kRows + ty * 4 + i;
+        const int m = rt * ROWS + ty * 4 + i;
         live[i] = m < M;
         row[i] = live[i] ? m / G : 0;
         head[i] = g * G + (live[i] ? m - row[i] * G : 0);
@@ -82,8 +93,8 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_attn_simt_kernel(CacheA
         *reinterpret_cast<float4 *>(dst) = *reinterpret_cast<const float4 *>(src);
     };
     constexpr int VR = DH / 4;  // 16-byte vectors a row
-    for (int e = tid; e < kRows * VR; e += kSimtThreads) {
-        const int lr = e / VR, c = (e - lr * VR) * 4, m = rt * kRows + lr;
+    for (int e = tid; e < ROWS * VR; e += THREADS) {
+        const int lr = e / VR, c = (e - lr * VR) * 4, m = rt * ROWS + lr;
         const int r = m < M ? m / G : 0, h = g * G + (m < M ? m - r * G : 0);
         put(qs + lr * LD + c, static_cast<const float *>(a.q) + (((size_t)b * R + r) * a.H + h) * DH + c);
     }
@@ -100,59 +111,67 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_attn_simt_kernel(CacheA
     const int W = (R + 63) / 64;
     const float *kp = static_cast<const float *>(a.kp), *vp = static_cast<const float *>(a.vp);
     // slots below this are seen by every row of the tile
-    const int all = a.anc_mask ? P : P + rt * kRows / G + 1;
-    for (int k0 = kbeg; k0 < kend; k0 += kKeys) {
-        __syncthreads();
-        bool bad = false;
-        for (int e = tid; e < kKeys * VR; e += kSimtThreads) {
-            const int kk = e / VR, c = (e - kk * VR) * 4, slot = k0 + kk;
+    const int all = a.anc_mask ? P : P + rt * ROWS / G + 1;
+    auto load = [&](int k0, int buf) {
+        float *ks = tiles + buf * L::TILE, *vs = ks + kKeys * LD;
+#pragma unroll
+        for (int u = 0; u < kKeys * VR / THREADS; ++u) {
+            const int e = tid + u * THREADS, kk = e / VR, c = (e - kk * VR) * 4, slot = k0 + kk;
             bool ok = slot < kend;
+            size_t at = 0;
             if (ok) {
                 const int page = a.map.page_of(b, slot);
-                if (a.map.good(page)) {
-                    const size_t at = (a.map.row(page, slot) * a.Hkv + g) * DH + c;
-                    put(ks + kk * LD + c, kp + at);
-                    put(vs + kk * LD + c, vp + at);
-                } else {
-                    ok = false;
+                ok = a.map.good(page);
+                if (ok) {
+                    at = (a.map.row(page, slot) * a.Hkv + g) * DH + c;
+                } else if (c == 0) {
+                    bad_at[buf] = k0;
                     set_status(a.status, MEDUSA_DEV_BAD_PAGE);
                 }
             }
-            if (!ok) {
-                bad = true;
-                store4(ks + kk * LD + c, make_float4(0.f, 0.f, 0.f, 0.f));
-                store4(vs + kk * LD + c, make_float4(0.f, 0.f, 0.f, 0.f));
-            }
-            if (c == 0) key_ok[kk] = ok;
+            cp_async16(smem_at(ks + kk * LD + c), kp + at, ok);
+            cp_async16(smem_at(vs + kk * LD + c), vp + at, ok);
+            if (c == 0) key_ok[buf * kKeys + kk] = ok;
         }
-        const bool masked = __syncthreads_or(bad) || k0 + kKeys > all;
-        float s[4][4];
+        asm volatile("cp.async.commit_group;\n" ::: "memory");
+    };
+    if (tid < 2) bad_at[tid] = -1;
+    __syncthreads();
+    load(kbeg, 0);
+    int buf = 0;
+    for (int k0 = kbeg; k0 < kend; k0 += kKeys, buf ^= 1) {
+        asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+        __syncthreads();  // the stage is there, and the other place is free
+        if (k0 + kKeys < kend) load(k0 + kKeys, buf ^ 1);
+        const float *ks = tiles + buf * L::TILE, *vs = ks + kKeys * LD;
+        const bool masked = bad_at[buf] == k0 || k0 + kKeys > min(all, kend);
+        float s[4][2];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+            for (int j = 0; j < 2; ++j) s[i][j] = 0.f;
 #pragma unroll 4
         for (int c = 0; c < DH; c += 4) {
-            float4 q[4], k[4];
+            float4 q[4], k[2];
 #pragma unroll
             for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4 *>(qs + (ty * 4 + i) * LD + c);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const float4 *>(ks + (tx + 16 * j) * LD + c);
+            for (int j = 0; j < 2; ++j) k[j] = *reinterpret_cast<const float4 *>(ks + (tx + 16 * j) * LD + c);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < 2; ++j)
                     s[i][j] = fmaf(q[i].x, k[j].x, fmaf(q[i].y, k[j].y, fmaf(q[i].z, k[j].z, fmaf(q[i].w, k[j].w, s[i][j]))));
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float cm = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 2; ++j) {
                 bool see = true;
                 if (masked) {
                     const int kk = tx + 16 * j, slot = k0 + kk, t = slot - P;
-                    see = live[i] && key_ok[kk];
+                    see = live[i] && key_ok[buf * kKeys + kk];
                     if (see && t >= 0)
                         see = a.anc_mask ? (a.anc_mask[((size_t)b * R + row[i]) * W + (t >> 6)] >> (t & 63)) & 1u
                                          : t <= row[i];
@@ -168,7 +187,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_attn_simt_kernel(CacheA
             m_run[i] = m_new;
             l_run[i] *= alpha;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 2; ++j) {
                 const float p = exp2f(s[i][j] - mu);
                 l_run[i] += p;
                 ps[(ty * 4 + i) * LP + tx + 16 * j] = p;
@@ -218,6 +237,179 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_attn_simt_kernel(CacheA
                 *reinterpret_cast<float4 *>(a.part_o + part_row(i) * DH + tx * 4 + 64 * c) = v;
         }
         if (a.ns > 1 && tx == 0) a.part_ml[part_row(i)] = make_float2(m_run[i], l_run[i]);
+    }
+}
+
+// ---- few rows
+//
+// fp32, at most kVecRows rows a KV head.  128 threads, ROWS rows: a warp scores four keys
+// at a time, eight lanes a key, a lane holding DH / 8 of its elements and of the rows'
+// outputs; the next keys are on their way meanwhile.  Every eight lanes keep a running
+// maximum and sum of their own, which are joined at the end.
+//
+// Bound by the bytes for a row or two: 8 single tokens x 8 heads behind 2048 slots, dh 128
+// (134 MB): 26.6 us, 5.1 TB/s, then by the fp32 products and the exchanges that sum a score
+// over its lanes: 4 rows 38, 8 rows 60, 16 rows 100, where tiles of 32 rows take 114 whatever
+// they hold.
+constexpr int kVecRows = 16, kVecTile = 4, kVecThreads = 128;
+constexpr int vec_ctas_per_sm(int rows) { return rows == 1 ? 4 : rows == 2 ? 3 : 2; }  // registers
+
+template <int DH, int ROWS>
+__global__ void __launch_bounds__(kVecThreads, vec_ctas_per_sm(ROWS)) paged_attn_vec_kernel(CacheAttnArgs a) {
+    pdl_enter();
+    constexpr int V = DH / 32, WARPS = kVecThreads / 32, STEP = 4 * WARPS;
+    __shared__ float s_o[WARPS][ROWS][DH];
+    __shared__ float2 s_ml[WARPS][ROWS];
+    const int g = blockIdx.x / a.row_tiles, m0 = (blockIdx.x - g * a.row_tiles) * ROWS;
+    const int R = a.R, G = a.H / a.Hkv, W = (R + 63) / 64;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, part = lane & 7, mine = lane >> 3;
+    CacheItem it;
+    find_item<false, kRangeUnit, true>(a, [&](int P, int b) {
+        const int n = live_rows(a, b);
+        return n == 0 ? 0 : P + (a.anc_mask ? n : min(n, (m0 + ROWS - 1) / G + 1));
+    }, it);
+    const int b = it.b, P = it.P, kend = it.kend, M = live_rows(a, b) * G;
+    if (m0 >= M) return;  // uniform over the CTA
+    int row[ROWS], head[ROWS];
+    float4 q[ROWS][V], acc[ROWS][V];
+    float m_run[ROWS], l_run[ROWS];
+#pragma unroll
+    for (int u = 0; u < ROWS; ++u) {
+        const int m = min(m0 + u, M - 1);
+        row[u] = m / G;
+        head[u] = g * G + m - row[u] * G;
+        const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) +
+                                                             (((size_t)b * R + row[u]) * a.H + head[u]) * DH);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            q[u][v] = src[8 * v + part];
+            acc[u][v] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        m_run[u] = -INFINITY;
+        l_run[u] = 0.f;
+    }
+    float4 k[V], v[V];
+    bool ok = false;
+    int page = 0;
+    auto look_up = [&](int k0) { page = k0 < kend ? a.map.page_of(b, k0) : 0; };
+    // the lane's piece of key k0 + mine, whose page has been looked up (the four are in one);
+    // looks up the next ones'
+    auto load = [&](int k0) {
+        const int slot = k0 + mine;
+        ok = slot < kend;
+        if (k0 < kend && !a.map.good(page)) {
+            set_status(a.status, MEDUSA_DEV_BAD_PAGE);
+            ok = false;
+        }
+        if (ok) {
+            const size_t at = (a.map.row(page, slot) * a.Hkv + g) * DH;
+            const float4 *ks = reinterpret_cast<const float4 *>(static_cast<const float *>(a.kp) + at) + part;
+            const float4 *vs = reinterpret_cast<const float4 *>(static_cast<const float *>(a.vp) + at) + part;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                k[e] = ks[8 * e];
+                v[e] = vs[8 * e];
+            }
+        }
+        look_up(k0 + STEP);
+    };
+    auto dot4 = [](const float4 &x, const float4 &y, float s) {
+        return fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s))));
+    };
+    const int first = it.kbeg + 4 * warp;
+    look_up(first);
+    load(first);
+    for (int k0 = first; k0 < kend; k0 += STEP) {
+        float s[ROWS];
+#pragma unroll
+        for (int u = 0; u < ROWS; ++u) {
+            s[u] = 0.f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) s[u] = dot4(q[u][e], k[e], s[u]);
+        }
+        float4 x[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) x[e] = v[e];
+        const bool here = ok;
+        const int t = k0 + mine - P;
+        load(k0 + STEP);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+            for (int u = 0; u < ROWS; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
+#pragma unroll
+        for (int u = 0; u < ROWS; ++u) {
+            bool see = here;
+            if (see && t >= 0)
+                see = a.anc_mask ? (a.anc_mask[((size_t)b * R + row[u]) * W + (t >> 6)] >> (t & 63)) & 1u : t <= row[u];
+            if (!see) continue;  // (whatever V holds)
+            const float y = s[u] * a.scale_log2;
+            if (y > m_run[u]) {
+                const float alpha = exp2f(m_run[u] - y);
+                m_run[u] = y;
+                l_run[u] *= alpha;
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    acc[u][e] = make_float4(acc[u][e].x * alpha, acc[u][e].y * alpha, acc[u][e].z * alpha, acc[u][e].w * alpha);
+            }
+            const float p = exp2f(y - (m_run[u] == -INFINITY ? 0.f : m_run[u]));
+            l_run[u] += p;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                acc[u][e].x = fmaf(p, x[e].x, acc[u][e].x);
+                acc[u][e].y = fmaf(p, x[e].y, acc[u][e].y);
+                acc[u][e].z = fmaf(p, x[e].z, acc[u][e].z);
+                acc[u][e].w = fmaf(p, x[e].w, acc[u][e].w);
+            }
+        }
+        __syncwarp();
+    }
+    // ---- the warp's four sums, then the CTA's
+#pragma unroll
+    for (int u = 0; u < ROWS; ++u) {
+        float top = m_run[u];
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        const float f = exp2f(m_run[u] - (top == -INFINITY ? 0.f : top));
+        float l = f * l_run[u];
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (lane == 0) s_ml[warp][u] = make_float2(top, l);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            // (a sum with a weight of zero adds nothing)
+            float y[4] = {acc[u][e].x, acc[u][e].y, acc[u][e].z, acc[u][e].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                y[i] = f == 0.f ? 0.f : y[i] * f;
+                y[i] += __shfl_xor_sync(0xffffffffu, y[i], 8);
+                y[i] += __shfl_xor_sync(0xffffffffu, y[i], 16);
+            }
+            if (mine == 0)
+                *reinterpret_cast<float4 *>(&s_o[warp][u][(8 * e + part) * 4]) = make_float4(y[0], y[1], y[2], y[3]);
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < ROWS * DH; i += kVecThreads) {
+        const int u = i / DH, c = i - u * DH;
+        if (m0 + u >= M) break;
+        float top = -INFINITY, l = 0.f, y = 0.f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) top = fmaxf(top, s_ml[w][u].x);
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            const float f = exp2f(s_ml[w][u].x - (top == -INFINITY ? 0.f : top));
+            l = fmaf(f, s_ml[w][u].y, l);
+            if (f != 0.f) y = fmaf(f, s_o[w][u][c], y);
+        }
+        const int m = m0 + u, r = m / G, h = g * G + m - r * G;
+        if (a.ns == 1) {
+            static_cast<float *>(a.out)[(((size_t)b * R + r) * a.H + h) * DH + c] = l == 0.f ? 0.f : y / l;
+        } else {
+            const size_t at = ((size_t)it.range * a.H + h) * R + r;
+            a.part_o[at * DH + c] = y;
+            if (c == 0) a.part_ml[at] = make_float2(top, l);
+        }
     }
 }
 
@@ -290,7 +482,8 @@ __global__ void __launch_bounds__(128, 4) paged_join_rows_kernel(CacheAttnArgs a
     for (int v = 0; v < V; ++v) store_row4(dst + 4 * v, acc[v], inv);
 }
 
-// Few rows: a CTA a row, its ranges dealt to groups of DH / 4 threads.  grid B * H * R
+// Few rows: a CTA a row, its ranges dealt to groups of DH / 4 threads (32 rows of some 60
+// ranges: 14 us for the whole call, 29 with eight lanes a row).  grid B * H * R
 template <typename T, int DH>
 __global__ void __launch_bounds__(256) paged_join_ranges_kernel(CacheAttnArgs a) {
     pdl_enter();
@@ -347,7 +540,8 @@ __global__ void __launch_bounds__(256) paged_join_ranges_kernel(CacheAttnArgs a)
 }
 
 // Up to kJoinFewRows rows the time is the latency of a row's ranges, beyond it is how
-// many rows are on their way.
+// many rows are on their way: a CTA a row takes 8.9 us for 2080 rows of 2 ranges, eight
+// lanes a row 4.3; 42.7 and 7.5 for 16384.
 constexpr int kJoinFewRows = 1024;
 
 template <typename T, int DH>
@@ -365,6 +559,8 @@ struct PagedPlan {
     int row_tiles, ns;
     int ranges;    // in all
     bool few;      // at most kFewRows rows a KV head
+    bool vec;      // fp32, at most kVecRows
+    int simt_rows;  // of a tile of the fp32 kernel for more
     bool deal;     // ranges dealt out by the sequences' lengths
     bool cluster;  // the ranges of a row are the CTAs of a cluster
 };
@@ -387,8 +583,12 @@ PagedPlan paged_plan(medusa_dtype dtype, int B, int R, int H, int Hkv, int dh, i
     const int M = R * (H / Hkv);
     const bool simt = dtype == MEDUSA_F32;
     p.few = !simt && M <= kFewRows;
-    const int rows = simt ? kRows : kPagedTileRows, sub = simt || p.few ? kKeys : kPagedStage;
-    const int slots = (p.few ? cache_few_ctas_per_sm(false, M) : simt ? 2 : 1) * device_sm_count();
+    p.vec = simt && M <= kVecRows;
+    // (tiles of 64 rows where there are enough of them to go round)
+    const long long wide = (long long)B * Hkv * ((M + 63) / 64) * ((P_max + R + kRangeUnit - 1) / kRangeUnit);
+    p.simt_rows = M > 32 && 2 * wide >= 3 * device_sm_count() ? 64 : 32;
+    const int rows = p.vec ? kVecTile : simt ? p.simt_rows : kPagedTileRows, sub = simt || p.few ? kRangeUnit : kPagedStage;
+    const int slots = (p.few ? cache_few_ctas_per_sm(false, M) : p.vec ? vec_ctas_per_sm(M) : simt ? 2 : 1) * device_sm_count();
     p.row_tiles = p.few ? 1 : (M + rows - 1) / rows;
     const int subs = (P_max + R + sub - 1) / sub;
     const long long ctas = (long long)B * Hkv * p.row_tiles;
@@ -425,6 +625,15 @@ PagedPlan paged_plan(medusa_dtype dtype, int B, int R, int H, int Hkv, int dh, i
         p.ranges = B + (B + 1) / 2;
     }
     return p;
+}
+
+template <int DH, int ROWS>
+cudaError_t launch_simt(const CacheAttnArgs &a, const PagedPlan &p, cudaStream_t stream) {
+    auto kern = paged_attn_simt_kernel<DH, ROWS>;
+    constexpr int smem = SimtSmem<DH, ROWS>::TOTAL;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e) return e;
+    return launch_pdl(kern, dim3(a.Hkv * p.row_tiles, p.ns, a.B), dim3(4 * ROWS), (size_t)smem, stream, a);
 }
 
 }  // namespace
@@ -472,13 +681,19 @@ cudaError_t launch_paged_attention(medusa_dtype dtype, const void *q, const void
     a.wait_polls = wait_budget();
     a.ranges = p.deal && !p.few ? p.ranges : 0;
     a.cluster = p.cluster;
+    const int M = R * (H / Hkv);
     cudaError_t e;
-    if (dtype == MEDUSA_F32) {
-        auto kern = dh == 128 ? paged_attn_simt_kernel<128> : paged_attn_simt_kernel<64>;
-        const int smem = dh == 128 ? SimtSmem<128>::TOTAL : SimtSmem<64>::TOTAL;
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e) return e;
-        e = launch_pdl(kern, dim3(Hkv * p.row_tiles, p.ns, B), dim3(kSimtThreads), (size_t)smem, stream, a);
+    if (p.vec) {
+        auto kern = dh == 128 ? (M == 1   ? paged_attn_vec_kernel<128, 1>
+                                 : M == 2 ? paged_attn_vec_kernel<128, 2>
+                                          : paged_attn_vec_kernel<128, kVecTile>)
+                              : (M == 1   ? paged_attn_vec_kernel<64, 1>
+                                 : M == 2 ? paged_attn_vec_kernel<64, 2>
+                                          : paged_attn_vec_kernel<64, kVecTile>);
+        e = launch_pdl(kern, dim3(Hkv * p.row_tiles, p.ns, B), dim3(kVecThreads), 0, stream, a);
+    } else if (dtype == MEDUSA_F32) {
+        e = p.simt_rows == 32 ? (dh == 128 ? launch_simt<128, 32>(a, p, stream) : launch_simt<64, 32>(a, p, stream))
+                              : (dh == 128 ? launch_simt<128, 64>(a, p, stream) : launch_simt<64, 64>(a, p, stream));
     } else {
         e = p.few ? launch_cache_attention_few(a, false, dh, stream) : launch_paged_attention_tc(a, dh, stream);
     }

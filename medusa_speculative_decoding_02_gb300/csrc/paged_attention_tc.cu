@@ -12,9 +12,10 @@
 //              works, the products of the other run.
 //   warps 9, 10  copies: K and V of a stage, one TMA box a page (and 64 columns),
 //              into a ring each.
-//   warp 11    nothing (register budgets are by four warps).
+//   warp 11    sets the barriers up, then nothing (register budgets are by four warps).
 // With at most 128 rows the two tiles hold the same rows, A the even stages and B the
-// odd ones, so that the work still takes turns; their results are joined at the end.
+// odd ones, so that the work still takes turns; their results are joined at the end, and
+// those of the CTAs of a cluster after that, where each has a range of the keys.
 //
 // Tensor memory (512 columns): S / P of A, S / P of B, O of A, O of B.  The reference
 // m moves only when a stage's maximum exceeds it by 2^8, and O is then rescaled in
@@ -27,6 +28,28 @@
 // itself.  Every wait is bounded; on a timeout the CTA sets the status, waits
 // (bounded) for its products and copies, frees its tensor memory and publishes
 // nothing.
+//
+// What bounds it: the products and what feeds them.  A stage of two tiles takes
+// 2490-2550 cycles, of which 2048 are its four products at the rate of the tensor cores;
+// the two of them that read both operands from shared memory leave its ports no room.  A
+// stage of one tile, by halves, takes 1470-1830.  A CTA's ends cost 11000 cycles: 4260
+// to the first copy's landing, 3090 to the first scores, 3890 behind the last product, and
+// nothing of the next CTA overlaps them, as one takes the SM's shared memory.
+// Measured: a prompt of 8192 rows, 32 heads over 8, dh 128: 342 us, 1610 TFLOP/s (370 us where
+// it runs without a break, at the power limit; dh 64 275 us); six chunks of 1 to 509 rows
+// behind up to 5001 slots, 28 heads over 4: 80 us, 1150 TFLOP/s, where the busiest SM has
+// two CTAs and 48 stages against 40 on average; eight trees of 65 rows behind up to 8192
+// slots, 32 heads over 8: 65 us, 2.7 TB/s; one of 32 heads behind 1024: 12.5 us (14.7 with
+// a cold L2), nearly all of it the ends.
+// Pages: a page is a TMA box of up to 128 rows, whose row a lane has looked up while the
+// stage before was under way, so that 16-row pages cost what 128-row pages do (338 and 350
+// us); copies issued by one lane took 571 us at 16 rows.
+// Measured and not kept: K and V copied by one warp (367, and 468 us at 16 rows), Q and O
+// moved by their rows' threads (375), weights computed against the reference before the
+// stage's maximum is known (394; registers spill), one arrival for a stage's weights instead
+// of two (383 against 376), the rows behind the last whole tile (260 rows are 256 and 4)
+// on register-operand products by warp 11 from the same stages (112-119 us against 91:
+// 58 cycles an instruction beside the others').
 #include "cache_attention.cuh"
 #include "tensor_map.h"
 
@@ -227,7 +250,8 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
         }
     };
     // CLUSTER: the CTAs of the cluster hold a range of the same rows each, and take turns at
-    // joining them.  Rows of DH / 4 threads.
+    // joining them, DH / 4 threads a row.  (Several rows at once, for few ranges, spills at the
+    // 72 registers that the copying warps keep: 14.6 us for 10.8.)
     auto join_cluster = [&] {
         __syncwarp();
         cluster_arrive();

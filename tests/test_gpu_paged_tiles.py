@@ -300,3 +300,44 @@ def test_ranges_in_clusters(dev, P, R, H, Hkv, dh, B):
         mask, _ = cache_ops_ref.tree(1, R, np.random.RandomState(R))
         got = m.tree_attention_paged(q.to(dev), *args, mask.to(dev), ws=ws)
         check(got, q, c, lambda b: ref.tree_sees(P, R, mask[b]))
+
+
+@pytest.mark.parametrize("R,H,Hkv,dh,prefix", [
+    (1, 4, 4, 128, (300, 0)), (2, 2, 1, 64, (75, 700)), (3, 1, 1, 128, (1000,)), (5, 6, 2, 128, (129, 64, 1)),
+    (16, 3, 3, 64, (500,)), (17, 2, 2, 128, (257, 31)), (33, 8, 8, 64, (2000, 2100)), (64, 6, 3, 128, (1500, 0)),
+    (70, 20, 10, 64, (700,)), (129, 8, 8, 128, (900,))])
+def test_fp32_tiles(dev, R, H, Hkv, dh, prefix):
+    """fp32: tiles of 1 to 64 rows, with bad pages, masks and V that few rows see."""
+    B = len(prefix)
+    rows = [max(1, R - b) for b in range(B)]
+    c = Case(R + H, prefix, rows, Hkv, dh, 16, F32, R=R, std=1.5)
+    q = c.randn(B, R, H, dh)
+    for b in range(B):  # seen by the last row alone
+        i, r = ref.spots(c.tab, b, 16, prefix[b] + rows[b] - 1, 1)
+        c.vp[i, r, 0, 5] = -math.inf
+    ws = workspace(c, H, F32)
+    out = torch.full_like(q, 7.0).to(dev)
+    args, n = c.to(dev), i32(*rows).to(dev)
+    m.chunk_attention_paged(q.to(dev), *args, n_rows=n, out=out, ws=ws)
+    check(out, q, c, lambda b: ref.causal(prefix[b], rows[b]))
+    assert status(ws) == "ok"
+    at = prefix[0] // 32
+    args[2][0, at] = -5
+    m.chunk_attention_paged(q.to(dev), *args, n_rows=n, out=out, ws=ws)
+
+    def sees(b):
+        see = ref.causal(prefix[b], rows[b])
+        if b == 0:
+            see[:, 16 * at:16 * at + 16] = False
+        return see
+    check(out, q, c, sees)
+    for b in range(B):
+        assert (out[b, rows[b]:] == 7).all()
+    assert status(ws) == "bad page"
+    m.clear_device_status(ws)
+    args[2].copy_(c.tab)
+    mask, _ = cache_ops_ref.tree(B, R, np.random.RandomState(R))
+    full = Case(R + H, prefix, [R] * B, Hkv, dh, 16, F32, std=1.5)
+    got = m.tree_attention_paged(q.to(dev), *full.to(dev), mask.to(dev), ws=ws)
+    check(got, q, full, lambda b: ref.tree_sees(prefix[b], R, mask[b]))
+    assert status(ws) == "ok"
