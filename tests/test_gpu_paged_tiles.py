@@ -341,3 +341,32 @@ def test_fp32_tiles(dev, R, H, Hkv, dh, prefix):
     got = m.tree_attention_paged(q.to(dev), *full.to(dev), mask.to(dev), ws=ws)
     check(got, q, full, lambda b: ref.tree_sees(prefix[b], R, mask[b]))
     assert status(ws) == "ok"
+
+
+def test_clusters_captured_and_on_two_streams(dev):
+    """Calls whose ranges clusters join: a captured call replayed on new inputs, next to
+    another such call on another stream."""
+    a, b = Case(5, (900,), (40,), 4, 128, 32, BF), Case(6, (1500,), (60,), 8, 64, 64, BF)
+    q = [c.randn(3, c.R, 2 * c.Hkv, c.dh) for c in (a, b)]
+    args = [c.to(dev) for c in (a, b)]
+    ws = [m.new_workspace(m.paged_attention_workspace_size(m.BF16, 1, c.R, 2 * c.Hkv, c.Hkv, c.dh, c.P_max))
+          for c in (a, b)]
+    assert [w.numel() for w in ws] == [m.WS_HEADER] * 2  # no partial results
+    src = [x[:1].to(dev) for x in q]
+    out = [torch.zeros_like(x) for x in src]
+    side = torch.cuda.Stream()
+
+    def issue(i, stream=None):
+        m.chunk_attention_paged(src[i], *args[i], out=out[i], ws=ws[i], stream=stream)
+    graph = m.StepGraph(lambda: issue(0))
+    for k in range(3):
+        for i in range(2):
+            src[i].copy_(q[i][k:k + 1])
+        torch.cuda.synchronize()
+        for _ in range(5):
+            graph.replay()
+            issue(1, side)
+        torch.cuda.synchronize()
+        for i, c in enumerate((a, b)):
+            check(out[i], q[i][k:k + 1], c, lambda _: ref.causal(c.prefix[0], c.R))
+            assert status(ws[i]) == "ok"
