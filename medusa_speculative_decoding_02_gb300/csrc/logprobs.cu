@@ -725,11 +725,15 @@ cudaError_t launch_token_logprobs(medusa_dtype dtype, const void *logits, long l
     a.top_ids = top_ids;
     a.top_logp = top_logp;
     a.status = static_cast<int *>(ws);
-    // CTAs a row: as many as fit at once, none with less than a chunk
-    const int slots = kLpCtas * device_sm_count();
+    // CTAs a row: as many as run at once, none with less than a chunk, or than three chunks
+    // where half the SMs have a row of their own.  Rows of 4 chunks (32000 in bf16): 65 of
+    // them 7.8 us with one CTA a row and 7.1 with four, 100 8.0 and 8.0, 200 9.6 and (two CTAs)
+    // 10.5; of 16 chunks: 65 22.8 and 14.0, 300 28.3 and (two) 23.8.  Clusters of four get no more than
+    // about 5/6 of the places: 125 of them 8.3 us, 150 14.2.
+    const int slots = kLpCtas * device_sm_count(), least = 2 * N > device_sm_count() ? 3 : 1;
     const int chunks = (int)(((long long)V * (dtype == MEDUSA_F32 ? 4 : 2) + kChunk * 16 - 1) / (kChunk * 16));
     int C = 1;
-    while (C < kMaxCluster && (long long)N * C * 2 <= slots && 2 * C <= chunks) C *= 2;
+    while (C < kMaxCluster && (long long)N * C * 2 <= (C == 1 ? slots : slots * 5 / 6) && 2 * C * least <= chunks) C *= 2;
     auto kern = dtype == MEDUSA_F32
                     ? (C > 1 ? token_logprobs_kernel<float, true> : token_logprobs_kernel<float, false>)
                     : (C > 1 ? token_logprobs_kernel<bf16, true> : token_logprobs_kernel<bf16, false>);
