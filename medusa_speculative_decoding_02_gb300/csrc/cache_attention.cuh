@@ -36,6 +36,7 @@ struct CacheAttnArgs {
     // than B; grid.y).  A sequence that gets one is written without the join.
     int ranges;
     int cluster;  // the ns ranges are the CTAs of a cluster, which join them
+    int pair;     // a CTA works on two KV heads
 };
 
 // A sequence's visible slots, numbered without a gap.

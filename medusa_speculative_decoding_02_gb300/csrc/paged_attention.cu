@@ -563,9 +563,12 @@ struct PagedPlan {
     int simt_rows;  // of a tile of the fp32 kernel for more
     bool deal;     // ranges dealt out by the sequences' lengths
     bool cluster;  // the ranges of a row are the CTAs of a cluster
+    bool pair;     // a CTA works on two KV heads
 };
 
 constexpr int kLongStages = 64, kClusterStages = 16;
+constexpr int kPairStages = 24;
+constexpr double kPairStage = 1.7;  // a stage of two heads, in stages of one
 
 // Key ranges: the count that makes (waves of CTAs) x (stages per CTA + 3) smallest, with 3
 // stages (4 of one tile) for the join, 2 where a cluster of up to 8 CTAs joins its own ranges.
@@ -578,6 +581,13 @@ constexpr int kLongStages = 64, kClusterStages = 16;
 // dealt out in clusters, so those are for up to kClusterStages stages a CTA: 3 x 65 rows, 8
 // heads, up to 3000 slots 19.1 -> 13.0; 4 x 65 up to 8000 (16 stages) 24.9 -> 22.1, equally
 // long 35.0 -> 30.2, but with one long sequence among short ones up to 11 stages more.
+//
+// More tiles of at most 128 rows than SMs: two KV heads a CTA, whose ends are then those of
+// one and whose products hide one another's softmax.  Trees of 65 rows, 32 heads, prefix 1024:
+// 8 39.0 -> 31.1 us, 16 76.4 -> 60.4, 5 29.5 -> 21.3; 128 of 16 rows, 32 heads over 8, 133 -> 117.
+// In one wave that is nearly full the longest sequence sets the time, so that long
+// ones (kPairStages) stay apart there: 8 ragged ones up to 4096 slots would take 69 us for 63
+// (equally long 86 for 95).  In ranges they lose to single heads (12 up to 2048: 105 for 87).
 PagedPlan paged_plan(medusa_dtype dtype, int B, int R, int H, int Hkv, int dh, int P_max) {
     PagedPlan p;
     const int M = R * (H / Hkv);
@@ -591,23 +601,31 @@ PagedPlan paged_plan(medusa_dtype dtype, int B, int R, int H, int Hkv, int dh, i
     const int slots = (p.few ? cache_few_ctas_per_sm(false, M) : p.vec ? vec_ctas_per_sm(M) : simt ? 2 : 1) * device_sm_count();
     p.row_tiles = p.few ? 1 : (M + rows - 1) / rows;
     const int subs = (P_max + R + sub - 1) / sub;
-    const long long ctas = (long long)B * Hkv * p.row_tiles;
     double best = 0;
     p.ns = 1;
-    p.cluster = false;
+    p.cluster = p.pair = false;
     const bool split = !simt && !p.few && M <= kPagedTileRows / 2;
-    const int most = std::min<long long>(subs, std::max<long long>(1, 4LL * slots / ctas));
-    for (int ns = 1; ns <= most; ++ns) {
-        const int per = (subs + ns - 1) / ns;
-        if ((subs + per - 1) / per != ns) continue;
-        const bool cluster = split && ns > 1 && ns <= kClusterRanges && (B == 1 || per <= kClusterStages) &&
-                             ctas <= paged_cluster_slots(dh, ns);
-        const double waves = cluster ? 1.0 : (double)((ctas * ns + slots - 1) / slots);
-        const double cost = waves * (per + 3) + (cluster ? 2.0 : ns > 1 ? (split ? 4.0 : 3.0) + 0.05 * ns : 0.0);
-        if (ns == 1 || cost < best) {
-            best = cost;
-            p.ns = ns;
-            p.cluster = cluster;
+    long long ctas = 0;
+    for (int pair = 0; pair <= (split && Hkv > 1 && B * (long long)Hkv > slots); ++pair) {
+        const long long of_ns = (long long)B * (pair ? (Hkv + 1) / 2 : Hkv) * p.row_tiles;
+        const double stage = pair ? kPairStage : 1.0;
+        if (pair && of_ns <= slots && 4 * of_ns > 3 * slots && subs > kPairStages) continue;
+        const int most = pair ? 1 : std::min<long long>(subs, std::max<long long>(1, 4LL * slots / of_ns));
+        for (int ns = 1; ns <= most; ++ns) {
+            const int per = (subs + ns - 1) / ns;
+            if ((subs + per - 1) / per != ns) continue;
+            const bool cluster = split && ns > 1 && ns <= kClusterRanges &&
+                                 (B == 1 || per <= kClusterStages) && of_ns <= paged_cluster_slots(dh, ns);
+            const double waves = cluster ? 1.0 : (double)((of_ns * ns + slots - 1) / slots);
+            const double cost =
+                waves * (stage * per + 3) + (cluster ? 2.0 : ns > 1 ? (split ? 4.0 : 3.0) + 0.05 * ns : 0.0);
+            if (best == 0 || cost < best) {
+                best = cost;
+                ctas = of_ns;
+                p.ns = ns;
+                p.cluster = cluster;
+                p.pair = pair;
+            }
         }
     }
     p.deal = !simt && p.ns > 1 && !p.cluster && B > 1 && B <= 32;
@@ -681,6 +699,7 @@ cudaError_t launch_paged_attention(medusa_dtype dtype, const void *q, const void
     a.wait_polls = wait_budget();
     a.ranges = p.deal && !p.few ? p.ranges : 0;
     a.cluster = p.cluster;
+    a.pair = p.pair;
     const int M = R * (H / Hkv);
     cudaError_t e;
     if (p.vec) {

@@ -15,7 +15,9 @@
 //   warp 11    sets the barriers up, then nothing (register budgets are by four warps).
 // With at most 128 rows the two tiles hold the same rows, A the even stages and B the
 // odd ones, so that the work still takes turns; their results are joined at the end, and
-// those of the CTAs of a cluster after that, where each has a range of the keys.
+// those of the CTAs of a cluster after that, where each has a range of the keys.  Where
+// there are more such tiles than SMs, A and B are the same rows of two KV heads, and the
+// ring holds the stages of one and of the other by turns.
 //
 // Tensor memory (512 columns): S / P of A, S / P of B, O of A, O of B.  The reference
 // m moves only when a stage's maximum exceeds it by 2^8, and O is then rescaled in
@@ -103,7 +105,7 @@ struct Divisor {
 
 struct PagedMaps {
     CUtensorMap k, v;
-    Divisor by_g, by_hkv;  // division by G and by the KV heads
+    Divisor by_g, by_units;  // division by G and by the CTAs of a row tile
 };
 
 __device__ __forceinline__ bool pair_not_finite(uint4 w) {
@@ -136,10 +138,15 @@ __device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
     }
 }
 
-template <int DH, bool DEAL, bool CLUSTER>
+// What a CTA's tiles are: 256 rows or the halves of 128; halves whose CTAs are a cluster; 128
+// rows of two KV heads.
+enum Rows { kTiles, kCluster, kPair };
+
+template <int DH, bool DEAL, Rows MODE>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs a) {
     using L = PagedSmem<DH>;
+    constexpr bool CLUSTER = MODE == kCluster, PAIR = MODE == kPair;
     constexpr int NK = L::NK, NT = 2 * NK;
     extern __shared__ __align__(1024) unsigned char sm[];
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BAR), *empty = full + NT, *bar_q = empty + NT,
@@ -185,7 +192,8 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
     pdl_enter();
 
     // the longest first: a chunk's last rows see the most keys, a tree's last tile has the fewest rows
-    const int rt_up = maps.by_hkv(blockIdx.x), g = blockIdx.x - rt_up * a.Hkv;
+    const int units = PAIR ? (a.Hkv + 1) / 2 : a.Hkv;
+    const int rt_up = maps.by_units(blockIdx.x), g = (blockIdx.x - rt_up * units) * (PAIR ? 2 : 1);
     const int rt = a.anc_mask ? rt_up : a.row_tiles - 1 - rt_up;
     const int R = a.R, G = a.H / a.Hkv;
     const bool tree = a.anc_mask != nullptr;
@@ -204,18 +212,21 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
     const int n = live_rows(a, b), M = n * G;
     if (m0 >= M) return;  // uniform over the CTA
     const int rows = min(kPagedTileRows, M - m0);
-    const bool split = CLUSTER || rows <= 128;  // A and B are the same rows, by turns of the stages
+    // PAIR: A and B are the same rows of two KV heads, but for the last head of an odd number
+    const bool pair = PAIR && g + 1 < a.Hkv;
+    const bool turns = CLUSTER || PAIR || rows <= 128;  // A and B take turns at the stages
+    const bool split = turns && !pair;                  // ... and are the same rows
     const int kbeg = it.kbeg, kend = min(it.kend, keys_of(P, n, m0 + rows));
 
     // row of a softmax thread
-    const int side = (warp >> 2) & 1, t = tid & 127;
-    const int m = m0 + (split ? 0 : side * 128) + t;
+    const int side = (warp >> 2) & 1, t = tid & 127, gs = pair ? g + side : g;
+    const int m = m0 + (turns ? 0 : side * 128) + t;
     const bool live = tid < 256 && m < M;
     const int r = live ? by_g(m) : 0;
-    const int mw = m0 + (split ? 0 : side * 128) + (warp & 3) * 32;  // the warp's first row
+    const int mw = m0 + (turns ? 0 : side * 128) + (warp & 3) * 32;  // the warp's first row
     // row of q and out, and of the partial results, in rows of DH elements
-    auto row_at = [&](int r, int gq) { return ((size_t)b * R + r) * a.H + g * G + gq; };
-    auto part_at = [&](int r, int gq) { return ((size_t)it.range * a.H + g * G + gq) * R + r; };
+    auto row_at = [&](int r, int gq) { return ((size_t)b * R + r) * a.H + gs * G + gq; };
+    auto part_at = [&](int r, int gq) { return ((size_t)it.range * a.H + gs * G + gq) * R + r; };
     float *const part_o = reinterpret_cast<float *>(sm + L::PART);  // CLUSTER: [128][LD]
     float2 *const part_ml = reinterpret_cast<float2 *>(sm + L::PART_ML);
     auto publish_nothing = [&] {
@@ -292,13 +303,15 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
         if constexpr (CLUSTER) join_cluster();
         return;
     }
-    const int nsub = (kend - kbeg + kPagedStage - 1) / kPagedStage;
+    // stages; of a pair by turns, A's first
+    const int nsub = ((kend - kbeg + kPagedStage - 1) / kPagedStage) << pair;
     // stages of tile A that hold keys one of its rows sees (of B: all nsub)
-    const int nsub_a = split ? nsub
+    const int nsub_a = turns ? nsub
                              : max(0, min(nsub, (keys_of(P, n, m0 + 128) - kbeg + kPagedStage - 1) / kPagedStage));
     // the first stage that some row of the CTA does not see wholly
     const int all = tree ? P : min(P + by_g(m0) + 1, kend);
-    const int j_masked = max(0, (all - kbeg) / kPagedStage);
+    const int j_masked = max(0, (all - kbeg) / kPagedStage) << pair;
+    auto first_key = [&](int j) { return kbeg + (j >> pair) * kPagedStage; };
 
     // place of stage j's K or V among the slots, a ring for each
     auto slot_of = [&](int j, bool vs) { return (vs ? NK : 0) + j % NK; };
@@ -315,7 +328,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
     const int end = P + n;
     const bool vs = warp == 10;
     auto row_of = [&](int j) {  // the lane's pool row of stage j
-        const int slot = kbeg + j * kPagedStage + my * box;
+        const int slot = first_key(j) + my * box;
         if (lane >= copy_boxes || slot >= end) return rows_end;
         const int page = a.map.page_of(b, slot);
         return a.map.good(page) ? (int)a.map.row(page, slot) : rows_end;
@@ -328,7 +341,8 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
         if (lane == 0) tc::mbar_arrive_expect_tx(full + i, L::TILE);
         __syncwarp();
         if (lane < copy_boxes)
-            tc::tma_load_3d(sm + L::RING + i * L::TILE + to, vs ? &maps.v : &maps.k, 0, row, g * L::NB + half, full + i);
+            tc::tma_load_3d(sm + L::RING + i * L::TILE + to, vs ? &maps.v : &maps.k, 0, row,
+                            (pair ? g + (j & 1) : g) * L::NB + half, full + i);
         // (a phase of `full` can be told from the one two before it only by who knows
         // which stage is in the slot: the checking warps wait from here on)
         if (vs && j >= j_masked && lane == 0) tc::mbar_arrive(armed + (j - j_masked));
@@ -415,8 +429,9 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
                 return true;
             };
             bool go = wait_or_fail(bar_q, 0, a.wait_polls, failed);
-            if (split) {
-                go = go && scores(0, 0, true) && (nsub == 1 || scores(1, 1, true));
+            if (turns) {
+                go = go && scores(0, 0, true) && (!pair || wait_or_fail(bar_q + 1, 0, a.wait_polls, failed)) &&
+                     (nsub == 1 || scores(1, 1, true));
                 for (int j = 0; j < nsub && go; ++j)
                     go = values(j & 1, j, j >> 1, true) && (j + 2 >= nsub || scores(j & 1, j + 2, true));
             } else {
@@ -469,18 +484,18 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
             return live ? vis : 0ull;
         };
         const int box_log2 = min(a.map.shift, 7), boxes = 128 >> box_log2;
-        const int step = split ? 2 : 1, mine_n = side == 0 ? nsub_a : nsub;
+        const int step = turns ? 2 : 1, mine_n = side == 0 ? nsub_a : nsub;
 
         float m_run = -INFINITY, l_run = 0.f;
         bool dead = false;  // warp-uniform
         int use = 0;
-        for (int j = split ? side : 0; j < mine_n && !dead; j += step, ++use) {
-            const int k0 = kbeg + j * kPagedStage;
+        for (int j = turns ? side : 0; j < mine_n && !dead; j += step, ++use) {
+            const int k0 = first_key(j);
             // pages of the stage, one a lane
             bool bad_page = false;
             if (lane < boxes && k0 + (lane << box_log2) < kend)
                 bad_page = !a.map.good(a.map.page_of(b, k0 + (lane << box_log2)));
-            if (j >= j_masked && (split || side)) {
+            if (j >= j_masked && (turns || side)) {
                 // ---- infinities and NaNs in V of a stage that some row does not see wholly
                 dead = !wait_or_fail(armed + (j - j_masked), 0, a.wait_polls, failed) || !wait_full(j, true);
                 if (dead) break;
@@ -607,15 +622,15 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
             const bf16 *q_row = static_cast<const bf16 *>(a.q) + row_at(r, m - r * G) * DH;
 #pragma unroll 1
             for (int j = j_masked; j < nsub; ++j) {
-                if (split && (j & 1) != side) continue;
+                if (turns && (j & 1) != side) continue;
 #pragma unroll 1
                 for (int key = 0; key < kPagedStage; ++key) {
                     if (!((bad_keys[4 * (j - j_masked) + (key >> 5)] >> (key & 31)) & 1u)) continue;
-                    const int slot = kbeg + j * kPagedStage + key;
+                    const int slot = first_key(j) + key;
                     if (!((sees64(slot & ~63) >> (slot & 63)) & 1ull)) continue;
                     const int page = a.map.page_of(b, slot);
                     if (!a.map.good(page)) continue;
-                    const size_t at = (a.map.row(page, slot) * a.Hkv + g) * DH;
+                    const size_t at = (a.map.row(page, slot) * a.Hkv + gs) * DH;
                     const bf16 *kr = static_cast<const bf16 *>(a.kp) + at;
                     const bf16 *vr = static_cast<const bf16 *>(a.vp) + at;
                     float s = 0.f;
@@ -762,15 +777,19 @@ bool encode_pool(CUtensorMap *map, const void *pool, const CacheAttnArgs &a, int
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// CTAs of a row tile
+int units_of(const CacheAttnArgs &a) { return a.pair ? (a.Hkv + 1) / 2 : a.Hkv; }
+
 template <int DH>
 cudaError_t launch(const PagedMaps &maps, const CacheAttnArgs &a, cudaStream_t stream) {
-    auto kern = a.starts    ? paged_attn_tc_kernel<DH, true, false>
-                : a.cluster ? paged_attn_tc_kernel<DH, false, true>
-                            : paged_attn_tc_kernel<DH, false, false>;
+    auto kern = a.starts    ? paged_attn_tc_kernel<DH, true, kTiles>
+                : a.pair    ? paged_attn_tc_kernel<DH, false, kPair>
+                : a.cluster ? paged_attn_tc_kernel<DH, false, kCluster>
+                            : paged_attn_tc_kernel<DH, false, kTiles>;
     constexpr int smem = PagedSmem<DH>::TOTAL;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e) return e;
-    const dim3 grid(a.Hkv * a.row_tiles, a.ranges ? a.ranges : a.ns, a.ranges ? 1 : a.B);
+    const dim3 grid(units_of(a) * a.row_tiles, a.ranges ? a.ranges : a.ns, a.ranges ? 1 : a.B);
     if (a.cluster)
         return launch_pdl_cluster(kern, grid, dim3(kThreads), dim3(1, a.ns, 1), (size_t)smem, stream, maps, a);
     return launch_pdl(kern, grid, dim3(kThreads), (size_t)smem, stream, maps, a);
@@ -784,7 +803,7 @@ int paged_cluster_slots(int dh, int size) {
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
     std::atomic<int> &k = known[dev][dh == 128][size];
     if (int x = k.load(std::memory_order_relaxed)) return x - 1;
-    auto kern = dh == 128 ? paged_attn_tc_kernel<128, false, true> : paged_attn_tc_kernel<64, false, true>;
+    auto kern = dh == 128 ? paged_attn_tc_kernel<128, false, kCluster> : paged_attn_tc_kernel<64, false, kCluster>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1, size);
     cfg.blockDim = dim3(kThreads);
@@ -808,7 +827,7 @@ int paged_cluster_slots(int dh, int size) {
 cudaError_t launch_paged_attention_tc(const CacheAttnArgs &a, int dh, cudaStream_t stream) {
     PagedMaps maps;
     maps.by_g = Divisor(a.H / a.Hkv);
-    maps.by_hkv = Divisor(a.Hkv);
+    maps.by_units = Divisor(units_of(a));
     if (!encode_pool(&maps.k, a.kp, a, dh) || !encode_pool(&maps.v, a.vp, a, dh)) {
         set_last_error("tensor maps of the pools could not be made (cuTensorMapEncodeTiled failed)");
         return cudaErrorInvalidValue;

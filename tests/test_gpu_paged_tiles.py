@@ -370,3 +370,59 @@ def test_clusters_captured_and_on_two_streams(dev):
         for i, c in enumerate((a, b)):
             check(out[i], q[i][k:k + 1], c, lambda _: ref.causal(c.prefix[0], c.R))
             assert status(ws[i]) == "ok"
+
+
+@pytest.mark.parametrize("B,R,H,Hkv,dh,P", [
+    (20, 20, 8, 8, 128, 300), (31, 65, 10, 5, 64, 200), (52, 33, 9, 3, 128, 90), (20, 17, 16, 8, 64, 8000),
+    (40, 128, 5, 5, 64, 130), (153, 18, 2, 1, 128, 60)])
+def test_more_tiles_than_one_wave(dev, B, R, H, Hkv, dh, P):
+    """One tile a KV head and more of those than SMs: two heads a CTA (a last one alone),
+    rows and sequences that are missing, bad pages, masks, non-finite V, waits that run out."""
+    prefix = [P] + [(37 * b) % (P if P < 400 else 150) for b in range(1, B)]
+    rows = [R, 0, 1] + [max(1, R - b % 7) for b in range(3, B)]
+    c = Case(P + R, prefix, rows, Hkv, dh, 16, BF, R=R, std=1.5)
+    q = c.randn(B, R, H, dh)
+    for h in range(Hkv):  # (what the last row of a sequence alone sees)
+        i, r = ref.spots(c.tab, 3 + h, 16, prefix[3 + h] + rows[3 + h] - 1, 1)
+        c.vp[i, r, h, 3 * h] = math.nan if h % 2 else math.inf
+    ws = workspace(c, H)
+    out = torch.full_like(q, 7.0).to(dev)
+    args, n = c.to(dev), i32(*rows).to(dev)
+
+    def call(expect="ok"):
+        m.chunk_attention_paged(q.to(dev), *args, n_rows=n, out=out, ws=ws)
+        assert status(ws) == expect
+        m.clear_device_status(ws)
+    call()
+    check(out, q, c, lambda b: ref.causal(prefix[b], rows[b]))
+    for b in range(B):
+        assert (out[b, rows[b]:] == 7).all()
+    at = P // 32
+    args[2][0, at] = c.pages
+    call("bad page")
+
+    def sees(b):
+        see = ref.causal(prefix[b], rows[b])
+        if b == 0:
+            see[:, 16 * at:16 * at + 16] = False
+        return see
+    check(out, q, c, sees)
+    args[2].copy_(c.tab)
+    budget = m.wait_budget()
+    try:
+        m.set_wait_budget(0)
+        call("timeout")
+    finally:
+        m.set_wait_budget(budget)
+    for b in range(B):
+        assert (out[b, :rows[b]] == 0).all()
+    args[3][2] = P + 1
+    call("bad prefix")
+    assert (out[2, :1] == 0).all()
+    args[3][2] = prefix[2]
+    call()
+    check(out, q, c, lambda b: ref.causal(prefix[b], rows[b]))
+    mask, _ = cache_ops_ref.tree(B, R, np.random.RandomState(R))
+    full = Case(P + R, prefix, [R] * B, Hkv, dh, 16, BF, std=1.5)
+    got = m.tree_attention_paged(q.to(dev), *full.to(dev), mask.to(dev), ws=ws)
+    check(got, q, full, lambda b: ref.tree_sees(prefix[b], R, mask[b]))
