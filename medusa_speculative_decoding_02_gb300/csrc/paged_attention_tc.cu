@@ -198,18 +198,30 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
     const int R = a.R, G = a.H / a.Hkv;
     const bool tree = a.anc_mask != nullptr;
     const int m0 = rt * kPagedTileRows;
+    const int box = min(1 << a.map.shift, 128);
+    // lane of a copying warp: one box of the tile (a box of 128 rows brings all columns)
+    const int per = box == 128 ? 1 : L::NB, copy_boxes = box == 128 ? 1 : 128 / box * L::NB;
+    const int my = lane / per, half = lane % per;
+    // What the first copies need is read at once with the prefix, not after it: the rows of the
+    // sequence, and the pages where its keys begin (of its first keys, if all are this CTA's)
+    int n_first = 0, page_first = 0;
+    if (!DEAL) {
+        n_first = live_rows(a, blockIdx.z);
+        const int at = my * box >> a.map.shift;
+        if (a.ns == 1 && warp >= 9 && at < a.map.stride) page_first = a.map.table[(size_t)blockIdx.z * a.map.stride + at];
+    }
     CacheItem it;
     // slots that the last of the first `rows` rows sees (a tree's rows: all)
     auto by_g = [&](int x) { return maps.by_g(x); };  // x / G
     auto keys_of = [&](int P, int n, int rows) { return P + (tree ? n : min(n, by_g(rows - 1) + 1)); };
     if (!find_item<DEAL, kPagedStage, true>(a, [&](int P, int b) {
-            const int n = live_rows(a, b);
+            const int n = DEAL ? live_rows(a, b) : n_first;
             return n == 0 ? 0 : DEAL ? P + n : keys_of(P, n, m0 + kPagedTileRows);
         }, it))
         return;
     const bool direct = DEAL ? it.alone : a.ns == 1;  // no join
     const int b = it.b, P = it.P;
-    const int n = live_rows(a, b), M = n * G;
+    const int n = DEAL ? live_rows(a, b) : n_first, M = n * G;
     if (m0 >= M) return;  // uniform over the CTA
     const int rows = min(kPagedTileRows, M - m0);
     // PAIR: A and B are the same rows of two KV heads, but for the last head of an odd number
@@ -241,22 +253,25 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
             a.part_ml[part_at(r, m - r * G)] = make_float2(-INFINITY, 0.f);
         }
     };
-    // The warp's 32 rows in pieces of 16 bytes, kCols pieces a row: f(row of the 32,
-    // piece, new row, query head of the group) for the lane's of each kPass rows,
-    // so that a warp's accesses to global memory are whole rows.
+    // The warp's 32 rows in pieces of 16 bytes, kCols pieces a row: f(row of the 32, piece,
+    // the row's number) for the lane's of each kPass rows, so that a warp's accesses to global
+    // memory are whole rows.  Row numbers are at(new row, query head of the group): `head` apart
+    // from head to head, `next` from the last head of a row to the first of the one after it.
     constexpr int kCols = DH / 8, kPass = 32 / kCols;
-    auto for_rows = [&](auto f) {
+    auto for_rows = [&](auto at, long long head, long long next, auto f) {
         const int first = mw + lane / kCols;
-        int rr = by_g(first), gg = first - rr * G;
-        const int dr = by_g(kPass), dg = kPass - dr * G;
-#pragma unroll 4
+        const int rr = by_g(first), dr = by_g(kPass), dg = kPass - dr * G;
+        int gg = first - rr * G;
+        const long long wrap = next - head, step = kPass * head + dr * wrap;  // (a row of G heads is passed dr times)
+        long long row = at(rr, gg);
+#pragma unroll 8
         for (int i = 0; i < 32; i += kPass) {
-            f(i + lane / kCols, lane % kCols, rr, gg);
-            rr += dr;
+            f(i + lane / kCols, lane % kCols, row);
+            row += step;
             gg += dg;
             if (gg >= G) {
                 gg -= G;
-                ++rr;
+                row += wrap;
             }
         }
     };
@@ -319,10 +334,6 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
         return wait_or_fail(full + slot_of(j, vs), (j / NK) & 1, a.wait_polls, failed);
     };
 
-    const int box = min(1 << a.map.shift, 128);
-    // lane: one box of the tile (a box of 128 rows brings all columns)
-    const int per = box == 128 ? 1 : L::NB, copy_boxes = box == 128 ? 1 : 128 / box * L::NB;
-    const int my = lane / per, half = lane % per;
     const uint32_t to = half * L::BLOCK + my * box * 128;
     const int rows_end = a.map.n_pages << a.map.shift;  // past the pool: zeros
     const int end = P + n;
@@ -330,7 +341,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
     auto row_of = [&](int j) {  // the lane's pool row of stage j
         const int slot = first_key(j) + my * box;
         if (lane >= copy_boxes || slot >= end) return rows_end;
-        const int page = a.map.page_of(b, slot);
+        const int page = !DEAL && a.ns == 1 && first_key(j) == 0 ? page_first : a.map.page_of(b, slot);
         return a.map.good(page) ? (int)a.map.row(page, slot) : rows_end;
     };
     // The copies of stage j, whose row the lane has looked up; looks up the next stage's.
@@ -357,10 +368,10 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
     if (warp < 8 && !(split && side)) {  // Q: rows that are not there are zeros
         const uint32_t qt = tc::smem_addr(sm + side * L::TILE);
         const bf16 *q = static_cast<const bf16 *>(a.q);
-        for_rows([&](int i, int c, int rr, int gg) {
+        for_rows(row_at, 1, a.H - G + 1, [&](int i, int c, long long row) {
             const bool ok = mw + i < M;
             cp_async16(qt + (c >> 3) * L::BLOCK + tc::sw128((warp & 3) * 32 + i, c & 7),
-                       ok ? q + row_at(rr, gg) * DH + c * 8 : q, ok);
+                       ok ? q + row * DH + c * 8 : q, ok);
         });
         asm volatile("cp.async.commit_group;\n" ::: "memory");
     }
@@ -739,13 +750,16 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
                 }
                 if (CLUSTER) continue;
                 __syncwarp();
-                for_rows([&](int i, int c, int rr, int gg) {
-                    if (mw + i >= M) return;
-                    if (direct)
-                        *reinterpret_cast<uint4 *>(static_cast<bf16 *>(a.out) + row_at(rr, gg) * DH + c * 8) = *piece(i, c);
-                    else
-                        *reinterpret_cast<uint4 *>(a.part_o + part_at(rr, gg) * DH + pass * wide + c * 4) = *piece(i, c);
-                });
+                if (direct)
+                    for_rows(row_at, 1, a.H - G + 1, [&](int i, int c, long long row) {
+                        const uint4 y = *piece(i, c);
+                        if (mw + i < M) *reinterpret_cast<uint4 *>(static_cast<bf16 *>(a.out) + row * DH + c * 8) = y;
+                    });
+                else
+                    for_rows(part_at, R, 1 - (long long)(G - 1) * R, [&](int i, int c, long long row) {
+                        const uint4 y = *piece(i, c);
+                        if (mw + i < M) *reinterpret_cast<uint4 *>(a.part_o + row * DH + pass * wide + c * 4) = y;
+                    });
                 __syncwarp();
             }
             if (CLUSTER)
