@@ -34,14 +34,15 @@
 // What bounds it: the products and what feeds them.  A stage of two tiles takes
 // 2490-2550 cycles, of which 2048 are its four products at the rate of the tensor cores;
 // the two of them that read both operands from shared memory leave its ports no room.  A
-// stage of one tile, by halves, takes 1470-1830.  A CTA's ends cost 11000 cycles: 4260
-// to the first copy's landing, 3090 to the first scores, 3890 behind the last product, and
-// nothing of the next CTA overlaps them, as one takes the SM's shared memory.
+// stage of one tile, by halves, takes 1470-1830.  A CTA's ends cost some 12000 cycles: 1900
+// to learn where its keys are, 3000 for the first copies and 900 for the first scores; 900
+// behind the last weights for the last product, 3900 for a tile's rows and 1600 for the
+// other's.  Nothing of the next CTA overlaps them, as one takes the SM's shared memory.
 // Measured: a prompt of 8192 rows, 32 heads over 8, dh 128: 342 us, 1610 TFLOP/s (370 us where
 // it runs without a break, at the power limit; dh 64 275 us); six chunks of 1 to 509 rows
-// behind up to 5001 slots, 28 heads over 4: 80 us, 1150 TFLOP/s, where the busiest SM has
+// behind up to 5001 slots, 28 heads over 4: 79 us, 1170 TFLOP/s, where the busiest SM has
 // two CTAs and 48 stages against 40 on average; eight trees of 65 rows behind up to 8192
-// slots, 32 heads over 8: 65 us, 2.7 TB/s; one of 32 heads behind 1024: 12.5 us (14.7 with
+// slots, 32 heads over 8: 64 us, 2.8 TB/s; one of 32 heads behind 1024: 12.5 us (14.7 with
 // a cold L2), nearly all of it the ends.
 // Pages: a page is a TMA box of up to 128 rows, whose row a lane has looked up while the
 // stage before was under way, so that 16-row pages cost what 128-row pages do (338 and 350
@@ -49,7 +50,8 @@
 // Measured and not kept: K and V copied by one warp (367, and 468 us at 16 rows), Q and O
 // moved by their rows' threads (375), weights computed against the reference before the
 // stage's maximum is known (394; registers spill), one arrival for a stage's weights instead
-// of two (383 against 376), the rows behind the last whole tile (260 rows are 256 and 4)
+// of two (383 against 376), 64 of a row's columns at a time on its way out (no change, partial
+// rows 2-4 % slower), the rows behind the last whole tile (260 rows are 256 and 4)
 // on register-operand products by warp 11 from the same stages (112-119 us against 91:
 // 58 cycles an instruction beside the others').
 #include "cache_attention.cuh"
