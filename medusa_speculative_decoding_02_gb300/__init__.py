@@ -969,6 +969,13 @@ class TokenLogprobs:
     top_logp: torch.Tensor  # fp32 [..., top]
 
 
+def _logprob_outputs(shape, top: int, device) -> TokenLogprobs:
+    f32, empty, more = torch.float32, torch.empty, (*shape, top)
+    return TokenLogprobs(empty(shape, dtype=f32, device=device), empty(shape, dtype=f32, device=device),
+                         empty(shape, dtype=_INT, device=device), empty(more, dtype=_INT, device=device),
+                         empty(more, dtype=f32, device=device))
+
+
 def token_logprobs(logits, tokens, top: int = 0, temperature: float = 1.0,
                    out: Optional[TokenLogprobs] = None, ws=None, stream=None) -> TokenLogprobs:
     """ln p of the given tokens under softmax(logits / temperature), their ranks (0: the
@@ -983,19 +990,23 @@ def token_logprobs(logits, tokens, top: int = 0, temperature: float = 1.0,
     _ints(N, V, top)
     step = _row_step(logits, "logits")
     if out is None:
-        f32, more = torch.float32, (*shape, top)
-        out = TokenLogprobs(_new(stream, logits, shape, f32), _new(stream, logits, shape, f32),
-                            _new(stream, logits, shape, _INT), _new(stream, logits, more, _INT),
-                            _new(stream, logits, more, f32))
+        if stream is None:
+            out = _logprob_outputs(shape, top, logits.device)
+        else:
+            with torch.cuda.stream(stream):
+                out = _logprob_outputs(shape, top, logits.device)
+        outs = [t.data_ptr() for t in (out.logp, out.entropy, out.rank, out.top_ids, out.top_logp)]
+    else:
+        f32 = torch.float32
+        outs = [_vec(out.logp, N, f32, dev, "logp"), _vec(out.entropy, N, f32, dev, "entropy"),
+                _vec(out.rank, N, _INT, dev, "rank")]
+        outs += [_vec(out.top_ids, N * top, _INT, dev, "top_ids"),
+                 _vec(out.top_logp, N * top, f32, dev, "top_logp")] if top else [None, None]
     if ws is None:
         ws = _scratch(WS_HEADER, logits.device, stream)
     ws_ptr, ws_n = _ws_args(ws, dev)
-    _check(lib().medusa_token_logprobs(
-        dt, logits.data_ptr(), step, _vec(tokens, N, _INT, dev, "tokens"), N, V, top, temperature,
-        _vec(out.logp, N, torch.float32, dev, "logp"), _vec(out.entropy, N, torch.float32, dev, "entropy"),
-        _vec(out.rank, N, _INT, dev, "rank"),
-        _vec(out.top_ids, N * top, _INT, dev, "top_ids") if top else None,
-        _vec(out.top_logp, N * top, torch.float32, dev, "top_logp") if top else None, ws_ptr, ws_n, st))
+    _check(lib().medusa_token_logprobs(dt, logits.data_ptr(), step, _vec(tokens, N, _INT, dev, "tokens"), N, V,
+                                       top, temperature, *outs, ws_ptr, ws_n, st))
     return out
 
 
