@@ -24,8 +24,8 @@
 //              reaches it as well), the elements that reach it are the candidates, and
 //              a candidate's place in the order is the number of better ones among them.
 //
-// What this form does not take (a NaN, +inf or nothing above -1e29 in the row, the token
-// at -inf, too many candidates because of ties, fewer possible tokens
+// What this form does not take (a NaN or +inf in the row, a largest y outside -2^29 .. 2^30,
+// the token at -inf, too many candidates because of ties, fewer possible tokens
 // than alternatives, temperatures below 1e-7) is done by slow_row, by plain passes over
 // the row: the results are the same by definition.
 //
@@ -58,7 +58,11 @@ constexpr int kCandidates = 256;
 constexpr int kMaxCluster = 4;  // 65 x 32000: 7.0 us, with 8 8.5
 constexpr uint32_t kLpPolls = 1u << 20;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kLowest = -1e30f, kNothing = -1e29f, kHighest = 1e30f, kLag = 8.f;
+constexpr float kLowest = -1e30f, kLag = 8.f;
+// References in base 2.  One of 2^30 is off by up to 32, and weights relative to it reach 2^32
+// (2^40 with kLag); further out they would leave fp32 (2^439 at a logit of -1e10).  Below -kFar
+// a thread sums nothing, which is nothing beside a row's largest of -kFar / 2 at least.
+constexpr float kFar = 0x1p30f;
 static_assert(kMaxCluster * MEDUSA_MAX_TOP_S <= kCandidates, "the parts' lists");
 
 struct LogprobArgs {
@@ -320,7 +324,8 @@ __device__ __forceinline__ void bulk_copy(void *dst, const void *src, uint32_t b
 
 // What the one pass holds for; otherwise slow_row.
 __device__ __forceinline__ bool fast_form(const LogprobArgs &a, float top, bool many, int n, int tok, float xt) {
-    return top >= kNothing && top <= kHighest && !many && n >= a.top && (tok < 0 || xt > -INFINITY) &&
+    const float t2 = __fmul_rn(top, a.y_scale);
+    return t2 >= -kFar / 2 && t2 <= kFar && !many && n >= a.top && (tok < 0 || xt > -INFINITY) &&
            a.y_scale <= 1e7f;
 }
 
@@ -435,13 +440,13 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
             const typename Lp<T>::Bound after_it = Lp<T>::bound(xt), up_to_it = Lp<T>::bound(Lp<T>::below(xt));
             typename Lp<T>::Count above;
             // m2: what the sums are relative to, in base 2 (-inf: nothing summed yet), at
-            // most kLag below the largest
+            // most kLag below the largest, and -kFar or above
             float m = -INFINITY, other = -INFINITY, m2 = -INFINITY;
             int before = 0, chunk = 0;
             float2 S[2] = {}, A[2] = {};
             auto grow = [&](float top) {
                 const float n2 = __fmul_rn(top, a.y_scale);
-                if (n2 > m2 + kLag && top >= kNothing) {  // m2 = -inf: the first possible token
+                if (n2 > m2 + kLag && n2 >= -kFar) {  // m2 = -inf: the first token that counts
                     const float d = m2 - n2, f = exp2f(d);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -665,7 +670,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
                     const float m = mine ? p->m : -INFINITY;
                     asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;\n" : "=f"(top) : "f"(m));
                     sum = asum = 0.f;
-                    if (mine && m >= kNothing) {
+                    if (mine && __fmul_rn(m, a.y_scale) >= -kFar) {  // (something was summed)
                         const float d = __fmul_rn(m, a.y_scale) - __fmul_rn(top, a.y_scale), f = exp2f(d);
                         sum = f * p->S;
                         asum = f * fmaf(p->S, d, p->A);
