@@ -25,9 +25,9 @@
 //              a candidate's place in the order is the number of better ones among them.
 //
 // What this form does not take (a NaN or +inf in the row, a largest y outside -2^29 .. 2^30,
-// the token at -inf, too many candidates because of ties, fewer possible tokens
-// than alternatives, temperatures below 1e-7) is done by slow_row, by plain passes over
-// the row: the results are the same by definition.
+// the token at -inf, too many candidates because of ties, fewer possible tokens than
+// alternatives, temperatures below 1.44e-7 or above 1.44e18) is done by slow_row, by plain
+// passes over the row: the results are the same by definition.
 //
 // Bound by issue (50 % of the slots over a launch, 67 % while all four CTAs of an SM are
 // in their rows): conversions, two packed products, an exponential and two packed sums an
@@ -63,6 +63,7 @@ constexpr float kLowest = -1e30f, kLag = 8.f;
 // (2^40 with kLag); further out they would leave fp32 (2^439 at a logit of -1e10).  Below -kFar
 // a thread sums nothing, which is nothing beside a row's largest of -kFar / 2 at least.
 constexpr float kFar = 0x1p30f;
+constexpr float kMostScale = 1e7f, kLeastScale = 1e-18f;  // log2(e) / T
 static_assert(kMaxCluster * MEDUSA_MAX_TOP_S <= kCandidates, "the parts' lists");
 
 struct LogprobArgs {
@@ -322,11 +323,13 @@ __device__ __forceinline__ void bulk_copy(void *dst, const void *src, uint32_t b
                  : "memory");
 }
 
-// What the one pass holds for; otherwise slow_row.
+// What the one pass holds for; otherwise slow_row.  Below kLeastScale (temperatures above
+// 1.4e18) kLowest, to which smaller logits and -inf are lifted, would no longer lie far below a
+// largest y of -kFar / 2 or above: there it does, by 1e30 kLeastScale - kFar / 2 > 9e11.
 __device__ __forceinline__ bool fast_form(const LogprobArgs &a, float top, bool many, int n, int tok, float xt) {
     const float t2 = __fmul_rn(top, a.y_scale);
     return t2 >= -kFar / 2 && t2 <= kFar && !many && n >= a.top && (tok < 0 || xt > -INFINITY) &&
-           a.y_scale <= 1e7f;
+           a.y_scale <= kMostScale && a.y_scale >= kLeastScale;
 }
 
 // ln p of logits of a row whose largest is `top`, with the sum relative to it

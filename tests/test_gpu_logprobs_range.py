@@ -51,3 +51,23 @@ def test_far_logits(dev, dtype, low, temp):
     x = x.to(dtype)
     for at in (0, V - 1):
         check_repeated(dev, x, torch.full((6,), at, dtype=torch.int32), 5, temp)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [8, 40, 1001, 32000])
+@pytest.mark.parametrize("temp", [1e17, 1e19, 1e25, 1e28, 4e28, 1e29, 9e29])
+def test_high_temperatures(dev, dtype, V, temp):
+    """However high the temperature, -inf is a token of probability zero, and what lies behind a
+    row in its last chunk is none at all."""
+    g = torch.Generator().manual_seed(V)
+    x = rows(g, 7, V, F32)
+    x[1] = 1.0
+    x[2, : V - 1] = -math.inf                          # one token is possible
+    x[3, 5:] = -math.inf
+    x[4, torch.rand(V, generator=g) < 0.5] = -math.inf
+    x[4, 3] = 2.0
+    x[5] = torch.rand(V, generator=g) * -3.0e38        # as far apart as the types reach
+    x[6] = torch.rand(V, generator=g) * -4e29
+    x = x.to(dtype)
+    for at in (3, V - 1):
+        check_repeated(dev, x, torch.full((7,), at, dtype=torch.int32), 5, temp)
