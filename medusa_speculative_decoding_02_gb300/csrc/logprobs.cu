@@ -287,7 +287,10 @@ __device__ __noinline__ void slow_row(const LogprobArgs &a, int row, int tok) {
     before = __reduce_add_sync(0xffffffffu, before);
     const bool none = m == -INFINITY;  // nothing is possible
     const float ls = log2f(S);
-    auto logp_of = [&](float f) { return bad ? NAN : none ? -INFINITY : (f - m) * a.inv_T - ls * kLn2; };
+    // (halves: logits may lie further apart than fp32 reaches)
+    auto logp_of = [&](float f) {
+        return bad ? NAN : none ? -INFINITY : (0.5f * f - 0.5f * m) * (2.f * a.inv_T) - ls * kLn2;
+    };
     if (lane == 0) {
         a.logp[row] = tok < 0 ? 0.f : logp_of(xt);
         a.rank[row] = tok < 0 || isnan(xt) ? -1 : before;

@@ -71,3 +71,16 @@ def test_high_temperatures(dev, dtype, V, temp):
     x = x.to(dtype)
     for at in (3, V - 1):
         check_repeated(dev, x, torch.full((7,), at, dtype=torch.int32), 5, temp)
+
+
+@pytest.mark.parametrize("temp", [1.0, 4.0, 1e3, 1e30 * 0.999])
+def test_differences_past_the_type(dev, temp):
+    """fp32 logits further apart than fp32 reaches: their log probabilities are finite where the
+    temperature makes them so."""
+    g = torch.Generator().manual_seed(3)
+    for V in (10, 5000):
+        x = (torch.rand((3, V), generator=g) * 2 - 1) * 3.3e38
+        x[1, 1:] = -3.3e38
+        x[2, 2] = -math.inf
+        for at in (1, V - 1):
+            check_repeated(dev, x, torch.full((3,), at, dtype=torch.int32), 4, temp)
