@@ -137,7 +137,9 @@ MEDUSA_API uint64_t medusa_launch_count(void);
  * fixed limit, frees its tensor memory and publishes an empty key range, so
  * the context stays usable.  Freeing assumes an issued MMA finishes within
  * the drain's limit (2^16 polls, far beyond an MMA's latency); if the drain
- * gives up too, the status reads MEDUSA_DEV_DRAIN_TIMEOUT instead.  Default 65536 polls; the environment variable
+ * gives up too, the status reads MEDUSA_DEV_DRAIN_TIMEOUT instead.  The
+ * tensor-core heads and medusa_token_logprobs wait in the same way for their
+ * copies.  Default 65536 polls; the environment variable
  * MEDUSA_FAULT_WAIT_BUDGET sets the value the library starts with.  A budget
  * of 0 makes every such wait fail at once: it exercises the timeout path
  * without a hung GPU.  Process-wide; affects launches made after the call. */
@@ -844,7 +846,9 @@ MEDUSA_API medusa_status medusa_tree_attention_paged(
  * entropy).  Where every logit is -inf, logp is -inf and the entropy 0.  A row
  * that holds a NaN or +inf has NaN in logp, entropy and top_logp; a NaN comes
  * behind all numbers in the order, has rank -1 itself and no place among the
- * alternatives (a place that no number fills has id -1).
+ * alternatives (a place that no number fills has id -1).  After a wait that ran
+ * out (MEDUSA_DEV_TIMEOUT), rows whose logits did not come have NaN in logp,
+ * entropy and top_logp, and -1 in rank and top_ids.
  * Requirements: 1 <= N <= 2^30; 1 <= V <= 2^24; top in 0..min(V, 16); temperature in
  * 1e-30..1e30.  Workspace: MEDUSA_WS_HEADER bytes (the status word).
  * ---------------------------------------------------------------------- */

@@ -15,7 +15,8 @@
 //              that are not fused, so that all sums are relative to the same number.
 //              Ranks are packed comparisons with the token's logit, or up to its place
 //              with the number below it.
-//   warp 4     bulk copies into a ring of three chunks
+//   warp 4     bulk copies into a ring of three chunks.  A wait whose polls run out sets the
+//              status, and the rows from there on get NaN
 //   warp 5     ends a row while the others are at the next: it joins the threads' sums,
 //              and finds the alternatives.  The k-th largest of 32 groups of threads'
 //              maxima (T0) is at most the row's k-th largest logit.  The few threads
@@ -56,7 +57,7 @@ constexpr int kChunk = 1024, kPer = kChunk / kConsumers;  // vectors of a chunk,
 constexpr int kRing = 3, kLpCtas = 4;
 constexpr int kCandidates = 256;
 constexpr int kMaxCluster = 4;  // 65 x 32000: 7.0 us, with 8 8.5
-constexpr uint32_t kLpPolls = 1u << 20;
+constexpr uint32_t kLpDrain = 1u << 16;  // polls for a CTA's own copies before its shared memory goes
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -1e30f, kLag = 8.f;
 // References in base 2.  One of 2^30 is off by up to 32, and weights relative to it reach 2^32
@@ -77,18 +78,21 @@ struct LogprobArgs {
     int32_t *top_ids;
     float *top_logp;
     int *status;
+    uint32_t wait_polls;  // after which a wait gives up
 };
 
 // What a CTA of a cluster knows of its part of a row.
 struct RowPart {
     float m;       // largest logit (NaN if there is one)
     float S, A;    // relative to m
-    int before, n; // tokens before the row's token; candidates (-1: too many)
+    int before, n; // tokens before the row's token; candidates (-1: too many, kLost)
     uint64_t key[MEDUSA_MAX_TOP_S];  // the part's first tokens (0: none)
 };
 
-// A thread's share of a row: the largest logit of its vectors, the chunk that holds it,
-// the largest of the other chunks; its sums and their reference in base 2.
+constexpr int kLost = -2;  // a wait for the row's logits ran out
+
+// A thread's share of a row: the largest logit of its vectors, the chunk that holds it (or
+// kLost), the largest of the other chunks; its sums and their reference in base 2.
 struct Sums {
     float m, other;
     int chunk;
@@ -104,7 +108,7 @@ struct LpSmem {
     static constexpr int SUMS = PART + (int)(sizeof(RowPart) + 15) / 16 * 16;  // of the threads
     static constexpr int COLUMNS = SUMS + kConsumers * (int)sizeof(Sums);      // [kConsumers]
     static constexpr int BAR = (COLUMNS + kConsumers * 4 + 7) / 8 * 8;
-    static constexpr int WORDS = BAR + 2 * kRing * 8;  // vectors; failed
+    static constexpr int WORDS = BAR + 2 * kRing * 8;  // vectors; failed; beat
     static constexpr int TOTAL = WORDS + 32;
     static_assert(kLpCtas * (TOTAL + 1024) <= 228 * 1024, "CTAs of an SM");
 };
@@ -254,34 +258,46 @@ struct RowShape {
     __device__ __forceinline__ int edge(int i) const { return i < left ? i : i + (last - first) * Lp<T>::N; }
 };
 
+// f(i) for the lane's share of the row's logits.  `beat` goes on with every kBeat of them, some
+// 50 us where all SMs are at this.
+constexpr int kBeat = 4096;
+template <typename F>
+__device__ __forceinline__ void each_logit(int V, volatile int *beat, F f) {
+    const int lane = threadIdx.x & 31;
+    for (int at = 0; at < V; at += kBeat) {
+        const int end = min(at + kBeat, V);
+#pragma unroll 8
+        for (int i = at + lane; i < end; i += 32) f(i);
+        if (lane == 0) *beat = *beat + 1;
+    }
+}
+
 // A row by the definition, by one warp: a pass for the maximum, one for the sums, one
 // for each alternative.
 template <typename T>
-__device__ __noinline__ void slow_row(const LogprobArgs &a, int row, int tok) {
+__device__ __noinline__ void slow_row(const LogprobArgs &a, int row, int tok, volatile int *beat) {
     const int lane = threadIdx.x & 31;
     const T *x = static_cast<const T *>(a.logits) + (long long)row * a.stride;
     const float xt = tok >= 0 ? Vec16<T>::load1(x + tok) : NAN;
     float m = -INFINITY;
     bool bad = false;  // +inf or NaN in the row
-#pragma unroll 8
-    for (int i = lane; i < a.V; i += 32) {
+    each_logit(a.V, beat, [&](int i) {
         const float f = Vec16<T>::load1(x + i);
         m = fmaxf(m, f);
         bad = bad || !(f < INFINITY);
-    }
+    });
     bad = __any_sync(0xffffffffu, bad);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float S = 0.f, A = 0.f;
     int before = 0;
-#pragma unroll 8
-    for (int i = lane; i < a.V; i += 32) {
+    each_logit(a.V, beat, [&](int i) {
         const float f = Vec16<T>::load1(x + i);
         const float t = fmaxf((f - m) * a.y_scale, -127.f), p = ex2_approx(t);
         S += p;
         A = fmaf(p, t, A);
         before += f > xt || (f == xt && i < tok);
-    }
+    });
     S = warp_sum(S);
     A = warp_sum(A);
     before = __reduce_add_sync(0xffffffffu, before);
@@ -300,12 +316,11 @@ __device__ __noinline__ void slow_row(const LogprobArgs &a, int row, int tok) {
     for (int k = 0; k < a.top; ++k) {
         uint64_t best = 0;
         if (last)
-#pragma unroll 8
-            for (int i = lane; i < a.V; i += 32) {
+            each_logit(a.V, beat, [&](int i) {
                 const float f = Vec16<T>::load1(x + i);
                 const uint64_t c = isnan(f) ? 0 : key_of(f, i);
                 if (c < last && c > best) best = c;
-            }
+            });
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             const uint64_t c = __shfl_xor_sync(0xffffffffu, (unsigned long long)best, o);
@@ -324,6 +339,29 @@ __device__ __forceinline__ void bulk_copy(void *dst, const void *src, uint32_t b
                      tc::smem_addr(dst)),
                  "l"(src), "r"(bytes), "r"(tc::smem_addr(bar))
                  : "memory");
+}
+
+// A row whose logits did not come: nothing is said of it.
+__device__ __forceinline__ void lost_row(const LogprobArgs &a, int row) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) {
+        a.logp[row] = a.entropy[row] = NAN;
+        a.rank[row] = -1;
+    }
+    if (lane < a.top) {
+        a.top_ids[(size_t)row * a.top + lane] = -1;
+        a.top_logp[(size_t)row * a.top + lane] = NAN;
+    }
+}
+
+// Wait of a converged warp for a chunk; false: the polls or another warp's ran out.
+__device__ __forceinline__ bool wait_chunk(uint64_t *bar, uint32_t parity, uint32_t limit, volatile int *failed) {
+    for (uint32_t i = 0; i < limit; ++i) {
+        if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, *failed)) return false;
+    }
+    *failed = 1;
+    return false;
 }
 
 // What the one pass holds for; otherwise slow_row.  Below kLeastScale (temperatures above
@@ -362,7 +400,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
     Sums *sums = reinterpret_cast<Sums *>(sm + LpSmem::SUMS);
     int *columns = reinterpret_cast<int *>(sm + LpSmem::COLUMNS);
     int *vectors = reinterpret_cast<int *>(sm + LpSmem::VECTORS), *n_vec = reinterpret_cast<int *>(sm + LpSmem::WORDS);
-    volatile int *failed = reinterpret_cast<volatile int *>(n_vec + 1);
+    volatile int *failed = reinterpret_cast<volatile int *>(n_vec + 1), *beat = failed + 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank_in = CLUSTER ? (int)cluster_rank() : 0;
     const int row0 = CLUSTER ? (int)blockIdx.x / C : blockIdx.x, row_step = CLUSTER ? a.N : gridDim.x;
@@ -372,7 +410,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
             tc::mbar_init(full + i, 1);
             tc::mbar_init(empty + i, kWarps);
         }
-        *failed = 0;
+        *failed = *beat = 0;
         tc::fence_mbarrier_init();
     }
     __syncthreads();
@@ -405,9 +443,17 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
                 for (int v = lo; v < hi; v += kChunk, ++it) {
                     const int at = it % kRing;
                     if (it >= kRing) {
-                        uint32_t i = 0;
-                        while (go && !tc::mbar_try_wait(empty + at, (it / kRing - 1) & 1))
-                            go = !*failed && ++i < kLpPolls;
+                        // (a row by plain passes may hold this place up for longer than the
+                        // polls last, 0.1 to 1.4 us each: they count from its last beat)
+                        int seen = *beat;
+                        go = false;
+                        for (uint32_t i = 0; i < a.wait_polls && !go && !*failed; ++i) {
+                            go = tc::mbar_try_wait(empty + at, (it / kRing - 1) & 1);
+                            if (const int now = *beat; now != seen) {
+                                seen = now;
+                                i = 0;
+                            }
+                        }
                         if (!go) {
                             *failed = 1;
                             break;
@@ -420,13 +466,14 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
             }
             // every copy has landed before the shared memory goes
             for (int i = max(0, it - kRing); i < it; ++i)
-                if (!tc::mbar_wait_bounded(full + i % kRing, (i / kRing) & 1, kLpPolls)) *failed = 1;
+                if (!tc::mbar_wait_bounded(full + i % kRing, (i / kRing) & 1, kLpDrain)) *failed = 1;
         }
         __syncwarp();
     } else if (warp < kWarps) {
         // -------------------------------------------------------------- sums
         int it = 0, tok = token_of(row0), next_tok = CLUSTER ? -1 : token_of(row0 + row_step);
         float xt = logit_of(row0, tok);
+        bool here = true;  // no wait has run out (uniform over the warp)
         for (int row = row0; row < a.N; row += row_step) {
             // (the next row's logit, and the token after it, are on their way while this row is
             // done)
@@ -465,12 +512,11 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
             };
             for (int v0 = lo; v0 < hi; v0 += kChunk, ++it) {
                 const int at = it % kRing;
-                uint32_t polls = 0;
-                while (!tc::mbar_try_wait(full + at, (it / kRing) & 1))
-                    if (*failed || ++polls == kLpPolls) {
-                        *failed = 1;
-                        break;
-                    }
+                here = here && wait_chunk(full + at, (it / kRing) & 1, a.wait_polls, failed);
+                if (!here) {
+                    chunk = kLost;
+                    break;
+                }
                 const uint4 *src = reinterpret_cast<const uint4 *>(sm + LpSmem::RING + at * kChunk * 16);
                 uint4 w[kPer];
 #pragma unroll
@@ -536,6 +582,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) x[w] = sums[w * 32 + lane];
             if (row + row_step < a.N) row_arrive<kRead>();
+            const bool lost = __any_sync(0xffffffffu, x[0].chunk == kLost || x[1].chunk == kLost ||
+                                                          x[2].chunk == kLost || x[3].chunk == kLost);
             float top = max_nan(max_nan(x[0].m, x[1].m), max_nan(x[2].m, x[3].m));
             static_assert(kWarps == 4, "four shares a lane");
             if (at_edge) top = max_nan(top, f_edge);
@@ -556,7 +604,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
             asum = warp_sum(asum);
             before = __reduce_add_sync(0xffffffffu, before);
             int n = 0;
-            if (a.top) {
+            if (a.top && !lost) {
                 float mine = -INFINITY;  // (NaNs are left out: such a row is not done here)
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) mine = fmaxf(mine, x[w].m);
@@ -633,7 +681,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
             };
             auto finish = [&](bool many, int n) {
                 if (!fast_form(a, top, many, n, tok, xt)) {
-                    slow_row<T>(a, row, tok);
+                    slow_row<T>(a, row, tok, beat);
                     return;
                 }
                 const LogP logp_of(a, top, sum);
@@ -665,7 +713,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
                     part->S = sum;
                     part->A = asum;
                     part->before = before;
-                    part->n = many ? -1 : min(n, a.top);
+                    part->n = lost ? kLost : many ? -1 : min(n, a.top);
                 }
                 __syncwarp();
                 cluster_arrive();  // the part is written
@@ -685,18 +733,23 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
                     asum = warp_sum(asum);
                     before = __reduce_add_sync(0xffffffffu, mine ? p->before : 0);
                     n = mine ? p->n : 0;
-                    const bool over = __any_sync(0xffffffffu, n < 0);
+                    const bool over = __any_sync(0xffffffffu, n < 0), gone = __any_sync(0xffffffffu, n == kLost);
                     n = __reduce_add_sync(0xffffffffu, n);
-                    if (fast_form(a, top, over, n, tok, xt)) {
+                    if (!gone && fast_form(a, top, over, n, tok, xt)) {
                         // the parts' first tokens, gathered, then placed as the candidates are
                         for (int i = lane; i < C * a.top; i += 32)
                             cand[i] = cluster_ptr(part, i / a.top)->key[i % a.top];
                         n = C * a.top;
                         __syncwarp();
                     }
-                    finish(over, n);
+                    if (gone)
+                        lost_row(a, row);
+                    else
+                        finish(over, n);
                 }
                 __syncwarp();
+            } else if (lost) {
+                lost_row(a, row);
             } else {
                 finish(many, n);
             }
@@ -736,6 +789,7 @@ cudaError_t launch_token_logprobs(medusa_dtype dtype, const void *logits, long l
     a.top_ids = top_ids;
     a.top_logp = top_logp;
     a.status = static_cast<int *>(ws);
+    a.wait_polls = wait_budget();
     // CTAs a row: as many as run at once, none with less than a chunk, or than three chunks
     // where half the SMs have a row of their own.  Rows of 4 chunks (32000 in bf16): 65 of
     // them 7.8 us with one CTA a row and 7.1 with four, 100 8.0 and 8.0, 200 9.6 and (two CTAs)
