@@ -606,9 +606,10 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(CacheAttnA
                     factor = eb < 254u ? __uint_as_float((254u - eb) << 23) : 0x1p-127f;
                     row_scale *= __uint_as_float(eb << 23);
                 }
+                // a masked score, -inf, times the scale has to stay -inf (a score, of a query
+                // below 2 and keys of at most 6 x 448, is nothing at such a scale)
+                row_scale = fmaxf(row_scale, 0x1p-126f);
             }
-            // a masked score, -inf, times the scale has to stay -inf
-            row_scale = fmaxf(row_scale, 0x1p-126f);
 #pragma unroll
             for (int half = 0; half < DH / 64; ++half) {
                 uint32_t qr[32];

@@ -413,12 +413,13 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<KV4, NQ>) cache_attn_few
                 factor = eb < 254u ? __uint_as_float((254u - eb) << 23) : 0x1p-127f;
                 row_scale *= __uint_as_float(eb << 23);
             }
+            // a masked score, -inf, times the scale has to stay -inf (a score, of a query
+            // below 2 and keys of at most 6 x 448, is nothing at such a scale)
+            row_scale = fmaxf(row_scale, 0x1p-126f);
 #pragma unroll
             for (int i = 0; i < 4 * NI; ++i)
                 qf[n][i] = pack_weights<true>(bf_lo(qf[n][i]) * factor, bf_hi(qf[n][i]) * factor);
         }
-        // a masked score, -inf, times the scale has to stay -inf
-        row_scale = fmaxf(row_scale, 0x1p-126f);
         scale[n][0] = __shfl_sync(0xffffffffu, row_scale, 8 * t);
         scale[n][1] = __shfl_sync(0xffffffffu, row_scale, 8 * t + 4);
     }

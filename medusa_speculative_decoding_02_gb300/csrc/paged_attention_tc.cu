@@ -469,8 +469,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + side * 128 + lane_base, t_o = tmem + 256 + side * DH + lane_base;
         const bool rows_live = mw < M;  // warp-uniform
-        // a masked score, -inf, times the scale has to stay -inf
-        const float row_scale = fmaxf(a.scale_log2, 0x1p-126f);
+        const float row_scale = a.scale_log2;
         if (!(split && side)) {
             asm volatile("cp.async.wait_group 0;\n" ::: "memory");
             tc::fence_proxy_async_smem();
