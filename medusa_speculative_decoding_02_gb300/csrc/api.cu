@@ -920,10 +920,9 @@ medusa_status paged_attention(const char *who, medusa_dtype dtype, const void *q
         return fail(MEDUSA_ERR_INVALID_ARG, "%s: scale must be positive and finite", who);
     if (!aligned16(q) || !aligned16(out))
         return fail(MEDUSA_ERR_INVALID_ARG, "%s: tensor pointers must be 16-byte aligned", who);
-    if (medusa_status s = check_ws(
-            ws, ws_bytes, paged_attention_workspace_bytes(dtype, B, R, H, Hkv, dh, P_max), who))
-        return s;
-    cudaError_t e = launch_paged_attention(dtype, q, k_pages, v_pages, cache, prefix_len, P_max,
+    const PagedPlan plan = paged_plan(dtype, B, R, H, Hkv, dh, P_max);
+    if (medusa_status s = check_ws(ws, ws_bytes, plan.workspace, who)) return s;
+    cudaError_t e = launch_paged_attention(plan, dtype, q, k_pages, v_pages, cache, prefix_len, P_max,
                                            anc_mask, n_rows, B, R, H, Hkv, dh, scale, out, ws,
                                            static_cast<cudaStream_t>(stream));
     if (e) return cuda_fail(e, who);
@@ -993,7 +992,7 @@ size_t medusa_paged_attention_workspace_size(medusa_dtype dtype, int B, int R, i
     if (!is_dtype(dtype) || B < 1 || B > 65535 || R < 1 || R > kMaxChunkRows || Hkv < 1 || H < Hkv ||
         H > 1024 || H % Hkv || (dh != 64 && dh != 128) || P_max < 0 || P_max > kMaxPrefix)
         return 0;
-    return paged_attention_workspace_bytes(dtype, B, R, H, Hkv, dh, P_max);
+    return paged_plan(dtype, B, R, H, Hkv, dh, P_max).workspace;
 }
 
 medusa_status medusa_chunk_attention_paged(

@@ -187,10 +187,23 @@ cudaError_t launch_commit_paged(size_t elt, void *k_pages, void *v_pages, const 
                                 const int32_t *accept_len, int B, int K, int R, int Hkv, int dh,
                                 int32_t *new_prefix_len, void *ws, cudaStream_t stream);
 
+// How an attention over pages is cut up.  A call makes one plan, for the check of its workspace
+// and for its launch.
+struct PagedPlan {
+    int row_tiles, ns;
+    int ranges;     // in all
+    bool few;       // at most kFewRows rows a KV head
+    bool vec;       // fp32, at most kVecRows
+    int simt_rows;  // of a tile of the fp32 kernel for more
+    bool deal;      // ranges dealt out by the sequences' lengths
+    bool cluster;   // the ranges of a row are the CTAs of a cluster
+    bool pair;      // a CTA works on two KV heads
+    size_t workspace;  // bytes
+};
+PagedPlan paged_plan(medusa_dtype dtype, int B, int R, int H, int Hkv, int dh, int P_max);
+
 // anc_mask == nullptr: causal rows (with n_rows or all R), otherwise a tree's.
-size_t paged_attention_workspace_bytes(medusa_dtype dtype, int B, int R, int H, int Hkv, int dh,
-                                       int P_max);
-cudaError_t launch_paged_attention(medusa_dtype dtype, const void *q, const void *k_pages,
+cudaError_t launch_paged_attention(const PagedPlan &plan, medusa_dtype dtype, const void *q, const void *k_pages,
                                    const void *v_pages, const PagedCache &cache,
                                    const int32_t *prefix_len, int P_max, const uint64_t *anc_mask,
                                    const int32_t *n_rows, int B, int R, int H, int Hkv, int dh,

@@ -555,17 +555,6 @@ cudaError_t launch_join(const CacheAttnArgs &a, cudaStream_t stream) {
 
 // ------------------------------------------------------------------- host ---
 
-struct PagedPlan {
-    int row_tiles, ns;
-    int ranges;    // in all
-    bool few;      // at most kFewRows rows a KV head
-    bool vec;      // fp32, at most kVecRows
-    int simt_rows;  // of a tile of the fp32 kernel for more
-    bool deal;     // ranges dealt out by the sequences' lengths
-    bool cluster;  // the ranges of a row are the CTAs of a cluster
-    bool pair;     // a CTA works on two KV heads
-};
-
 constexpr int kLongStages = 64, kClusterStages = 16;
 constexpr int kPairStages = 24;
 constexpr double kPairStage = 1.7;  // a stage of two heads, in stages of one
@@ -588,7 +577,7 @@ constexpr double kPairStage = 1.7;  // a stage of two heads, in stages of one
 // In one wave that is nearly full the longest sequence sets the time, so that long
 // ones (kPairStages) stay apart there: 8 ragged ones up to 4096 slots would take 69 us for 63
 // (equally long 86 for 95).  In ranges they lose to single heads (12 up to 2048: 105 for 87).
-PagedPlan paged_plan(medusa_dtype dtype, int B, int R, int H, int Hkv, int dh, int P_max) {
+PagedPlan plan_ranges(medusa_dtype dtype, int B, int R, int H, int Hkv, int dh, int P_max) {
     PagedPlan p;
     const int M = R * (H / Hkv);
     const bool simt = dtype == MEDUSA_F32;
@@ -656,21 +645,21 @@ cudaError_t launch_simt(const CacheAttnArgs &a, const PagedPlan &p, cudaStream_t
 
 }  // namespace
 
-size_t paged_attention_workspace_bytes(medusa_dtype dtype, int B, int R, int H, int Hkv, int dh,
-                                       int P_max) {
-    const PagedPlan p = paged_plan(dtype, B, R, H, Hkv, dh, P_max);
-    if (p.cluster || (p.ns == 1 && !p.deal)) return MEDUSA_WS_HEADER;
+PagedPlan paged_plan(medusa_dtype dtype, int B, int R, int H, int Hkv, int dh, int P_max) {
+    PagedPlan p = plan_ranges(dtype, B, R, H, Hkv, dh, P_max);
     const size_t rows = (size_t)p.ranges * H * R;
-    return MEDUSA_WS_HEADER + align256(rows * dh * sizeof(float)) + align256(rows * sizeof(float2)) +
-           (p.deal ? align256((B + 1) * sizeof(int)) : 0);
+    p.workspace = MEDUSA_WS_HEADER;
+    if (!p.cluster && (p.ns > 1 || p.deal))
+        p.workspace += align256(rows * dh * sizeof(float)) + align256(rows * sizeof(float2)) +
+                       (p.deal ? align256((B + 1) * sizeof(int)) : 0);
+    return p;
 }
 
-cudaError_t launch_paged_attention(medusa_dtype dtype, const void *q, const void *k_pages,
+cudaError_t launch_paged_attention(const PagedPlan &p, medusa_dtype dtype, const void *q, const void *k_pages,
                                    const void *v_pages, const PagedCache &cache,
                                    const int32_t *prefix_len, int P_max, const uint64_t *anc_mask,
                                    const int32_t *n_rows, int B, int R, int H, int Hkv, int dh,
                                    float scale, void *out, void *ws, cudaStream_t stream) {
-    const PagedPlan p = paged_plan(dtype, B, R, H, Hkv, dh, P_max);
     CacheAttnArgs a = {};
     a.q = q;
     a.kp = k_pages;
