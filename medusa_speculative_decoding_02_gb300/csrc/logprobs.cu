@@ -715,7 +715,6 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
                     part->before = before;
                     part->n = lost ? kLost : many ? -1 : min(n, a.top);
                 }
-                __syncwarp();
                 cluster_arrive();  // the part is written
                 cluster_wait();
                 if (rank_in == 0) {
@@ -760,7 +759,6 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
             cluster_arrive();
             cluster_wait();
         }
-        __syncwarp();
         cluster_arrive();  // no CTA leaves while its part may be read
         cluster_wait();
     }

@@ -281,7 +281,6 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
     // joining them, DH / 4 threads a row.  (Several rows at once, for few ranges, spills at the
     // 72 registers that the copying warps keep: 14.6 us for 10.8.)
     auto join_cluster = [&] {
-        __syncwarp();
         cluster_arrive();
         cluster_wait();
         constexpr int COLS = DH / 4;
@@ -311,7 +310,6 @@ paged_attn_tc_kernel(const __grid_constant__ PagedMaps maps, const CacheAttnArgs
                 store_row4(static_cast<bf16 *>(a.out) + row_at(rr, i - rr * G) * DH + tid % COLS * 4, acc,
                            l == 0.f ? 0.f : 1.f / l);
             }
-        __syncwarp();
         cluster_arrive();  // no CTA leaves while its rows may be read
         cluster_wait();
     };
