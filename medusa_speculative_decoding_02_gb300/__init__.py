@@ -865,6 +865,13 @@ def _pages(k_pages, v_pages, page_table, B: int, Hkv: int, dh: int, dtype, dev: 
             ks[1], _vec(page_table, B * ts[1], _INT, dev, "page_table"), ts[1])
 
 
+def _pool_heads(k_pages):
+    """(Hkv, dh) of a pool."""
+    if len(k_pages.shape) != 4:
+        raise ValueError("the pools must be [pages,page,Hkv,dh]")
+    return k_pages.shape[2:]
+
+
 def paged_append(k, v, k_pages, v_pages, page_table, prefix_len, P_max: int, n_rows=None, ws=None,
                  stream=None):
     """Rows k, v [B,R,Hkv,dh] into slots prefix_len[b] + i of a cache in pages: pools
@@ -893,8 +900,11 @@ def commit_paged(k_pages, v_pages, page_table, prefix_len, P_max: int, path, acc
     dt = _dtype(k_pages)
     dev, st = _launch_on(path, stream)
     _ints(P_max, R)
+    if len(path.shape) != 2:
+        raise ValueError("path must be [B,K+1]")
     B, K1 = path.shape
-    cache = _pages(k_pages, v_pages, page_table, B, *k_pages.shape[2:], k_pages.dtype, dev)
+    Hkv, dh = _pool_heads(k_pages)
+    cache = _pages(k_pages, v_pages, page_table, B, Hkv, dh, k_pages.dtype, dev)
     if new_prefix_len is None:
         new_prefix_len = _new(stream, prefix_len)
     if ws is None:
@@ -903,7 +913,7 @@ def commit_paged(k_pages, v_pages, page_table, prefix_len, P_max: int, path, acc
     _check(lib().medusa_commit_paged(
         dt, *cache, _vec(prefix_len, B, _INT, dev, "prefix_len"), P_max,
         _vec(path, B * K1, _INT, dev, "path"), _vec(accept_len, B, _INT, dev, "accept_len"), B, K1 - 1, R,
-        *k_pages.shape[2:], _vec(new_prefix_len, B, _INT, dev, "new_prefix_len"), ws_ptr, ws_n, st))
+        Hkv, dh, _vec(new_prefix_len, B, _INT, dev, "new_prefix_len"), ws_ptr, ws_n, st))
     return new_prefix_len
 
 
@@ -919,9 +929,7 @@ def _paged_attention(fn, q, k_pages, v_pages, page_table, prefix_len, P_max, las
     if len(q.shape) != 4 or not q.is_contiguous():
         raise ValueError("q must be a contiguous [B,R,H,dh]")
     B, R, H, dh = q.shape
-    if len(k_pages.shape) != 4:
-        raise ValueError("the pools must be [pages,page,Hkv,dh]")
-    Hkv = k_pages.shape[2]
+    Hkv = _pool_heads(k_pages)[0]
     _ints(P_max)
     cache = _pages(k_pages, v_pages, page_table, B, Hkv, dh, q.dtype, dev)
     if out is None:
@@ -983,6 +991,8 @@ def token_logprobs(logits, tokens, top: int = 0, temperature: float = 1.0,
     over the logits [..., V] (rows evenly apart); tokens int32 [...], -1 for none."""
     dt = _dtype(logits)
     dev, st = _launch_on(logits, stream)
+    if not logits.shape:
+        raise ValueError("logits must be [...,V]")
     shape, V = logits.shape[:-1], logits.shape[-1]
     N = tokens.numel()
     if tokens.shape != shape:
