@@ -359,6 +359,8 @@ MEDUSA_API medusa_status medusa_tree_attention(medusa_dtype dtype, const void *q
  *   MEDUSA_GREEDY  ([P3] Part 2): accept iff the token is that row's argmax.
  *   MEDUSA_TYPICAL ([P2] §5):  accept iff p(x) > min(eps, delta*exp(-H(p))),
  *                  p = softmax(logits / temperature), H in nats.
+ *                  A logit below -1.48e9 * temperature (-2^31 in base 2) counts
+ *                  as -inf; a row of such logits alone accepts nothing.
  * The root (the LM head's greedy token) is accepted unconditionally ([P2] §5);
  * a node counts only if all its ancestors are accepted ([P3] Part 2); the
  * deepest such node wins, the smallest canonical index among equals.

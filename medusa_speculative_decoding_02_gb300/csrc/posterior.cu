@@ -130,7 +130,10 @@ posterior_rows_kernel(const T *__restrict__ logits, int R, int V, int splits, fl
                     graw = cur[u];
                 }
                 if (TYPICAL) {
-                    const float m_new = fmaxf(mo.m, vm * y_scale);
+                    // A reference of 2^31 is off by up to 64, and weights relative to it reach
+                    // 2^64; further out (a vocabulary masked by -1e10) they would leave fp32.
+                    // Logits below -2^31 weigh nothing beside one that does, as -inf.
+                    const float m_new = fmaxf(mo.m, fmaxf(vm * y_scale, -0x1p31f));
                     if (m_new > mo.m) {
                         if (mo.S != 0.f) {
                             const float f1 = exp2f(mo.m - m_new);
@@ -369,7 +372,7 @@ posterior_select_kernel(const T *__restrict__ logits, const int32_t *__restrict_
                     const float y = y_tok * y_scale;  // loaded before the launch wait
                     const float lp2 = y - m2 - log2s;
                     const float thr2 = fminf(log2_eps, log2_delta - H * kLog2e);
-                    acc = lp2 > thr2;
+                    acc = lp2 > thr2 && log2s > -INFINITY;  // (a row without a possible token)
                 }
             }
         }
