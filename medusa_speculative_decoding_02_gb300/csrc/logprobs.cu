@@ -272,6 +272,16 @@ __device__ __forceinline__ void each_logit(int V, volatile int *beat, F f) {
     }
 }
 
+// A sum that carries what its last addition lost: off by two roundings, however many terms.
+struct LongSum {
+    float s = 0.f, lost = 0.f;
+    __device__ __forceinline__ void add(float x) {
+        const float y = x - lost, t = s + y;
+        lost = (t - s) - y;
+        s = t;
+    }
+};
+
 // A row by the definition, by one warp: a pass for the maximum, one for the sums, one
 // for each alternative.
 template <typename T>
@@ -289,17 +299,16 @@ __device__ __noinline__ void slow_row(const LogprobArgs &a, int row, int tok, vo
     bad = __any_sync(0xffffffffu, bad);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float S = 0.f, A = 0.f;
+    LongSum S_lane, A_lane;  // (a lane adds V / 32 terms)
     int before = 0;
     each_logit(a.V, beat, [&](int i) {
         const float f = Vec16<T>::load1(x + i);
         const float t = fmaxf((f - m) * a.y_scale, -127.f), p = ex2_approx(t);
-        S += p;
-        A = fmaf(p, t, A);
+        S_lane.add(p);
+        A_lane.add(p * t);
         before += f > xt || (f == xt && i < tok);
     });
-    S = warp_sum(S);
-    A = warp_sum(A);
+    const float S = warp_sum(S_lane.s), A = warp_sum(A_lane.s);
     before = __reduce_add_sync(0xffffffffu, before);
     const bool none = m == -INFINITY;  // nothing is possible
     const float ls = log2f(S);

@@ -84,3 +84,17 @@ def test_differences_past_the_type(dev, temp):
         x[2, 2] = -math.inf
         for at in (1, V - 1):
             check_repeated(dev, x, torch.full((3,), at, dtype=torch.int32), 4, temp)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [59599, 400_000, 3_000_001])
+def test_sums_of_rows_by_passes(dev, dtype, V):
+    """Rows that take plain passes (the token is impossible, or there are fewer possible ones than
+    alternatives) sum as exactly as the others, however long they are."""
+    g = torch.Generator().manual_seed(V)
+    x = torch.randn((3, V), generator=g) * 0.3
+    x[1] = torch.rand(V, generator=g) * 1e-3
+    x[2] = torch.where(torch.rand(V, generator=g) < 0.5, 0.7, 0.1)
+    x[:, 5] = -math.inf
+    x = x.to(dtype)
+    check_repeated(dev, x, torch.full((3,), 5, dtype=torch.int32), 6, 0.9)
