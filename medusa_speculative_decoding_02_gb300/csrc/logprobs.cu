@@ -480,9 +480,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
         __syncwarp();
     } else if (warp < kWarps) {
         // -------------------------------------------------------------- sums
+        // (it: the chunk's number, or kLost for good once a wait of the warp has run out)
         int it = 0, tok = token_of(row0), next_tok = CLUSTER ? -1 : token_of(row0 + row_step);
         float xt = logit_of(row0, tok);
-        bool here = true;  // no wait has run out (uniform over the warp)
         for (int row = row0; row < a.N; row += row_step) {
             // (the next row's logit, and the token after it, are on their way while this row is
             // done)
@@ -521,9 +521,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
             };
             for (int v0 = lo; v0 < hi; v0 += kChunk, ++it) {
                 const int at = it % kRing;
-                here = here && wait_chunk(full + at, (it / kRing) & 1, a.wait_polls, failed);
-                if (!here) {
-                    chunk = kLost;
+                if (it < 0 || !wait_chunk(full + at, (it / kRing) & 1, a.wait_polls, failed)) {
+                    it = chunk = kLost;
                     break;
                 }
                 const uint4 *src = reinterpret_cast<const uint4 *>(sm + LpSmem::RING + at * kChunk * 16);
@@ -591,8 +590,11 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) x[w] = sums[w * 32 + lane];
             if (row + row_step < a.N) row_arrive<kRead>();
-            const bool lost = __any_sync(0xffffffffu, x[0].chunk == kLost || x[1].chunk == kLost ||
-                                                          x[2].chunk == kLost || x[3].chunk == kLost);
+            const bool lost = __any_sync(0xffffffffu, (x[0].chunk | x[1].chunk | x[2].chunk | x[3].chunk) < 0);
+            if (!CLUSTER && lost) {
+                lost_row(a, row);
+                continue;
+            }
             float top = max_nan(max_nan(x[0].m, x[1].m), max_nan(x[2].m, x[3].m));
             static_assert(kWarps == 4, "four shares a lane");
             if (at_edge) top = max_nan(top, f_edge);
@@ -613,7 +615,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
             asum = warp_sum(asum);
             before = __reduce_add_sync(0xffffffffu, before);
             int n = 0;
-            if (a.top && !lost) {
+            if (a.top && !(CLUSTER && lost)) {
                 float mine = -INFINITY;  // (NaNs are left out: such a row is not done here)
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) mine = fmaxf(mine, x[w].m);
@@ -756,8 +758,6 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(Log
                         finish(over, n);
                 }
                 __syncwarp();
-            } else if (lost) {
-                lost_row(a, row);
             } else {
                 finish(many, n);
             }
