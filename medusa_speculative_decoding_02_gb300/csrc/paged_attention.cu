@@ -26,8 +26,8 @@ namespace {
 // of those rows' outputs.  The running maximum and sum of a row live in its 16 threads.
 // K and V of the next keys are copied while these are at work.
 //
-// Bound by the reads of shared memory and their latency: the scores read 32 bytes a thread
-// for every 8 products.  8 sequences x 8 heads behind 2048 slots, dh 128: 64 rows 171 us
+// Bound by the reads of shared memory and their latency: the scores read 96 bytes a thread
+// for every 32 products.  8 sequences x 8 heads behind 2048 slots, dh 128: 64 rows 171 us
 // (26 TFLOP/s), 32 rows 114; a single 32 x 64 tile with copies between the stages took
 // 295 and 167.  Tiles of 64 rows lose where they are too few for the SMs (two trees of 65
 // rows behind 300 slots: 17.5 us for 14.4).
