@@ -624,7 +624,11 @@ PagedPlan plan_ranges(medusa_dtype dtype, int B, int R, int H, int Hkv, int dh, 
     // out, which the longer ones take.  Trees of 64 or 65 rows, 32 heads over 8, dh 128, half the
     // sequences short: 8 of up to 8192 slots 91 -> 65 us and 16 of them 94 -> 74 (all
     // equally long 94 -> 98, 101 -> 106), but 16 of up to 4096 53 -> 53 and 8 of up to
-    // 2048 30 -> 35; with one tile of rows a CTA (4 of 65 rows, 32 heads over 32), where
+    // 2048 30 -> 35.  By the stages of the longest, 8 of 65 rows: 33 51 -> 45 (equally long 52
+    // -> 55), 40 60 -> 52 (61 -> 64), 48 70 -> 53 (71 -> 74), 56 80 -> 58 (81 -> 84); 16 of 64:
+    // 40 63 -> 59 (67 -> 71), 48 73 -> 64 (78 -> 83), 56 84 -> 69 (89 -> 93).  From
+    // kLongStages on it saves four to seven times what it costs where all are equally long.
+    // With one tile of rows a CTA (4 of 65 rows, 32 heads over 32), where
     // the copies set the time, 71 -> 78.
     if (!simt && !p.few && p.ns == 1 && B > 1 && B <= 32 && M > kPagedTileRows / 2 &&
         subs >= kLongStages && ctas <= slots) {
